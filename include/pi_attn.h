@@ -42,7 +42,7 @@
  * points take fp32.  alpha, lse and dalpha are always fp32.
  *
  * Ownership.  The caller owns every buffer and the stream.  The library never
- * allocates per call; the only device state it keeps is one int status word
+ * allocates per call; the only device state it keeps is two int status words
  * per device, a static device variable.
  *
  * Asynchrony.  Every compute entry point only enqueues work on `stream`
@@ -69,6 +69,11 @@
  *                      clears it, later launches on that device give up at their
  *                      first wait that is not already satisfied, so their
  *                      outputs are undefined.
+ *   PI_ERR_INDEX       (from pi_attn_status) a kernel of the paged cache met a
+ *                      page-table entry, offset or length out of range; nothing
+ *                      outside the caller's buffers was read or written, and the
+ *                      work concerned was left out (see each call).  Later launches
+ *                      are not affected.
  */
 #ifndef PI_ATTN_H_
 #define PI_ATTN_H_
@@ -89,7 +94,8 @@ typedef enum {
     PI_ERR_ALIGN = -4,
     PI_ERR_WORKSPACE = -5,
     PI_ERR_CUDA = -6,
-    PI_ERR_DEVICE_TIMEOUT = -7
+    PI_ERR_DEVICE_TIMEOUT = -7,
+    PI_ERR_INDEX = -8
 } pi_status_t;
 
 /*
@@ -273,10 +279,106 @@ int pi_attn_decode(const void *q, const void *k_cache, const void *v_cache, cons
                    int B, int H, int Hkv, int N, int d, int k_local, int period, int S, int mode,
                    void *out, float *lse, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Paged key/value cache: sequences of different lengths in one batch, their rows in
+ * pages that a table names, in bf16 or in 8 bits.
+ *
+ * pi_attn_cache_t -- the pages of one layer.
+ *   k, v [n_pages, Hkv, page, d]: bf16 (PI_KV_BF16), or one byte per element:
+ *   e4m3 codes (PI_KV_E4M3) or two's complement codes -127..127 (PI_KV_INT8).
+ *   k_scale, v_scale [n_pages, Hkv, page, d / 32] bytes (8 bits only; else NULL): byte s
+ *   scales the 32 codes of its block by 2^(s - 127).  A block's scale is the smallest
+ *   power of two, at least 2^-120, that brings its largest magnitude to at most 448
+ *   (e4m3) or 127 (int8); codes are rounded to nearest even.  Reading multiplies the
+ *   code by the scale, which bf16 holds exactly (a code that was rounded up to 2^128 or
+ *   more, which only an element above 0.96 * 2^128 can be, reads as an infinity).  A
+ *   block with an infinity or a NaN gets s = 255 and reads back as NaN.
+ *   d: 64 or 128; page: 16, 32, 64, 128 or 256 rows; n_pages * Hkv * page < 2^31;
+ *   all four pointers 16-byte aligned.
+ *
+ * pi_attn_batch_t -- B sequences and their packed tokens.
+ *   table [B, width] int32: page table[b][p / page] holds position p of sequence b in its
+ *   row p % page.  Only entries of pages that hold a row the call touches are read: a
+ *   page whose rows no later query attends may be taken away (any entry in its place).
+ *   cu [B + 1] int32: sequence b has the packed tokens cu[b] .. cu[b+1] - 1, possibly
+ *   none; cu[0] = 0 and cu[B] <= T.  Tokens cu[B] .. T - 1 belong to no sequence: nothing
+ *   of theirs is written.  ctx [B] int32: the position of a sequence's first token, i.e.
+ *   the rows it has in the cache already.  ctx[b] + cu[b+1] - cu[b] <= width * page.
+ *   These three live on the device; the kernels check them (PI_ERR_INDEX).
+ *
+ * Ownership, asynchrony and errors are those of the other calls.  Sequences that share
+ * pages may read them; two tokens of one call written to the same row race.
+ */
+typedef enum { PI_KV_BF16 = 0, PI_KV_E4M3 = 1, PI_KV_INT8 = 2 } pi_kv_type_t;
+
+typedef struct {
+    void *k, *v;
+    void *k_scale, *v_scale;
+    int kv_type, n_pages, Hkv, page, d;
+} pi_attn_cache_t;
+
+typedef struct {
+    const int *table, *cu, *ctx;
+    int B, T, width;
+} pi_attn_batch_t;
+
+/*
+ * pi_attn_cache_append -- writes the batch's new key and value rows into the cache,
+ * quantised where it holds 8 bits.
+ *   k, v [T, Hkv, d] bf16; a token's Hkv * d elements are contiguous, tokens lie k_stride
+ *   (v_stride) elements apart: at least Hkv * d, a multiple of 8 (else PI_ERR_SHAPE), so
+ *   that both may be slices of one projection's output.  16-byte aligned.
+ *   A token whose sequence or page is out of range is not written.
+ */
+int pi_attn_cache_append(const void *k, const void *v, long long k_stride, long long v_stride,
+                         const pi_attn_cache_t *cache, const pi_attn_batch_t *batch, void *stream);
+
+/*
+ * pi_attn_cache_read -- the cache's rows at the batch's positions, as bf16:
+ *   k, v [T, Hkv, d], contiguous.  Exact: what an 8-bit cache holds are bf16 numbers.
+ *   Rows of tokens that belong to no sequence, or whose sequence or page is out of range, are
+ *   left as they were.
+ */
+int pi_attn_cache_read(const pi_attn_cache_t *cache, const pi_attn_batch_t *batch, void *k, void *v,
+                       void *stream);
+
+/*
+ * pi_attn_extend -- pi_attn_fwd's rows for a chunk of new tokens per sequence, against a
+ * paged cache that holds their sequences' rows up to and including the chunk's own
+ * (append first).  The token at position i of its sequence attends U(i) in causal pi mode
+ * or ECP mode (bidirectional: PI_ERR_UNSUPPORTED).
+ *   q [T, H, d] bf16 with tokens q_stride elements apart (rules as for
+ *   pi_attn_cache_append), alpha [T, H] fp32 (NULL in ECP mode), out [T, H, d] bf16 and
+ *   lse [T, H] fp32, contiguous.  H % Hkv == 0; T * H < 2^31.
+ *   A sequence with an offset or length out of range is left out, its rows of out and lse
+ *   as they were; a row that attends a key on a page out of range is undefined.
+ *   Non-finite values in cache rows that no query of the chunk attends do not matter;
+ *   a non-finite value in a row that some query attends may reach the outputs of the
+ *   sequence's other queries within 128 positions.
+ */
+int pi_attn_extend(const void *q, long long q_stride, const pi_attn_cache_t *cache,
+                   const pi_attn_batch_t *batch, const float *alpha, int H, int k_local, int period,
+                   int S, int mode, void *out, float *lse, void *stream);
+
+/*
+ * pi_attn_decode_paged -- pi_attn_extend for one new token per sequence: pi_attn_decode
+ * against a paged cache with a length for each sequence.
+ *   lens [B] int32 (device): rows of sequence b in the cache, the new token's own among
+ *   them (its position is lens[b] - 1).  lens[b] = 0 gives out = 0 and lse = -inf, as does
+ *   a length out of range.  q [B, H, d] bf16 with sequences q_stride elements apart,
+ *   alpha [B, H] fp32 (NULL in ECP mode), out [B, H, d] bf16, lse [B, H] fp32; table
+ *   [B, width] as above.  H / Hkv <= 16; B and Hkv <= 65535.  A row that attends a key on
+ *   a page out of range is undefined.
+ */
+int pi_attn_decode_paged(const void *q, long long q_stride, const pi_attn_cache_t *cache,
+                         const int *table, const int *lens, int B, int width, const float *alpha,
+                         int H, int k_local, int period, int S, int mode, void *out, float *lse,
+                         void *stream);
+
 /*
  * pi_attn_status -- synchronises `stream`, reads the current device's status
- * word, resets it to PI_OK and returns what it held (PI_OK or
- * PI_ERR_DEVICE_TIMEOUT), or PI_ERR_CUDA if the synchronisation failed.
+ * word, resets it to PI_OK and returns what it held (PI_OK, PI_ERR_DEVICE_TIMEOUT or
+ * PI_ERR_INDEX), or PI_ERR_CUDA if the synchronisation failed.
  */
 int pi_attn_status(void *stream);
 

@@ -10,17 +10,22 @@
 
 #include "pi_attn.h"
 #include "pi_launch.h"
+#include "pi_paged.h"
 
 namespace {
 
-__device__ int g_status_word;
+__device__ int g_words[2];  // status of the bounded waits; out-of-range indexes
 
 constexpr uint64_t kWaitTimeoutNs = 2000000000ull;  // bound on every device-side wait
 constexpr int kMaxDevices = 64;
 constexpr int kDebugMaxN = 2048;
 
-// Device address of g_status_word for the current device, looked up once per device (two
-// threads may both look it up the first time; they store the same address).
+}  // namespace
+
+namespace pi {
+
+// Device address of g_words for the current device, looked up once per device (two threads may
+// both look it up the first time; they store the same address).
 int *status_word() {
     static std::atomic<int *> cache[kMaxDevices];
     int dev = 0;
@@ -28,12 +33,23 @@ int *status_word() {
     int *p = cache[dev].load(std::memory_order_acquire);
     if (!p) {
         void *a = nullptr;
-        if (cudaGetSymbolAddress(&a, g_status_word) != cudaSuccess) return nullptr;
+        if (cudaGetSymbolAddress(&a, g_words) != cudaSuccess) return nullptr;
         p = static_cast<int *>(a);
         cache[dev].store(p, std::memory_order_release);
     }
     return p;
 }
+
+int *index_word() {
+    int *p = status_word();
+    return p ? p + 1 : nullptr;
+}
+
+}  // namespace pi
+
+namespace {
+
+using pi::status_word;
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -292,11 +308,11 @@ int pi_attn_status(void *stream) {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return PI_ERR_CUDA;
     int *status = status_word();
     if (!status) return PI_ERR_CUDA;
-    int value = 0;
-    if (cudaMemcpy(&value, status, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return PI_ERR_CUDA;
-    const int zero = 0;
-    if (cudaMemcpy(status, &zero, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess) return PI_ERR_CUDA;
-    return value;
+    int value[2] = {0, 0};
+    if (cudaMemcpy(value, status, sizeof(value), cudaMemcpyDeviceToHost) != cudaSuccess) return PI_ERR_CUDA;
+    const int zero[2] = {0, 0};
+    if (cudaMemcpy(status, zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess) return PI_ERR_CUDA;
+    return value[0] != PI_OK ? value[0] : value[1];
 }
 
 const char *pi_attn_strerror(int code) {
@@ -309,6 +325,7 @@ const char *pi_attn_strerror(int code) {
         case PI_ERR_WORKSPACE: return "PI_ERR_WORKSPACE: workspace missing or too small";
         case PI_ERR_CUDA: return "PI_ERR_CUDA: CUDA runtime error";
         case PI_ERR_DEVICE_TIMEOUT: return "PI_ERR_DEVICE_TIMEOUT: a device-side wait gave up";
+        case PI_ERR_INDEX: return "PI_ERR_INDEX: a page-table entry, offset or length out of range";
         default: return "unknown pi_attn status";
     }
 }

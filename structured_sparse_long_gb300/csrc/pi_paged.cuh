@@ -1,0 +1,124 @@
+// pi_paged.cuh -- the paged key/value cache: where a position's row is, and what an 8-bit row holds.
+//
+// Position p of sequence b is row p % page of page table[b][p / page]; a page holds, per KV head,
+// `page` rows of d elements ([n_pages][Hkv][page][d]).  An 8-bit row keeps, per block of 32
+// elements, codes c and one byte s standing for the scale 2^(s - 127): element = c * 2^(s - 127).
+// The scale is the smallest power of two, at least 2^-120, that brings the block's largest
+// magnitude to at most 448 (e4m3) or 127 (int8).  A power of two scales exactly, so a code is the
+// element rounded once (half a step of the code's own grid), and c * 2^(s - 127) is a bf16 number:
+// an e4m3 code has 4 significant bits and an int8 code at most 7, and with scales of 2^-120 or more the
+// smallest code, 2^-9 * 2^-120, is still a multiple of bf16's smallest 2^-133 (an element above
+// 0.96 * 2^128 may round up to 2^128, which reads as an infinity).  A block with an
+// infinity or a NaN gets the byte 255 (NaN) and reads back as NaN.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "pi_common.cuh"
+#include "pi_paged.h"
+
+namespace pi {
+
+constexpr int kScaleBlock = 32;       // elements per scale byte
+constexpr int kScaleNan = 255;        // byte of a block with a non-finite element
+constexpr int kMinScaleExp = -120;
+
+__device__ __forceinline__ void record_index(int *word) { atomicCAS(word, kStatusOk, kStatusIndex); }
+
+// Row of the cache (of the [n_pages * Hkv * page] rows) that holds position pos of sequence b for
+// KV head 0, or -1 for a page-table entry outside the pool.  pos must be inside [0, width * page).
+__device__ __forceinline__ int page_of(const PagedCache &c, const int *table, long long b, int pos) {
+    const int pg = __ldg(table + b * c.width + (pos >> c.page_log2));
+    return (unsigned)pg < (unsigned)c.n_pages ? pg : -1;
+}
+__device__ __forceinline__ int row_in_page(const PagedCache &c, int pg, int g, int pos) {
+    return ((pg * c.Hkv + g) << c.page_log2) + (pos & (c.page - 1));
+}
+
+// 2^(byte - 127) as fp32 (255: NaN).
+__device__ __forceinline__ float scale_of(int byte) {
+    return byte == kScaleNan ? __int_as_float(0x7fffffff) : __int_as_float(byte << 23);
+}
+
+// Exponent e of a block's scale 2^e from its largest magnitude (finite, >= 0): the smallest
+// e >= kMinScaleExp with amax <= Q * 2^e.  448 = 1.75 * 2^8 and 127 = 1.984375 * 2^6, so e follows
+// from amax's exponent and from whether its significand exceeds Q's.
+template <int KV>
+__device__ __forceinline__ int scale_exp(float amax) {
+    const uint32_t u = __float_as_uint(amax);
+    constexpr uint32_t kTop = KV == kKvE4m3 ? 0x600000u : 0x7e0000u;  // fraction bits of 1.75, 1.984375
+    constexpr int kUp = KV == kKvE4m3 ? 8 : 6;
+    const int e = (int)(u >> 23) - 127 - kUp + ((u & 0x7fffffu) > kTop ? 1 : 0);
+    return max(e, kMinScaleExp);  // subnormal amax: far below the floor of the scales
+}
+
+// Sequence of packed token t: the number of j in [1, B] with cu[j] <= t (B: t is behind the last
+// sequence).  Searched by the whole warp, 32 probes at a time; ends for any contents of cu.
+__device__ __forceinline__ int find_sequence(const int *cu, int B, int t) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, len = B;
+    while (len > 0) {
+        const int step = (len + 31) >> 5;
+        const int k = (lane + 1) * step;
+        const bool below = k <= len && __ldg(cu + lo + k) <= t;
+        const int c = __popc(__ballot_sync(0xffffffffu, below));
+        lo += c * step;
+        len = min(step - 1, len - c * step);
+    }
+    return lo;
+}
+
+// Whether a sequence's offsets and context are in range: its tokens inside the batch, its rows inside
+// its page table.
+__device__ __forceinline__ bool sequence_ok(const PagedCache &c, const PagedBatch &bt, int t0, int t1, int ctx) {
+    return t0 >= 0 && t0 <= t1 && t1 <= bt.T && ctx >= 0 && (long long)ctx + (t1 - t0) <= (long long)c.width << c.page_log2;
+}
+
+// Position of packed token t in its sequence b, or -1 (t behind the last sequence, or an index out of
+// range, which is recorded).  For the whole warp.
+__device__ __forceinline__ int locate(const PagedCache &c, const PagedBatch &bt, int t, int &b, int *index_word) {
+    b = find_sequence(bt.cu, bt.B, t);
+    if (b >= bt.B) return -1;
+    const int t0 = __ldg(bt.cu + b), t1 = __ldg(bt.cu + b + 1), ctx = __ldg(bt.ctx + b);
+    if (!sequence_ok(c, bt, t0, t1, ctx) || t < t0 || t >= t1) {
+        record_index(index_word);
+        return -1;
+    }
+    return ctx + t - t0;
+}
+
+// Eight codes and their scale to eight bf16 (exact, see above).
+template <int KV>
+__device__ __forceinline__ uint4 decode8(uint2 c, float scale) {
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t two = (i < 2 ? c.x : c.y) >> (16 * (i & 1)) & 0xffffu;
+        float a, b;
+        if (KV == kKvE4m3) {
+            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+            const float2 f = __half22float2(__half2(h));
+            a = f.x;
+            b = f.y;
+        } else {
+            a = (float)(int8_t)(two & 0xffu);
+            b = (float)(int8_t)(two >> 8);
+        }
+        const __nv_bfloat162 r = __floats2bfloat162_rn(a * scale, b * scale);
+        o[i] = *reinterpret_cast<const uint32_t *>(&r);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Eight elements of a cache row as bf16.
+template <int KV>
+__device__ __forceinline__ uint4 get8(const PagedCache &c, const void *pages, const uint8_t *scales, long long row, int col) {
+    if (KV == kKvBf16) return __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(pages) + row * c.d + col));
+    const uint2 codes = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(pages) + row * c.d + col));
+    return decode8<KV>(codes, scale_of(__ldg(scales + row * (c.d / kScaleBlock) + col / kScaleBlock)));
+}
+
+}  // namespace pi

@@ -1,0 +1,89 @@
+// pi_paged.h -- host-side launch descriptors of the paged key/value cache's operators, shared by the
+// C ABI and the kernel files.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "pi_common.cuh"
+
+namespace pi {
+
+constexpr int kStatusIndex = -8;  // a device-side index out of range (PI_ERR_INDEX)
+
+// What the pages of a paged cache hold (pi_kv_type_t).
+constexpr int kKvBf16 = 0, kKvE4m3 = 1, kKvInt8 = 2;
+
+// A paged key/value cache and the width of its users' page tables; sizes are checked on the host
+// (page a power of two, d 64 or 128, n_pages * Hkv * page < 2^31 rows).
+struct PagedCache {
+    void *k, *v;                 // [n_pages, Hkv, page, d] bf16 or 8-bit codes
+    uint8_t *k_scale, *v_scale;  // [n_pages, Hkv, page, d / 32], 8 bits only
+    int kv_type, n_pages, Hkv, page, page_log2, d, d_log2;
+    int width;                   // page-table entries per sequence
+};
+
+// A packed batch: sequence b has the tokens cu[b] .. cu[b+1]-1 of T, at positions ctx[b] ...
+struct PagedBatch {
+    const int *table;  // [B, width]
+    const int *cu;     // [B + 1]
+    const int *ctx;    // [B]
+    int B, T;
+};
+
+struct AppendArgs {
+    const __nv_bfloat16 *k, *v;     // [T, Hkv, d], tokens k_stride and v_stride elements apart
+    long long k_stride, v_stride;
+    PagedCache cache;
+    PagedBatch batch;
+    int *index_word;
+};
+
+struct ReadArgs {
+    __nv_bfloat16 *k, *v;  // [T, Hkv, d]
+    PagedCache cache;
+    PagedBatch batch;
+    int *index_word;
+};
+
+struct ExtendArgs {
+    const __nv_bfloat16 *q;  // [T, H, d], tokens q_stride elements apart
+    long long q_stride;
+    const float *alpha;      // [T, H] or null (ECP)
+    __nv_bfloat16 *out;      // [T, H, d]
+    float *lse;              // [T, H]
+    Shape s;                 // H, Hkv, d, k_local, period, S, mode, scale_log2
+    PagedCache cache;
+    PagedBatch batch;
+    int *status, *index_word;
+    uint64_t timeout_ns;
+};
+
+struct DecodePagedArgs {
+    const __nv_bfloat16 *q;  // [B, H, d], sequences q_stride elements apart
+    long long q_stride;
+    const float *alpha;      // [B, H] or null (ECP)
+    const int *table;        // [B, width]
+    const int *lens;         // [B] rows of the cache, the new token's among them
+    __nv_bfloat16 *out;      // [B, H, d]
+    float *lse;              // [B, H]
+    Shape s;
+    PagedCache cache;
+    int *index_word;
+};
+
+// rows into and out of a paged cache (pi_cache.cu)
+cudaError_t launch_append(const AppendArgs &a, cudaStream_t st);
+cudaError_t launch_cache_read(const ReadArgs &a, cudaStream_t st);
+
+// attention over a paged cache: a chunk of new tokens per sequence, one new token per sequence
+cudaError_t launch_extend(const ExtendArgs &a, cudaStream_t st);
+cudaError_t launch_decode_paged(const DecodePagedArgs &a, cudaStream_t st);
+
+// Device words of the current device, looked up once per device (api.cu): the status word of the
+// bounded waits, and the one that out-of-range indexes are recorded in.  Null on a CUDA error.
+int *status_word();
+int *index_word();
+
+}  // namespace pi

@@ -1,0 +1,451 @@
+"""GPU parity of the paged key/value cache: append, read back, chunk attention, single-token attention.
+
+Codes, scales and read-back values are compared bit for bit with a 64-bit restatement of the formats;
+attention with the fp64 oracle, sequence by sequence, on the values the cache holds.  Page tables are
+shuffled, contexts ragged; every page row that no query attends holds NaN."""
+import numpy as np
+import pytest
+import torch
+
+import paged_ref as ref
+import structured_sparse_long_gb300 as pa
+from structured_sparse_long_gb300 import build as pbuild
+
+pytestmark = pytest.mark.gpu
+
+PI, ECP = pa.MODE_PI, pa.MODE_ECP
+ERR_INDEX = -8
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    pbuild.build()
+    assert torch.cuda.is_available(), "GPU tests need CUDA"
+    pa.load()
+    yield
+    assert pa.status() == 0
+
+
+def dev(x):
+    return torch.as_tensor(np.ascontiguousarray(x), dtype=torch.int32).cuda()
+
+
+def nan_cache(pages, Hkv, page, d, kv):
+    """A cache whose every row reads as NaN."""
+    if kv == "bf16":
+        return pa.PagedCache(*(torch.full((pages, Hkv, page, d), float("nan"), dtype=torch.bfloat16).cuda() for _ in range(2)))
+    k, v = (torch.full((pages, Hkv, page, d), 0x7F, dtype=torch.uint8).cuda().view(ref.DTYPE[kv]) for _ in range(2))
+    return pa.PagedCache(k, v, *(torch.full((pages, Hkv, page, d // 32), 255, dtype=torch.uint8).cuda() for _ in range(2)))
+
+
+def normal(gen, *shape):
+    return torch.randn(*shape, generator=gen).to(torch.bfloat16)
+
+
+class Batch:
+    """Sequences with ctx cached rows and n new ones, their values, and a cache of NaN rows."""
+
+    def __init__(self, ctx, n, Hkv, d, page, kv, seed, extra_tokens=0):
+        self.rng, self.gen = np.random.default_rng(seed), torch.Generator().manual_seed(seed)
+        self.ctx, self.n, self.kv, self.page, self.Hkv, self.d = ctx, n, kv, page, Hkv, d
+        self.table, pages = ref.make_table(ctx, n, page, self.rng)
+        self.cache = nan_cache(pages, Hkv, page, d, kv)
+        self.cu = ref.offsets(n)
+        self.T = int(self.cu[-1]) + extra_tokens
+        self.k = [normal(self.gen, c + m, Hkv, d) for c, m in zip(ctx, n)]
+        self.v = [normal(self.gen, c + m, Hkv, d) for c, m in zip(ctx, n)]
+
+    def write(self, what="all", keep=None):
+        """Appends rows 0 .. ctx + n of every sequence (those of the pages in keep[b], if given)."""
+        for b, (c, m) in enumerate(zip(self.ctx, self.n)):
+            for p in range(0, c + m, self.page):
+                if keep is not None and p // self.page not in keep[b]:
+                    continue
+                rows = slice(p, min(p + self.page, c + m))
+                cnt = rows.stop - rows.start
+                pa.cache_append(self.k[b][rows].cuda(), self.v[b][rows].cuda(), self.cache, dev(self.table[b:b + 1]),
+                                dev([0, cnt]), dev([p]))
+
+    def held(self):
+        """The values the cache holds for each sequence's rows, as bf16 tensors."""
+        if self.kv == "bf16":
+            return self.k, self.v
+        return tuple([torch.from_numpy(ref.decode(*ref.encode(x.float().numpy(), self.kv), self.kv)).to(torch.bfloat16)
+                      for x in xs] for xs in (self.k, self.v))
+
+
+# ------------------------------------------------------------------ append and read
+
+APPEND = [
+    # kv, d, Hkv, page, ctx, n, tokens of no sequence behind the last
+    ("e4m3", 128, 4, 64, [0, 63, 64, 100], [1, 1, 1, 1], 0),
+    ("int8", 64, 1, 16, [5], [70], 0),
+    ("bf16", 128, 2, 32, [0, 31, 7], [33, 0, 1], 5),
+    ("e4m3", 64, 3, 16, [15, 0, 16, 2, 9], [0, 17, 0, 47, 1], 3),
+    ("int8", 128, 12, 256, [250, 1], [7, 300], 1),
+    ("bf16", 64, 16, 128, [127], [130], 0),
+]
+
+
+@pytest.mark.parametrize("case", APPEND, ids=[f"{c[0]}-d{c[1]}-h{c[2]}-p{c[3]}" for c in APPEND])
+def test_append_writes_the_new_rows_and_nothing_else(case):
+    kv, d, Hkv, page, ctx, n, extra = case
+    bt = Batch(ctx, n, Hkv, d, page, kv, seed=d + page, extra_tokens=extra)
+    H = 2 * Hkv  # the projection's output: queries in front of the keys and values
+    qkv = normal(bt.gen, bt.T, H + 2 * Hkv, d)
+    before = [None if t is None else ref.bits(t).copy() for t in (bt.cache.k, bt.cache.v, bt.cache.k_scale, bt.cache.v_scale)]
+    x = qkv.cuda()
+    pa.cache_append(x[:, H:H + Hkv], x[:, H + Hkv:], bt.cache, dev(bt.table), dev(bt.cu), dev(bt.ctx))
+    torch.cuda.synchronize()
+    for i, (pages, scales, first) in enumerate(((bt.cache.k, bt.cache.k_scale, H), (bt.cache.v, bt.cache.v_scale, H + Hkv))):
+        rows = qkv[:, first:first + Hkv]
+        want, want_s = before[i], before[i + 2]
+        codes, sc = (ref.bits(rows), None) if kv == "bf16" else ref.encode(rows.float().numpy(), kv)
+        for b in range(len(ctx)):
+            for t in range(bt.cu[b], bt.cu[b + 1]):
+                pos = ctx[b] + t - bt.cu[b]
+                at = (bt.table[b, pos // page], slice(None), pos % page)
+                want[at] = codes[t]
+                if sc is not None:
+                    want_s[at] = sc[t]
+        assert np.array_equal(ref.bits(pages), want)
+        if sc is not None:
+            assert np.array_equal(ref.bits(scales), want_s)
+    # and back: exactly what the codes stand for, nothing of the tokens of no sequence
+    k, v = (torch.full((bt.T, Hkv, d), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    got = pa.cache_read(bt.cache, dev(bt.table), dev(bt.cu), dev(bt.ctx), bt.T, k=k, v=v)
+    torch.cuda.synchronize()
+    m = int(bt.cu[-1])
+    for t, first in zip(got, (H, H + Hkv)):
+        rows = qkv[:m, first:first + Hkv].float().numpy()
+        want = rows if kv == "bf16" else ref.decode(*ref.encode(rows, kv), kv)
+        assert np.array_equal(t[:m].float().cpu().numpy().astype(np.float64), want)
+        assert (t[m:] == 7.0).all()
+
+
+@pytest.mark.parametrize("kv", ["e4m3", "int8"])
+def test_quantisation_at_the_edges(kv):
+    """Blocks whose largest magnitude is zero, the type's smallest and largest, exactly a scaled code's largest
+    and just above it; every tie between codes; an infinity or a NaN in one block only."""
+    q = ref.QMAX[kv]
+    rows = []
+    for amax in (0.0, 2.0 ** -133, 2.0 ** -120, q * 2.0 ** -120, 2.0 ** -100, 1.0, q, q * 2, 2.0 ** 100, 3.3895e38, q * 2.0 ** 110):
+        for up in (1.0, 1 + 2.0 ** -7, 1 - 2.0 ** -7):
+            x = np.linspace(-1, 1, 128) * amax * up
+            x[::32] = amax * up
+            rows.append(x)
+    ties = np.concatenate([np.arange(128) + 0.5, -(np.arange(128) + 0.5)]).reshape(2, 128) * (1 if kv == "int8" else 2.0 ** -9)
+    rows += [np.clip(t, -q, q) for t in ties]
+    bad = np.ones((3, 128))
+    bad[0, 40], bad[1, 127], bad[2, 0] = np.inf, np.nan, -np.inf
+    x = torch.from_numpy(np.concatenate([np.stack(rows), bad])).to(torch.bfloat16)[:, None].contiguous()
+    T = x.shape[0]
+    cache = pa.PagedCache.empty(-(-T // 16), 1, 16, 128, ref.DTYPE[kv])
+    table, cu, ctx = dev(np.arange(-(-T // 16))[None]), dev([0, T]), dev([0])
+    pa.cache_append(x.cuda(), (-x).cuda(), cache, table, cu, ctx)
+    k, v = pa.cache_read(cache, table, cu, ctx, T)
+    torch.cuda.synchronize()
+    for got, pages, scales, src in ((k, cache.k, cache.k_scale, x), (v, cache.v, cache.v_scale, -x)):
+        codes, sc = ref.encode(src.float().numpy(), kv)
+        assert np.array_equal(ref.bits(pages).reshape(-1, 1, 128)[:T], codes)
+        assert np.array_equal(ref.bits(scales).reshape(-1, 1, 4)[:T], sc)
+        assert np.array_equal(got.float().cpu().numpy().astype(np.float64), ref.decode(codes, sc, kv), equal_nan=True)
+
+
+@pytest.mark.parametrize("B", [1, 31, 32, 33, 300, 1100])
+def test_tokens_find_their_sequence(B):
+    """Batches up to several rounds of the search, empty sequences among them."""
+    rng = np.random.default_rng(B)
+    n = rng.integers(0, 3, B)
+    n[rng.integers(0, B)] = 40
+    ctx = rng.integers(0, 20, B)
+    bt = Batch(list(ctx), list(n), 1, 64, 16, "bf16", seed=B)
+    pos = np.concatenate([c + np.arange(m) for c, m in zip(ctx, n)])
+    seq = np.repeat(np.arange(B), n)
+    x = (torch.from_numpy(seq * 64.0 + pos)[:, None, None] % 251 + torch.arange(64)).to(torch.bfloat16)
+    pa.cache_append(x.cuda(), x.cuda(), bt.cache, dev(bt.table), dev(bt.cu), dev(ctx))
+    k, _ = pa.cache_read(bt.cache, dev(bt.table), dev(bt.cu), dev(ctx), len(x))
+    torch.cuda.synchronize()
+    assert torch.equal(k.cpu(), x)
+    got = bt.cache.k.cpu()[bt.table[seq, pos // 16], 0, pos % 16]
+    assert torch.equal(got, x[:, 0])
+
+
+# ------------------------------------------------------------------ attention
+
+EXTEND = [
+    # name, kv, H, Hkv, d, page, ctx, n, k_local, period, S, mode
+    ("one-token", "bf16", 4, 2, 64, 16, [0], [1], 8, 16, 2, PI),
+    ("one-after-many", "bf16", 16, 4, 128, 64, [777], [1], 256, 128, 4, PI),
+    ("draft", "bf16", 16, 4, 128, 32, [30, 64, 500, 31], [5, 3, 6, 2], 100, 150, 3, PI),
+    ("aligned-chunk", "bf16", 8, 2, 128, 64, [256], [256], 128, 128, 3, PI),
+    ("odd-all", "bf16", 4, 1, 64, 16, [37, 0, 5], [133, 71, 1], 45, 67, 3, PI),
+    ("mha", "bf16", 3, 3, 64, 32, [129, 3], [200, 140], 64, 96, 2, PI),
+    ("gqa2", "bf16", 4, 2, 128, 128, [70], [161], 33, 50, 4, PI),
+    ("gqa3", "bf16", 6, 2, 64, 64, [11, 90], [64, 40], 50, 64, 2, PI),
+    ("gqa7", "bf16", 7, 1, 128, 16, [40], [130], 31, 37, 5, PI),
+    ("empty-sequences", "bf16", 4, 2, 64, 16, [0, 10, 0, 99], [0, 20, 0, 64], 20, 32, 2, PI),
+    ("no-skips", "bf16", 4, 4, 64, 256, [300], [100], 70, 1, 0, PI),
+    ("band-of-one", "bf16", 4, 2, 128, 32, [50], [90], 0, 7, 6, PI),
+    ("skips-in-band", "bf16", 4, 2, 64, 32, [100], [70], 40, 16, 6, PI),
+    ("many-skips", "bf16", 4, 2, 64, 64, [900], [40], 5, 9, 90, PI),
+    ("band-over-everything", "bf16", 8, 2, 128, 64, [200], [150], 100000, 64, 2, PI),
+    ("period-over-everything", "bf16", 4, 2, 64, 16, [60], [60], 10, 100000, 4, PI),
+    ("ecp", "bf16", 4, 4, 64, 32, [100, 0], [150, 65], 64, 0, 0, ECP),
+    ("ecp-odd", "bf16", 4, 2, 128, 16, [61], [77], 27, 0, 0, ECP),
+    ("e4m3", "e4m3", 8, 2, 128, 64, [333, 5], [130, 31], 128, 96, 3, PI),
+    ("e4m3-d64-page16", "e4m3", 6, 2, 64, 16, [90, 17], [40, 70], 50, 70, 3, PI),
+    ("int8", "int8", 8, 2, 128, 32, [200, 64], [64, 100], 100, 128, 2, PI),
+    ("int8-ecp-d64", "int8", 4, 4, 64, 128, [300], [200], 96, 0, 0, ECP),
+    ("int8-one-token", "int8", 16, 1, 128, 16, [400, 3], [1, 1], 64, 100, 3, PI),
+    ("long", "e4m3", 16, 4, 128, 64, [2500], [700], 256, 1024, 4, PI),
+    ("ragged-batch", "bf16", 16, 4, 128, 64, [0, 1500, 31, 640, 77], [300, 1, 33, 128, 5], 256, 512, 2, PI),
+]
+
+
+def run_attention(case, decode=False, seed=0):
+    name, kv, H, Hkv, d, page, ctx, n, kl, per, S, mode = case
+    bt = Batch(ctx, n, Hkv, d, page, kv, seed=seed + len(name) + d, extra_tokens=0 if decode else 2)
+    keep = [ref.attended_pages(c, c + m - 1, page, kl, per, S, mode == ECP) if m else set() for c, m in zip(ctx, n)]
+    bt.write(keep=keep)
+    for b, pages in enumerate(keep):  # pages that no query attends are gone from the table
+        for p in range(bt.table.shape[1]):
+            if p not in pages:
+                bt.table[b, p] = -1 if p % 2 else 2 ** 30
+    q = normal(bt.gen, bt.T, H, d)
+    alpha = None if mode == ECP else torch.sigmoid(1.5 * torch.randn(bt.T, H, generator=bt.gen))
+    if alpha is not None:
+        alpha[0, 0], alpha[-1, -1] = 1.0, 0.0
+    wide = torch.full((bt.T, H + 3, d), float("nan"), dtype=torch.bfloat16)
+    wide[:, :H] = q
+    qd, ad = wide.cuda()[:, :H], None if alpha is None else alpha.cuda()
+    out = torch.full((bt.T, H, d), 9.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((bt.T, H), 9.0, device="cuda")
+    if decode:
+        call = lambda: pa.decode_paged(qd, bt.cache, dev(bt.table), dev(np.array(ctx) + 1), ad, kl, per, S, mode,  # noqa: E731
+                                       out=out, lse=lse)
+    else:
+        call = lambda: pa.extend(qd, bt.cache, dev(bt.table), dev(bt.cu), dev(ctx), ad, kl, per, S, mode,  # noqa: E731
+                                 out=out, lse=lse)
+    call()
+    torch.cuda.synchronize()
+    assert pa.status() == 0
+    K, V = bt.held()
+    for b, (c, m) in enumerate(zip(ctx, n)):
+        if m:
+            t = slice(bt.cu[b], bt.cu[b + 1])
+            want = ref.attention(q[t], K[b], V[b], None if alpha is None else alpha[t], c, kl, per, S, mode)
+            ref.check_attention(f"{name} sequence {b}", out[t], lse[t], want)
+    assert (out[bt.cu[-1]:] == 9.0).all() and (lse[bt.cu[-1]:] == 9.0).all()
+    first = out.clone(), lse.clone()
+    call()
+    torch.cuda.synchronize()
+    assert torch.equal(first[0], out) and torch.equal(first[1], lse), "not the same twice"
+
+
+@pytest.mark.parametrize("case", EXTEND, ids=[c[0] for c in EXTEND])
+def test_extend_matches_the_oracle(case):
+    run_attention(case)
+
+
+DECODE = [
+    ("first-token", "bf16", 4, 2, 64, 16, [0, 0], [1, 1], 8, 4, 2, PI),
+    ("short", "bf16", 4, 4, 64, 32, [19, 3, 15], [1] * 3, 40, 16, 2, PI),
+    ("ragged", "bf16", 16, 4, 128, 64, [999, 4, 63, 64, 300], [1] * 5, 256, 150, 3, PI),
+    ("gqa16", "bf16", 16, 1, 128, 16, [700, 31], [1, 1], 64, 90, 5, PI),
+    ("gqa8", "bf16", 8, 1, 64, 128, [500], [1], 64, 100, 4, PI),
+    ("gqa9", "e4m3", 9, 1, 64, 64, [321, 7], [1, 1], 50, 60, 4, PI),
+    ("gqa3", "int8", 6, 2, 128, 256, [400, 255], [1, 1], 90, 100, 3, PI),
+    ("mha-e4m3", "e4m3", 12, 12, 64, 16, [127, 128, 129], [1] * 3, 128, 64, 1, PI),
+    ("e4m3", "e4m3", 16, 4, 128, 64, [1200, 90, 0], [1] * 3, 256, 300, 4, PI),
+    ("int8", "int8", 16, 4, 128, 32, [600, 2], [1, 1], 77, 128, 4, PI),
+    ("band-of-one", "bf16", 4, 2, 128, 16, [50], [1], 0, 7, 6, PI),
+    ("no-skips", "int8", 4, 2, 64, 16, [333], [1], 70, 1, 0, PI),
+    ("many-skips", "bf16", 4, 2, 64, 64, [1500], [1], 5, 9, 160, PI),
+    ("long-band", "bf16", 8, 2, 128, 64, [2500], [1], 2400, 64, 2, PI),
+    ("ecp", "bf16", 4, 2, 64, 32, [776, 127, 128], [1] * 3, 128, 0, 0, ECP),
+    ("ecp-e4m3-d128", "e4m3", 4, 4, 128, 64, [512, 1], [1, 1], 256, 0, 0, ECP),
+    ("big-batch", "bf16", 4, 2, 64, 16, list(range(0, 300, 4)), [1] * 75, 64, 96, 2, PI),
+]
+
+
+@pytest.mark.parametrize("case", DECODE, ids=[c[0] for c in DECODE])
+def test_decode_matches_the_oracle(case):
+    run_attention(case, decode=True)
+
+
+def test_decode_without_rows():
+    """A sequence of length zero among others: out 0 and lse -inf, as for a row without a finite logit."""
+    bt = Batch([40, 7], [1, 1], 2, 64, 16, "bf16", seed=3)
+    bt.write()
+    q, a = normal(bt.gen, 2, 4, 64).cuda(), torch.full((2, 4), 0.5, device="cuda")
+    out, lse = pa.decode_paged(q, bt.cache, dev(bt.table), dev([41, 0]), a, 16, 8, 2)
+    torch.cuda.synchronize()
+    assert pa.status() == 0
+    assert torch.isfinite(out[0].float()).all() and torch.isfinite(lse[0]).all()
+    assert (out[1] == 0).all() and torch.isneginf(lse[1]).all()
+
+
+# ------------------------------------------------------------------ indexes out of range
+
+def test_bad_indexes_are_reported_and_left_out():
+    """Offsets, contexts, lengths and pages out of range: reported once by status(), the rest of the batch
+    served, nothing written for the sequences concerned."""
+    bt = Batch([20, 20, 20], [10, 10, 10], 2, 64, 16, "bf16", seed=5)
+    bt.write()
+    q, a = normal(bt.gen, 30, 4, 64).cuda(), torch.full((30, 4), 0.5, device="cuda")
+    args = (a, 16, 8, 2)
+    good, good_lse = pa.extend(q, bt.cache, dev(bt.table), dev(bt.cu), dev(bt.ctx), *args)
+    rows = torch.zeros(30, 2, 64, dtype=torch.bfloat16, device="cuda")
+    ok = [0, 10, 20, 30]
+    for cu, ctx in (([0, 10, 20, 31], [20] * 3), ([0, 10, 20, 2 ** 31 - 1], [20] * 3), (ok, [20, 20, -1]),
+                    (ok, [20, 20, 2 ** 31 - 1]), (ok, [20, 20, 16 * bt.table.shape[1] - 9])):
+        out, lse = torch.full_like(good, 9.0), torch.full_like(good_lse, 9.0)
+        pa.extend(q, bt.cache, dev(bt.table), dev(cu), dev(ctx), *args, out=out, lse=lse)
+        assert pa.status() == ERR_INDEX and pa.status() == 0
+        assert torch.equal(out[:20], good[:20]) and torch.equal(lse[:20], good_lse[:20])
+        assert (out[20:] == 9.0).all() and (lse[20:] == 9.0).all()
+    before = [x.clone() for x in (bt.cache.k, bt.cache.v)]
+    table = bt.table.copy()
+    table[2] = 2 ** 31 - 1
+    pa.cache_append(rows[20:], rows[20:], bt.cache, dev(table[2:]), dev([0, 10]), dev([20]))
+    assert pa.status() == ERR_INDEX
+    assert torch.equal(before[0].view(torch.int16), bt.cache.k.view(torch.int16))
+    assert torch.equal(before[1].view(torch.int16), bt.cache.v.view(torch.int16))
+    k, _ = pa.cache_read(bt.cache, dev(table), dev(ok), dev([20, 20, 20]), 30, k=torch.full_like(rows, 9.0))
+    assert pa.status() == ERR_INDEX
+    assert (k[20:] == 9.0).all() and torch.equal(k[:10].cpu(), bt.k[0][20:30])
+    pa.extend(q, bt.cache, dev(table), dev(ok), dev(bt.ctx), *args)
+    assert pa.status() == ERR_INDEX
+    d3, a3 = q[:3].contiguous(), a[:3].contiguous()
+    want = pa.decode_paged(d3, bt.cache, dev(bt.table), dev([30, 30, 0]), a3, 16, 8, 2)
+    for lens in ([30, 30, -1], [30, 30, 16 * bt.table.shape[1] + 1], [30, 30, 2 ** 31 - 1]):
+        got = pa.decode_paged(d3, bt.cache, dev(bt.table), dev(lens), a3, 16, 8, 2)
+        assert pa.status() == ERR_INDEX and pa.status() == 0
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    pa.decode_paged(d3, bt.cache, dev(table), dev([30, 30, 30]), a3, 16, 8, 2)
+    assert pa.status() == ERR_INDEX and pa.status() == 0
+
+
+# ------------------------------------------------------------------ as they are used together
+
+@pytest.mark.parametrize("kv,H,Hkv,d,page,kl,per,S,mode", [
+    ("bf16", 8, 2, 128, 32, 64, 96, 3, PI), ("e4m3", 8, 2, 128, 64, 64, 100, 3, PI),
+    ("int8", 4, 4, 64, 16, 48, 0, 0, ECP)])
+def test_serving_run(kv, H, Hkv, d, page, kl, per, S, mode):
+    """Prompts written and attended chunk by chunk, then tokens one by one, in one batch: every output row is
+    the whole sequence's forward's on the values the cache holds."""
+    gen = torch.Generator().manual_seed(7)
+    chunks = [[130, 40], [77, 0], [1, 64], [1, 1], [1, 1], [1, 1]]  # new rows of the two sequences per step
+    total = np.sum(chunks, 0)
+    rng = np.random.default_rng(1)
+    table, pages = ref.make_table([0, 0], list(total), page, rng)
+    cache = nan_cache(pages, Hkv, page, d, kv)
+    seqs = [dict(q=normal(gen, m, H, d), k=normal(gen, m, Hkv, d), v=normal(gen, m, Hkv, d),
+                 a=None if mode == ECP else torch.sigmoid(torch.randn(m, H, generator=gen)), out=[], lse=[]) for m in total]
+    at = [0, 0]
+    for n in chunks:
+        part = lambda name: torch.cat([s[name][p:p + m] for s, p, m in zip(seqs, at, n)]).cuda()  # noqa: E731
+        cu, ctx = ref.offsets(n), list(at)
+        pa.cache_append(part("k"), part("v"), cache, dev(table), dev(cu), dev(ctx))
+        a = None if mode == ECP else part("a")
+        if n == [1, 1]:
+            out, lse = pa.decode_paged(part("q"), cache, dev(table), dev(np.add(ctx, 1)), a, kl, per, S, mode)
+        else:
+            out, lse = pa.extend(part("q"), cache, dev(table), dev(cu), dev(ctx), a, kl, per, S, mode)
+        for b, s in enumerate(seqs):
+            s["out"].append(out[cu[b]:cu[b + 1]].cpu())
+            s["lse"].append(lse[cu[b]:cu[b + 1]].cpu())
+            at[b] += n[b]
+    K, V = pa.cache_read(cache, dev(table), dev(ref.offsets(total)), dev([0, 0]), int(total.sum()))
+    assert pa.status() == 0
+    for b, s in enumerate(seqs):
+        rows = slice(*ref.offsets(total)[b:b + 2])
+        held = K[rows].cpu(), V[rows].cpu()
+        if kv == "bf16":
+            assert torch.equal(held[0], s["k"]) and torch.equal(held[1], s["v"])
+        want = ref.attention(s["q"], *held, s["a"], 0, kl, per, S, mode)
+        ref.check_attention(f"sequence {b}", torch.cat(s["out"]), torch.cat(s["lse"]), want)
+
+
+def test_captured_step_follows_its_inputs():
+    """Append, extend and decode captured into one graph on a stream of their own and replayed with other offsets,
+    contexts and values in the same tensors, an empty sequence and padding tokens among them."""
+    H, Hkv, d, page, kl, per, S = 8, 2, 64, 16, 40, 50, 2
+    bt = Batch([100, 60], [30, 20], Hkv, d, page, "e4m3", seed=11)
+    bt.write()
+    T = 50
+    k, v, q = (normal(bt.gen, T, h, d).cuda() for h in (Hkv, Hkv, H))
+    a = torch.rand(T, H, generator=bt.gen).cuda()
+    table, cu, ctx, lens = dev(bt.table), dev([0, 30, 50]), dev([100, 60]), dev([130, 80])
+    out, lse = torch.zeros(T, H, d, dtype=torch.bfloat16, device="cuda"), torch.zeros(T, H, device="cuda")
+    dout, dlse = torch.zeros(2, H, d, dtype=torch.bfloat16, device="cuda"), torch.zeros(2, H, device="cuda")
+
+    def step():
+        pa.cache_append(k, v, bt.cache, table, cu, ctx)
+        pa.extend(q, bt.cache, table, cu, ctx, a, kl, per, S, out=out, lse=lse)
+        pa.decode_paged(q[:2], bt.cache, table, lens, a[:2], kl, per, S, out=dout, lse=dlse)
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            step()
+    for n, c in (([30, 20], [100, 60]), ([0, 45], [100, 10]), ([7, 1], [64, 79])):
+        for t in (k, v, q):
+            t.copy_(normal(bt.gen, *t.shape))
+        cu.copy_(dev(ref.offsets(n)))
+        ctx.copy_(dev(c))
+        lens.copy_(dev(np.add(c, n)))
+        results = []
+        for run in (step, graph.replay):
+            for t in (out, lse, dout, dlse):
+                t.fill_(5.0)
+            torch.cuda.synchronize()
+            run()
+            torch.cuda.synchronize()
+            results.append([t.clone() for t in (out, lse, dout, dlse)] + [bt.cache.k.clone().view(torch.uint8)])
+        assert all(torch.equal(x, y) for x, y in zip(*results))
+        assert (results[0][0][sum(n):] == 5.0).all()
+    assert pa.status() == 0
+
+
+def test_streams_run_side_by_side():
+    """Two streams with their own tensors and a common cache give what one stream gives."""
+    bt = Batch([300, 200], [64, 40], 2, 128, 64, "bf16", seed=13)
+    bt.write()
+    q, a = normal(bt.gen, bt.T, 8, 128).cuda(), torch.rand(bt.T, 8, generator=bt.gen).cuda()
+    table, cu, ctx = dev(bt.table), dev(bt.cu), dev(bt.ctx)
+    want = pa.extend(q, bt.cache, table, cu, ctx, a, 100, 64, 3)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [(torch.empty_like(want[0]), torch.empty_like(want[1])) for _ in range(2)]
+    for _ in range(10):
+        for st, (o, ls) in zip(streams, outs):
+            pa.extend(q, bt.cache, table, cu, ctx, a, 100, 64, 3, out=o, lse=ls, stream=st)
+    torch.cuda.synchronize()
+    for o, ls in outs:
+        assert torch.equal(o, want[0]) and torch.equal(ls, want[1])
+
+
+def test_offsets_past_32_bits():
+    """Rows whose byte and element offsets in the pool pass 2^32: the last pages of a large 8-bit pool."""
+    page, Hkv, d = 256, 8, 128
+    pages = (1 << 32) // (page * Hkv * d) + 40  # codes alone pass 4 GiB, K and V each
+    cache = pa.PagedCache.empty(pages, Hkv, page, d, torch.int8)
+    gen = torch.Generator().manual_seed(2)
+    n, H = 500, 16
+    k, v, q = (normal(gen, n, h, d) for h in (Hkv, Hkv, H))
+    a = torch.rand(n, H, generator=gen)
+    table, cu, ctx = dev([[pages - 1, pages - 3]]), dev([0, n]), dev([0])
+    pa.cache_append(k.cuda(), v.cuda(), cache, table, cu, ctx)
+    out, lse = pa.extend(q.cuda(), cache, table, cu, ctx, a.cuda(), 64, 100, 2)
+    o1, l1 = pa.decode_paged(q[-1:].cuda(), cache, table, dev([n]), a[-1:].cuda(), 64, 100, 2)
+    K, V = pa.cache_read(cache, table, cu, ctx, n)
+    assert pa.status() == 0
+    held = [torch.from_numpy(ref.decode(*ref.encode(x.float().numpy(), "int8"), "int8")).to(torch.bfloat16) for x in (k, v)]
+    assert torch.equal(K.cpu(), held[0]) and torch.equal(V.cpu(), held[1])
+    want = ref.attention(q, *held, a, 0, 64, 100, 2, PI)
+    ref.check_attention("extend", out, lse, want)
+    ref.check_attention("decode", o1, l1, [x[-1:] for x in want])

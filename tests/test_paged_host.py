@@ -1,0 +1,193 @@
+"""Host-only tests of the paged cache: refusals of the C ABI and of the binding before anything is launched,
+the 64-bit format reference against torch's own conversions, and the sequence search's arithmetic."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import paged_ref as ref
+from structured_sparse_long_gb300 import build as pbuild
+from structured_sparse_long_gb300 import paged
+
+PI_ERR_NULL, PI_ERR_SHAPE, PI_ERR_UNSUPPORTED, PI_ERR_ALIGN = -1, -2, -3, -4
+A16 = 0x10000  # fake, 16-byte aligned, never dereferenced: validation fails first
+
+
+@pytest.fixture(scope="module")
+def lib():
+    pbuild.build()
+    return paged._load()
+
+
+def cache(k=A16, v=A16, ks=None, vs=None, kv_type=0, n_pages=4, Hkv=2, page=32, d=64):
+    return ctypes.byref(paged._CacheStruct(k, v, ks, vs, kv_type, n_pages, Hkv, page, d))
+
+
+def batch(table=A16, cu=A16, ctx=A16, B=2, T=5, width=4):
+    return ctypes.byref(paged._BatchStruct(table, cu, ctx, B, T, width))
+
+
+def append(lib, k=A16, v=A16, ks=128, vs=128, c=None, b=None):
+    return lib.pi_attn_cache_append(k, v, ks, vs, c or cache(), b or batch(), None)
+
+
+def read(lib, k=A16, v=A16, c=None, b=None):
+    return lib.pi_attn_cache_read(c or cache(), b or batch(), k, v, None)
+
+
+def extend(lib, q=A16, qs=256, c=None, b=None, alpha=A16, H=4, kl=8, per=16, S=1, mode=0, out=A16, lse=A16):
+    return lib.pi_attn_extend(q, qs, c or cache(), b or batch(), alpha, H, kl, per, S, mode, out, lse, None)
+
+
+def decode(lib, q=A16, qs=256, c=None, table=A16, lens=A16, B=2, width=4, alpha=A16, H=4, kl=8, per=16, S=1, mode=0,
+           out=A16, lse=A16):
+    return lib.pi_attn_decode_paged(q, qs, c or cache(), table, lens, B, width, alpha, H, kl, per, S, mode, out, lse, None)
+
+
+CALLS = [append, read, extend, decode]
+
+
+@pytest.mark.parametrize("call", CALLS, ids=lambda f: f.__name__)
+@pytest.mark.parametrize("kw,code", [
+    (dict(k=None), PI_ERR_NULL), (dict(v=None), PI_ERR_NULL), (dict(kv_type=3), PI_ERR_UNSUPPORTED),
+    (dict(kv_type=1), PI_ERR_NULL), (dict(kv_type=2, ks=A16), PI_ERR_NULL), (dict(n_pages=0), PI_ERR_SHAPE),
+    (dict(Hkv=0), PI_ERR_SHAPE), (dict(d=32), PI_ERR_UNSUPPORTED), (dict(d=96), PI_ERR_UNSUPPORTED),
+    (dict(page=8), PI_ERR_UNSUPPORTED), (dict(page=48), PI_ERR_UNSUPPORTED), (dict(page=512), PI_ERR_UNSUPPORTED),
+    (dict(n_pages=1 << 26, page=16), PI_ERR_UNSUPPORTED),  # 2^31 rows
+    (dict(k=A16 + 8), PI_ERR_ALIGN), (dict(v=A16 + 4), PI_ERR_ALIGN),
+    (dict(kv_type=1, ks=A16, vs=A16 + 8), PI_ERR_ALIGN)])
+def test_cache_is_checked(lib, call, kw, code):
+    assert call(lib, c=cache(**kw)) == code
+
+
+@pytest.mark.parametrize("call", [append, read, extend], ids=lambda f: f.__name__)
+@pytest.mark.parametrize("kw,code", [
+    (dict(table=None), PI_ERR_NULL), (dict(cu=None), PI_ERR_NULL), (dict(ctx=None), PI_ERR_NULL), (dict(B=0), PI_ERR_SHAPE),
+    (dict(T=0), PI_ERR_SHAPE), (dict(width=0), PI_ERR_SHAPE), (dict(width=1 << 26), PI_ERR_UNSUPPORTED),
+    (dict(cu=A16 + 2), PI_ERR_ALIGN)])
+def test_batch_is_checked(lib, call, kw, code):
+    assert call(lib, b=batch(**kw)) == code
+
+
+def test_rows_are_checked(lib):
+    for call, first in ((append, "k"), (read, "k"), (extend, "q"), (decode, "q")):
+        assert call(lib, **{first: None}) == PI_ERR_NULL
+        assert call(lib, **{first: A16 + 8}) == PI_ERR_ALIGN
+    assert append(lib, v=None) == PI_ERR_NULL and read(lib, v=A16 + 2) == PI_ERR_ALIGN
+    for bad in (127, 120, 132, 0, -128, 1 << 41):  # below a token's elements, not a multiple of 8, absurd
+        assert append(lib, ks=bad) == PI_ERR_SHAPE and append(lib, vs=bad) == PI_ERR_SHAPE
+    for call in (extend, decode):
+        assert call(lib, qs=248) == PI_ERR_SHAPE and call(lib, qs=260) == PI_ERR_SHAPE
+
+
+@pytest.mark.parametrize("call", [extend, decode], ids=lambda f: f.__name__)
+def test_attention_is_checked(lib, call):
+    assert call(lib, out=None) == PI_ERR_NULL and call(lib, lse=None) == PI_ERR_NULL
+    assert call(lib, alpha=None) == PI_ERR_NULL                       # pi mode needs alpha
+    assert call(lib, H=3) == PI_ERR_SHAPE and call(lib, H=0) == PI_ERR_SHAPE
+    assert call(lib, kl=-1) == PI_ERR_SHAPE and call(lib, S=-1) == PI_ERR_SHAPE
+    assert call(lib, per=0) == PI_ERR_SHAPE
+    assert call(lib, mode=2) == PI_ERR_UNSUPPORTED and call(lib, mode=5) == PI_ERR_UNSUPPORTED
+    assert call(lib, mode=1, kl=0, S=0) == PI_ERR_SHAPE and call(lib, mode=1, kl=8, S=1) == PI_ERR_SHAPE
+    assert call(lib, out=A16 + 8) == PI_ERR_ALIGN and call(lib, lse=A16 + 2) == PI_ERR_ALIGN
+    assert call(lib, alpha=A16 + 1) == PI_ERR_ALIGN
+
+
+def test_sizes_past_the_limits(lib):
+    assert extend(lib, b=batch(T=1 << 29), H=4) == PI_ERR_UNSUPPORTED    # 2^31 rows of lse
+    assert decode(lib, H=34, qs=34 * 64) == PI_ERR_UNSUPPORTED           # 17 query heads per KV head
+    assert decode(lib, B=70000) == PI_ERR_UNSUPPORTED and decode(lib, B=0) == PI_ERR_SHAPE
+    assert decode(lib, width=0) == PI_ERR_SHAPE and decode(lib, lens=None) == PI_ERR_NULL
+    assert decode(lib, table=A16 + 2) == PI_ERR_ALIGN
+
+
+def test_strerror_names_the_index_error(lib):
+    assert lib.pi_attn_strerror(-8).startswith(b"PI_ERR_INDEX")
+
+
+def test_binding_refuses_host_tensors_and_wrong_types(monkeypatch):
+    z = torch.zeros(2, 2, 16, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):
+        paged.PagedCache(z, z)
+    with pytest.raises(ValueError, match="dtype"):
+        paged.PagedCache(z.float(), z.float())
+    with pytest.raises(ValueError, match="k_scale"):
+        paged.PagedCache(z.to(torch.int8), z.to(torch.int8))
+    with pytest.raises(ValueError, match="no scales"):
+        paged.PagedCache(z, z, z, z)
+    # past the device check (stubbed: no GPU here), everything else is still checked before the library
+    monkeypatch.setattr(paged, "_load", lambda: pytest.fail("the library was reached"))
+    monkeypatch.setattr(paged._binding, "_expect_like", lambda t, name, like, dtype, shape: None)
+    c = paged.PagedCache(z, z)
+    table, cu, ctx = torch.zeros(1, 4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    q, a = torch.zeros(5, 4, 64, dtype=torch.bfloat16), torch.zeros(5, 4)
+    kv = torch.zeros(5, 2, 64, dtype=torch.bfloat16)
+    for bad in (dict(table=table.long()), dict(table=table[0]), dict(cu=cu[:1]), dict(ctx=ctx.float()),
+                dict(table=table.expand(1, 4)[:, ::2]), dict(q=q.float()), dict(q=q[:, :, :32]), dict(q=q.transpose(0, 1)),
+                dict(alpha=None)):
+        kw = {**dict(q=q, cache=c, table=table, cu=cu, ctx=ctx, alpha=a), **bad}
+        with pytest.raises(ValueError):
+            paged.extend(*kw.values(), 8, 16, 1)
+    for k, v in ((kv[:, :1], kv), (kv, kv[:4]), (kv[:, :, ::2], kv), (kv.float(), kv)):
+        with pytest.raises(ValueError):
+            paged.cache_append(k, v, c, table, cu, ctx)
+    with pytest.raises(ValueError):
+        paged.decode_paged(q, c, table, ctx, a, 8, 16, 1)  # five queries, one sequence
+
+
+def test_reference_codes_are_torch_codes():
+    """The reference's own rounding against torch's conversions, on scaled values."""
+    gen = torch.Generator().manual_seed(0)
+    x = (torch.randn(300, 64, generator=gen) * torch.exp2(torch.randint(-125, 110, (300, 1), generator=gen).float()))
+    x = x.to(torch.bfloat16)
+    for kv in ("e4m3", "int8"):
+        codes, s = ref.encode(x.float().numpy(), kv)
+        y = x.double().unflatten(-1, (-1, 32)) * torch.exp2(127.0 - torch.from_numpy(s).double())[..., None]
+        assert (y.abs() <= ref.QMAX[kv]).all()
+        grown = (y.abs().amax(-1) * 2 > ref.QMAX[kv]) | (torch.from_numpy(s) == 7)
+        assert grown.all(), "a smaller scale would have done"
+        y = y.flatten(-2)
+        want = y.float().to(torch.float8_e4m3fn).view(torch.uint8) if kv == "e4m3" else torch.round(y).to(torch.int8).view(torch.uint8)
+        assert np.array_equal(codes, want.numpy())
+        held = ref.decode(codes, s, kv)
+        assert np.array_equal(held, torch.from_numpy(held).to(torch.bfloat16).double().numpy())  # bf16 holds them
+        # half a step of the code's grid: 2^-4 of an e4m3 value (2^-10 below its normals), 1/2 of an int8 step
+        step = np.repeat(np.exp2(s.astype(float) - 127), 32, -1)
+        off = np.abs(held - x.double().numpy())
+        assert (off <= (np.maximum(2.0 ** -4 * np.abs(x.double().numpy()), 2.0 ** -10 * step) if kv == "e4m3" else step / 2)).all()
+
+
+def search(cu, B, t, seen):
+    """The kernels' sequence search (find_sequence), probe by probe."""
+    lo, length = 0, B
+    while length > 0:
+        step = (length + 31) >> 5
+        below = []
+        for lane in range(32):
+            k = (lane + 1) * step
+            if k <= length:
+                seen.append(lo + k)
+            below.append(k <= length and cu[lo + k] <= t)
+        c = sum(below)
+        lo += c * step
+        length = min(step - 1, length - c * step)
+    return lo
+
+
+def test_sequence_search():
+    """Finds every token's sequence in sorted offsets, and stays inside cu[1 .. B] and ends for any others."""
+    rng = np.random.default_rng(0)
+    for B in list(range(1, 70)) + [300, 1024, 1100, 5000]:
+        n = rng.integers(0, 3, B)
+        cu = np.concatenate([[0], np.cumsum(n)])
+        for t in rng.integers(0, cu[-1] + 3, 20):
+            seen = []
+            b = search(cu, B, t, seen)
+            assert b == np.searchsorted(cu[1:], t, side="right")
+            assert min(seen) >= 1 and max(seen) <= B
+        wild = rng.integers(-2 ** 31, 2 ** 31, B + 1)
+        for t in rng.integers(0, 1000, 5):
+            seen = []
+            assert 0 <= search(wild, B, t, seen) <= B
+            assert min(seen) >= 1 and max(seen) <= B
