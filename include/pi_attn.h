@@ -301,7 +301,7 @@ int pi_attn_decode(const void *q, const void *k_cache, const void *v_cache, cons
  *   row p % page.  Only entries of pages that hold a row the call touches are read: a
  *   page whose rows no later query attends may be taken away (any entry in its place).
  *   cu [B + 1] int32: sequence b has the packed tokens cu[b] .. cu[b+1] - 1, possibly
- *   none; cu[0] = 0 and cu[B] <= T.  Tokens cu[B] .. T - 1 belong to no sequence: nothing
+ *   none; cu[0] = 0, cu does not decrease, and cu[B] <= T.  Tokens cu[B] .. T - 1 belong to no sequence: nothing
  *   of theirs is written.  ctx [B] int32: the position of a sequence's first token, i.e.
  *   the rows it has in the cache already.  ctx[b] + cu[b+1] - cu[b] <= width * page.
  *   These three live on the device; the kernels check them (PI_ERR_INDEX).
@@ -326,7 +326,7 @@ typedef struct {
  * pi_attn_cache_append -- writes the batch's new key and value rows into the cache,
  * quantised where it holds 8 bits.
  *   k, v [T, Hkv, d] bf16; a token's Hkv * d elements are contiguous, tokens lie k_stride
- *   (v_stride) elements apart: at least Hkv * d, a multiple of 8 (else PI_ERR_SHAPE), so
+ *   (v_stride) elements apart: at least Hkv * d, below 2^38, a multiple of 8 (else PI_ERR_SHAPE), so
  *   that both may be slices of one projection's output.  16-byte aligned.
  *   A token whose sequence or page is out of range is not written.
  */
@@ -351,14 +351,19 @@ int pi_attn_cache_read(const pi_attn_cache_t *cache, const pi_attn_batch_t *batc
  *   pi_attn_cache_append), alpha [T, H] fp32 (NULL in ECP mode), out [T, H, d] bf16 and
  *   lse [T, H] fp32, contiguous.  H % Hkv == 0; T * H < 2^31.
  *   A sequence with an offset or length out of range is left out, its rows of out and lse
- *   as they were; a row that attends a key on a page out of range is undefined.
+ *   as they were (all sequences, where cu decreases anywhere); a row that attends a key on a page out of range is undefined.
  *   Non-finite values in cache rows that no query of the chunk attends do not matter;
  *   a non-finite value in a row that some query attends may reach the outputs of the
  *   sequence's other queries within 128 positions.
+ *   workspace: device buffer of at least pi_attn_extend_workspace_size(B, T) bytes
+ *   (about T + 64 B), 32-byte aligned, owned by the caller, contents ignored on entry; calls
+ *   that may overlap need one each.  Deterministic.
  */
+size_t pi_attn_extend_workspace_size(int B, int T);
 int pi_attn_extend(const void *q, long long q_stride, const pi_attn_cache_t *cache,
                    const pi_attn_batch_t *batch, const float *alpha, int H, int k_local, int period,
-                   int S, int mode, void *out, float *lse, void *stream);
+                   int S, int mode, void *out, float *lse, void *workspace,
+                   size_t workspace_bytes, void *stream);
 
 /*
  * pi_attn_decode_paged -- pi_attn_extend for one new token per sequence: pi_attn_decode

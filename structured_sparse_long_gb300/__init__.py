@@ -12,10 +12,10 @@ from ._binding import (MODE_ECP, MODE_PI, MODE_PI_BIDIR, PiAttnError, bwd, bwd_n
                        debug_wait_timeout, decode, fwd, fwd_gated, fwd_shard, lib_path, load, status,
                        strerror)
 from .paged import (KV_BF16, KV_E4M3, KV_INT8, PagedCache, cache_append, cache_read, decode_paged,  # noqa: F401
-                    extend)
+                    extend, extend_workspace_size)
 
 __all__ = ["fwd", "fwd_gated", "fwd_shard", "bwd", "bwd_shard", "decode", "bwd_noalloc",
            "bwd_workspace_size", "status", "strerror", "debug_counts", "debug_probs", "debug_trace",
            "debug_wait_timeout", "load", "lib_path", "PiAttnError", "MODE_PI", "MODE_ECP",
-           "MODE_PI_BIDIR", "PagedCache", "cache_append", "cache_read", "extend", "decode_paged", "KV_BF16",
+           "MODE_PI_BIDIR", "PagedCache", "cache_append", "cache_read", "extend", "extend_workspace_size", "decode_paged", "KV_BF16",
            "KV_E4M3", "KV_INT8"]

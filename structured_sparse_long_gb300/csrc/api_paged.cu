@@ -28,7 +28,7 @@ int make_cache(const pi_attn_cache_t *c, int width, pi::PagedCache &out) {
     if (c->d != 64 && c->d != 128) return PI_ERR_UNSUPPORTED;
     if (c->page < 16 || c->page > 256 || (c->page & (c->page - 1))) return PI_ERR_UNSUPPORTED;
     if ((long long)c->n_pages * c->Hkv > 0x7fffffffLL / c->page) return PI_ERR_UNSUPPORTED;
-    if ((long long)width * c->page > 0x7fffffffLL) return PI_ERR_UNSUPPORTED;
+    if ((long long)width * c->page > 0x7fff0000LL) return PI_ERR_UNSUPPORTED;  // positions and a few tiles fit int
     if (!aligned(c->k, 16) || !aligned(c->v, 16)) return PI_ERR_ALIGN;
     if (quant && (!aligned(c->k_scale, 16) || !aligned(c->v_scale, 16))) return PI_ERR_ALIGN;
     out.k = c->k; out.v = c->v;
@@ -51,7 +51,7 @@ int make_batch(const pi_attn_batch_t *b, pi::PagedBatch &out) {
 
 // A token's rows lie `heads * d` elements one after the other; tokens are `stride` elements apart.
 int check_stride(long long stride, int heads, int d) {
-    if (stride < (long long)heads * d || stride > (1LL << 40) || stride % 8) return PI_ERR_SHAPE;
+    if (stride < (long long)heads * d || stride >= (1LL << 38) || stride % 8) return PI_ERR_SHAPE;
     return PI_OK;
 }
 
@@ -61,6 +61,9 @@ int make_attention(const pi::PagedCache &c, int H, int k_local, int period, int 
     if (H <= 0 || H % c.Hkv != 0 || k_local < 0 || S < 0) return PI_ERR_SHAPE;
     if (mode != PI_MODE_ECP && S > 0 && period <= 0) return PI_ERR_SHAPE;
     if (mode == PI_MODE_ECP && (k_local <= 0 || S != 0)) return PI_ERR_SHAPE;
+    // key lists and tile counts fit int
+    const long long positions = (long long)c.width * c.page;
+    if (mode != PI_MODE_ECP && S > 0 && std::min<long long>(S, positions / period) > (1LL << 27)) return PI_ERR_UNSUPPORTED;
     s = pi::Shape{};
     s.H = H; s.Hkv = c.Hkv; s.d = c.d;
     s.k_local = k_local; s.period = period; s.S = S; s.mode = mode;
@@ -104,8 +107,11 @@ int pi_attn_cache_read(const pi_attn_cache_t *cache, const pi_attn_batch_t *batc
     return map_cuda(pi::launch_cache_read(a, static_cast<cudaStream_t>(stream)));
 }
 
+size_t pi_attn_extend_workspace_size(int B, int T) { return B > 0 && T > 0 ? pi::extend_workspace_bytes(B, T) : 0; }
+
 int pi_attn_extend(const void *q, long long q_stride, const pi_attn_cache_t *cache, const pi_attn_batch_t *batch,
-                   const float *alpha, int H, int k_local, int period, int S, int mode, void *out, float *lse, void *stream) {
+                   const float *alpha, int H, int k_local, int period, int S, int mode, void *out, float *lse,
+                   void *workspace, size_t workspace_bytes, void *stream) {
     if (!q || !batch || !out || !lse) return PI_ERR_NULL;
     pi::ExtendArgs a{};
     int rc = make_cache(cache, batch->width, a.cache);
@@ -120,6 +126,9 @@ int pi_attn_extend(const void *q, long long q_stride, const pi_attn_cache_t *cac
     a.alpha = mode != PI_MODE_ECP ? alpha : nullptr;
     a.out = static_cast<__nv_bfloat16 *>(out);
     a.lse = lse;
+    if (!workspace || workspace_bytes < pi_attn_extend_workspace_size(batch->B, batch->T)) return PI_ERR_WORKSPACE;
+    if (!aligned(workspace, 32)) return PI_ERR_ALIGN;
+    a.workspace = static_cast<int *>(workspace);
     a.timeout_ns = kWaitTimeoutNs;
     if (!(a.status = pi::status_word()) || !(a.index_word = pi::index_word())) return PI_ERR_CUDA;
     return map_cuda(pi::launch_extend(a, static_cast<cudaStream_t>(stream)));

@@ -2,6 +2,8 @@
 // C ABI and the kernel files.
 #pragma once
 
+#include <algorithm>
+#include <atomic>
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -56,6 +58,7 @@ struct ExtendArgs {
     Shape s;                 // H, Hkv, d, k_local, period, S, mode, scale_log2
     PagedCache cache;
     PagedBatch batch;
+    int *workspace;          // extend_workspace_bytes(B, T)
     int *status, *index_word;
     uint64_t timeout_ns;
 };
@@ -77,7 +80,9 @@ struct DecodePagedArgs {
 cudaError_t launch_append(const AppendArgs &a, cudaStream_t st);
 cudaError_t launch_cache_read(const ReadArgs &a, cudaStream_t st);
 
-// attention over a paged cache: a chunk of new tokens per sequence, one new token per sequence
+// attention over a paged cache: a chunk of new tokens per sequence (pi_extend_tc.cu), one new token per
+// sequence (pi_decode_paged.cu)
+size_t extend_workspace_bytes(long long B, long long T);
 cudaError_t launch_extend(const ExtendArgs &a, cudaStream_t st);
 cudaError_t launch_decode_paged(const DecodePagedArgs &a, cudaStream_t st);
 
@@ -85,5 +90,19 @@ cudaError_t launch_decode_paged(const DecodePagedArgs &a, cudaStream_t st);
 // bounded waits, and the one that out-of-range indexes are recorded in.  Null on a CUDA error.
 int *status_word();
 int *index_word();
+
+// Streaming multiprocessors of the current device (1 on a CUDA error).
+inline int sm_count() {
+    constexpr int kMaxDev = 64;
+    static std::atomic<int> cache[kMaxDev];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return 1;
+    n = cache[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 1;
+        cache[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
 
 }  // namespace pi

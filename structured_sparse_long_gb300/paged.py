@@ -39,7 +39,9 @@ def _load():
         lib.pi_attn_cache_append.argtypes = [P, P, L, L, C, B, P]
         lib.pi_attn_cache_read.argtypes = [C, B, P, P, P]
         lib.pi_attn_decode_paged.argtypes = [P, L, C, P, P, I, I, P, I, I, I, I, I, P, P, P]
-        lib.pi_attn_extend.argtypes = [P, L, C, B, P, I, I, I, I, I, P, P, P]
+        lib.pi_attn_extend.argtypes = [P, L, C, B, P, I, I, I, I, I, P, P, P, ctypes.c_size_t, P]
+        lib.pi_attn_extend_workspace_size.argtypes = [I, I]
+        lib.pi_attn_extend_workspace_size.restype = ctypes.c_size_t
         for name in ("cache_append", "cache_read", "decode_paged", "extend"):
             getattr(lib, "pi_attn_" + name).restype = I
     return lib
@@ -193,8 +195,13 @@ def _outputs(q, cache, alpha, mode, out, lse):
     return out, lse
 
 
+def extend_workspace_size(B: int, T: int) -> int:
+    """pi_attn_extend_workspace_size: bytes of device workspace for B sequences with T packed tokens."""
+    return int(_load().pi_attn_extend_workspace_size(B, T))
+
+
 def extend(q, cache: PagedCache, table, cu, ctx, alpha, k_local: int, period: int, S: int, mode: int = MODE_PI,
-           out=None, lse=None, stream=None, check=False):
+           out=None, lse=None, workspace=None, stream=None, check=False):
     """pi_attn_extend: the packed new tokens q [T, H, d] bf16 (any token stride) against their sequences' cached
     rows, which hold the chunk's own already.  alpha [T, H] fp32 (None in ECP mode).  Returns (out, lse)."""
     qs = _packed_rows(q, "q", cache)
@@ -203,9 +210,18 @@ def extend(q, cache: PagedCache, table, cu, ctx, alpha, k_local: int, period: in
     batch = _batch(table, cu, ctx, T, cache)
     if T > 0:
         with _on(cache.device):
-            rc = _load().pi_attn_extend(q.data_ptr(), qs, cache._ref, ctypes.byref(batch),
+            lib = _load()
+            nbytes = lib.pi_attn_extend_workspace_size(batch.B, T)
+            if workspace is None:
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
+            else:
+                _binding._expect_like(workspace, "workspace", cache, torch.uint8, None)
+                if workspace.numel() < nbytes:
+                    raise ValueError(f"workspace must hold {nbytes} bytes, got {workspace.numel()}")
+            rc = lib.pi_attn_extend(q.data_ptr(), qs, cache._ref, ctypes.byref(batch),
                                         None if alpha is None else alpha.data_ptr(), H, k_local, period, S, mode,
-                                        out.data_ptr(), lse.data_ptr(), _stream_of(stream, cache.device))
+                                        out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                    _stream_of(stream, cache.device))
             _check("pi_attn_extend", rc, stream, check)
     return out, lse
 

@@ -10,7 +10,7 @@ import paged_ref as ref
 from structured_sparse_long_gb300 import build as pbuild
 from structured_sparse_long_gb300 import paged
 
-PI_ERR_NULL, PI_ERR_SHAPE, PI_ERR_UNSUPPORTED, PI_ERR_ALIGN = -1, -2, -3, -4
+PI_ERR_NULL, PI_ERR_SHAPE, PI_ERR_UNSUPPORTED, PI_ERR_ALIGN, PI_ERR_WORKSPACE = -1, -2, -3, -4, -5
 A16 = 0x10000  # fake, 16-byte aligned, never dereferenced: validation fails first
 
 
@@ -36,8 +36,9 @@ def read(lib, k=A16, v=A16, c=None, b=None):
     return lib.pi_attn_cache_read(c or cache(), b or batch(), k, v, None)
 
 
-def extend(lib, q=A16, qs=256, c=None, b=None, alpha=A16, H=4, kl=8, per=16, S=1, mode=0, out=A16, lse=A16):
-    return lib.pi_attn_extend(q, qs, c or cache(), b or batch(), alpha, H, kl, per, S, mode, out, lse, None)
+def extend(lib, q=A16, qs=256, c=None, b=None, alpha=A16, H=4, kl=8, per=16, S=1, mode=0, out=A16, lse=A16, ws=A16,
+           ws_bytes=1 << 20):
+    return lib.pi_attn_extend(q, qs, c or cache(), b or batch(), alpha, H, kl, per, S, mode, out, lse, ws, ws_bytes, None)
 
 
 def decode(lib, q=A16, qs=256, c=None, table=A16, lens=A16, B=2, width=4, alpha=A16, H=4, kl=8, per=16, S=1, mode=0,
@@ -75,7 +76,7 @@ def test_rows_are_checked(lib):
         assert call(lib, **{first: None}) == PI_ERR_NULL
         assert call(lib, **{first: A16 + 8}) == PI_ERR_ALIGN
     assert append(lib, v=None) == PI_ERR_NULL and read(lib, v=A16 + 2) == PI_ERR_ALIGN
-    for bad in (127, 120, 132, 0, -128, 1 << 41):  # below a token's elements, not a multiple of 8, absurd
+    for bad in (127, 120, 132, 0, -128, 1 << 38):  # below a token's elements, not a multiple of 8, absurd
         assert append(lib, ks=bad) == PI_ERR_SHAPE and append(lib, vs=bad) == PI_ERR_SHAPE
     for call in (extend, decode):
         assert call(lib, qs=248) == PI_ERR_SHAPE and call(lib, qs=260) == PI_ERR_SHAPE
@@ -98,8 +99,63 @@ def test_sizes_past_the_limits(lib):
     assert extend(lib, b=batch(T=1 << 29), H=4) == PI_ERR_UNSUPPORTED    # 2^31 rows of lse
     assert decode(lib, H=34, qs=34 * 64) == PI_ERR_UNSUPPORTED           # 17 query heads per KV head
     assert decode(lib, B=70000) == PI_ERR_UNSUPPORTED and decode(lib, B=0) == PI_ERR_SHAPE
+    for call, kw in ((extend, dict(b=batch(width=1 << 25))), (decode, dict(width=1 << 25))):  # 2^30 positions, as many skips
+        assert call(lib, per=1, S=1 << 30, **kw) == PI_ERR_UNSUPPORTED
     assert decode(lib, width=0) == PI_ERR_SHAPE and decode(lib, lens=None) == PI_ERR_NULL
     assert decode(lib, table=A16 + 2) == PI_ERR_ALIGN
+
+
+def test_extend_workspace(lib):
+    """A plan of at most T / 32 + 2 min(B, T) blocks of 32 bytes and its head."""
+    for B, T in ((1, 1), (1, 65536), (16, 80), (1000, 30)):
+        need = lib.pi_attn_extend_workspace_size(B, T)
+        assert need == 32 + 32 * (T // 32 + 2 * min(B, T))
+        assert extend(lib, b=batch(B=B, T=T), ws_bytes=need - 1) == PI_ERR_WORKSPACE
+    assert lib.pi_attn_extend_workspace_size(0, 5) == 0 and lib.pi_attn_extend_workspace_size(5, 0) == 0
+    assert extend(lib, ws=None) == PI_ERR_WORKSPACE and extend(lib, ws=A16 + 16) == PI_ERR_ALIGN
+
+
+def plan(n, ctx, R):
+    """The plan kernel's blocks of one sequence: (p0, first, last)."""
+    p = ctx if n <= R else ctx // R * R
+    return [(x, max(x, ctx), min(x + R, ctx + n) - 1) for x in range(p, ctx + n, R)]
+
+
+@pytest.mark.parametrize("R", [32, 64, 128])
+def test_plan_covers_every_token_within_the_bound(R):
+    rng = np.random.default_rng(R)
+    for n in list(range(1, 3 * R + 2)) + [1000, 65536]:
+        ctx = int(rng.integers(0, 1000))
+        blocks = plan(n, ctx, R)
+        assert [i for _, f, la in blocks for i in range(f, la + 1)] == list(range(ctx, ctx + n))
+        assert len(blocks) <= n // R + 2
+
+
+@pytest.mark.parametrize("period", [1, 7, 31, 32, 33, 64, 100, 1024])
+def test_key_tiles_cover_what_the_queries_attend(period):
+    """The 32-key tiles of a block (band, then skip windows) hold every attended key once, whatever the period."""
+    rng = np.random.default_rng(period)
+    for _ in range(200):
+        first = int(rng.integers(0, 3000))
+        last = first + int(rng.integers(0, 128))
+        k, S = int(rng.integers(0, 200)), int(rng.integers(0, 6))
+        m_first = min(k // period + 1, S + 1)
+        lo = max(0, first - k)
+        band = [(lo & ~31) + 32 * t for t in range((last - (lo & ~31)) // 32 + 1)]
+        windows = max(0, min(S, last // period) - m_first + 1) if S else 0
+        cpb = (last >> 5) - (first >> 5) + 1 if period % 32 == 0 else ((last - first) >> 5) + 2
+        inv = 0xFFFFFFFF // cpb + 1 & 0xFFFFFFFF
+        for i in (first, last, int(rng.integers(first, last + 1))):
+            got = [j for t in band for j in range(max(t, max(0, i - k)), min(t + 31, i) + 1)]
+            for x in range(windows * cpb):
+                w = x * inv >> 32 if inv else x
+                assert w == x // cpb
+                back = (m_first + w) * period
+                key0 = ((first - back) & ~31) + 32 * (x - w * cpb)
+                if i - back >= 0 and key0 <= i - back < key0 + 32:
+                    got.append(i - back)
+            want = list(range(max(0, i - k), i + 1)) + [i - m * period for m in range(1, S + 1) if m * period > k and i >= m * period]
+            assert sorted(got) == sorted(want)
 
 
 def test_strerror_names_the_index_error(lib):
