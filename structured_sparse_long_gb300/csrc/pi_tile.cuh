@@ -12,6 +12,18 @@ namespace tc {
 constexpr int CHUNK = 32;                 // keys per tile (TMA box rows; the N of the S products)
 constexpr float kRescaleThreshold = 8.f;  // log2 units
 
+// Waits for the TMEM loads issued before, of which r[0 .. 31] (r[0 .. 15]) is one.  The registers are operands: without them
+// nothing keeps the compiler from using their values before the wait, while the load is in flight.
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t *r) {
+#define PI_R4(i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3])
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : PI_R4(0), PI_R4(4), PI_R4(8), PI_R4(12), PI_R4(16), PI_R4(20), PI_R4(24), PI_R4(28)::"memory");
+}
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t *r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : PI_R4(0), PI_R4(4), PI_R4(8), PI_R4(12)::"memory");
+#undef PI_R4
+}
+
 // Phase 1 of a tile for one row (general path): mask the scores outside [clo, chi] and return
 // the tile's largest logit in log2 units (prior included).  A skip tile holds at most one
 // valid column per row (its diagonal), read with a select tree instead of a full pass.
@@ -28,12 +40,14 @@ __device__ __forceinline__ float tile_max(float *f, int clo, int chi, bool skip,
     float m0 = max3(f[0], f[1], f[2]), m1 = max3(f[3], f[4], f[5]);
     float m2 = max3(f[6], f[7], f[8]), m3 = max3(f[9], f[10], f[11]);
 #pragma unroll
-    for (int c = 12; c < 32; c += 8) {
+    for (int c = 12; c < 28; c += 8) {
         m0 = max3(m0, f[c], f[c + 1]);
         m1 = max3(m1, f[c + 2], f[c + 3]);
         m2 = max3(m2, f[c + 4], f[c + 5]);
         m3 = max3(m3, f[c + 6], f[c + 7]);
     }
+    m0 = max3(m0, f[28], f[29]);
+    m1 = max3(m1, f[30], f[31]);
     const float mx = fmaxf(max3(m0, m1, m2), m3);
     return (mx == -INFINITY) ? -INFINITY : fmaf(mx, sc, off);
 }
@@ -77,10 +91,12 @@ __device__ __forceinline__ float tile_raw_max(const uint32_t *r) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) m[k] = max3(__uint_as_float(r[k]), __uint_as_float(r[k + 4]), __uint_as_float(r[k + 8]));
 #pragma unroll
-    for (int c = 12; c < CHUNK; c += 8) {
+    for (int c = 12; c < 28; c += 8) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) m[k] = max3(m[k], __uint_as_float(r[c + k]), __uint_as_float(r[c + 4 + k]));
     }
+    m[0] = max3(m[0], __uint_as_float(r[28]), __uint_as_float(r[29]));
+    m[1] = max3(m[1], __uint_as_float(r[30]), __uint_as_float(r[31]));
     return fmaxf(max3(m[0], m[1], m[2]), m[3]);
 }
 
