@@ -355,11 +355,18 @@ int pi_attn_cache_read(const pi_attn_cache_t *cache, const pi_attn_batch_t *batc
  *   Non-finite values in cache rows that no query of the chunk attends do not matter;
  *   a non-finite value in a row that some query attends may reach the outputs of the
  *   sequence's other queries within 128 positions.
- *   workspace: device buffer of at least pi_attn_extend_workspace_size(B, T) bytes
- *   (about T + 64 B), 32-byte aligned, owned by the caller, contents ignored on entry; calls
- *   that may overlap need one each.  Deterministic.
+ *   workspace: device buffer of at least pi_attn_extend_workspace_size() bytes for these
+ *   sizes, 256-byte aligned, owned by the caller, contents ignored on entry; calls that may
+ *   overlap need one each.  It holds the call's plan (about 2.5 T + 160 B bytes) and, for an
+ *   8-bit cache, the attended rows as bf16: 4 d Hkv bytes for each of at most
+ *   min(T (1 + S) + B k_local, T + B max(k_local, S period)) rows and a few tiles of 32 per
+ *   sequence and skip window.  Deterministic.
+ *
+ * pi_attn_extend_workspace_size -- those bytes (0 for sizes that pi_attn_extend refuses);
+ * of the cache only its sizes, type and pointers' alignment matter.
  */
-size_t pi_attn_extend_workspace_size(int B, int T);
+size_t pi_attn_extend_workspace_size(const pi_attn_cache_t *cache, int B, int T, int width, int H,
+                                     int k_local, int period, int S, int mode);
 int pi_attn_extend(const void *q, long long q_stride, const pi_attn_cache_t *cache,
                    const pi_attn_batch_t *batch, const float *alpha, int H, int k_local, int period,
                    int S, int mode, void *out, float *lse, void *workspace,

@@ -117,15 +117,15 @@ __device__ __forceinline__ void scores(const Frag<D, KV> &f, const uint2 (&q)[NH
 #pragma unroll
         for (int x = 0; x < f.C; ++x) {
             // elements 64 x + 16 t ... of a row lie in block 2 x + t / 2
-            const Scale2 s0 = scale_same(f.ks[0] >> (8 * (2 * x + (t >> 1))) & 0xffu);
-            const Scale2 s1 = scale_same(f.ks[1] >> (8 * (2 * x + (t >> 1))) & 0xffu);
+            const Scale2<KV> s0 = scale_same<KV>(f.ks[0] >> (8 * (2 * x + (t >> 1))) & 0xffu);
+            const Scale2<KV> s1 = scale_same<KV>(f.ks[1] >> (8 * (2 * x + (t >> 1))) & 0xffu);
             const uint32_t w0[4] = {f.k[0][x].x, f.k[0][x].y, f.k[0][x].z, f.k[0][x].w};
             const uint32_t w1[4] = {f.k[1][x].x, f.k[1][x].y, f.k[1][x].z, f.k[1][x].w};
 #pragma unroll
             for (int w = 0; w < 4; ++w) {  // one k step per word: four elements of each row
                 uint32_t a0, a2, a1, a3;
-                codes_to_bf16<KV>(w0[w], s0, a0, a2);
-                codes_to_bf16<KV>(w1[w], s1, a1, a3);
+                codes_to_bf16<KV>(w0[w], s0, s0.big, a0, a2);
+                codes_to_bf16<KV>(w1[w], s1, s1.big, a1, a3);
 #pragma unroll
                 for (int nh = 0; nh < NH; ++nh) mma_bf16(s[nh], a0, a1, a2, a3, q[nh][4 * x + w].x, q[nh][4 * x + w].y);
             }
@@ -170,15 +170,15 @@ __device__ __forceinline__ void accumulate(const Frag<D, KV> &f, const uint32_t 
             }
         }
     } else {
-        const Scale2 s01 = scale_pair(f.vs[0], f.vs[1]), s23 = scale_pair(f.vs[2], f.vs[3]);
+        const Scale2<KV> s01 = scale_pair<KV>(f.vs[0], f.vs[1]), s23 = scale_pair<KV>(f.vs[2], f.vs[3]);
 #pragma unroll
         for (int w = 0; w < f.VW; ++w) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {  // codes 2h, 2h + 1 of the word, each with its pair of keys
                 const uint32_t sel = h ? 0x7362 : 0x5140;
                 uint32_t a0, a1, a2, a3;
-                codes_to_bf16<KV>(__byte_perm(f.v[0][w], f.v[1][w], sel), s01, a0, a1);
-                codes_to_bf16<KV>(__byte_perm(f.v[2][w], f.v[3][w], sel), s23, a2, a3);
+                codes_to_bf16<KV>(__byte_perm(f.v[0][w], f.v[1][w], sel), s01, s01.big, a0, a1);
+                codes_to_bf16<KV>(__byte_perm(f.v[2][w], f.v[3][w], sel), s23, s23.big, a2, a3);
 #pragma unroll
                 for (int nh = 0; nh < NH; ++nh) mma_bf16(o[nh][2 * w + h], a0, a1, a2, a3, p[nh][0], p[nh][1]);
             }

@@ -22,9 +22,11 @@
 //   * Rows of V that no query of the block attends may hold anything (evicted or unwritten rows, NaN among them):
 //     they are zeroed in shared memory before the product, since 0 * NaN is not 0.  Scores of K rows outside
 //     a row's range are replaced before they are used.
-//   * 8-bit caches: a producer warp brings codes and scale bytes into a ring of raw tiles, and four more
-//     warps turn them into the bf16 tiles of the pipeline (exact, see pi_paged.cuh).  One lane takes 16 codes
-//     of a row; raw and converted tiles are both swizzled, so that neither side has bank conflicts.
+//   * 8-bit caches: the 32-key tiles that the chunk attends are first turned into bf16 tiles in the workspace (exact,
+//     see pi_paged.cuh), which the same kernel then reads instead of pages.  A key tile serves up to a dozen blocks,
+//     and each of them converting its own (four converter warps per CTA between a ring of raw tiles and the pipeline)
+//     put so much into the SM's instruction stream that a 65536-token chunk (16 heads on 4, d = 128, band 256,
+//     4 skips of 1024) took 480-640 us against 250 us of the bf16 cache.
 #include <cuda.h>
 
 #include "pi_launch.h"
@@ -41,15 +43,76 @@ using namespace tc;
 constexpr int BM = 128;         // rows per block (MMA M)
 constexpr int TMEM_COLS = 256;  // per CTA, two CTAs per SM
 constexpr int ROW_BYTES = 128;  // one 64-element bf16 swizzle row
+constexpr int THREADS = 256;
 
 // ------------------------------------------------------------------ the plan
 
-// A position block of one sequence: positions first .. last hold its queries, row 0 is position p0 and packed
-// token tq (possibly before the sequence's own).
+// A position block of one sequence and its key tiles, the same for every group of heads.
 struct PlanBlock {
-    int b, p0, tq, first, last, pad[3];
+    int p0, tq, first, last;  // positions first .. last hold queries; row 0 is position p0 and packed token tq
+                              // (possibly before the sequence's own)
+    int b, lo, n_band, n_tiles;  // sequence; first band key of the first query; tiles from lo rounded down to 32, and all
+    int cpb;                     // tiles per skip window
+    uint32_t inv_cpb;            // ceil(2^32 / cpb), 0 for one tile
+    int full_lo, full_hi;        // tiles inside the band of every query
+    int slot, slot_lo, slot_windows, ctx;  // 8-bit caches: where the sequence's bf16 tiles are (SeqTiles);
+    int per_window, pad[3];                // slot_windows < 0: all in one run
 };
-constexpr int PLAN_HEAD = 32;  // bytes before the blocks: [0] their number
+static_assert(sizeof(PlanBlock) == 80, "16-byte loads");
+
+// The bf16 tiles of a sequence over an 8-bit cache, `slots` of them from slot on: either all tiles from its first
+// attended key to its last (band_tiles = 0: tile x, keys 32 x ..., in slot + x - lo), or the band's tiles followed by
+// `per_window` for each skip window, whichever is fewer (a long chunk's windows overlap).
+struct SeqTiles {
+    int lo;          // first tile of all, or of the band
+    int band_tiles;
+    int per_window;
+    int slots;
+};
+
+__host__ __device__ __forceinline__ SeqTiles seq_tiles(const Shape &s, int m_first, int n, int ctx) {
+    const int last = ctx + n - 1, band0 = band_lo(ctx, s.mode, s.k_local);
+    int windows = 0;
+    if (s.mode != kModeEcp && s.S > 0) {
+        const int m_last = last / s.period < s.S ? last / s.period : s.S;
+        windows = m_last >= m_first ? m_last - m_first + 1 : 0;
+    }
+    SeqTiles q;
+    q.lo = band0 >> 5;
+    q.band_tiles = (last >> 5) - q.lo + 1;
+    q.per_window = ((n - 1) >> 5) + 2;
+    q.slots = q.band_tiles;
+    if (windows > 0) {
+        const long long far = (long long)ctx - (long long)(m_first + windows - 1) * s.period;
+        int lo = far > 0 ? (int)(far >> 5) : 0;
+        if (q.lo < lo) lo = q.lo;
+        const long long each = q.band_tiles + (long long)windows * q.per_window;
+        const int all = (last >> 5) - lo + 1;
+        if (all <= each) {
+            q.lo = lo;
+            q.band_tiles = 0;
+            q.slots = all;
+        } else {
+            q.slots = (int)each;
+        }
+    }
+    return q;
+}
+
+// Most slots that a batch can take, from its sizes alone (cap: positions a page table reaches).
+static long long most_slots(const Shape &s, long long B, long long T, long long cap) {
+    const long long seqs = std::min(B, T);
+    const long long band = std::min<long long>(cap, s.mode == kModeEcp ? 2LL * s.k_local : s.k_local);
+    long long windows = 0, reach = band;
+    if (s.mode != kModeEcp && s.S > 0) {
+        windows = std::min<long long>(s.S, cap / s.period);
+        reach = std::min<long long>(cap, std::max(band, windows * s.period));
+    }
+    const long long each = (T + seqs * band) / 32 + 2 * seqs + windows * (T / 32 + 2 * seqs);
+    const long long all = (T + seqs * reach) / 32 + 2 * seqs;
+    return std::min(each, all);
+}
+constexpr int PLAN_HEAD = 32;  // bytes before the blocks: [0] their number, [1] the slots used
 
 __host__ __device__ __forceinline__ long long max_blocks(long long T, long long B, int R) {
     // n tokens lie in at most floor(n / R) + 2 blocks, and a sequence without tokens in none
@@ -58,8 +121,45 @@ __host__ __device__ __forceinline__ long long max_blocks(long long T, long long 
 
 constexpr int PLAN_THREADS = 1024;
 
-__global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(PagedCache c, PagedBatch bt, int R, int *plan, int *index_word) {
+struct PlanArgs {
+    Shape s;
+    PagedCache c;
+    PagedBatch bt;
+    int R, m_first;
+    int aligned;  // period % 32 == 0: every skip window has the same place in its tiles
+    int *plan, *index_word;
+    int2 *slots;  // 8-bit caches: [slot] sequence and tile (negative: before the sequence); else null
+};
+
+__device__ __forceinline__ PlanBlock plan_block(const PlanArgs &a, int b, int t0, int n, int ctx, int p0) {
+    const Shape &s = a.s;
+    PlanBlock k;
+    k.p0 = p0;
+    k.tq = t0 + p0 - ctx;
+    k.first = max(p0, ctx);
+    k.last = min(p0 + a.R, ctx + n) - 1;
+    k.b = b;
+    k.lo = band_lo(k.first, s.mode, s.k_local);
+    const int key0 = k.lo & ~(CHUNK - 1);
+    k.n_band = (k.last - key0) / CHUNK + 1;
+    int windows = 0;
+    if (s.mode != kModeEcp && s.S > 0) windows = max(0, min(s.S, k.last / s.period) - a.m_first + 1);
+    k.cpb = a.aligned ? (k.last >> 5) - (k.first >> 5) + 1 : ((k.last - k.first) >> 5) + 2;
+    k.inv_cpb = 0xffffffffu / (uint32_t)k.cpb + 1u;
+    k.n_tiles = k.n_band + windows * k.cpb;
+    k.full_lo = (band_lo(k.last, s.mode, s.k_local) - key0 + CHUNK - 1) / CHUNK;
+    const int span = k.first - (CHUNK - 1) - key0;
+    k.full_hi = span >= 0 ? span / CHUNK : -1;
+    return k;
+}
+
+__global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PlanArgs a) {
+    const PagedCache &c = a.c;
+    const PagedBatch &bt = a.bt;
+    const int R = a.R;
+    int *plan = a.plan, *index_word = a.index_word;
     __shared__ int upto[PLAN_THREADS];  // blocks of the round's sequences up to and including each
+    __shared__ int slots_upto[PLAN_THREADS];
     __shared__ int warp_sum[PLAN_THREADS / 32];
     asm volatile("griddepcontrol.launch_dependents;");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -70,79 +170,198 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(PagedCache c, PagedB
     if (!__syncthreads_and(sorted)) {
         if (tid == 0) {
             record_index(index_word);
-            plan[0] = 0;
+            plan[0] = plan[1] = 0;
         }
         return;
     }
     // n tokens at ctx ..: blocks at multiples of R, or one where a short chunk starts
     auto start = [&](int n, int ctx) { return n <= R ? ctx : ctx / R * R; };
-    int base = 0;
+    // inclusive sums over the CTA's threads into buf; returns the total
+    auto scan = [&](int x, int *buf) -> int {
+        int sum = x;
+#pragma unroll
+        for (int w = 1; w < 32; w <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, sum, w);
+            if (lane >= w) sum += y;
+        }
+        __syncthreads();  // warp_sum and buf are free
+        if (lane == 31) warp_sum[warp] = sum;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) sum += warp_sum[w];
+        buf[tid] = sum;
+        __syncthreads();
+        return buf[PLAN_THREADS - 1];
+    };
+    // the thread whose share of the sums holds item x, and the item's place in it
+    auto owner = [&](const int *buf, int x, int &place) -> int {
+        int lo = 0, hi = PLAN_THREADS - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (buf[mid] > x) hi = mid;
+            else lo = mid + 1;
+        }
+        place = x - (lo > 0 ? buf[lo - 1] : 0);
+        return lo;
+    };
+    int base = 0, slot_base = 0;
     for (int b0 = 0; b0 < bt.B; b0 += PLAN_THREADS) {
         const int b = b0 + tid;
-        int cnt = 0;
+        int cnt = 0, slots = 0;
         if (b < bt.B) {
             const int t0 = bt.cu[b], t1 = bt.cu[b + 1], ctx = bt.ctx[b];
             if (!sequence_ok(c, bt, t0, t1, ctx)) record_index(index_word);
-            else if (t1 > t0) cnt = (ctx + (t1 - t0) - 1 - start(t1 - t0, ctx)) / R + 1;
-        }
-        int sum = cnt;
-#pragma unroll
-        for (int w = 1; w < 32; w <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, sum, w);
-            if (lane >= w) sum += x;
-        }
-        if (lane == 31) warp_sum[warp] = sum;
-        __syncthreads();
-        int before = 0;
-        for (int w = 0; w < warp; ++w) before += warp_sum[w];
-        upto[tid] = sum + before;
-        __syncthreads();
-        const int total = upto[PLAN_THREADS - 1];
-        for (int x = tid; x < total; x += PLAN_THREADS) {
-            int lo = 0, hi = PLAN_THREADS - 1;  // first sequence of the round with more than x blocks up to it
-            while (lo < hi) {
-                const int mid = (lo + hi) >> 1;
-                if (upto[mid] > x) hi = mid;
-                else lo = mid + 1;
+            else if (t1 > t0) {
+                cnt = (ctx + (t1 - t0) - 1 - start(t1 - t0, ctx)) / R + 1;
+                if (a.slots) slots = seq_tiles(a.s, a.m_first, t1 - t0, ctx).slots;
             }
-            const int t0 = bt.cu[b0 + lo], n = bt.cu[b0 + lo + 1] - t0, ctx = bt.ctx[b0 + lo];
-            const int p0 = start(n, ctx) + (x - (lo > 0 ? upto[lo - 1] : 0)) * R;
-            const int4 d = make_int4(b0 + lo, p0, t0 + p0 - ctx, max(p0, ctx));
-            *reinterpret_cast<int4 *>(&blocks[base + x]) = d;
-            blocks[base + x].last = min(p0 + R, ctx + n) - 1;
+        }
+        const int total = scan(cnt, upto);
+        const int total_slots = a.slots ? scan(slots, slots_upto) : 0;
+        for (int x = tid; x < total; x += PLAN_THREADS) {
+            int place;
+            const int o = owner(upto, x, place);
+            const int t0 = bt.cu[b0 + o], n = bt.cu[b0 + o + 1] - t0, ctx = bt.ctx[b0 + o];
+            const PlanBlock k = plan_block(a, b0 + o, t0, n, ctx, start(n, ctx) + place * R);
+            int4 *out = reinterpret_cast<int4 *>(blocks + base + x);
+            out[0] = make_int4(k.p0, k.tq, k.first, k.last);
+            out[1] = make_int4(k.b, k.lo, k.n_band, k.n_tiles);
+            out[2] = make_int4(k.cpb, (int)k.inv_cpb, k.full_lo, k.full_hi);
+            if (a.slots) {
+                const SeqTiles q = seq_tiles(a.s, a.m_first, n, ctx);
+                // a tile of the band (or any, where they are all in one run) is in slot + x - slot_lo, one of skip
+                // window w in slot_windows + w * per_window + x - (its first tile)
+                const int slot = slot_base + (o > 0 ? slots_upto[o - 1] : 0);
+                out[3] = make_int4(slot, q.lo, q.band_tiles ? slot + q.band_tiles : -1, ctx);
+                blocks[base + x].per_window = q.per_window;
+            }
+        }
+        for (int x = tid; x < total_slots; x += PLAN_THREADS) {
+            int place;
+            const int o = owner(slots_upto, x, place);
+            const int n = bt.cu[b0 + o + 1] - bt.cu[b0 + o], ctx = bt.ctx[b0 + o];
+            const SeqTiles q = seq_tiles(a.s, a.m_first, n, ctx);
+            int tile = q.lo + place;
+            if (q.band_tiles && place >= q.band_tiles) {
+                const int w = (place - q.band_tiles) / q.per_window;
+                tile = ((ctx - (a.m_first + w) * a.s.period) >> 5) + (place - q.band_tiles) % q.per_window;
+                // the window's last tile may lie past it, and a whole tile before the sequence
+                if (tile > (ctx + n - 1 - (a.m_first + w) * a.s.period) >> 5) tile = -1;
+            }
+            a.slots[slot_base + x] = make_int2(b0 + o, tile);
         }
         base += total;
-        __syncthreads();
+        slot_base += total_slots;
     }
-    if (tid == 0) plan[0] = base;
+    if (tid == 0) {
+        plan[0] = base;
+        plan[1] = slot_base;
+    }
+}
+
+// ------------------------------------------------------------------ 8-bit tiles to bf16
+
+struct ConvertArgs {
+    Shape s;
+    PagedCache c;
+    PagedBatch bt;
+    int m_first;
+    const int *plan;
+    const int2 *slots;
+    __nv_bfloat16 *k, *v;  // [slots, Hkv, 32, d]
+    int *index_word;
+};
+
+constexpr int CONVERT_WARPS = 8;
+
+// Whether some query of the chunk attends a key in x .. y of its sequence.
+__device__ __forceinline__ bool attended(const ConvertArgs &a, int b, int x, int y) {
+    const int t0 = a.bt.cu[b], n = a.bt.cu[b + 1] - t0, ctx = a.bt.ctx[b], last = ctx + n - 1;
+    if (y >= band_lo(ctx, a.s.mode, a.s.k_local) && x <= last) return true;
+    if (a.s.mode == kModeEcp || a.s.S == 0 || x > last) return false;
+    // a window's keys are ctx - m * period .. last - m * period
+    const int m_hi = min(a.s.S, (last - x) / a.s.period);
+    const int m_lo = max(a.m_first, ctx > y ? (ctx - y + a.s.period - 1) / a.s.period : 0);
+    return m_lo <= m_hi;
+}
+
+// One warp per (slot, KV head, K or V): 32 rows of codes, all of them in flight at once, to 32 rows of bf16.  Rows of a page
+// out of range become zeros.
+template <int D, int KV>
+__global__ void __launch_bounds__(CONVERT_WARPS * 32) convert_kernel(const ConvertArgs a) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan is written
+    const PagedCache &c = a.c;
+    const int lane = threadIdx.x & 31;
+    constexpr int PER_ROW = D / 16, ITER = CHUNK * PER_ROW / 32;  // 16-code pieces; pieces per lane
+    const long long items = (long long)a.plan[1] * c.Hkv * 2;
+    for (long long x = (long long)blockIdx.x * CONVERT_WARPS + (threadIdx.x >> 5); x < items; x += (long long)gridDim.x * CONVERT_WARPS) {
+        const int v = (int)(x & 1);
+        const long long sh = x >> 1;  // slot * Hkv + head
+        const int slot = (int)(sh / c.Hkv), g = (int)(sh - (long long)slot * c.Hkv);
+        const int2 st = a.slots[slot];
+        if (st.y < 0) continue;
+        const int pos = st.y * CHUNK;
+        // the page of the tile (page 16: of its halves)
+        const int half = c.page < CHUNK ? lane >> 4 : 0;
+        int pg = -1;
+        if (pos + half * 16 < c.width << c.page_log2) {
+            pg = __ldg(a.bt.table + (long long)st.x * c.width + ((pos + half * 16) >> c.page_log2));
+            if ((unsigned)pg >= (unsigned)c.n_pages) {
+                pg = -1;
+                if ((lane & 15) == 0 && attended(a, st.x, pos + half * 16, pos + (c.page < CHUNK ? half * 16 + 15 : CHUNK - 1)))
+                    record_index(a.index_word);
+            }
+        }
+        const uint8_t *codes = static_cast<const uint8_t *>(v ? c.v : c.k), *scales = v ? c.v_scale : c.k_scale;
+        uint4 w[ITER];
+        uint32_t sc[ITER];
+#pragma unroll
+        for (int u = 0; u < ITER; ++u) {
+            const int piece = u * 32 + lane, r = piece / PER_ROW, col = piece % PER_ROW * 16;
+            const int p = __shfl_sync(0xffffffffu, pg, c.page < CHUNK && r >= 16 ? 16 : 0);
+            w[u] = make_uint4(0u, 0u, 0u, 0u);
+            sc[u] = 0u;
+            if (p >= 0) {
+                const long long row = row_in_page(c, p, g, pos + r);
+                w[u] = ldg_stream(reinterpret_cast<const uint4 *>(codes + row * D + col));
+                sc[u] = __ldg(scales + row * (D / kScaleBlock) + col / kScaleBlock);
+            }
+        }
+        uint4 *out = reinterpret_cast<uint4 *>((v ? a.v : a.k) + sh * (CHUNK * D));
+#pragma unroll
+        for (int u = 0; u < ITER; ++u) {
+            const Scale2<KV> s2 = scale_same<KV>(sc[u]);
+            uint32_t o[8];
+            codes_to_bf16<KV>(w[u].x, s2, s2.big, o[0], o[1]);
+            codes_to_bf16<KV>(w[u].y, s2, s2.big, o[2], o[3]);
+            codes_to_bf16<KV>(w[u].z, s2, s2.big, o[4], o[5]);
+            codes_to_bf16<KV>(w[u].w, s2, s2.big, o[6], o[7]);
+            out[2 * (u * 32 + lane)] = make_uint4(o[0], o[1], o[2], o[3]);
+            out[2 * (u * 32 + lane) + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+    }
 }
 
 // ------------------------------------------------------------------ shared memory, TMEM, barriers
 
-template <int D, int KV>
+template <int D>
 struct Cfg {
-    static constexpr bool QUANT = KV != kKvBf16;
     static constexpr int NB = D == 64 ? 4 : 2;  // S buffers; TMEM columns as in the forward
     static constexpr int O_COL = 128, Q_COL = D == 128 ? 64 : 192;
     static constexpr int KD = D / 64;
     static constexpr int Q_BYTES = BM * D * 2, Q_DBLK = BM * ROW_BYTES;
     static constexpr int KV_STAGE = CHUNK * D * 2, KV_DBLK = CHUNK * ROW_BYTES;
-    static constexpr int KSTAGES = (QUANT ? 24576 : 49152) / KV_STAGE;
-    static constexpr int VSTAGES = (QUANT ? 24576 : 32768) / KV_STAGE;
-    static constexpr int RSTAGES = QUANT ? 24576 / (2 * CHUNK * D) : 0;  // raw tiles: K then V codes
-    static constexpr int RAW = CHUNK * D;                                // bytes of one tile's codes
-    static constexpr int SCALES = CHUNK * (D / kScaleBlock);             // bytes of one tile's scales
+    static constexpr int KSTAGES = 49152 / KV_STAGE;
+    static constexpr int VSTAGES = 32768 / KV_STAGE;
     static constexpr int Q_OFF = 0;
     static constexpr int K_OFF = Q_OFF + Q_BYTES;
     static constexpr int V_OFF = K_OFF + KSTAGES * KV_STAGE;
-    static constexpr int R_OFF = V_OFF + VSTAGES * KV_STAGE;
-    static constexpr int SC_OFF = R_OFF + RSTAGES * 2 * RAW;
-    static constexpr int DATA_BYTES = SC_OFF + RSTAGES * 2 * SCALES;
+    static constexpr int DATA_BYTES = V_OFF + VSTAGES * KV_STAGE;
     // barriers; tiles are counted across the blocks a CTA processes, block k completes the per-block
     // ones in phase k
     static constexpr int B_Q = 0;                 // Q tile landed
-    static constexpr int B_KF = 1;                // K tile in its bf16 stage
-    static constexpr int B_KE = B_KF + KSTAGES;   // that stage free
+    static constexpr int B_KF = 1;                // K tile landed
+    static constexpr int B_KE = B_KF + KSTAGES;   // its stage free
     static constexpr int B_VF = B_KE + KSTAGES;
     static constexpr int B_VE = B_VF + VSTAGES;
     static constexpr int B_SF = B_VE + VSTAGES;   // [NB] S in TMEM
@@ -155,19 +374,15 @@ struct Cfg {
     static constexpr int B_DR = B_STR + 1;        // drains of the two MMA issuers
     static constexpr int B_DR2 = B_DR + 1;
     static constexpr int B_SD = B_DR2 + 1;        // S products of the block done
-    static constexpr int B_RF = B_SD + 1;         // [RSTAGES] raw tile landed
-    static constexpr int B_RE = B_RF + RSTAGES;   // [RSTAGES] raw tile read (4 warps)
-    static constexpr int NBARS = B_RE + RSTAGES;
+    static constexpr int NBARS = B_SD + 1;
     static constexpr int arrivals(int idx) {
         if ((idx >= B_PR && idx < B_PR + NB) || idx == B_STF) return 128;
-        if (QUANT && ((idx >= B_KF && idx < B_KF + KSTAGES) || (idx >= B_VF && idx < B_VF + VSTAGES) || idx >= B_RE)) return 4;
         return 1;
     }
     static constexpr int BAR_BYTES = NBARS * 8 + 16;
     static_assert(BAR_BYTES <= 512, "barriers must fit the alignment gap or its complement");
     static constexpr int SMEM_BYTES = DATA_BYTES + 1024;  // data from a 1024-byte boundary; barriers in the gap or behind
     static_assert(SMEM_BYTES <= 115712, "two CTAs per SM");
-    static constexpr int THREADS = QUANT ? 384 : 256;
 };
 
 struct Args {
@@ -175,52 +390,49 @@ struct Args {
     const int *plan;
     int GP, R, R_log2, ngrp;
     int m_first;
-    int aligned;  // period % 32 == 0: every skip window has the same place in its tiles
+    int aligned;  // period % 32 == 0
     int box;      // rows of a TMA box: min(32, page)
-    FastDiv div_ngrp, div_G, div_period;
+    int n_planes; // pages, or slots of converted tiles
+    FastDiv div_ngrp, div_G;
 };
 
-// One block: a plan block x one group of GP heads, and its key tiles.
-struct Block {
-    int b, p0, tq, first, last, h0, g;
-    int lo, n_band;       // first band key of the first query; tiles from lo rounded down to 32
-    int cpb;              // tiles per skip window
-    uint32_t inv_cpb;     // ceil(2^32 / cpb)
-    int n_tiles;
-    int full_lo, full_hi; // tiles inside the band of every query
+// One block: a plan block x one group of GP heads.
+struct Block : PlanBlock {
+    int h0, g;
 };
 
-__device__ __forceinline__ PlanBlock load_plan(const Args &a, int L) {
-    const int4 *p = reinterpret_cast<const int4 *>(reinterpret_cast<const char *>(a.plan) + PLAN_HEAD) + 2 * a.div_ngrp.div(L);
-    const int4 x = p[0];
-    PlanBlock d;
-    d.b = x.x; d.p0 = x.y; d.tq = x.z; d.first = x.w;
-    d.last = *reinterpret_cast<const int *>(p + 1);
-    return d;
+__device__ __forceinline__ const int4 *plan_at(const Args &a, int L) {
+    return reinterpret_cast<const int4 *>(reinterpret_cast<const char *>(a.plan) + PLAN_HEAD) + 5 * a.div_ngrp.div(L);
 }
-
-__device__ __forceinline__ void describe(const Args &a, const PlanBlock &d, int L, Block &k) {
-    const Shape &s = a.a.s;
-    k.b = d.b; k.p0 = d.p0; k.tq = d.tq; k.first = d.first; k.last = d.last;
-    k.h0 = (L - a.div_ngrp.div(L) * a.ngrp) * a.GP;
+__device__ __forceinline__ void load_rows(const Args &a, int L, PlanBlock &k) {  // the block's rows only
+    const int4 x = plan_at(a, L)[0];
+    k.p0 = x.x; k.tq = x.y; k.first = x.z; k.last = x.w;
+}
+__device__ __forceinline__ void load_tiles(const Args &a, int L, PlanBlock &k) {  // the rest
+    const int4 *p = plan_at(a, L);
+    const int4 y = p[1], z = p[2];
+    k.b = y.x; k.lo = y.y; k.n_band = y.z; k.n_tiles = y.w;
+    k.cpb = z.x; k.inv_cpb = (uint32_t)z.y; k.full_lo = z.z; k.full_hi = z.w;
+}
+__device__ __forceinline__ void load_slots(const Args &a, int L, PlanBlock &k) {  // where its converted tiles are
+    const int4 *p = plan_at(a, L);
+    const int4 x = p[3];
+    k.slot = x.x; k.slot_lo = x.y; k.slot_windows = x.z; k.ctx = x.w;
+    k.per_window = reinterpret_cast<const int *>(p + 4)[0];
+}
+__device__ __forceinline__ int first_head(const Args &a, int L) { return (L - a.div_ngrp.div(L) * a.ngrp) * a.GP; }
+template <bool CONVERTED>
+__device__ __forceinline__ void load_block(const Args &a, int L, Block &k) {
+    load_rows(a, L, k);
+    load_tiles(a, L, k);
+    if (CONVERTED) load_slots(a, L, k);
+    k.h0 = first_head(a, L);
     k.g = a.div_G.div(k.h0);
-    k.lo = band_lo(d.first, s.mode, s.k_local);
-    const int key0 = k.lo & ~(CHUNK - 1);
-    k.n_band = (d.last - key0) / CHUNK + 1;
-    int windows = 0;
-    if (s.mode != kModeEcp && s.S > 0) windows = max(0, min(s.S, a.div_period.div(d.last)) - a.m_first + 1);
-    k.cpb = a.aligned ? (d.last >> 5) - (d.first >> 5) + 1 : ((d.last - d.first) >> 5) + 2;
-    k.inv_cpb = 0xffffffffu / (uint32_t)k.cpb + 1u;  // 0 for one tile per window
-    k.n_tiles = k.n_band + windows * k.cpb;
-    const int lo_last = band_lo(d.last, s.mode, s.k_local);
-    k.full_lo = (lo_last - key0 + CHUNK - 1) / CHUNK;
-    const int span = d.first - (CHUNK - 1) - key0;
-    k.full_hi = span >= 0 ? span / CHUNK : -1;
 }
 
 // Tile ti of a block: its first key (negative: a tile wholly before the sequence), whether it is a skip tile,
 // and its skip distance.
-__device__ __forceinline__ int tile_key0(const Args &a, const Block &k, int ti, int &back, bool &skip) {
+__device__ __forceinline__ int tile_key0(const Args &a, const PlanBlock &k, int ti, int &back, bool &skip) {
     skip = ti >= k.n_band;
     if (!skip) {
         back = 0;
@@ -233,7 +445,7 @@ __device__ __forceinline__ int tile_key0(const Args &a, const Block &k, int ti, 
 }
 
 // Keys of tile ti that some query of the block attends or may attend: lo .. hi (empty: lo > hi).
-__device__ __forceinline__ int tile_range(const Args &a, const Block &k, int ti, int &lo, int &hi) {
+__device__ __forceinline__ int tile_range(const Args &a, const PlanBlock &k, int ti, int &lo, int &hi) {
     int back;
     bool skip;
     const int key0 = tile_key0(a, k, ti, back, skip);
@@ -244,13 +456,13 @@ __device__ __forceinline__ int tile_range(const Args &a, const Block &k, int ti,
 
 constexpr int NO_PAGE = -2;  // a box without an attended row
 
-template <int D, int KV>
-__global__ void __launch_bounds__(Cfg<D, KV>::THREADS, 2)
+// CONVERTED: key and value tiles from the workspace (8-bit caches) instead of pages.
+template <int D, bool CONVERTED>
+__global__ void __launch_bounds__(THREADS, 2)
 extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                  const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO, const Args args) {
-    using C = Cfg<D, KV>;
+    using C = Cfg<D>;
     constexpr int KST = C::KSTAGES, VST = C::VSTAGES, NB = C::NB;
-    constexpr int RST = C::QUANT ? C::RSTAGES : 1;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
     const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
@@ -287,68 +499,78 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = *tmem_slot;
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan is written
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan is written, and the tiles are converted
 
     const int n_blocks = args.plan[0] * args.ngrp;
     const int L0 = blockIdx.x, LS = gridDim.x;
     auto next_block = [&](int L) -> int { return (L < n_blocks - LS) ? L + LS : n_blocks; };
 
     // ---- page lookup of a producer warp: lane x holds the page-table entries of tile t0 + x (page 16: of
-    // both halves), NO_PAGE where a box has no attended row
-    auto lookup = [&](const Block &k, int t0, int &e0, int &e1) {
+    // both halves; NO_PAGE where a box has no attended row) and the tile's first row in its page
+    auto lookup = [&](const Block &k, int t0, int &e0, int &e1, int &row) {
         e0 = e1 = NO_PAGE;
+        row = 0;
         if (t0 + lane >= k.n_tiles) return;
         int lo, hi;
         const int key0 = tile_range(args, k, t0 + lane, lo, hi);
-        const int *row = ea.batch.table + (long long)k.b * cache.width;
+        if (CONVERTED) {
+            if (lo > hi) return;
+            int back;
+            bool skip;
+            tile_key0(args, k, t0 + lane, back, skip);
+            e0 = skip && k.slot_windows >= 0
+                     ? k.slot_windows + (back / s.period - args.m_first) * k.per_window + (key0 >> 5) - ((k.ctx - back) >> 5)
+                     : k.slot + (key0 >> 5) - k.slot_lo;
+            return;
+        }
+        const int *table = ea.batch.table + (long long)k.b * cache.width;
+        row = key0 & (cache.page - 1);
         if (args.box == CHUNK) {
-            if (lo <= hi) e0 = __ldg(row + (key0 >> cache.page_log2));
+            if (lo <= hi) e0 = __ldg(table + (key0 >> cache.page_log2));
         } else {
-            if (lo <= min(hi, key0 + 15)) e0 = __ldg(row + (key0 >> cache.page_log2));
-            if (max(lo, key0 + 16) <= hi) e1 = __ldg(row + ((key0 + 16) >> cache.page_log2));
+            if (lo <= min(hi, key0 + 15)) e0 = __ldg(table + (key0 >> cache.page_log2));
+            if (max(lo, key0 + 16) <= hi) e1 = __ldg(table + ((key0 + 16) >> cache.page_log2));
         }
     };
-    // page-table entry -> plane of the page maps (one past the last, which reads as zeros, where there is no page)
+    // page-table entry (or slot) -> plane of the page maps (one past the last, which reads as zeros, where there is no page)
     auto plane = [&](const Block &k, int e) -> int {
-        if ((unsigned)e < (unsigned)cache.n_pages) return e * cache.Hkv + k.g;
+        if ((unsigned)e < (unsigned)args.n_planes) return e * cache.Hkv + k.g;
         if (e != NO_PAGE) record_index(ea.index_word);
-        return cache.n_pages * cache.Hkv;
+        return args.n_planes * cache.Hkv;
     };
-    // Walks the tiles of every block of the CTA: issue(block, tile, number, z0, z1, row) by the whole warp, with the
-    // entries of a block's first 32 tiles requested a block ahead.  before/after a block: hooks.
-    auto walk_tiles = [&](auto &&issue, auto &&block_end) {
+    // Walks the tiles of every block of the CTA: issue(block, the next one, is there one, tile, tiles so far, planes and
+    // row) by the whole warp, with the entries of a block's first 32 tiles requested a block ahead.
+    auto walk_tiles = [&](auto &&issue) {
         if (L0 >= n_blocks) return true;
-        Block k;
-        int e0, e1;
-        describe(args, load_plan(args, L0), L0, k);
-        lookup(k, 0, e0, e1);
-        PlanBlock pn = load_plan(args, min(L0 + LS, n_blocks - 1));
+        Block k, kn;
+        int e0, e1, row;
+        load_block<CONVERTED>(args, L0, k);
+        lookup(k, 0, e0, e1, row);
         uint32_t n = 0;
-        for (int L = L0, kb = 0;; ++kb) {
+        for (int L = L0;;) {
             const int Ln = next_block(L);
-            Block kn = k;
-            int n0 = NO_PAGE, n1 = NO_PAGE;
+            int n0 = NO_PAGE, n1 = NO_PAGE, nrow = 0;
             if (Ln < n_blocks) {
-                describe(args, pn, Ln, kn);
-                lookup(kn, 0, n0, n1);
-                const int Lnn = next_block(Ln);
-                if (Lnn < n_blocks) pn = load_plan(args, Lnn);
+                load_block<CONVERTED>(args, Ln, kn);
+                lookup(kn, 0, n0, n1, nrow);
             }
             int z0 = 0, z1 = 0;
             for (int t = 0; t < k.n_tiles; ++t, ++n) {
                 if ((t & 31) == 0) {
-                    if (t) lookup(k, t, e0, e1);
+                    if (t) lookup(k, t, e0, e1, row);
                     z0 = plane(k, e0);
                     z1 = plane(k, e1);
                 }
-                if (!issue(k, t, n, __shfl_sync(0xffffffffu, z0, t & 31), __shfl_sync(0xffffffffu, z1, t & 31))) return false;
+                if (!issue(k, kn, Ln < n_blocks, t, n, __shfl_sync(0xffffffffu, z0, t & 31), __shfl_sync(0xffffffffu, z1, t & 31),
+                           __shfl_sync(0xffffffffu, row, t & 31)))
+                    return false;
             }
-            if (!block_end(k, kn, kb, Ln < n_blocks)) return false;
             if (Ln >= n_blocks) return true;
             L = Ln;
             k = kn;
             e0 = n0;
             e1 = n1;
+            row = nrow;
         }
     };
     // one lane: a tile's boxes of bf16 rows
@@ -360,17 +582,12 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 tma_load_3d_hint(dst + dc * C::KV_DBLK + 16 * ROW_BYTES, tm, dc * 64, 0, z1, full, policy);
         }
     };
-    auto page_row = [&](const Block &k, int t) -> int {
-        int back;
-        bool skip;
-        return tile_key0(args, k, t, back, skip) & (cache.page - 1);
-    };
     auto issue_q = [&](const Block &k) {  // one lane
         mbar_expect_tx(bar(C::B_Q), C::Q_BYTES);
         for (int dc = 0; dc < C::KD; ++dc)
             tma_load_3d_hint(sQ + dc * C::Q_DBLK, &tmQ, dc * 64, k.tq, k.h0, bar(C::B_Q), policy_evict_first());
     };
-    auto is_whole = [&](const Block &k) -> bool { return k.first == k.p0 && k.last == k.p0 + args.R - 1; };
+    auto is_whole = [&](const PlanBlock &k) -> bool { return k.first == k.p0 && k.last == k.p0 + args.R - 1; };
     // The staged output of block kb (one lane): stored if the block is full (else its rows went out from registers).
     auto store_out = [&](const Block &k, int kb) -> bool {
         if (!wait_bar(bar(C::B_STF), (uint32_t)(kb & 1), wc)) return false;
@@ -391,57 +608,32 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     };
 
     if (warp == 0) {
-        // ================= producer: K tiles (bf16), or the raw K and V tiles with their scales (8 bits)
+        // ================= producer: K tiles
         const uint64_t reused = policy_evict_last();
         uint32_t issued = 0;
-        auto issue = [&](const Block &k, int t, uint32_t n, int z0, int z1) -> bool {
-            const int stages = C::QUANT ? RST : KST, full = C::QUANT ? C::B_RF : C::B_KF, empty = C::QUANT ? C::B_RE : C::B_KE;
-            const int st = (int)(n % stages);
-            const uint32_t round = n / stages;
-            const bool ok = round == 0 || wait_bar(bar(empty + st), (round - 1) & 1, wc);
+        auto issue = [&](const Block &, const Block &, bool, int, uint32_t n, int z0, int z1, int row) -> bool {
+            const int st = (int)(n % KST);
+            const uint32_t round = n / KST;
+            const bool ok = round == 0 || wait_bar(bar(C::B_KE + st), (round - 1) & 1, wc);
             if (!__all_sync(0xffffffffu, ok)) return false;
             issued = n + 1;
-            if (lane == 0) {
-                const int row = page_row(k, t);
-                if constexpr (!C::QUANT) {
-                    load_tile(&tmK, sK + st * C::KV_STAGE, bar(full + st), row, z0, z1, reused);
-                } else {
-                    // codes by TMA (zeros where there is no page), scales as contiguous bytes: where there is no page
-                    // the converters take any scale (a code of zero, or a masked row)
-                    const uint32_t dst = sbase + C::R_OFF + st * 2 * C::RAW, sc = sbase + C::SC_OFF + st * 2 * C::SCALES;
-                    const int none = cache.n_pages * cache.Hkv, halves = args.box == CHUNK ? 1 : 2;
-                    const uint32_t bytes = C::SCALES / halves;
-                    uint32_t total = 2 * C::RAW;
-                    for (int h = 0; h < halves; ++h) total += (h ? z1 : z0) != none ? 2 * bytes : 0;
-                    mbar_expect_tx(bar(full + st), total);
-                    for (int h = 0; h < halves; ++h) {
-                        const int z = h ? z1 : z0, r = h ? 0 : row;
-                        tma_load_3d_hint(dst + h * 16 * D, &tmK, 0, r, z, bar(full + st), reused);
-                        tma_load_3d_hint(dst + C::RAW + h * 16 * D, &tmV, 0, r, z, bar(full + st), reused);
-                        if (z == none) continue;
-                        const long long at = (((long long)z << cache.page_log2) + r) * (D / kScaleBlock);
-                        bulk_load(sc + h * bytes, cache.k_scale + at, bytes, bar(full + st));
-                        bulk_load(sc + C::SCALES + h * bytes, cache.v_scale + at, bytes, bar(full + st));
-                    }
-                }
-            }
+            if (lane == 0) load_tile(&tmK, sK + st * C::KV_STAGE, bar(C::B_KF + st), row, z0, z1, reused);
             __syncwarp();
             return true;
         };
-        walk_tiles(issue, [](const Block &, const Block &, int, bool) { return true; });
-        if (*abort_flag && lane == 0) drain(C::QUANT ? C::B_RF : C::B_KF, C::QUANT ? RST : KST, issued);
+        walk_tiles(issue);
+        if (*abort_flag && lane == 0) drain(C::B_KF, KST, issued);
         __syncwarp();
     } else if (warp == 2) {
-        // ================= Q tiles, the stores of staged output, and (bf16) the V tiles.  At V tile t_st of block k
+        // ================= Q tiles, the stores of staged output, and the V tiles.  At V tile t_st of block k
         // the output of block k-1 has been staged; once its store has read the buffer, the Q tile of block
         // k+1 takes its place (that of block k is in TMEM by then).
         const uint64_t reused = policy_evict_last();
         uint32_t issued = 0;
         int q_loads = 0;
-        Block prev, nx;
-        bool have_next = false;
-        int kb_now = 0;
-        auto turn = [&](int kb) -> bool {  // the whole warp: store block kb-1, load block kb+1's queries
+        Block prev;
+        int kb = 0;
+        auto turn = [&](const Block &nx, bool have_next) -> bool {  // the whole warp: store block kb-1, load block kb+1's queries
             bool ok = true;
             if (lane == 0) {
                 if (kb > 0) ok = store_out(prev, kb - 1);
@@ -457,52 +649,34 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         bool ok = true;
         if (L0 < n_blocks) {
             Block k;
-            describe(args, load_plan(args, L0), L0, k);
+            load_block<CONVERTED>(args, L0, k);
             if (lane == 0) issue_q(k);
             q_loads = 1;
             __syncwarp();
         }
-        if constexpr (!C::QUANT) {
-            int L = L0;
-            auto issue = [&](const Block &k, int t, uint32_t n, int z0, int z1) -> bool {
-                if (t == 0) {
-                    const int Ln = next_block(L);
-                    have_next = Ln < n_blocks;
-                    if (have_next) describe(args, load_plan(args, Ln), Ln, nx);
-                }
-                const int st = (int)(n % VST);
-                const uint32_t round = n / VST;
-                const bool w = round == 0 || wait_bar(bar(C::B_VE + st), (round - 1) & 1, wc);
-                if (!__all_sync(0xffffffffu, w)) return false;
-                issued = n + 1;
-                if (lane == 0) load_tile(&tmV, sV + st * C::KV_STAGE, bar(C::B_VF + st), page_row(k, t), z0, z1, reused);
-                __syncwarp();
-                return t != min(4, k.n_tiles - 1) || turn(kb_now);
-            };
-            ok = walk_tiles(issue, [&](const Block &k, const Block &, int kb, bool) {
+        auto issue = [&](const Block &k, const Block &nx, bool have_next, int t, uint32_t n, int z0, int z1, int row) -> bool {
+            const int st = (int)(n % VST);
+            const uint32_t round = n / VST;
+            const bool w = round == 0 || wait_bar(bar(C::B_VE + st), (round - 1) & 1, wc);
+            if (!__all_sync(0xffffffffu, w)) return false;
+            issued = n + 1;
+            if (lane == 0) load_tile(&tmV, sV + st * C::KV_STAGE, bar(C::B_VF + st), row, z0, z1, reused);
+            __syncwarp();
+            if (t == min(4, k.n_tiles - 1) && !turn(nx, have_next)) return false;
+            if (t == k.n_tiles - 1) {
                 prev = k;
-                kb_now = kb + 1;
-                L = next_block(L);
-                return true;
-            });
-        } else {
-            for (int L = L0; ok && L < n_blocks; L = next_block(L), ++kb_now) {
-                Block k;
-                describe(args, load_plan(args, L), L, k);
-                const int Ln = next_block(L);
-                have_next = Ln < n_blocks;
-                if (have_next) describe(args, load_plan(args, Ln), Ln, nx);
-                ok = turn(kb_now);
-                prev = k;
+                ++kb;
             }
-        }
-        if (ok && kb_now > 0 && lane == 0) ok = store_out(prev, kb_now - 1);  // the CTA's last block
+            return true;
+        };
+        ok = walk_tiles(issue);
+        if (ok && kb > 0 && lane == 0) ok = store_out(prev, kb - 1);  // the CTA's last block
         __syncwarp();
         if (*abort_flag && lane == 0) {
             volatile uint32_t zero = 0;
             WaitCtx w2{&zero, nullptr, 20000000ull};
             if (q_loads > 0) wait_bar(bar(C::B_Q), (uint32_t)((q_loads - 1) & 1), w2);
-            if (!C::QUANT) drain(C::B_VF, VST, issued);
+            drain(C::B_VF, VST, issued);
             tma_store_commit_and_wait();
         }
         __syncwarp();
@@ -514,12 +688,10 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         uint32_t gs = 0;
         int kb = 0;
         bool ok = true;
-        PlanBlock pd{};
-        if (L0 < n_blocks) pd = load_plan(args, L0);
+        int n_next = L0 < n_blocks ? plan_at(args, L0)[1].w : 0;
         for (int L = L0; ok && L < n_blocks; L = next_block(L), ++kb) {
-            Block k;
-            describe(args, pd, L, k);
-            if (next_block(L) < n_blocks) pd = load_plan(args, next_block(L));
+            const int n_tiles = n_next;
+            if (next_block(L) < n_blocks) n_next = plan_at(args, next_block(L))[1].w;
             bool w = (kb == 0) || wait_bar(bar(C::B_SD), (uint32_t)((kb - 1) & 1), wc);
             if (w) w = wait_bar(bar(C::B_Q), (uint32_t)(kb & 1), wc);
             ok = __all_sync(0xffffffffu, w);
@@ -535,7 +707,7 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 tc_commit(bar(C::B_QT));
             }
             __syncwarp();
-            for (int t = 0; t < k.n_tiles; ++t, ++gs) {
+            for (int t = 0; t < n_tiles; ++t, ++gs) {
                 const int st = (int)(gs % KST), buf = (int)(gs % NB);
                 bool r = wait_bar(bar(C::B_KF + st), (gs / KST) & 1, wc);
                 if (r && gs >= NB) r = wait_bar(bar(C::B_PV + buf), ((gs - NB) / NB) & 1, wc);
@@ -554,7 +726,7 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                                    idesc, (dc | ks) != 0);
                     tc_commit(bar(C::B_SF + buf));
                     tc_commit(bar(C::B_KE + st));
-                    if (t == k.n_tiles - 1) tc_commit(bar(C::B_SD));
+                    if (t == n_tiles - 1) tc_commit(bar(C::B_SD));
                 }
                 __syncwarp();
             }
@@ -569,17 +741,22 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         const uint32_t idesc = idesc_bf16(BM, D, 0, 1);
         uint32_t gp = 0;
         bool ok = true;
-        PlanBlock pd{};
-        if (L0 < n_blocks) pd = load_plan(args, L0);
+        PlanBlock kn{};
+        auto load = [&](int L) {
+            load_rows(args, L, kn);
+            load_tiles(args, L, kn);
+        };
+        if (L0 < n_blocks) load(L0);
         for (int L = L0; ok && L < n_blocks; L = next_block(L)) {
-            Block k;
-            describe(args, pd, L, k);
-            if (next_block(L) < n_blocks) pd = load_plan(args, next_block(L));
+            const PlanBlock k = kn;
+            if (next_block(L) < n_blocks) load(next_block(L));
+            // (otherwise every tile's rows are all attended, or all before the sequence and loaded as zeros)
+            const bool ragged = ((k.lo | k.first | (k.last + 1)) & (CHUNK - 1)) != 0 || (k.n_tiles > k.n_band && !args.aligned);
             for (int t = 0; t < k.n_tiles; ++t, ++gp) {
                 const int buf = (int)(gp % NB), st = (int)(gp % VST);
                 bool w = wait_bar(bar(C::B_VF + st), (gp / VST) & 1, wc);
-                if (!C::QUANT && w) {
-                    // rows of V that no query attends: zero (the converters do this for 8-bit tiles)
+                if (w && ragged) {
+                    // rows of V that no query attends: zero
                     int lo, hi;
                     const int key0 = tile_range(args, k, t, lo, hi);
                     if (lo > key0 || hi < key0 + CHUNK - 1) {  // the same for the warp
@@ -617,7 +794,7 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         volatile uint32_t zero = 0;
         WaitCtx w2{&zero, ea.status, ea.timeout_ns};
         wait_bar(bar(C::B_DR2), 0, w2);
-    } else if (warp < 8) {
+    } else {
         // ================= softmax and epilogue: one thread per row
         const int q4 = warp & 3;
         const int r = q4 * 32 + lane;
@@ -628,28 +805,27 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         auto alpha_of = [&](const PlanBlock &d, int L) -> float {
             const int i = d.p0 + trow;
             if (!ea.alpha || i < d.first || i > d.last) return 1.f;
-            const int h0 = (L - args.div_ngrp.div(L) * args.ngrp) * args.GP;
-            return __ldg(ea.alpha + (long long)(d.tq + trow) * s.H + h0 + hh);
+            return __ldg(ea.alpha + (long long)(d.tq + trow) * s.H + first_head(args, L) + hh);
         };
         bool ok = true;
         uint32_t gsm = 0;
         int kb = 0;
-        PlanBlock pd{}, pn{};
+        PlanBlock k{}, kn{};  // this block and the next one (its rows; its tiles are loaded before the epilogue)
         float al_next = 1.f;
         if (L0 < n_blocks) {
-            pd = load_plan(args, L0);
-            al_next = alpha_of(pd, L0);
+            load_rows(args, L0, k);
+            load_tiles(args, L0, k);
+            if (next_block(L0) < n_blocks) load_rows(args, next_block(L0), kn);
+            al_next = alpha_of(k, L0);
         }
         for (int L = L0; ok && L < n_blocks; ++kb) {
-            Block k;
-            describe(args, pd, L, k);
             const int Ln = next_block(L);
             const bool has_next = Ln < n_blocks;
-            if (has_next) pn = load_plan(args, Ln);
             const float al = al_next;
+            if (has_next) al_next = alpha_of(kn, Ln);  // requested now, used after this block
             const float off_band = ea.alpha ? log2f(al) : 0.f, off_skip = log2f(1.f - al);
             // a row without a query takes the part of the nearest one; its result is dropped
-            const int i = min(max(k.p0 + trow, k.first), k.last), h = k.h0 + hh;
+            const int i = min(max(k.p0 + trow, k.first), k.last), h = first_head(args, L) + hh;
             const bool row_ok = i == k.p0 + trow;
             const int lo_i = band_lo(i, s.mode, s.k_local);
 
@@ -663,7 +839,7 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 const uint32_t tS = tbase + lane_base + buf * CHUNK;
                 uint32_t ra[CHUNK];
                 tmem_ld32(tS, ra);
-                tmem_wait_ld();
+                tmem_wait_ld32(ra);
                 // Tiles inside every query's band: P with the running reference; the maximum only once some P
                 // exceeds 2^8, which a sum above 2^8 is the first sign of.
                 const bool fast = t >= k.full_lo && t <= k.full_hi && __all_sync(0xffffffffu, m_ref != -INFINITY);
@@ -710,7 +886,7 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                         lsum = tile_exp(ra, sc, bo);
                         if (!fast || pass > 0 || !__any_sync(0xffffffffu, !(lsum <= 256.f))) break;
                         tmem_ld32(tS, ra);
-                        tmem_wait_ld();
+                        tmem_wait_ld32(ra);
                         const float mt = fmaf(tile_raw_max(ra), sc, off_band);
                         if (mt > m_ref + kRescaleThreshold) {
                             corr = fast_exp2(m_ref - mt);
@@ -738,7 +914,7 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                     for (int oc = 0; oc < D / 16; ++oc) {
                         uint32_t x[16];
                         tmem_ld16(tbase + lane_base + C::O_COL + oc * 16, x);
-                        tmem_wait_ld();
+                        tmem_wait_ld16(x);
 #pragma unroll
                         for (int c = 0; c < 16; ++c) x[c] = __float_as_uint(__uint_as_float(x[c]) * f);
                         tmem_st16(tbase + lane_base + C::O_COL + oc * 16, x);
@@ -748,11 +924,11 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 tc_fence_before();
                 mbar_arrive(bar(C::B_PR + buf));
             }
-            if (ok && has_next) al_next = alpha_of(pn, Ln);  // used after the epilogue
 
             // ---- epilogue: O / l as bf16, staged in shared memory for its TMA store, or (a block that is not full)
             // straight to the rows that hold queries
             const bool whole = is_whole(k);
+            if (has_next) load_tiles(args, Ln, kn);
             if (ok) ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_OF), (uint32_t)(kb & 1), wc));
             if (ok && kb > 0) ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_STR), (uint32_t)((kb - 1) & 1), wc));
             if (ok && has_next) ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_QT), (uint32_t)((kb + 1) & 1), wc));
@@ -767,7 +943,8 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 uint32_t x[64];
                 tmem_ld32(tbase + lane_base + C::O_COL + oh * 32, x);
                 tmem_ld32(tbase + lane_base + C::O_COL + oh * 32 + 32, x + 32);
-                tmem_wait_ld();
+                tmem_wait_ld32(x);
+                tmem_wait_ld32(x + 32);
                 uint8_t *rowp = smem + C::Q_OFF + (oh >> 1) * C::Q_DBLK + r * ROW_BYTES;
 #pragma unroll
                 for (int w = 0; w < 8; ++w) {
@@ -782,71 +959,9 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             tc_fence_before();
             mbar_arrive(bar(C::B_STF));
             if (row_ok) ea.lse[row_g] = (l > 0.f) ? (m_ref + log2f(l)) * kLn2 : -INFINITY;
+            k = kn;
             L = Ln;
-            pd = pn;
-        }
-    } else if constexpr (C::QUANT) {
-        // ================= converters (warps 8-11): raw tiles -> bf16 tiles.  Lane = row of the tile; warp w takes
-        // the codes of columns (D / 4) w ... (D / 4) w + D / 4 - 1, which share a scale block.
-        const int w = warp - 8;
-        constexpr int CH = D / 64;  // 16-code chunks per lane and tile
-        uint32_t n = 0;
-        bool ok = true;
-        PlanBlock pd{};
-        if (L0 < n_blocks) pd = load_plan(args, L0);
-        for (int L = L0; ok && L < n_blocks; L = next_block(L)) {
-            Block k;
-            describe(args, pd, L, k);
-            if (next_block(L) < n_blocks) pd = load_plan(args, next_block(L));
-            for (int t = 0; t < k.n_tiles; ++t, ++n) {
-                const int rs = (int)(n % RST);
-                int lo, hi;
-                const int key0 = tile_range(args, k, t, lo, hi);
-                const bool used = key0 + lane >= lo && key0 + lane <= hi;
-                ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_RF + rs), (n / RST) & 1, wc));
-                if (!ok) break;
-#pragma unroll
-                for (int kv = 0; kv < 2; ++kv) {
-                    const uint8_t *raw = smem + C::R_OFF + rs * 2 * C::RAW + kv * C::RAW + lane * D;
-                    uint4 x[CH];
-#pragma unroll
-                    for (int u = 0; u < CH; ++u) {
-                        // raw rows of 128 bytes are swizzled over 8 rows, rows of 64 bytes over pairs of rows
-                        const int chunk = w * CH + u;
-                        x[u] = *reinterpret_cast<const uint4 *>(raw + ((D == 128 ? chunk ^ (lane & 7) : chunk ^ ((lane >> 1) & 3)) << 4));
-                    }
-                    const uint32_t sb = smem[C::SC_OFF + (rs * 2 + kv) * C::SCALES + lane * (D / kScaleBlock) + w * (D / 4) / kScaleBlock];
-                    const Scale2 s2 = scale_same(sb);
-                    if (kv == 1) {  // both raw tiles are read
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar(C::B_RE + rs));
-                    }
-                    const int stages = kv ? VST : KST, st = (int)(n % stages);
-                    const uint32_t round = n / stages;
-                    if (round > 0) ok = __all_sync(0xffffffffu, wait_bar(bar((kv ? C::B_VE : C::B_KE) + st), (round - 1) & 1, wc));
-                    if (!ok) break;
-                    uint8_t *out = smem + (kv ? C::V_OFF : C::K_OFF) + st * C::KV_STAGE + lane * ROW_BYTES;
-#pragma unroll
-                    for (int u = 0; u < CH; ++u) {
-                        uint32_t o[8];
-                        const uint32_t c4[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) codes_to_bf16<KV>(c4[y], s2, o[2 * y], o[2 * y + 1]);
-                        if (!used) {  // may hold anything: zero for the PV product, any score is masked
-#pragma unroll
-                            for (int y = 0; y < 8; ++y) o[y] = 0u;
-                        }
-                        const int col = (w * CH + u) * 16, c16 = (col & 63) >> 3;  // 16-byte pieces c16, c16 + 1 of the row
-                        uint8_t *blk = out + (col >> 6) * C::KV_DBLK;
-                        *reinterpret_cast<uint4 *>(blk + ((c16 ^ (lane & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-                        *reinterpret_cast<uint4 *>(blk + (((c16 + 1) ^ (lane & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar((kv ? C::B_VF : C::B_KF) + st));
-                }
-                if (!ok) break;
-            }
+            if (L < n_blocks && next_block(L) < n_blocks) load_rows(args, next_block(L), kn);
         }
     }
 
@@ -862,82 +977,113 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 
 // ------------------------------------------------------------------ host side
 
-// 3-D map of 16-bit (bf16) or 8-bit elements: [n2][n1][n0] with strides in bytes and a box (b0, b1, b2).
-static bool encode(CUtensorMap *m, const void *ptr, bool bf16, int n0, long long n1, long long n2, long long st1, long long st2,
-                   int b0, int b1, int b2, CUtensorMapSwizzle swizzle) {
+// 3-D bf16 map [n2][n1][d] with strides in bytes and a box (64, b1, b2), 128-byte swizzle.
+static bool encode(CUtensorMap *m, const void *ptr, int d, long long n1, long long n2, long long st1, long long st2, int b1, int b2) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
-    const cuuint64_t dims[3] = {(cuuint64_t)n0, (cuuint64_t)n1, (cuuint64_t)n2};
+    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)n1, (cuuint64_t)n2};
     const cuuint64_t strides[2] = {(cuuint64_t)st1, (cuuint64_t)st2};
-    const cuuint32_t box[3] = {(cuuint32_t)b0, (cuuint32_t)b1, (cuuint32_t)b2};
+    const cuuint32_t box[3] = {64u, (cuuint32_t)b1, (cuuint32_t)b2};
     const cuuint32_t estr[3] = {1u, 1u, 1u};
-    return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(ptr), dims, strides,
-              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int KV>
-static cudaError_t launch(const Args &a, cudaStream_t st) {
-    using C = Cfg<D, KV>;
-    const ExtendArgs &e = a.a;
-    const PagedCache &c = e.cache;
-    const long long planes = (long long)c.n_pages * c.Hkv, row = (long long)D * (C::QUANT ? 1 : 2);
-    const CUtensorMapSwizzle page_swizzle = !C::QUANT || D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
-    CUtensorMap mq, mk, mv, mo;
-    if (!encode(&mq, e.q, true, D, e.batch.T, e.s.H, e.q_stride * 2, D * 2, 64, a.R, a.GP, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode(&mo, e.out, true, D, e.batch.T, e.s.H, (long long)e.s.H * D * 2, D * 2, 64, a.R, a.GP, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode(&mk, c.k, !C::QUANT, D, c.page, planes, row, row * c.page, C::QUANT ? D : 64, a.box, 1, page_swizzle) ||
-        !encode(&mv, c.v, !C::QUANT, D, c.page, planes, row, row * c.page, C::QUANT ? D : 64, a.box, 1, page_swizzle))
-        return cudaErrorNotSupported;
-    static PerDeviceOnce configured;
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (configured.needed(dev)) {
-        const cudaError_t err = cudaFuncSetAttribute(extend_tc_kernel<D, KV>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
-        if (err != cudaSuccess) return err;
-        configured.mark(dev);
-    }
-    const long long most = max_blocks(e.batch.T, e.batch.B, a.R) * a.ngrp;
+static int packed_heads(int G) { return G % 4 == 0 ? 4 : G % 2 == 0 ? 2 : 1; }
+
+// The workspace: the plan; for an 8-bit cache the slots' list and the converted tiles.
+struct Layout {
+    size_t slots, k, v, bytes;  // offsets
+    long long n_slots;
+};
+static Layout layout(const Shape &s, int kv_type, long long B, long long T, long long cap) {
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    Layout l{};
+    const int GP = packed_heads(s.H / s.Hkv);
+    l.bytes = l.slots = up((size_t)(PLAN_HEAD + max_blocks(T, B, BM / GP) * (long long)sizeof(PlanBlock)));
+    if (kv_type == kKvBf16) return l;
+    l.n_slots = most_slots(s, B, T, cap);
+    const size_t tiles = up((size_t)l.n_slots * s.Hkv * CHUNK * s.d * 2);
+    l.k = l.slots + up((size_t)l.n_slots * sizeof(int2));
+    l.v = l.k + tiles;
+    l.bytes = l.v + tiles;
+    return l;
+}
+
+// Launches a kernel that may start while the one before it on the stream still runs (it waits for it itself).
+template <typename K, typename... A>
+static cudaError_t launch_dependent(K kernel, long long grid, int threads, int smem, cudaStream_t st, const A &...a) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)std::min<long long>(most, 2LL * pi::sm_count()), 1, 1);
-    cfg.blockDim = dim3(C::THREADS, 1, 1);
-    cfg.dynamicSmemBytes = C::SMEM_BYTES;
+    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, extend_tc_kernel<D, KV>, mq, mk, mv, mo, a);
+    return cudaLaunchKernelEx(&cfg, kernel, a...);
 }
 
-static int packed_heads(int G) { return G % 4 == 0 ? 4 : G % 2 == 0 ? 2 : 1; }
+template <int D, bool CONVERTED>
+static cudaError_t launch(const Args &a, const void *k, const void *v, cudaStream_t st) {
+    const ExtendArgs &e = a.a;
+    const PagedCache &c = e.cache;
+    const long long planes = (long long)a.n_planes * c.Hkv, rows = CONVERTED ? CHUNK : c.page;
+    CUtensorMap mq, mk, mv, mo;
+    if (!encode(&mq, e.q, D, e.batch.T, e.s.H, e.q_stride * 2, D * 2, a.R, a.GP) ||
+        !encode(&mo, e.out, D, e.batch.T, e.s.H, (long long)e.s.H * D * 2, D * 2, a.R, a.GP) ||
+        !encode(&mk, k, D, rows, planes, D * 2, D * 2 * rows, a.box, 1) || !encode(&mv, v, D, rows, planes, D * 2, D * 2 * rows, a.box, 1))
+        return cudaErrorNotSupported;
+    constexpr int smem = Cfg<D>::SMEM_BYTES;
+    static PerDeviceOnce configured;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (configured.needed(dev)) {
+        const cudaError_t err = cudaFuncSetAttribute(extend_tc_kernel<D, CONVERTED>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (err != cudaSuccess) return err;
+        configured.mark(dev);
+    }
+    const long long most = max_blocks(e.batch.T, e.batch.B, a.R) * a.ngrp;
+    return launch_dependent(extend_tc_kernel<D, CONVERTED>, std::min<long long>(most, 2LL * pi::sm_count()), THREADS, smem, st, mq, mk, mv,
+                            mo, a);
+}
 
 }  // namespace ext
 
-size_t extend_workspace_bytes(long long B, long long T) {
-    // blocks of at least 32 positions
-    return (size_t)(ext::PLAN_HEAD + ext::max_blocks(T, B, ext::BM / 4) * (long long)sizeof(ext::PlanBlock));
+size_t extend_workspace_bytes(const Shape &s, int kv_type, long long B, long long T, long long cap) {
+    return ext::layout(s, kv_type, B, T, cap).bytes;
 }
 
 cudaError_t launch_extend(const ExtendArgs &e, cudaStream_t st) {
     using namespace ext;
     const Shape &s = e.s;
+    const PagedCache &c = e.cache;
     const int G = s.H / s.Hkv, GP = packed_heads(G), R = BM / GP, ngrp = s.H / GP;
-    if (max_blocks(e.batch.T, e.batch.B, R) * ngrp > 0x7fffffffLL - 1024) return cudaErrorInvalidConfiguration;
-    const bool skips = s.mode != kModeEcp && s.S > 0;
+    const bool quant = c.kv_type != kKvBf16, skips = s.mode != kModeEcp && s.S > 0;
+    const Layout l = layout(s, c.kv_type, e.batch.B, e.batch.T, (long long)c.width << c.page_log2);
+    if (max_blocks(e.batch.T, e.batch.B, R) * ngrp > 0x7fffffffLL - 1024 || l.n_slots * s.Hkv > 0x7fffffffLL / CHUNK)
+        return cudaErrorInvalidConfiguration;
+    char *ws = reinterpret_cast<char *>(e.workspace);
+    int2 *slots = quant ? reinterpret_cast<int2 *>(ws + l.slots) : nullptr;
     Args a{e, e.workspace, GP, R, R == 32 ? 5 : R == 64 ? 6 : 7, ngrp, skips ? first_skip_multiple(s) : 1,
-           skips && s.period % CHUNK == 0, std::min(CHUNK, e.cache.page), make_fastdiv(ngrp), make_fastdiv(G),
-           make_fastdiv(skips ? s.period : 1)};
-    plan_kernel<<<1, PLAN_THREADS, 0, st>>>(e.cache, e.batch, R, e.workspace, e.index_word);
-    const cudaError_t err = cudaGetLastError();
+           skips && s.period % CHUNK == 0, quant ? CHUNK : std::min(CHUNK, c.page), quant ? (int)l.n_slots : c.n_pages,
+           make_fastdiv(ngrp), make_fastdiv(G)};
+    plan_kernel<<<1, PLAN_THREADS, 0, st>>>(PlanArgs{s, c, e.batch, R, a.m_first, a.aligned, e.workspace, e.index_word, slots});
+    cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
-    const bool d64 = s.d == 64;
-    switch (e.cache.kv_type) {
-        case kKvBf16: return d64 ? launch<64, kKvBf16>(a, st) : launch<128, kKvBf16>(a, st);
-        case kKvE4m3: return d64 ? launch<64, kKvE4m3>(a, st) : launch<128, kKvE4m3>(a, st);
-        default: return d64 ? launch<64, kKvInt8>(a, st) : launch<128, kKvInt8>(a, st);
-    }
+    if (!quant) return s.d == 64 ? launch<64, false>(a, c.k, c.v, st) : launch<128, false>(a, c.k, c.v, st);
+    __nv_bfloat16 *k = reinterpret_cast<__nv_bfloat16 *>(ws + l.k), *v = reinterpret_cast<__nv_bfloat16 *>(ws + l.v);
+    const ConvertArgs ca{s, c, e.batch, a.m_first, e.workspace, slots, k, v, e.index_word};
+    const long long items = l.n_slots * s.Hkv * 2;
+    const long long grid = std::min<long long>((items + CONVERT_WARPS - 1) / CONVERT_WARPS, 4LL * pi::sm_count());
+    auto convert = s.d == 64 ? (c.kv_type == kKvE4m3 ? convert_kernel<64, kKvE4m3> : convert_kernel<64, kKvInt8>)
+                             : (c.kv_type == kKvE4m3 ? convert_kernel<128, kKvE4m3> : convert_kernel<128, kKvInt8>);
+    err = launch_dependent(convert, grid, CONVERT_WARPS * 32, 0, st, ca);
+    if (err != cudaSuccess) return err;
+    return s.d == 64 ? launch<64, true>(a, k, v, st) : launch<128, true>(a, k, v, st);
 }
 
 }  // namespace pi

@@ -5,6 +5,7 @@
 #include <cstdint>
 
 #include "pi_paged.cuh"
+#include "pi_tc_ptx.cuh"
 
 namespace pi {
 
@@ -38,34 +39,75 @@ __device__ __forceinline__ uint4 ldg_stream(const uint4 *p) {
     return r;
 }
 
-// Scales of the two codes of a pair, from their bytes.
-struct Scale2 {
-    float lo, hi;
-};
-__device__ __forceinline__ Scale2 scale_pair(uint32_t lo, uint32_t hi) { return Scale2{scale_of((int)lo), scale_of((int)hi)}; }
-__device__ __forceinline__ Scale2 scale_same(uint32_t b) { return scale_pair(b, b); }
-
-// The four codes of a word to two bf16 pairs: codes 0, 1 to `a` and 2, 3 to `b`, the even ones times
-// s.lo, the odd ones times s.hi.
+// Scales of the two codes of a pair, from their bytes, as codes_to_bf16 takes them.
+//   int8: as fp32.
+//   e4m3: as a bf16 pair of factors 2^120 s; what of 2^120 s exceeds 2^127 is in a second pair.
 template <int KV>
-__device__ __forceinline__ void codes_to_bf16(uint32_t w, const Scale2 &s, uint32_t &a, uint32_t &b) {
-    float f[4];
-    if (KV == kKvE4m3) {
-        const __half2_raw h0 = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
-        const __half2_raw h1 = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
-        const float2 x = __half22float2(__half2(h0)), y = __half22float2(__half2(h1));
-        f[0] = x.x; f[1] = x.y; f[2] = y.x; f[3] = y.y;
+struct Scale2;
+template <>
+struct Scale2<kKvInt8> {
+    uint64_t s;
+    bool big;  // not used
+};
+template <>
+struct Scale2<kKvE4m3> {
+    uint32_t f, more;
+    bool big;
+};
+
+template <int KV>
+__device__ __forceinline__ Scale2<KV> scale_pair(uint32_t lo, uint32_t hi) {
+    Scale2<KV> r;
+    if constexpr (KV == kKvInt8) {
+        r.s = tc::pack2(scale_of((int)lo), scale_of((int)hi));
+        r.big = false;
     } else {
-        // 2^23 + (code + 128) from its bits, less 2^23 + 128
-        const uint32_t u = w ^ 0x80808080u;
-        const float off = 8388608.f + 128.f;
-        f[0] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440)) - off;
-        f[1] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7441)) - off;
-        f[2] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7442)) - off;
-        f[3] = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7443)) - off;
+        // byte b: 2^120 * 2^(b - 127) has the bf16 exponent field b + 120, at most 254; 255 is a NaN
+        auto factor = [](uint32_t b) -> uint32_t { return b == (uint32_t)kScaleNan ? 0x7fffu : min(b + 120u, 254u) << 7; };
+        auto rest = [](uint32_t b) -> uint32_t { return (b > 134u ? b - 134u + 127u : 127u) << 7; };
+        r.f = factor(lo) | factor(hi) << 16;
+        r.big = max(lo, hi) > 134u;
+        r.more = rest(lo) | rest(hi) << 16;
     }
-    a = pack_bf16x2(f[0] * s.lo, f[1] * s.hi);
-    b = pack_bf16x2(f[2] * s.lo, f[3] * s.hi);
+    return r;
+}
+template <int KV>
+__device__ __forceinline__ Scale2<KV> scale_same(uint32_t b) { return scale_pair<KV>(b, b); }
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// The four codes of a word to two bf16 pairs: codes 0, 1 to `a` and 2, 3 to `b`, the even ones times the
+// pair's low scale, the odd ones times the high one.
+//   e4m3: the code's sign, exponent and fraction moved to bf16's places are the value times 2^-120 (both formats hold
+//   their subnormals alike), which the factor makes up for: exact, five instructions per pair.
+//   int8: code + 128 as the low byte of an fp32 number 2^23 + code + 128, less 2^23 + 128, times s.
+// `big`: whether the second factors are needed (some scale above 2^7; a caller may ask once for a whole tile).
+template <int KV>
+__device__ __forceinline__ void codes_to_bf16(uint32_t w, const Scale2<KV> &s, bool big, uint32_t &a, uint32_t &b) {
+    if constexpr (KV == kKvE4m3) {
+        const uint32_t x = __byte_perm(w, 0u, 0x1404), y = __byte_perm(w, 0u, 0x3424);  // code << 8 per half
+        a = mul_bf16x2((x & 0x7f007f00u) >> 4 | (x & 0x80008000u), s.f);
+        b = mul_bf16x2((y & 0x7f007f00u) >> 4 | (y & 0x80008000u), s.f);
+        if (big) {
+            a = mul_bf16x2(a, s.more);
+            b = mul_bf16x2(b, s.more);
+        }
+    } else {
+        const uint32_t u = w ^ 0x80808080u;
+        float f[4];
+        const uint64_t off = tc::pack2(-8388736.f, -8388736.f);
+        auto two = [&](uint32_t sel0, uint32_t sel1) {
+            return tc::mul2(tc::add2(tc::pack2(__uint_as_float(__byte_perm(u, 0x4b000000u, sel0)),
+                                               __uint_as_float(__byte_perm(u, 0x4b000000u, sel1))), off), s.s);
+        };
+        tc::unpack2(two(0x7440, 0x7441), f[0], f[1]);
+        tc::unpack2(two(0x7442, 0x7443), f[2], f[3]);
+        a = pack_bf16x2(f[0], f[1]);
+        b = pack_bf16x2(f[2], f[3]);
+    }
 }
 
 // Contiguous bytes (a multiple of 16, both addresses 16-byte aligned) into shared memory, counted on an mbarrier.

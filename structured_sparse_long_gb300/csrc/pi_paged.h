@@ -58,7 +58,7 @@ struct ExtendArgs {
     Shape s;                 // H, Hkv, d, k_local, period, S, mode, scale_log2
     PagedCache cache;
     PagedBatch batch;
-    int *workspace;          // extend_workspace_bytes(B, T)
+    int *workspace;          // extend_workspace_bytes()
     int *status, *index_word;
     uint64_t timeout_ns;
 };
@@ -82,7 +82,7 @@ cudaError_t launch_cache_read(const ReadArgs &a, cudaStream_t st);
 
 // attention over a paged cache: a chunk of new tokens per sequence (pi_extend_tc.cu), one new token per
 // sequence (pi_decode_paged.cu)
-size_t extend_workspace_bytes(long long B, long long T);
+size_t extend_workspace_bytes(const Shape &s, int kv_type, long long B, long long T, long long cap);
 cudaError_t launch_extend(const ExtendArgs &a, cudaStream_t st);
 cudaError_t launch_decode_paged(const DecodePagedArgs &a, cudaStream_t st);
 

@@ -40,7 +40,7 @@ def _load():
         lib.pi_attn_cache_read.argtypes = [C, B, P, P, P]
         lib.pi_attn_decode_paged.argtypes = [P, L, C, P, P, I, I, P, I, I, I, I, I, P, P, P]
         lib.pi_attn_extend.argtypes = [P, L, C, B, P, I, I, I, I, I, P, P, P, ctypes.c_size_t, P]
-        lib.pi_attn_extend_workspace_size.argtypes = [I, I]
+        lib.pi_attn_extend_workspace_size.argtypes = [C, I, I, I, I, I, I, I, I]
         lib.pi_attn_extend_workspace_size.restype = ctypes.c_size_t
         for name in ("cache_append", "cache_read", "decode_paged", "extend"):
             getattr(lib, "pi_attn_" + name).restype = I
@@ -195,9 +195,11 @@ def _outputs(q, cache, alpha, mode, out, lse):
     return out, lse
 
 
-def extend_workspace_size(B: int, T: int) -> int:
-    """pi_attn_extend_workspace_size: bytes of device workspace for B sequences with T packed tokens."""
-    return int(_load().pi_attn_extend_workspace_size(B, T))
+def extend_workspace_size(cache: PagedCache, B: int, T: int, width: int, H: int, k_local: int, period: int, S: int,
+                          mode: int = MODE_PI) -> int:
+    """pi_attn_extend_workspace_size: bytes of device workspace that :func:`extend` needs for B sequences with T packed
+    tokens and page tables of `width` entries (0 for sizes that it refuses)."""
+    return int(_load().pi_attn_extend_workspace_size(cache._ref, B, T, width, H, k_local, period, S, mode))
 
 
 def extend(q, cache: PagedCache, table, cu, ctx, alpha, k_local: int, period: int, S: int, mode: int = MODE_PI,
@@ -211,9 +213,9 @@ def extend(q, cache: PagedCache, table, cu, ctx, alpha, k_local: int, period: in
     if T > 0:
         with _on(cache.device):
             lib = _load()
-            nbytes = lib.pi_attn_extend_workspace_size(batch.B, T)
+            nbytes = lib.pi_attn_extend_workspace_size(cache._ref, batch.B, T, batch.width, H, k_local, period, S, mode)
             if workspace is None:
-                workspace = torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
+                workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=cache.device)
             else:
                 _binding._expect_like(workspace, "workspace", cache, torch.uint8, None)
                 if workspace.numel() < nbytes:

@@ -449,3 +449,30 @@ def test_offsets_past_32_bits():
     want = ref.attention(q, *held, a, 0, 64, 100, 2, PI)
     ref.check_attention("extend", out, lse, want)
     ref.check_attention("decode", o1, l1, [x[-1:] for x in want])
+
+
+@pytest.mark.parametrize("kv", ["e4m3", "int8"])
+@pytest.mark.parametrize("where", ["k", "v"])
+def test_attention_with_scales_of_any_size(kv, where):
+    """Keys (against queries that make up for it) and values 2^-100 to 2^100 times their usual size: the kernels'
+    conversions hold over the whole range of the scales."""
+    Hkv, H, d, page, N, n = 2, 8, 128, 16, 150, 40
+    gen = torch.Generator().manual_seed(4)
+    table, cu, ctx = dev(np.arange(10)[None]), dev([0, n]), dev([N - n])
+    for power in (-100, -20, 10, 60, 100):
+        size = 2.0 ** power
+        k, v, q = (normal(gen, m, h, d) for m, h in ((N, Hkv), (N, Hkv), (n, H)))
+        if where == "k":
+            k, q = k * size, q / size
+        else:
+            v = v * size
+        cache = pa.PagedCache.empty(10, Hkv, page, d, ref.DTYPE[kv])
+        pa.cache_append(k.cuda(), v.cuda(), cache, table, dev([0, N]), dev([0]))
+        a = torch.rand(n, H, generator=gen)
+        out, lse = pa.extend(q.cuda(), cache, table, cu, ctx, a.cuda(), 64, 50, 2)
+        o1, l1 = pa.decode_paged(q[-1:].cuda(), cache, table, dev([N]), a[-1:].cuda(), 64, 50, 2)
+        torch.cuda.synchronize()
+        held = [torch.from_numpy(ref.decode(*ref.encode(x.float().numpy(), kv), kv)).to(torch.bfloat16) for x in (k, v)]
+        want = ref.attention(q, *held, a, N - n, 64, 50, 2, PI)
+        ref.check_attention(f"extend 2^{power}", out, lse, want)
+        ref.check_attention(f"decode 2^{power}", o1, l1, [x[-1:] for x in want])

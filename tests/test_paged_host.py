@@ -105,14 +105,67 @@ def test_sizes_past_the_limits(lib):
     assert decode(lib, table=A16 + 2) == PI_ERR_ALIGN
 
 
+def workspace(lib, c=None, B=2, T=5, width=4, H=4, kl=8, per=16, S=1, mode=0):
+    return lib.pi_attn_extend_workspace_size(c or cache(), B, T, width, H, kl, per, S, mode)
+
+
 def test_extend_workspace(lib):
-    """A plan of at most T / 32 + 2 min(B, T) blocks of 32 bytes and its head."""
+    """A plan of at most T / R + 2 min(B, T) blocks of 80 bytes and its head; refused where the call would be."""
     for B, T in ((1, 1), (1, 65536), (16, 80), (1000, 30)):
-        need = lib.pi_attn_extend_workspace_size(B, T)
-        assert need == 32 + 32 * (T // 32 + 2 * min(B, T))
-        assert extend(lib, b=batch(B=B, T=T), ws_bytes=need - 1) == PI_ERR_WORKSPACE
-    assert lib.pi_attn_extend_workspace_size(0, 5) == 0 and lib.pi_attn_extend_workspace_size(5, 0) == 0
+        need = workspace(lib, B=B, T=T, width=1 << 20)
+        plan = 32 + 80 * (T // 64 + 2 * min(B, T))  # two query heads per KV head: 64 positions per block
+        assert need == -(-plan // 256) * 256
+        assert extend(lib, b=batch(B=B, T=T, width=1 << 20), ws_bytes=need - 1) == PI_ERR_WORKSPACE
+    quant = dict(kv_type=1, ks=A16, vs=A16)
+    assert workspace(lib, cache(**quant)) > workspace(lib)
+    assert extend(lib, c=cache(**quant), ws_bytes=workspace(lib, cache(**quant)) - 1) == PI_ERR_WORKSPACE
+    for bad in (dict(B=0), dict(T=0), dict(width=0), dict(H=3), dict(kl=-1), dict(mode=2), dict(c=cache(d=96))):
+        assert workspace(lib, **bad) == 0
     assert extend(lib, ws=None) == PI_ERR_WORKSPACE and extend(lib, ws=A16 + 16) == PI_ERR_ALIGN
+
+
+def seq_tiles(n, ctx, k, period, S, ecp):
+    """The plan kernel's bf16 tiles of one sequence over an 8-bit cache: their list, and the slot of a band tile or of
+    tile x of the window at distance back."""
+    last = ctx + n - 1
+    band0 = max(0, (ctx // k - 1) * k) if ecp else max(0, ctx - k)
+    m_first = 1 if ecp or not S else min(k // period + 1, S + 1)
+    windows = 0 if ecp or not S else max(0, min(S, last // period) - m_first + 1)
+    lo, per_window = band0 >> 5, ((n - 1) >> 5) + 2
+    band = (last >> 5) - lo + 1
+    if windows:
+        first = min(lo, max(0, ctx - (m_first + windows - 1) * period) >> 5)
+        if (last >> 5) - first + 1 <= band + windows * per_window:
+            return list(range(first, (last >> 5) + 1)), lambda x, back: x - first
+    tiles = list(range(lo, (last >> 5) + 1))
+    for m in range(m_first, m_first + windows):
+        start = (ctx - m * period) >> 5
+        tiles += [x if x <= (last - m * period) >> 5 else -1 for x in range(start, start + per_window)]
+    return tiles, lambda x, back: x - lo if not back else band + (back // period - m_first) * per_window + x - ((ctx - back) >> 5)
+
+
+def test_converted_tiles_hold_every_attended_key_within_the_bound(lib):
+    """Every attended key's tile has a slot that holds it, and a batch's slots fit the workspace whatever its lengths."""
+    rng = np.random.default_rng(0)
+    for _ in range(400):
+        ecp = rng.random() < 0.2
+        k, period, S = int(rng.integers(1, 300)), int(rng.integers(1, 400)), 0 if ecp else int(rng.integers(0, 6))
+        used, T, B = 0, 0, int(rng.integers(1, 4))
+        for _ in range(B):
+            ctx, n = int(rng.integers(0, 2000)), int(rng.integers(1, 400))
+            tiles, slot = seq_tiles(n, ctx, k, period, S, ecp)
+            used, T = used + len(tiles), T + n
+            for i in {ctx, ctx + n - 1, int(rng.integers(ctx, ctx + n))}:
+                lo = max(0, (i // k - 1) * k) if ecp else max(0, i - k)
+                for j in range(lo, i + 1):
+                    assert tiles[slot(j >> 5, 0)] == j >> 5
+                for m in range(1, S + 1):
+                    if m * period > k and i >= m * period:
+                        assert tiles[slot((i - m * period) >> 5, m * period)] == (i - m * period) >> 5
+        c = dict(Hkv=1, d=64, page=16)
+        kw = dict(B=B, T=T, width=150, H=1, kl=k, per=period, S=S, mode=int(ecp))
+        room = workspace(lib, cache(kv_type=1, ks=A16, vs=A16, **c), **kw) - workspace(lib, cache(**c), **kw)
+        assert used * (8 + 2 * 32 * 64 * 2) <= room
 
 
 def plan(n, ctx, R):
