@@ -841,7 +841,7 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 tmem_ld32(tS, ra);
                 tmem_wait_ld32(ra);
                 // Tiles inside every query's band: P with the running reference; the maximum only once some P
-                // exceeds 2^8, which a sum above 2^8 is the first sign of.
+                // exceeds 2^12, which a sum above 2^12 is the first sign of.
                 const bool fast = t >= k.full_lo && t <= k.full_hi && __all_sync(0xffffffffu, m_ref != -INFINITY);
                 float corr = 1.f, lsum, bo;
                 bool need_o = false, diag = false;
@@ -884,7 +884,7 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 #pragma unroll 1
                     for (int pass = 0;; ++pass) {
                         lsum = tile_exp(ra, sc, bo);
-                        if (!fast || pass > 0 || !__any_sync(0xffffffffu, !(lsum <= 256.f))) break;
+                        if (!fast || pass > 0 || !__any_sync(0xffffffffu, !(lsum <= kRescaleSum))) break;
                         tmem_ld32(tS, ra);
                         tmem_wait_ld32(ra);
                         const float mt = fmaf(tile_raw_max(ra), sc, off_band);

@@ -30,7 +30,7 @@
 //     MMAs and the commits).
 //   * Warps 4-7 run the softmax, one thread per row (TMEM lane = row): masks,
 //     adds the prior, keeps the running max m and sum l (rescaling O in TMEM only
-//     when the max grows by more than 2^8), writes P as bf16 over its S, and at
+//     when the max grows by more than 2^12), writes P as bf16 over its S, and at
 //     the end of the block normalises O and stages it in shared memory.
 //   * The fused gate (GATE) puts one more tile in front of a block's key tiles: the
 //     W1 rows of the block's heads, so that its S product is the heads' hidden
@@ -671,8 +671,8 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 if (k == 0 && warp == 4 && lane == 0) stamp_tile(184, t);
 
                 // Full tile (the same for every thread of the CTA): P with the running reference;
-                // the maximum is only needed when some P exceeds 2^8 (the lazy-rescale bound),
-                // which a sum above 2^8 is the first sign of.  Rows with no reference yet take the
+                // the maximum is only needed when some P exceeds 2^12 (the lazy-rescale bound),
+                // which a sum above 2^12 is the first sign of.  Rows with no reference yet take the
                 // general path, as do the debug modes that record per-row ranges.
                 const bool fast = (DBG == 0 || DBG == 3) && tk >= bd.full_lo && tk <= bd.full_hi &&
                                   __all_sync(0xffffffffu, m_ref != -INFINITY);
@@ -731,7 +731,7 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
 #pragma unroll 1
                     for (int pass = 0;; ++pass) {
                         lsum = tile_exp(ra, sc, bo);
-                        if (!fast || pass > 0 || !__any_sync(0xffffffffu, !(lsum <= 256.f))) break;
+                        if (!fast || pass > 0 || !__any_sync(0xffffffffu, !(lsum <= kRescaleSum))) break;
                         tmem_ld32(tS, ra);
                         tmem_wait_ld();
                         const float mt = fmaf(tile_raw_max(ra), sc, off_band);
