@@ -351,7 +351,7 @@ int pi_attn_cache_read(const pi_attn_cache_t *cache, const pi_attn_batch_t *batc
  *   pi_attn_cache_append), alpha [T, H] fp32 (NULL in ECP mode), out [T, H, d] bf16 and
  *   lse [T, H] fp32, contiguous.  H % Hkv == 0; T * H < 2^31.
  *   A sequence with an offset or length out of range is left out, its rows of out and lse
- *   as they were (all sequences, where cu decreases anywhere); a row that attends a key on a page out of range is undefined.
+ *   as they were (where cu decreases anywhere, any of the batch's rows may be); a row that attends a key on a page out of range is undefined.
  *   Non-finite values in cache rows that no query of the chunk attends do not matter;
  *   a non-finite value in a row that some query attends may reach the outputs of the
  *   sequence's other queries within 128 positions.

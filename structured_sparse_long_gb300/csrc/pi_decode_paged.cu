@@ -34,9 +34,20 @@ constexpr int MAX_P = 8;   // CTAs per cluster (portable limit)
 constexpr int KEYS = 16;   // keys per tile: the rows of S^T
 constexpr unsigned kFull = 0xffffffffu;
 
+// One step of decode (TOKENS = false: sequence b's one query at position lens[b] - 1), or a few new tokens per
+// sequence (TOKENS: packed queries as in pi_attn_extend, at most `group` of them per CTA).
 struct Args {
-    DecodePagedArgs a;
-    int m_first;
+    const __nv_bfloat16 *q;
+    long long q_stride;
+    const float *alpha;
+    const int *lens;
+    PagedBatch batch;  // B, table; cu, ctx and T with TOKENS
+    __nv_bfloat16 *out;
+    float *lse;
+    Shape s;
+    PagedCache cache;
+    int *index_word;
+    int m_first, group;
 };
 
 // ---- what a lane holds of a tile -------------------------------------------------------------
@@ -186,42 +197,105 @@ __device__ __forceinline__ void accumulate(const Frag<D, KV> &f, const uint32_t 
     }
 }
 
-// NH: groups of 8 query heads (1 or 2); WARPS per CTA
-template <int D, int KV, int NH, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32, NH == 1 ? 2 : 1) decode_paged_kernel(const Args args) {
-    const DecodePagedArgs &a = args.a;
+// Warps of a kernel that an SM holds, and the most of one CTA: by the registers that its fragments take (bf16 at d = 128
+// spills in 128; 16 columns need twice the queries and accumulators).
+constexpr int sm_warps(int D, int KV, int NH) { return NH == 2 ? 8 : D == 128 && KV == kKvBf16 ? 12 : 16; }
+constexpr int max_warps(int D, int KV, int NH) { return sm_warps(D, KV, NH) / (NH == 2 ? 1 : 2); }
+
+// NH: groups of 8 columns (1 or 2), a column being one query head of one token
+template <int D, int KV, int NH, bool TOKENS>
+__global__ void __launch_bounds__(max_warps(D, KV, NH) * 32, sm_warps(D, KV, NH) / max_warps(D, KV, NH))
+paged_rows_kernel(const Args a) {
     const Shape &s = a.s;
     const PagedCache &c = a.cache;
-    constexpr int PART = D + 4;  // floats of a head's partial state: o[D], m, l, padding to 16 bytes
-    extern __shared__ __align__(16) float part[];  // [WARPS][G][PART]
-    const int P = gridDim.x, rank = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
+    constexpr int MAX_W = max_warps(D, KV, NH);
+    constexpr int PART = D + 4;  // floats of a column's partial state: o[D], m, l, padding to 16 bytes
+    extern __shared__ __align__(16) float part[];  // [warps + 1][columns][PART]
+    const int P = gridDim.x, rank = blockIdx.x, kvh = blockIdx.y, warps = blockDim.x >> 5;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int G = s.H / s.Hkv, h0 = kvh * G;
 
-    int n = __ldg(a.lens + b);
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // ---- the CTA's sequence b, its queries' positions first .. last and their first packed token tok0
+    int b, first, last, tok0;
+    if constexpr (!TOKENS) {
+        b = tok0 = blockIdx.z;
+        last = __ldg(a.lens + b) - 1;
+        if (last < -1 || last >= (long long)c.width << c.page_log2) {
+            if (threadIdx.x == 0) record_index(a.index_word);
+            last = -1;
+        }
+        first = last;
+    } else {
+        if (blockIdx.z == 0 && kvh == 0 && rank == 0)  // offsets that decrease may hide their sequence from the search below
+            for (int j = threadIdx.x; j < a.batch.B; j += blockDim.x)
+                if (__ldg(a.batch.cu + j) > __ldg(a.batch.cu + j + 1)) record_index(a.index_word);
+        // sequence b's token groups are numbered from (cu[b] + b (group - 1)) / group on, which leaves each its ceil(n / group)
+        const int id = blockIdx.z;
+        auto start = [&](int j) -> long long { return ((long long)__ldg(a.batch.cu + j) + (long long)j * (a.group - 1)) / a.group; };
+        b = find_sequence(a.batch.B, [&](int j) { return start(j) <= id; });
+        if (b >= a.batch.B) return;
+        const int t0 = __ldg(a.batch.cu + b), t1 = __ldg(a.batch.cu + b + 1), ctx = __ldg(a.batch.ctx + b);
+        if (!sequence_ok(c, a.batch, t0, t1, ctx)) {
+            if (threadIdx.x == 0) record_index(a.index_word);
+            return;
+        }
+        const long long x = (id - start(b)) * a.group;
+        if (x < 0 || x >= t1 - t0) return;
+        const int x0 = (int)x;
+        tok0 = t0 + x0;
+        first = ctx + x0;
+        last = min(first + a.group, ctx + t1 - t0) - 1;
+    }
+    const int n_tok = TOKENS ? last - first + 1 : 1, cols = n_tok * G;
+    // column x: token x / G, head x % G
+    auto row_of = [&](int x) -> long long { return TOKENS ? (long long)(tok0 + x / G) * s.H + h0 + x % G : (long long)b * s.H + h0 + x; };
+
     uint2 q[NH][D / 16];
     float offb[NH][2], offs[NH][2];
+    int tok[NH][2];  // the token of the lane's columns
 #pragma unroll
     for (int nh = 0; nh < NH; ++nh) {
-        load_q<D, KV>(q[nh], a.q + (long long)b * a.q_stride + (h0 + 8 * nh + g) * D, 8 * nh + g < G, t);
+        const int x = 8 * nh + g;
+        load_q<D, KV>(q[nh], a.q + (TOKENS ? (tok0 + x / G) * a.q_stride + (h0 + x % G) * D : b * a.q_stride + (h0 + x) * D), x < cols, t);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int hh = 8 * nh + 2 * t + e;
-            const float al = a.alpha && hh < G ? __ldg(a.alpha + (long long)b * s.H + h0 + hh) : 1.f;
+            const int y = 8 * nh + 2 * t + e;
+            tok[nh][e] = TOKENS ? y / G : 0;
+            const float al = a.alpha && y < cols ? __ldg(a.alpha + row_of(y)) : 1.f;
             offb[nh][e] = a.alpha ? log2f(al) : 0.f;
             offs[nh][e] = log2f(1.f - al);
         }
     }
-    if (n < 0 || n > (long long)c.width << c.page_log2) {
-        if (threadIdx.x == 0) record_index(a.index_word);
-        n = 0;
-    }
-    // the key list: band lo .. n-1, then the skips n-1 - m * period, m = m_first ...
-    const int i = n - 1;
-    const int lo = n > 0 ? band_lo(i, s.mode, s.k_local) : 0, n_band = n - lo;
+    // ---- the key list: the band lo .. last, then for each skip distance m * period, m = m_first ..., the n_tok keys that
+    // many before the queries (some may lie before the sequence)
+    const int lo = last >= 0 ? band_lo(first, s.mode, s.k_local) : 0, n_band = last - lo + 1;
     int n_keys = n_band;
-    if (n > 0 && s.mode != kModeEcp && s.S > 0) n_keys += max(0, min(s.S, i / s.period) - args.m_first + 1);
+    if (last >= 0 && s.mode != kModeEcp && s.S > 0) n_keys += n_tok * max(0, min(s.S, last / s.period) - a.m_first + 1);
     const int n_tiles = (n_keys + KEYS - 1) / KEYS;
+    // Key kk: its cache row (-1: none) and, for the masks, its position (band) or -1 - u (the key of query first + u alone).
+    auto key = [&](int kk, int &row, int &tag) {
+        row = -1;
+        tag = -0x7fffffff;  // attended by nobody
+        if (kk >= n_keys) return;
+        int pos;
+        if (kk < n_band) {
+            pos = tag = lo + kk;
+        } else {
+            const int x = kk - n_band, w = TOKENS ? x / n_tok : x, u = TOKENS ? x - w * n_tok : 0;
+            pos = first + u - (a.m_first + w) * s.period;
+            if (pos < 0) return;
+            tag = -1 - u;
+        }
+        const int pg = page_of(c, a.batch.table, b, pos);
+        if (pg >= 0) {
+            row = row_in_page(c, pg, kvh, pos);
+        } else {
+            tag = -0x7fffffff;
+            record_index(a.index_word);
+        }
+    };
 
     float m[NH][2], l[NH][2], o[NH][D / 16][4];
 #pragma unroll
@@ -233,60 +307,64 @@ __global__ void __launch_bounds__(WARPS * 32, NH == 1 ? 2 : 1) decode_paged_kern
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[nh][j][e] = 0.f;
     }
-    const int step = P * WARPS;
-    for (int tile = rank * WARPS + warp; tile < n_tiles; tile += 2 * step) {
-        // rows of this tile (lanes 0-15) and of the warp's next one (16-31)
-        const int kk = (tile + (lane < KEYS ? 0 : step)) * KEYS + (lane & (KEYS - 1));
-        int row = -1;
-        if (kk < n_keys) {
-            const int pos = kk < n_band ? lo + kk : i - (args.m_first + kk - n_band) * s.period;
-            const int pg = page_of(c, a.table, b, pos);
-            if (pg >= 0) row = row_in_page(c, pg, kvh, pos);
-            else record_index(a.index_word);
-        }
+
+    // ---- the warp's tiles.  Lanes 0-15 hold the rows of one tile, 16-31 those of the warp's next one.  (Requesting the next
+    // tile's K after this one's scores, and its V after P V, took 15.8 us where this takes 12.7: the waits for the older
+    // loads also wait for the newer ones.)
+    const int step = P * warps;
+    int tile = rank * warps + warp;
+    Frag<D, KV> f;
+    int row, tag;
+    auto load_keys = [&](int u) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) load_k<D, KV>(f, c, x, __shfl_sync(kFull, row, u * KEYS + g + 8 * x), t);
+    };
+    auto load_values = [&](int u) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) load_v<D, KV>(f, c, x, __shfl_sync(kFull, row, u * KEYS + 2 * t + (x & 1) + 8 * (x >> 1)), g);
+    };
+    if (tile < n_tiles) key((tile + (lane < KEYS ? 0 : step)) * KEYS + (lane & (KEYS - 1)), row, tag);
 #pragma unroll 1
-        for (int u = 0; u < 2; ++u) {
-            const int t0 = (tile + u * step) * KEYS;
-            if (t0 >= n_keys) break;
-            Frag<D, KV> f;
+    for (int u = 0; tile < n_tiles; tile += step, u ^= 1) {
+        load_keys(u);
+        load_values(u);
+        const int tag0 = __shfl_sync(kFull, tag, u * KEYS + g), tag1 = __shfl_sync(kFull, tag, u * KEYS + g + 8);
+        float sc[NH][4] = {};
+        scores<D, KV, NH>(f, q, sc, t);
+        if (u == 1 && tile + step < n_tiles) key((tile + (lane < KEYS ? step : 2 * step)) * KEYS + (lane & (KEYS - 1)), row, tag);
+        uint32_t p[NH][2];
 #pragma unroll
-            for (int x = 0; x < 2; ++x) load_k<D, KV>(f, c, x, __shfl_sync(kFull, row, u * KEYS + g + 8 * x), t);
+        for (int nh = 0; nh < NH; ++nh) {
+            float pr[4];
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-                load_v<D, KV>(f, c, x, __shfl_sync(kFull, row, u * KEYS + 2 * t + (x & 1) + 8 * (x >> 1)), g);
-            const bool has0 = __shfl_sync(kFull, row, u * KEYS + g) >= 0, has1 = __shfl_sync(kFull, row, u * KEYS + g + 8) >= 0;
-            float sc[NH][4] = {};
-            scores<D, KV, NH>(f, q, sc, t);
-            uint32_t p[NH][2];
+            for (int e = 0; e < 2; ++e) {
+                const int i = first + tok[nh][e];
+                const int lo_i = TOKENS ? band_lo(i, s.mode, s.k_local) : lo;
+                auto logit = [&](int tg, float x) -> float {
+                    if (tg >= 0) return tg >= lo_i && tg <= i ? fmaf(x, s.scale_log2, offb[nh][e]) : -INFINITY;
+                    return tg == -1 - tok[nh][e] ? fmaf(x, s.scale_log2, offs[nh][e]) : -INFINITY;
+                };
+                const float z0 = logit(tag0, sc[nh][e]), z1 = logit(tag1, sc[nh][2 + e]);
+                float mx = fmaxf(z0, z1);
+                mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
+                mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
+                mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
+                const float mn = fmaxf(m[nh][e], mx), ref = mn == -INFINITY ? 0.f : mn;
+                const float corr = exp2f(m[nh][e] - ref);
+                pr[e] = exp2f(z0 - ref);
+                pr[2 + e] = exp2f(z1 - ref);
+                l[nh][e] = fmaf(l[nh][e], corr, pr[e] + pr[2 + e]);
+                m[nh][e] = mn;
 #pragma unroll
-            for (int nh = 0; nh < NH; ++nh) {
-                const bool b0 = t0 + g < n_band, b1 = t0 + g + 8 < n_band;
-                float pr[4];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float z0 = has0 ? fmaf(sc[nh][e], s.scale_log2, b0 ? offb[nh][e] : offs[nh][e]) : -INFINITY;
-                    const float z1 = has1 ? fmaf(sc[nh][2 + e], s.scale_log2, b1 ? offb[nh][e] : offs[nh][e]) : -INFINITY;
-                    float mx = fmaxf(z0, z1);
-                    mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
-                    mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
-                    mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
-                    const float mn = fmaxf(m[nh][e], mx), ref = mn == -INFINITY ? 0.f : mn;
-                    const float corr = exp2f(m[nh][e] - ref);
-                    pr[e] = exp2f(z0 - ref);
-                    pr[2 + e] = exp2f(z1 - ref);
-                    l[nh][e] = fmaf(l[nh][e], corr, pr[e] + pr[2 + e]);
-                    m[nh][e] = mn;
-#pragma unroll
-                    for (int j = 0; j < D / 16; ++j) {
-                        o[nh][j][e] *= corr;
-                        o[nh][j][2 + e] *= corr;
-                    }
+                for (int j = 0; j < D / 16; ++j) {
+                    o[nh][j][e] *= corr;
+                    o[nh][j][2 + e] *= corr;
                 }
-                p[nh][0] = transpose8(pack_bf16x2(pr[0], pr[1]));
-                p[nh][1] = transpose8(pack_bf16x2(pr[2], pr[3]));
             }
-            accumulate<D, KV, NH>(f, p, o);
+            p[nh][0] = transpose8(pack_bf16x2(pr[0], pr[1]));
+            p[nh][1] = transpose8(pack_bf16x2(pr[2], pr[3]));
         }
+        accumulate<D, KV, NH>(f, p, o);
     }
 
     // ---- the warps' partial states to shared memory
@@ -298,9 +376,9 @@ __global__ void __launch_bounds__(WARPS * 32, NH == 1 ? 2 : 1) decode_paged_kern
             sum += __shfl_xor_sync(kFull, sum, 4);
             sum += __shfl_xor_sync(kFull, sum, 8);
             sum += __shfl_xor_sync(kFull, sum, 16);
-            const int hh = 8 * nh + 2 * t + e;
-            if (hh < G) {
-                float *ps = part + (warp * G + hh) * PART;
+            const int x = 8 * nh + 2 * t + e;
+            if (x < cols) {
+                float *ps = part + (warp * cols + x) * PART;
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j)
                     *reinterpret_cast<float2 *>(ps + elem<D, KV>(j, g)) = make_float2(o[nh][j][e], o[nh][j][2 + e]);
@@ -309,128 +387,196 @@ __global__ void __launch_bounds__(WARPS * 32, NH == 1 ? 2 : 1) decode_paged_kern
         }
     __syncthreads();
 
-    // merge of `cnt` states `stride` floats apart: columns col, col + 1 of a head
-    auto finish = [&](int hh, int col, float mt, float lt, float x, float y) {
+    // merge of `n` states, state x at address at(x), for columns col, col + 1 of the head
+    auto finish = [&](int x, int col, float mt, float lt, float x0, float x1) {
         const float inv = lt > 0.f ? 1.f / lt : 0.f;
-        const long long at = (long long)b * s.H + h0 + hh;
-        *reinterpret_cast<uint32_t *>(a.out + at * D + col) = pack_bf16x2(x * inv, y * inv);
+        const long long at = row_of(x);
+        *reinterpret_cast<uint32_t *>(a.out + at * D + col) = pack_bf16x2(x0 * inv, x1 * inv);
         if (col == 0) a.lse[at] = lt > 0.f ? (mt + log2f(lt)) * kLn2 : -INFINITY;
     };
-    const int pairs = G * (D / 2);
-    for (int w = threadIdx.x; w < pairs; w += WARPS * 32) {
-        const int hh = w / (D / 2), col = 2 * (w % (D / 2));
-        float2 ml[WARPS], ov[WARPS];
+    const int pairs = cols * (D / 2);
+    for (int w = threadIdx.x; w < pairs; w += blockDim.x) {
+        const int x = w / (D / 2), col = 2 * (w % (D / 2));
+        float2 ml[MAX_W], ov[MAX_W];
 #pragma unroll
-        for (int x = 0; x < WARPS; ++x) {
-            const float *ps = part + (x * G + hh) * PART;
-            ml[x] = *reinterpret_cast<const float2 *>(ps + D);
-            ov[x] = *reinterpret_cast<const float2 *>(ps + col);
-        }
+        for (int y = 0; y < MAX_W; ++y)
+            if (y < warps) {
+                const float *ps = part + (y * cols + x) * PART;
+                ml[y] = *reinterpret_cast<const float2 *>(ps + D);
+                ov[y] = *reinterpret_cast<const float2 *>(ps + col);
+            }
         float mt = -INFINITY;
 #pragma unroll
-        for (int x = 0; x < WARPS; ++x) mt = fmaxf(mt, ml[x].x);
+        for (int y = 0; y < MAX_W; ++y)
+            if (y < warps) mt = fmaxf(mt, ml[y].x);
         float lt = 0.f, x0 = 0.f, x1 = 0.f;
         const float ref = mt == -INFINITY ? 0.f : mt;
 #pragma unroll
-        for (int x = 0; x < WARPS; ++x) {
-            const float e = exp2f(ml[x].x - ref);
-            lt = fmaf(e, ml[x].y, lt);
-            x0 = fmaf(e, ov[x].x, x0);
-            x1 = fmaf(e, ov[x].y, x1);
-        }
+        for (int y = 0; y < MAX_W; ++y)
+            if (y < warps) {
+                const float e = exp2f(ml[y].x - ref);
+                lt = fmaf(e, ml[y].y, lt);
+                x0 = fmaf(e, ov[y].x, x0);
+                x1 = fmaf(e, ov[y].y, x1);
+            }
         if (P == 1) {
-            finish(hh, col, mt, lt, x0, x1);
+            finish(x, col, mt, lt, x0, x1);
         } else {  // the CTA's state, behind the warps'
-            float *ps = part + (WARPS * G + hh) * PART;
+            float *ps = part + (warps * cols + x) * PART;
             *reinterpret_cast<float2 *>(ps + col) = make_float2(x0, x1);
             if (col == 0) *reinterpret_cast<float2 *>(ps + D) = make_float2(mt, lt);
         }
     }
     if (P == 1) return;
     cluster_sync();
-    const uint32_t base = smem_addr(part + WARPS * G * PART);
-    for (int w = rank * WARPS * 32 + threadIdx.x; w < pairs; w += P * WARPS * 32) {
-        const int hh = w / (D / 2), col = 2 * (w % (D / 2));
+    const uint32_t base = smem_addr(part + warps * cols * PART);
+    for (int w = rank * blockDim.x + threadIdx.x; w < pairs; w += P * blockDim.x) {
+        const int x = w / (D / 2), col = 2 * (w % (D / 2));
         float2 ml[MAX_P], ov[MAX_P];
 #pragma unroll
-        for (int x = 0; x < MAX_P; ++x)
-            if (x < P) {
-                const uint32_t at = peer_addr(base + (uint32_t)(hh * PART) * 4u, x);
-                ml[x] = ld_peer2(at + D * 4);
-                ov[x] = ld_peer2(at + col * 4);
+        for (int y = 0; y < MAX_P; ++y)
+            if (y < P) {
+                const uint32_t at = peer_addr(base + (uint32_t)(x * PART) * 4u, y);
+                ml[y] = ld_peer2(at + D * 4);
+                ov[y] = ld_peer2(at + col * 4);
             }
         float mt = -INFINITY;
 #pragma unroll
-        for (int x = 0; x < MAX_P; ++x)
-            if (x < P) mt = fmaxf(mt, ml[x].x);
+        for (int y = 0; y < MAX_P; ++y)
+            if (y < P) mt = fmaxf(mt, ml[y].x);
         float lt = 0.f, x0 = 0.f, x1 = 0.f;
         const float ref = mt == -INFINITY ? 0.f : mt;
 #pragma unroll
-        for (int x = 0; x < MAX_P; ++x)
-            if (x < P) {
-                const float e = exp2f(ml[x].x - ref);
-                lt = fmaf(e, ml[x].y, lt);
-                x0 = fmaf(e, ov[x].x, x0);
-                x1 = fmaf(e, ov[x].y, x1);
+        for (int y = 0; y < MAX_P; ++y)
+            if (y < P) {
+                const float e = exp2f(ml[y].x - ref);
+                lt = fmaf(e, ml[y].y, lt);
+                x0 = fmaf(e, ov[y].x, x0);
+                x1 = fmaf(e, ov[y].y, x1);
             }
-        finish(hh, col, mt, lt, x0, x1);
+        finish(x, col, mt, lt, x0, x1);
     }
     cluster_sync();  // every CTA's shared memory stays until the others have read it
 }
 
-template <int D, int KV, int NH>
-static cudaError_t launch(const Args &a, int P, cudaStream_t st) {
-    constexpr int WARPS = 8;
-    const int G = a.a.s.H / a.a.s.Hkv;
-    const int smem = (WARPS + 1) * G * (D + 4) * 4;
-    auto *kernel = decode_paged_kernel<D, KV, NH, WARPS>;
+// Warps per CTA and CTAs per cluster for `pairs` (token group, KV head) pairs of up to `tiles` key tiles each.  A warp takes
+// its tiles one after the other, each a round trip to memory; the CTAs that the SMs do not hold at once start another.
+// Measured: 64 sequences x 4 KV heads, 17 tiles, bf16, d = 128: 6 warps 10.3 us, 4 warps 12.6, 3 warps in clusters of two 11.8;
+// 32 x 12 pairs of 9 int8 tiles, d = 64: 5 warps 5.5, 4 warps 6.4, 6 warps (two waves) 8.2; one sequence x 4 heads, 17 e4m3
+// tiles: clusters of 6 x 3 warps 5.0, 5 x 4 5.2, 3 x 6 5.3, one CTA of 6 warps 7.2.
+struct Split {
+    int warps, ctas;
+};
+static Split split(int sm_w, int max_w, long long tiles, long long pairs) {
+    Split best{max_w, 1};
+    long long least = -1;
+    for (int ctas = 1; ctas <= MAX_P; ++ctas)
+        for (int w = 2; w <= max_w; ++w) {
+            const long long waves = (pairs * ctas - 1) / ((long long)(sm_w / w) * sm_count()) + 1, rounds = (tiles - 1) / (w * ctas) + 1;
+            // half a round for meeting across a cluster; then as few warps in all as do, then small CTAs
+            const long long cost = (2 * waves * (rounds + 2) + (ctas > 1 ? 1 : 0)) * 128 + w * ctas;
+            if (least < 0 || cost <= least) {
+                least = cost;
+                best = Split{w, ctas};
+            }
+        }
+    return best;
+}
+
+template <int D, int KV, int NH, bool TOKENS>
+static cudaError_t launch(const Args &a, int groups, long long keys, cudaStream_t st) {
+    const int cols = a.group * (a.s.H / a.s.Hkv);
+    const Split sp = split(sm_warps(D, KV, NH), max_warps(D, KV, NH), (keys + KEYS - 1) / KEYS, (long long)groups * a.s.Hkv);
+    auto *kernel = paged_rows_kernel<D, KV, NH, TOKENS>;
     static PerDeviceOnce configured;  // shared memory above the 48 KB default
     int dev = 0;
     cudaGetDevice(&dev);
     if (configured.needed(dev)) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (WARPS + 1) * 8 * NH * (D + 4) * 4);
+                                                   (max_warps(D, KV, NH) + 1) * 8 * NH * (D + 4) * 4);
         if (e != cudaSuccess) return e;
         configured.mark(dev);
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)P, (unsigned)a.a.s.Hkv, (unsigned)a.a.s.B);
-    cfg.blockDim = dim3(WARPS * 32, 1, 1);
-    cfg.dynamicSmemBytes = smem;
+    cfg.gridDim = dim3((unsigned)sp.ctas, (unsigned)a.s.Hkv, (unsigned)groups);
+    cfg.blockDim = dim3((unsigned)sp.warps * 32, 1, 1);
+    cfg.dynamicSmemBytes = (size_t)((sp.warps + 1) * cols * (D + 4) * 4);
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)P;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)sp.ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = P > 1 ? 1 : 0;
+    cfg.numAttrs = sp.ctas > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-template <int D, int KV>
-static cudaError_t launch_heads(const Args &a, int P, cudaStream_t st) {
-    return a.a.s.H / a.a.s.Hkv <= 8 ? launch<D, KV, 1>(a, P, st) : launch<D, KV, 2>(a, P, st);
+template <int D, int KV, bool TOKENS>
+static cudaError_t launch_shape(const Args &a, int groups, long long keys, cudaStream_t st) {
+    return a.group * (a.s.H / a.s.Hkv) <= 8 ? launch<D, KV, 1, TOKENS>(a, groups, keys, st) : launch<D, KV, 2, TOKENS>(a, groups, keys, st);
+}
+
+template <bool TOKENS>
+static cudaError_t launch_types(const Args &a, int groups, long long keys, cudaStream_t st) {
+    const bool d64 = a.s.d == 64;
+    switch (a.cache.kv_type) {
+        case kKvBf16: return d64 ? launch_shape<64, kKvBf16, TOKENS>(a, groups, keys, st) : launch_shape<128, kKvBf16, TOKENS>(a, groups, keys, st);
+        case kKvE4m3: return d64 ? launch_shape<64, kKvE4m3, TOKENS>(a, groups, keys, st) : launch_shape<128, kKvE4m3, TOKENS>(a, groups, keys, st);
+        default: return d64 ? launch_shape<64, kKvInt8, TOKENS>(a, groups, keys, st) : launch_shape<128, kKvInt8, TOKENS>(a, groups, keys, st);
+    }
+}
+
+// Keys of the longest list of `tokens` consecutive queries.
+static long long most_keys(const Shape &s, const PagedCache &c, int tokens) {
+    const long long cap = (long long)c.width << c.page_log2;
+    const long long band = s.mode == kModeEcp ? 2LL * s.k_local : (long long)s.k_local + 1;
+    return std::min(cap, band + tokens - 1) + (s.mode == kModeEcp ? 0 : std::min<long long>(s.S, cap) * tokens);
 }
 
 }  // namespace decp
 
-cudaError_t launch_decode_paged(const DecodePagedArgs &a, cudaStream_t st) {
+cudaError_t launch_decode_paged(const DecodePagedArgs &d, cudaStream_t st) {
     using namespace decp;
-    const Shape &s = a.s;
-    Args args{a, s.mode != kModeEcp && s.S > 0 ? first_skip_multiple(s) : 1};
-    // tiles of the longest key list, and CTAs per (sequence, KV head): one tile per warp while the
-    // grid stays within about two CTAs per SM
-    const long long cap = (long long)a.cache.width << a.cache.page_log2;
-    const long long keys = std::min<long long>(cap, s.mode == kModeEcp ? 2LL * s.k_local : (long long)s.k_local + 1 + s.S);
-    const long long tiles = (keys + KEYS - 1) / KEYS, pairs = (long long)s.B * s.Hkv;
-    const int P = (int)std::max<long long>(1, std::min<long long>({(long long)MAX_P, (tiles + 7) / 8, 2LL * sm_count() / pairs}));
-    const bool d64 = s.d == 64;
-    switch (a.cache.kv_type) {
-        case kKvBf16: return d64 ? launch_heads<64, kKvBf16>(args, P, st) : launch_heads<128, kKvBf16>(args, P, st);
-        case kKvE4m3: return d64 ? launch_heads<64, kKvE4m3>(args, P, st) : launch_heads<128, kKvE4m3>(args, P, st);
-        default: return d64 ? launch_heads<64, kKvInt8>(args, P, st) : launch_heads<128, kKvInt8>(args, P, st);
-    }
+    const Shape &s = d.s;
+    Args a{d.q, d.q_stride, d.alpha, d.lens, PagedBatch{d.table, nullptr, nullptr, s.B, s.B}, d.out, d.lse, s, d.cache, d.index_word,
+           s.mode != kModeEcp && s.S > 0 ? first_skip_multiple(s) : 1, 1};
+    return launch_types<false>(a, s.B, most_keys(s, d.cache, 1), st);
+}
+
+// Tokens per CTA: as many as 8 columns hold (16 took a batch of five drafted tokens, 4 heads per KV head, 15.0 us, 8 10.4).
+static int token_group(int G) { return std::max(1, 8 / G); }
+
+// Whether a call's chunks are so short that this kernel beats the tensor-core pipeline (pi_extend_tc.cu), whose blocks of 128
+// rows take about the same time however few of them hold queries.  Judged by the sizes that the host knows, as if all
+// sequences had the same length: the grid fits the SMs at once, or has at most 1.5 times as many CTAs as there would be
+// blocks (four times over an 8-bit cache, whose tiles the pipeline has to convert first).  Measured in us (this kernel /
+// pipeline), band 256, 4 skips, contexts of 8000:
+//   16 heads on 4, d = 128, bf16:  4 sequences x 32 tokens 11.2 / 13.5, x 64 15.7 / 13.7; 32 x 4 16.2 / 16.1, x 8 24.2 / 15.4;
+//                                  128 x 2 28.0 / 31.4, x 4 45.0 / 31.2;
+//                           e4m3:  32 x 8 20.3 / 29.0, x 16 35.0 / 28.3; 128 x 8 65 / 74, x 16 113 / 74
+//   12 on 12, d = 64, bf16: 32 x 16 20.2 / 21.6, x 32 34.7 / 20.6; 128 x 8 39.4 / 55.3, x 16 58.4 / 53.8
+bool extend_few_rows(const ExtendArgs &e) {
+    const Shape &s = e.s;
+    const int G = s.H / s.Hkv, group = token_group(G);
+    const long long T = e.batch.T, B = std::min<long long>(e.batch.B, T);
+    if (G > 16 || s.Hkv > 65535 || (T + e.batch.B * (long long)(group - 1)) / group > 65535) return false;
+    if (decp::most_keys(s, e.cache, group) >= (1LL << 30)) return false;
+    const long long n = (T + B - 1) / B, ctas = B * ((n + group - 1) / group) * s.Hkv;
+    const int heads = packed_heads(G), rows = 128 / heads;
+    const long long blocks = B * ((n + rows - 1) / rows) * (s.H / heads);
+    return ctas <= 2LL * sm_count() || 2 * ctas <= (e.cache.kv_type == kKvBf16 ? 3 : 8) * blocks;
+}
+
+cudaError_t launch_extend_few(const ExtendArgs &e, cudaStream_t st) {
+    using namespace decp;
+    const Shape &s = e.s;
+    const int group = token_group(s.H / s.Hkv);
+    Args a{e.q, e.q_stride, e.alpha, nullptr, e.batch, e.out, e.lse, s, e.cache, e.index_word,
+           s.mode != kModeEcp && s.S > 0 ? first_skip_multiple(s) : 1, group};
+    return launch_types<true>(a, (int)((e.batch.T + e.batch.B * (long long)(group - 1)) / group), most_keys(s, e.cache, group), st);
 }
 
 }  // namespace pi

@@ -990,8 +990,6 @@ static bool encode(CUtensorMap *m, const void *ptr, int d, long long n1, long lo
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-static int packed_heads(int G) { return G % 4 == 0 ? 4 : G % 2 == 0 ? 2 : 1; }
-
 // The workspace: the plan; for an 8-bit cache the slots' list and the converted tiles.
 struct Layout {
     size_t slots, k, v, bytes;  // offsets
@@ -1059,6 +1057,7 @@ size_t extend_workspace_bytes(const Shape &s, int kv_type, long long B, long lon
 
 cudaError_t launch_extend(const ExtendArgs &e, cudaStream_t st) {
     using namespace ext;
+    if (extend_few_rows(e)) return launch_extend_few(e, st);
     const Shape &s = e.s;
     const PagedCache &c = e.cache;
     const int G = s.H / s.Hkv, GP = packed_heads(G), R = BM / GP, ngrp = s.H / GP;

@@ -55,16 +55,17 @@ __device__ __forceinline__ int scale_exp(float amax) {
     return max(e, kMinScaleExp);  // subnormal amax: far below the floor of the scales
 }
 
-// Sequence of packed token t: the number of j in [1, B] with cu[j] <= t (B: t is behind the last
-// sequence).  Searched by the whole warp, 32 probes at a time; ends for any contents of cu.
-__device__ __forceinline__ int find_sequence(const int *cu, int B, int t) {
+// The number of j in [1, B] with below(j), which holds up to some j and for none after: with below(j) = (cu[j] <= t)
+// the sequence of packed token t (B: t is behind the last one).  Searched by the whole warp, 32 probes at a time; ends, with
+// every probe in [1, B], whatever below() answers.
+template <typename F>
+__device__ __forceinline__ int find_sequence(int B, F below) {
     const int lane = threadIdx.x & 31;
     int lo = 0, len = B;
     while (len > 0) {
         const int step = (len + 31) >> 5;
         const int k = (lane + 1) * step;
-        const bool below = k <= len && __ldg(cu + lo + k) <= t;
-        const int c = __popc(__ballot_sync(0xffffffffu, below));
+        const int c = __popc(__ballot_sync(0xffffffffu, k <= len && below(lo + k)));
         lo += c * step;
         len = min(step - 1, len - c * step);
     }
@@ -80,7 +81,7 @@ __device__ __forceinline__ bool sequence_ok(const PagedCache &c, const PagedBatc
 // Position of packed token t in its sequence b, or -1 (t behind the last sequence, or an index out of
 // range, which is recorded).  For the whole warp.
 __device__ __forceinline__ int locate(const PagedCache &c, const PagedBatch &bt, int t, int &b, int *index_word) {
-    b = find_sequence(bt.cu, bt.B, t);
+    b = find_sequence(bt.B, [&](int j) { return __ldg(bt.cu + j) <= t; });
     if (b >= bt.B) return -1;
     const int t0 = __ldg(bt.cu + b), t1 = __ldg(bt.cu + b + 1), ctx = __ldg(bt.ctx + b);
     if (!sequence_ok(c, bt, t0, t1, ctx) || t < t0 || t >= t1) {

@@ -76,6 +76,9 @@ struct DecodePagedArgs {
     int *index_word;
 };
 
+// Query heads of a KV group in one 128-row block of the chunk attention: the largest of 4, 2, 1 that divides the group.
+inline int packed_heads(int G) { return G % 4 == 0 ? 4 : G % 2 == 0 ? 2 : 1; }
+
 // rows into and out of a paged cache (pi_cache.cu)
 cudaError_t launch_append(const AppendArgs &a, cudaStream_t st);
 cudaError_t launch_cache_read(const ReadArgs &a, cudaStream_t st);
@@ -84,6 +87,9 @@ cudaError_t launch_cache_read(const ReadArgs &a, cudaStream_t st);
 // sequence (pi_decode_paged.cu)
 size_t extend_workspace_bytes(const Shape &s, int kv_type, long long B, long long T, long long cap);
 cudaError_t launch_extend(const ExtendArgs &a, cudaStream_t st);
+// the same for few tokens per sequence (pi_decode_paged.cu), and whether a call is one of those
+cudaError_t launch_extend_few(const ExtendArgs &a, cudaStream_t st);
+bool extend_few_rows(const ExtendArgs &a);
 cudaError_t launch_decode_paged(const DecodePagedArgs &a, cudaStream_t st);
 
 // Device words of the current device, looked up once per device (api.cu): the status word of the

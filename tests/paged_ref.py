@@ -21,7 +21,7 @@ def encode(x, kv):
     The scale is searched upwards from the smallest one, and an e4m3 code among all its neighbours:
     nothing here follows the kernel's bit arithmetic."""
     x = np.asarray(x, dtype=np.float64)
-    b = x.reshape(*x.shape[:-1], -1, 32)
+    b = x.reshape(*x.shape[:-1], x.shape[-1] // 32, 32)
     finite = np.isfinite(b).all(-1)
     b = np.where(finite[..., None], b, 0.0)
     amax = np.abs(b).max(-1)
@@ -47,7 +47,7 @@ def decode(codes, scales, kv):
     """Values of codes [..., d] (uint8 bits) with scale bytes [..., d / 32], float64; infinity from 2^128 on, which
     a code that was rounded up can stand for (255 * 2^120, bf16's largest number, is 256 * 2^120 in e4m3 and
     64 * 2^122 in int8) and neither bf16 nor fp32 holds."""
-    c = codes.reshape(*codes.shape[:-1], -1, 32)
+    c = codes.reshape(*codes.shape[:-1], codes.shape[-1] // 32, 32)
     if kv == "int8":
         v = c.view(np.int8).astype(np.float64)
     else:

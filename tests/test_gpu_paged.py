@@ -203,6 +203,49 @@ EXTEND = [
 ]
 
 
+# The same call has two kernels, for chunks of few tokens and for long ones; the cases above are small enough for the
+# first, these long enough for the second.
+EXTEND_LONG = [
+    ("aligned", "bf16", 8, 2, 128, 64, [256], [512], 128, 128, 3, PI),
+    ("one-block-and-one-token", "bf16", 16, 4, 128, 64, [0, 7], [320, 1], 100, 96, 2, PI),
+    ("odd-all", "bf16", 16, 4, 64, 16, [37, 0, 5], [233, 171, 1], 45, 67, 3, PI),
+    ("mha", "bf16", 6, 6, 64, 32, [129, 3], [400, 340], 64, 96, 2, PI),
+    ("gqa2", "bf16", 8, 4, 128, 128, [70, 900], [361, 63], 33, 50, 4, PI),
+    ("gqa3", "bf16", 12, 4, 64, 64, [11, 90, 31], [264, 140, 2], 50, 64, 2, PI),
+    ("gqa7", "bf16", 14, 2, 128, 16, [40, 8], [230, 130], 31, 37, 5, PI),
+    ("gqa16", "bf16", 32, 2, 64, 16, [100], [200], 64, 100, 3, PI),
+    ("gqa20", "bf16", 20, 1, 64, 32, [5, 3], [40, 9], 20, 30, 3, PI),
+    ("empty-sequences", "bf16", 16, 4, 64, 16, [0, 10, 0, 99, 3], [0, 220, 0, 164, 0], 20, 32, 2, PI),
+    ("no-skips", "bf16", 8, 8, 64, 256, [300], [500], 70, 1, 0, PI),
+    ("band-of-one", "bf16", 8, 4, 128, 32, [50], [390], 0, 7, 6, PI),
+    ("skips-in-band", "bf16", 8, 4, 64, 32, [100], [370], 40, 16, 6, PI),
+    ("many-skips", "bf16", 8, 4, 64, 64, [900], [340], 5, 9, 90, PI),
+    ("band-over-everything", "bf16", 16, 4, 128, 64, [200], [350], 100000, 64, 2, PI),
+    ("period-over-everything", "bf16", 8, 4, 64, 16, [60], [360], 10, 100000, 4, PI),
+    ("ecp", "bf16", 8, 8, 64, 32, [100, 0], [250, 265], 64, 0, 0, ECP),
+    ("ecp-odd", "bf16", 8, 4, 128, 16, [61], [377], 27, 0, 0, ECP),
+    ("ecp-long", "bf16", 8, 4, 64, 64, [1000], [400], 700, 0, 0, ECP),
+    ("e4m3", "e4m3", 16, 4, 128, 64, [333, 5], [430, 31], 128, 96, 3, PI),
+    ("e4m3-d64-page16", "e4m3", 12, 4, 64, 16, [90, 17], [240, 170], 50, 70, 3, PI),
+    ("e4m3-far-skips", "e4m3", 16, 4, 64, 16, [3000, 100], [130, 40], 40, 900, 3, PI),
+    ("int8", "int8", 16, 4, 128, 32, [200, 64], [264, 100], 100, 128, 2, PI),
+    ("int8-ecp-d64", "int8", 8, 8, 64, 128, [300], [500], 96, 0, 0, ECP),
+    ("int8-empty", "int8", 16, 4, 128, 256, [0, 500, 3], [0, 300, 1], 64, 50, 3, PI),
+    ("long", "e4m3", 16, 4, 128, 64, [2500], [700], 256, 1024, 4, PI),
+    ("long-bf16", "bf16", 16, 4, 128, 64, [2500], [700], 256, 1024, 4, PI),
+]
+
+
+def few_rows(case, sms=152):
+    """The rule that picks the kernel (extend_few_rows), for the cases above."""
+    _, kv, H, Hkv, d, page, ctx, n, kl, per, S, mode = case
+    T, B = sum(n) + 2, len(n)
+    G, B = H // Hkv, min(B, T)
+    group, heads, per_seq = max(1, 8 // G), 4 if G % 4 == 0 else 2 if G % 2 == 0 else 1, -(-T // B)
+    ctas, blocks = B * -(-per_seq // group) * Hkv, B * -(-per_seq // (128 // heads)) * (H // heads)
+    return G <= 16 and (ctas <= 2 * sms or 2 * ctas <= (3 if kv == "bf16" else 8) * blocks)
+
+
 def run_attention(case, decode=False, seed=0):
     name, kv, H, Hkv, d, page, ctx, n, kl, per, S, mode = case
     bt = Batch(ctx, n, Hkv, d, page, kv, seed=seed + len(name) + d, extra_tokens=0 if decode else 2)
@@ -248,6 +291,12 @@ def test_extend_matches_the_oracle(case):
     run_attention(case)
 
 
+@pytest.mark.parametrize("case", EXTEND_LONG, ids=[c[0] for c in EXTEND_LONG])
+def test_extend_of_long_chunks_matches_the_oracle(case):
+    assert not few_rows(case)
+    run_attention(case)
+
+
 DECODE = [
     ("first-token", "bf16", 4, 2, 64, 16, [0, 0], [1, 1], 8, 4, 2, PI),
     ("short", "bf16", 4, 4, 64, 32, [19, 3, 15], [1] * 3, 40, 16, 2, PI),
@@ -288,6 +337,35 @@ def test_decode_without_rows():
 
 # ------------------------------------------------------------------ indexes out of range
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_bad_indexes_of_long_chunks(kv):
+    """The same for the kernels of long chunks: a bad sequence is left out, a bad page reported, decreasing offsets end
+    the call's work."""
+    n, H, Hkv = 250, 16, 4
+    bt = Batch([20] * 3, [n] * 3, Hkv, 64, 16, kv, seed=6)
+    bt.write()
+    q, a = normal(bt.gen, bt.T, H, 64).cuda(), torch.full((bt.T, H), 0.5, device="cuda")
+    args = (a, 16, 8, 2)
+    good, good_lse = pa.extend(q, bt.cache, dev(bt.table), dev(bt.cu), dev(bt.ctx), *args)
+    torch.cuda.synchronize()
+    assert pa.status() == 0
+    ok = [0, n, 2 * n, 3 * n]
+    for cu, ctx, kept in ((ok[:3] + [3 * n + 1], [20] * 3, 2 * n), (ok[:3] + [2 ** 31 - 1], [20] * 3, 2 * n),
+                          (ok, [20, 20, -1], 2 * n), (ok, [20, 20, 2 ** 31 - 1], 2 * n),
+                          (ok, [20, 20, 16 * bt.table.shape[1] - n + 1], 2 * n), ([0, n, n - 1, 3 * n], [20] * 3, 0)):
+        out, lse = torch.full_like(good, 9.0), torch.full_like(good_lse, 9.0)
+        pa.extend(q, bt.cache, dev(bt.table), dev(cu), dev(ctx), *args, out=out, lse=lse)
+        assert pa.status() == ERR_INDEX and pa.status() == 0
+        assert torch.equal(out[:kept], good[:kept]) and torch.equal(lse[:kept], good_lse[:kept])
+        assert (out[kept:] == 9.0).all() and (lse[kept:] == 9.0).all()
+    for bad in (2 ** 31 - 1, -1):
+        table = bt.table.copy()
+        table[2, 3] = bad
+        out, lse = pa.extend(q, bt.cache, dev(table), dev(ok), dev(bt.ctx), *args)
+        assert pa.status() == ERR_INDEX and pa.status() == 0
+        assert torch.equal(out[:2 * n], good[:2 * n]) and torch.equal(lse[:2 * n], good_lse[:2 * n])
+
+
 def test_bad_indexes_are_reported_and_left_out():
     """Offsets, contexts, lengths and pages out of range: reported once by status(), the rest of the batch
     served, nothing written for the sequences concerned."""
@@ -295,6 +373,8 @@ def test_bad_indexes_are_reported_and_left_out():
     bt.write()
     q, a = normal(bt.gen, 30, 4, 64).cuda(), torch.full((30, 4), 0.5, device="cuda")
     args = (a, 16, 8, 2)
+    pa.extend(q, bt.cache, dev(bt.table), dev([0, 10, 9, 30]), dev(bt.ctx), *args)  # decreasing offsets
+    assert pa.status() == ERR_INDEX and pa.status() == 0
     good, good_lse = pa.extend(q, bt.cache, dev(bt.table), dev(bt.cu), dev(bt.ctx), *args)
     rows = torch.zeros(30, 2, 64, dtype=torch.bfloat16, device="cuda")
     ok = [0, 10, 20, 30]
@@ -368,16 +448,16 @@ def test_serving_run(kv, H, Hkv, d, page, kl, per, S, mode):
         ref.check_attention(f"sequence {b}", torch.cat(s["out"]), torch.cat(s["lse"]), want)
 
 
-def test_captured_step_follows_its_inputs():
+@pytest.mark.parametrize("T,sizes", [(50, ([30, 20], [0, 45], [7, 1])), (800, ([500, 300], [0, 777], [700, 3]))])
+def test_captured_step_follows_its_inputs(T, sizes):
     """Append, extend and decode captured into one graph on a stream of their own and replayed with other offsets,
     contexts and values in the same tensors, an empty sequence and padding tokens among them."""
     H, Hkv, d, page, kl, per, S = 8, 2, 64, 16, 40, 50, 2
-    bt = Batch([100, 60], [30, 20], Hkv, d, page, "e4m3", seed=11)
+    bt = Batch([100, 60], [T, T], Hkv, d, page, "e4m3", seed=11)  # pages for every step's rows
     bt.write()
-    T = 50
     k, v, q = (normal(bt.gen, T, h, d).cuda() for h in (Hkv, Hkv, H))
     a = torch.rand(T, H, generator=bt.gen).cuda()
-    table, cu, ctx, lens = dev(bt.table), dev([0, 30, 50]), dev([100, 60]), dev([130, 80])
+    table, cu, ctx, lens = dev(bt.table), dev(ref.offsets(sizes[0])), dev([100, 60]), dev([130, 80])
     out, lse = torch.zeros(T, H, d, dtype=torch.bfloat16, device="cuda"), torch.zeros(T, H, device="cuda")
     dout, dlse = torch.zeros(2, H, d, dtype=torch.bfloat16, device="cuda"), torch.zeros(2, H, device="cuda")
 
@@ -392,12 +472,12 @@ def test_captured_step_follows_its_inputs():
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph, stream=side):
             step()
-    for n, c in (([30, 20], [100, 60]), ([0, 45], [100, 10]), ([7, 1], [64, 79])):
+    for n, c in zip(sizes, ([100, 60], [100, 10], [64, 79])):
         for t in (k, v, q):
             t.copy_(normal(bt.gen, *t.shape))
         cu.copy_(dev(ref.offsets(n)))
         ctx.copy_(dev(c))
-        lens.copy_(dev(np.add(c, n)))
+        lens.copy_(dev(np.minimum(np.add(c, n), 130)))
         results = []
         for run in (step, graph.replay):
             for t in (out, lse, dout, dlse):
@@ -413,7 +493,7 @@ def test_captured_step_follows_its_inputs():
 
 def test_streams_run_side_by_side():
     """Two streams with their own tensors and a common cache give what one stream gives."""
-    bt = Batch([300, 200], [64, 40], 2, 128, 64, "bf16", seed=13)
+    bt = Batch([300, 200], [364, 240], 2, 128, 64, "e4m3", seed=13)
     bt.write()
     q, a = normal(bt.gen, bt.T, 8, 128).cuda(), torch.rand(bt.T, 8, generator=bt.gen).cuda()
     table, cu, ctx = dev(bt.table), dev(bt.cu), dev(bt.ctx)

@@ -168,6 +168,23 @@ def test_converted_tiles_hold_every_attended_key_within_the_bound(lib):
         assert used * (8 + 2 * 32 * 64 * 2) <= room
 
 
+@pytest.mark.parametrize("group", [1, 2, 3, 4, 8])
+def test_token_groups_have_their_places(group):
+    """The short chunks' kernel: every group of tokens of every sequence gets a CTA number of its own below the grid's size."""
+    rng = np.random.default_rng(group)
+    for B in (1, 2, 7, 40):
+        n = rng.integers(0, 12, B)
+        cu = np.concatenate([[0], np.cumsum(n)])
+        T = int(cu[-1]) + int(rng.integers(0, 5))
+        start = lambda j: (cu[j] + j * (group - 1)) // group  # noqa: E731
+        seen = []
+        for i in range((T + B * (group - 1)) // group):
+            b = sum(start(j) <= i for j in range(1, B + 1))
+            if b < B and 0 <= (i - start(b)) * group < n[b]:
+                seen.append((b, (i - start(b)) * group))
+        assert seen == [(b, x) for b in range(B) for x in range(0, n[b], group)]
+
+
 def plan(n, ctx, R):
     """The plan kernel's blocks of one sequence: (p0, first, last)."""
     p = ctx if n <= R else ctx // R * R
