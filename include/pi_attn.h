@@ -356,13 +356,13 @@ int pi_attn_cache_read(const pi_attn_cache_t *cache, const pi_attn_batch_t *batc
  *   a non-finite value in a row that some query attends may reach the outputs of the
  *   sequence's other queries within 128 positions.
  *   workspace: device buffer of at least pi_attn_extend_workspace_size() bytes for these
- *   sizes, 256-byte aligned, owned by the caller, contents ignored on entry; calls that may
+ *   sizes (none for short chunks: it may be NULL then), 256-byte aligned, owned by the caller, contents ignored on entry; calls that may
  *   overlap need one each.  It holds the call's plan (about 2.5 T + 160 B bytes) and, for an
  *   8-bit cache, the attended rows as bf16: 4 d Hkv bytes for each of at most
  *   min(T (1 + S) + B k_local, T + B max(k_local, S period)) rows and a few tiles of 32 per
  *   sequence and skip window.  Deterministic.
  *
- * pi_attn_extend_workspace_size -- those bytes (0 for sizes that pi_attn_extend refuses);
+ * pi_attn_extend_workspace_size -- those bytes (0: none, or sizes that pi_attn_extend refuses);
  * of the cache only its sizes, type and pointers' alignment matter.
  */
 size_t pi_attn_extend_workspace_size(const pi_attn_cache_t *cache, int B, int T, int width, int H,

@@ -109,13 +109,14 @@ int pi_attn_cache_read(const pi_attn_cache_t *cache, const pi_attn_batch_t *batc
 
 size_t pi_attn_extend_workspace_size(const pi_attn_cache_t *cache, int B, int T, int width, int H, int k_local, int period, int S,
                                      int mode) {
-    pi::PagedCache c;
-    pi::Shape s;
     static const float some_alpha = 0.f;
-    if (B <= 0 || T <= 0 || make_cache(cache, width, c) != PI_OK ||
-        make_attention(c, H, k_local, period, S, mode, &some_alpha, s) != PI_OK)
+    pi::ExtendArgs a{};
+    if (B <= 0 || T <= 0 || make_cache(cache, width, a.cache) != PI_OK ||
+        make_attention(a.cache, H, k_local, period, S, mode, &some_alpha, a.s) != PI_OK)
         return 0;
-    return pi::extend_workspace_bytes(s, c.kv_type, B, T, (long long)c.width << c.page_log2);
+    a.batch.B = B;
+    a.batch.T = T;
+    return pi::extend_workspace_bytes(a);
 }
 
 int pi_attn_extend(const void *q, long long q_stride, const pi_attn_cache_t *cache, const pi_attn_batch_t *batch,
@@ -135,9 +136,8 @@ int pi_attn_extend(const void *q, long long q_stride, const pi_attn_cache_t *cac
     a.alpha = mode != PI_MODE_ECP ? alpha : nullptr;
     a.out = static_cast<__nv_bfloat16 *>(out);
     a.lse = lse;
-    if (!workspace || workspace_bytes < pi::extend_workspace_bytes(a.s, a.cache.kv_type, a.batch.B, a.batch.T,
-                                                                  (long long)a.cache.width << a.cache.page_log2))
-        return PI_ERR_WORKSPACE;
+    const size_t need = pi::extend_workspace_bytes(a);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return PI_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return PI_ERR_ALIGN;
     a.workspace = static_cast<int *>(workspace);
     a.timeout_ns = kWaitTimeoutNs;

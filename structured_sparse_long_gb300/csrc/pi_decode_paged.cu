@@ -470,9 +470,10 @@ struct Split {
 static Split split(int sm_w, int max_w, long long tiles, long long pairs) {
     Split best{max_w, 1};
     long long least = -1;
+    const long long sms = sm_count();
     for (int ctas = 1; ctas <= MAX_P; ++ctas)
         for (int w = 2; w <= max_w; ++w) {
-            const long long waves = (pairs * ctas - 1) / ((long long)(sm_w / w) * sm_count()) + 1, rounds = (tiles - 1) / (w * ctas) + 1;
+            const long long waves = (pairs * ctas - 1) / (sm_w / w * sms) + 1, rounds = (tiles - 1) / (w * ctas) + 1;
             // half a round for meeting across a cluster; then as few warps in all as do, then small CTAs
             const long long cost = (2 * waves * (rounds + 2) + (ctas > 1 ? 1 : 0)) * 128 + w * ctas;
             if (least < 0 || cost <= least) {

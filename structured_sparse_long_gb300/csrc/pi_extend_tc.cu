@@ -1051,8 +1051,10 @@ static cudaError_t launch(const Args &a, const void *k, const void *v, cudaStrea
 
 }  // namespace ext
 
-size_t extend_workspace_bytes(const Shape &s, int kv_type, long long B, long long T, long long cap) {
-    return ext::layout(s, kv_type, B, T, cap).bytes;
+size_t extend_workspace_bytes(const ExtendArgs &e) {
+    if (extend_few_rows(e)) return 0;
+    const PagedCache &c = e.cache;
+    return ext::layout(e.s, c.kv_type, e.batch.B, e.batch.T, (long long)c.width << c.page_log2).bytes;
 }
 
 cudaError_t launch_extend(const ExtendArgs &e, cudaStream_t st) {

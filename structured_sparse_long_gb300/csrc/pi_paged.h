@@ -85,7 +85,7 @@ cudaError_t launch_cache_read(const ReadArgs &a, cudaStream_t st);
 
 // attention over a paged cache: a chunk of new tokens per sequence (pi_extend_tc.cu), one new token per
 // sequence (pi_decode_paged.cu)
-size_t extend_workspace_bytes(const Shape &s, int kv_type, long long B, long long T, long long cap);
+size_t extend_workspace_bytes(const ExtendArgs &a);
 cudaError_t launch_extend(const ExtendArgs &a, cudaStream_t st);
 // the same for few tokens per sequence (pi_decode_paged.cu), and whether a call is one of those
 cudaError_t launch_extend_few(const ExtendArgs &a, cudaStream_t st);

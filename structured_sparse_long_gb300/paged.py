@@ -13,11 +13,16 @@ from typing import Optional
 import torch
 
 from . import _binding
-from ._binding import MODE_ECP, MODE_PI, _check
+from ._binding import MODE_ECP, MODE_PI, PI_OK, _check
 
 KV_BF16, KV_E4M3, KV_INT8 = 0, 1, 2
 _KV_TYPES = {torch.bfloat16: KV_BF16, torch.float8_e4m3fn: KV_E4M3, torch.int8: KV_INT8}
 SCALE_BLOCK = 32  # elements per scale byte of an 8-bit cache
+
+
+_INT32, _BF16, _FP32 = torch.int32, torch.bfloat16, torch.float32
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 class _CacheStruct(ctypes.Structure):  # pi_attn_cache_t
@@ -74,7 +79,8 @@ class PagedCache:
         self._struct = _CacheStruct(*(None if t is None else t.data_ptr() for t in self._tensors),
                                     self.kv_type, n_pages, Hkv, page, d)
         self._ref = ctypes.byref(self._struct)
-        self.device = k.device
+        self._workspace = {}  # extend's workspace sizes by the call's sizes
+        self.device, self.index = k.device, k.get_device()
         self.Hkv, self.page, self.d = Hkv, page, d
 
     k = property(lambda self: self._tensors[0])
@@ -94,111 +100,116 @@ class PagedCache:
         return cls(new(dtype, d), new(dtype, d), *((new(torch.uint8, d // SCALE_BLOCK) for _ in range(2)) if quant else ()))
 
 
-class _on:
-    """Makes `device` current for a call (nothing to do where it is already)."""
-
-    __slots__ = ("guard",)
-
-    def __init__(self, device):
-        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _refuse(t, name, want):
+    raise ValueError(f"{name} must be {want}, got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}"
+                     if isinstance(t, torch.Tensor) else f"{name} must be {want}, got {type(t).__name__}")
 
 
-def _index_tensor(t, name, cache, shape):
-    if t.dtype != torch.int32 or t.device != cache.device or not t.is_contiguous() or t.shape != shape:
-        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)} on {cache.device}, got "
-                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+# Checks of a serving step's hot path: one C call's worth of them costs as much as the launch, so they compare device
+# indexes and dtype objects only.
+
+def _int32(t, name, index, *shape):
+    if t.dtype is not _INT32 or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        _refuse(t, name, f"a contiguous int32 tensor of shape {shape} on cuda:{index}")
+    return t.data_ptr()
 
 
-def _packed_rows(t, name, cache, heads=None):
-    """[T, heads, d] bf16 with contiguous tokens any stride apart; returns that stride."""
-    if t.dim() != 3 or t.dtype != torch.bfloat16 or t.device != cache.device or t.shape[2] != cache.d or (
-            heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must be bf16 [T, {heads or 'heads'}, {cache.d}] on {cache.device}, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
-    rows, heads, d = t.shape
+def _dense(t, name, index, dtype, shape):
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        _refuse(t, name, f"a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{index}")
+    return t.data_ptr()
+
+
+def _packed(t, name, cache, heads):
+    """Number of tokens, heads and the stride between the tokens of a packed [T, heads, d] bf16 tensor whose tokens are
+    contiguous."""
+    shape = t.shape
+    if len(shape) != 3 or t.dtype is not _BF16 or shape[2] != cache.d or t.get_device() != cache.index or (
+            heads is not None and shape[1] != heads):
+        _refuse(t, name, f"bf16 [T, {heads or 'heads'}, {cache.d}] on cuda:{cache.index}")
+    T, heads, d = shape
     s0, s1, s2 = t.stride()
     if s2 != 1 or (heads > 1 and s1 != d):
-        raise ValueError(f"{name}: the elements of a token must be contiguous, got strides {t.stride()}")
-    return s0 if rows > 1 else heads * d
+        _refuse(t, name, "a tensor whose tokens have contiguous elements")
+    return T, heads, (s0 if T > 1 else heads * d)
 
 
 def _batch(table, cu, ctx, T, cache):
     if table.dim() != 2:
-        raise ValueError("table must be [B, width]")
+        _refuse(table, "table", "[B, width]")
     B, width = table.shape
-    _index_tensor(table, "table", cache, (B, width))
-    _index_tensor(cu, "cu", cache, (B + 1,))
-    _index_tensor(ctx, "ctx", cache, (B,))
-    return _BatchStruct(table.data_ptr(), cu.data_ptr(), ctx.data_ptr(), B, T, width)
+    index = cache.index
+    return _BatchStruct(_int32(table, "table", index, B, width), _int32(cu, "cu", index, B + 1), _int32(ctx, "ctx", index, B), B, T,
+                        width)
 
 
-def _stream_of(stream, device):
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+_fns = {}  # entry points, once the library is loaded
+
+
+def _call(name, cache, stream, check, *args):
+    """Calls an entry point with `args` and the stream (the current one of the cache's device, if none is given) on that
+    device."""
+    fn = _fns.get(name)
+    if fn is None:
+        fn = _fns[name] = getattr(_load(), name)
+    index = cache.index
+    raw = _raw_stream(index) if stream is None else stream.cuda_stream
+    if index == _current_device():
+        rc = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, raw)
+    if rc != PI_OK or check:
+        with torch.cuda.device(index):
+            _check(name, rc, stream, check)
 
 
 def cache_append(k, v, cache: PagedCache, table, cu, ctx, stream=None, check=False) -> None:
     """pi_attn_cache_append: writes the packed rows k, v [T, Hkv, d] bf16 (tokens any stride apart) into the
     pages of their sequences, quantised where the cache holds 8 bits."""
-    ks = _packed_rows(k, "k", cache, cache.Hkv)
-    vs = _packed_rows(v, "v", cache, cache.Hkv)
-    if v.shape != k.shape:
-        raise ValueError(f"v must have shape {tuple(k.shape)}, got {tuple(v.shape)}")
-    batch = _batch(table, cu, ctx, k.shape[0], cache)
-    if k.shape[0] == 0:
-        return
-    with _on(cache.device):
-        rc = _load().pi_attn_cache_append(k.data_ptr(), v.data_ptr(), ks, vs, cache._ref, ctypes.byref(batch),
-                                          _stream_of(stream, cache.device))
-        _check("pi_attn_cache_append", rc, stream, check)
+    T, _, ks = _packed(k, "k", cache, cache.Hkv)
+    Tv, _, vs = _packed(v, "v", cache, cache.Hkv)
+    if Tv != T:
+        _refuse(v, "v", f"of shape {tuple(k.shape)}")
+    batch = _batch(table, cu, ctx, T, cache)
+    if T > 0:
+        _call("pi_attn_cache_append", cache, stream, check, k.data_ptr(), v.data_ptr(), ks, vs, cache._ref, batch)
 
 
 def cache_read(cache: PagedCache, table, cu, start, rows: int, k=None, v=None, stream=None, check=False):
     """pi_attn_cache_read: rows start[b] .. start[b] + cu[b+1] - cu[b] - 1 of every sequence, packed, as
     bf16 (k, v) [rows, Hkv, d]."""
-    shape = (rows, cache.Hkv, cache.d)
-    k = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if k is None else k
-    v = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if v is None else v
-    _binding._expect_like(k, "k", cache, torch.bfloat16, shape)
-    _binding._expect_like(v, "v", cache, torch.bfloat16, shape)
+    shape, dev = (rows, cache.Hkv, cache.d), cache.device
+    k = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k is None else k
+    v = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v is None else v
+    pk, pv = _dense(k, "k", cache.index, _BF16, shape), _dense(v, "v", cache.index, _BF16, shape)
     batch = _batch(table, cu, start, rows, cache)
     if rows > 0:
-        with _on(cache.device):
-            rc = _load().pi_attn_cache_read(cache._ref, ctypes.byref(batch), k.data_ptr(), v.data_ptr(),
-                                            _stream_of(stream, cache.device))
-            _check("pi_attn_cache_read", rc, stream, check)
+        _call("pi_attn_cache_read", cache, stream, check, cache._ref, batch, pk, pv)
     return k, v
 
 
-def _outputs(q, cache, alpha, mode, out, lse):
-    T, H, d = q.shape
-    if alpha is None:
-        if mode != MODE_ECP:
-            raise ValueError("alpha is needed in pi mode")
-    else:
-        _binding._expect_like(alpha, "alpha", cache, torch.float32, (T, H))
+def _rows(T, H, cache, alpha, mode, out, lse):
+    """Checks of an attention's packed rows: (alpha's pointer, out, lse)."""
+    if alpha is not None:
+        alpha = _dense(alpha, "alpha", cache.index, _FP32, (T, H))
+    elif mode != MODE_ECP:
+        raise ValueError("alpha is needed in pi mode")
     if out is None:
-        out = torch.empty((T, H, d), dtype=torch.bfloat16, device=cache.device)
+        out = torch.empty((T, H, cache.d), dtype=_BF16, device=cache.device)
     else:
-        _binding._expect_like(out, "out", cache, torch.bfloat16, (T, H, d))
+        _dense(out, "out", cache.index, _BF16, (T, H, cache.d))
     if lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=cache.device)
+        lse = torch.empty((T, H), dtype=_FP32, device=cache.device)
     else:
-        _binding._expect_like(lse, "lse", cache, torch.float32, (T, H))
-    return out, lse
+        _dense(lse, "lse", cache.index, _FP32, (T, H))
+    return alpha, out, lse
 
 
 def extend_workspace_size(cache: PagedCache, B: int, T: int, width: int, H: int, k_local: int, period: int, S: int,
                           mode: int = MODE_PI) -> int:
     """pi_attn_extend_workspace_size: bytes of device workspace that :func:`extend` needs for B sequences with T packed
-    tokens and page tables of `width` entries (0 for sizes that it refuses)."""
+    tokens and page tables of `width` entries (0: none, or sizes that it refuses)."""
     return int(_load().pi_attn_extend_workspace_size(cache._ref, B, T, width, H, k_local, period, S, mode))
 
 
@@ -206,25 +217,26 @@ def extend(q, cache: PagedCache, table, cu, ctx, alpha, k_local: int, period: in
            out=None, lse=None, workspace=None, stream=None, check=False):
     """pi_attn_extend: the packed new tokens q [T, H, d] bf16 (any token stride) against their sequences' cached
     rows, which hold the chunk's own already.  alpha [T, H] fp32 (None in ECP mode).  Returns (out, lse)."""
-    qs = _packed_rows(q, "q", cache)
-    T, H, _ = q.shape
-    out, lse = _outputs(q, cache, alpha, mode, out, lse)
+    T, H, qs = _packed(q, "q", cache, None)
+    alpha, out, lse = _rows(T, H, cache, alpha, mode, out, lse)
     batch = _batch(table, cu, ctx, T, cache)
     if T > 0:
-        with _on(cache.device):
-            lib = _load()
-            nbytes = lib.pi_attn_extend_workspace_size(cache._ref, batch.B, T, batch.width, H, k_local, period, S, mode)
-            if workspace is None:
-                workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=cache.device)
-            else:
-                _binding._expect_like(workspace, "workspace", cache, torch.uint8, None)
-                if workspace.numel() < nbytes:
-                    raise ValueError(f"workspace must hold {nbytes} bytes, got {workspace.numel()}")
-            rc = lib.pi_attn_extend(q.data_ptr(), qs, cache._ref, ctypes.byref(batch),
-                                        None if alpha is None else alpha.data_ptr(), H, k_local, period, S, mode,
-                                        out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                    _stream_of(stream, cache.device))
-            _check("pi_attn_extend", rc, stream, check)
+        key = (batch.B, T, batch.width, H, k_local, period, S, mode)
+        nbytes = cache._workspace.get(key)
+        if nbytes is None:
+            if len(cache._workspace) >= 256:
+                cache._workspace.clear()
+            nbytes = cache._workspace[key] = extend_workspace_size(cache, *key)
+        if workspace is None:
+            if nbytes:
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
+        else:
+            _dense(workspace, "workspace", cache.index, torch.uint8, workspace.shape)
+            if workspace.numel() < nbytes:
+                raise ValueError(f"workspace must hold {nbytes} bytes, got {workspace.numel()}")
+        _call("pi_attn_extend", cache, stream, check, q.data_ptr(), qs, cache._ref, batch, alpha, H, k_local, period, S, mode,
+              out.data_ptr(), lse.data_ptr(), None if workspace is None else workspace.data_ptr(),
+              0 if workspace is None else workspace.numel())
     return out, lse
 
 
@@ -232,18 +244,13 @@ def decode_paged(q, cache: PagedCache, table, lens, alpha, k_local: int, period:
                  out=None, lse=None, stream=None, check=False):
     """pi_attn_decode_paged: one new token per sequence, q [B, H, d] bf16, against lens[b] cached rows (its own
     among them).  alpha [B, H] fp32 (None in ECP mode).  Returns (out [B, H, d], lse [B, H])."""
-    qs = _packed_rows(q, "q", cache)
-    B, H, _ = q.shape
-    out, lse = _outputs(q, cache, alpha, mode, out, lse)
+    B, H, qs = _packed(q, "q", cache, None)
+    alpha, out, lse = _rows(B, H, cache, alpha, mode, out, lse)
     if table.dim() != 2:
-        raise ValueError("table must be [B, width]")
-    _index_tensor(table, "table", cache, (B, table.shape[1]))
-    _index_tensor(lens, "lens", cache, (B,))
+        _refuse(table, "table", "[B, width]")
+    width = table.shape[1]
+    pt, pl = _int32(table, "table", cache.index, B, width), _int32(lens, "lens", cache.index, B)
     if B > 0:
-        with _on(cache.device):
-            rc = _load().pi_attn_decode_paged(q.data_ptr(), qs, cache._ref, table.data_ptr(), lens.data_ptr(), B,
-                                              table.shape[1], None if alpha is None else alpha.data_ptr(), H, k_local,
-                                              period, S, mode, out.data_ptr(), lse.data_ptr(),
-                                              _stream_of(stream, cache.device))
-            _check("pi_attn_decode_paged", rc, stream, check)
+        _call("pi_attn_decode_paged", cache, stream, check, q.data_ptr(), qs, cache._ref, pt, pl, B, width, alpha, H, k_local,
+              period, S, mode, out.data_ptr(), lse.data_ptr())
     return out, lse
