@@ -5,27 +5,39 @@
 // written, or the other way round, so HBM bandwidth bounds long calls and the chain of dependent
 // loads (sequence, page, row) the short ones.
 //
-// One warp per packed token: its lanes take the token's Hkv * d elements eight at a time (16 bytes
-// of bf16), K and V together, so that a block of 32 elements lies in four neighbouring lanes and
-// its largest magnitude takes two shuffles.  The token's sequence is searched by the whole warp
-// (two rounds of probes for up to 1024 sequences) while its first elements are in flight.
+// A warp takes one packed token, or two neighbouring ones of a long call: its lanes take a token's Hkv * d elements K and V
+// together, 8 at a time, or 16 where they are quantised, so that a block of 32 elements lies in two neighbouring lanes and
+// its largest magnitude takes one shuffle.  The tokens' sequence is searched by the whole warp (two rounds of probes for up
+// to 1024 sequences) while their elements are in flight.
+#include "pi_mma.cuh"
 #include "pi_paged.cuh"
 
 namespace pi {
 namespace cache {
 
 constexpr int WARPS = 8;
-constexpr int PRE = 2;  // element groups per lane and tensor in flight before the row is known
+constexpr unsigned kFull = 0xffffffffu;
 
-__device__ __forceinline__ float absmax8(const uint4 &x) {
+// A lane's share of a row: 16 elements, or 8 that stay bf16.
+template <int KV>
+struct Piece {
+    static constexpr int N = KV == kKvBf16 ? 1 : 2;  // 16-byte pieces of bf16
+    static constexpr int E = 8 * N;
+    uint4 x[N];
+};
+
+// Largest magnitude of the 32 elements that this lane and the next hold.
+__device__ __forceinline__ float absmax32(const Piece<kKvE4m3> &p) {
     // bf16 magnitudes compare like their bits; infinities and NaN come out at 0x7f80 or above
     uint32_t m = 0;
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t w[4] = {p.x[i].x, p.x[i].y, p.x[i].z, p.x[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m = __vmaxu2(m, w[j] & 0x7fff7fffu);
+    }
     m = max(m >> 16, m & 0xffffu);
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    m = max(m, __shfl_xor_sync(kFull, m, 1));
     return __uint_as_float(m << 16);
 }
 
@@ -56,71 +68,116 @@ __device__ __forceinline__ uint2 encode8(const uint4 &x, int e) {
     return make_uint2(o[0], o[1]);
 }
 
-// Eight elements of a row into the cache (`in`: this lane has some; the others of the warp take part
-// in the block maxima only).
+// A piece into the cache (`in`: this lane has one; the others of the warp take part in the block maxima only).
 template <int KV>
-__device__ __forceinline__ void put8(const PagedCache &c, void *pages, uint8_t *scales, const uint4 &x, long long row, int col,
-                                     bool in) {
-    if (KV == kKvBf16) {
-        if (in) *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(pages) + row * c.d + col) = x;
-        return;
+__device__ __forceinline__ void put(const PagedCache &c, void *pages, uint8_t *scales, const Piece<KV> &p, long long row, int col,
+                                    bool in) {
+    if constexpr (KV == kKvBf16) {
+        if (in) *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(pages) + row * c.d + col) = p.x[0];
+    } else {
+        const float amax = absmax32(reinterpret_cast<const Piece<kKvE4m3> &>(p));
+        const bool finite = __float_as_uint(amax) < 0x7f800000u;
+        const int e = finite ? scale_exp<KV>(amax) : 0;
+        const uint2 lo = encode8<KV>(p.x[0], e), hi = encode8<KV>(p.x[1], e);
+        if (!in) return;
+        *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(pages) + row * c.d + col) =
+            finite ? make_uint4(lo.x, lo.y, hi.x, hi.y) : make_uint4(0u, 0u, 0u, 0u);
+        if ((col & (kScaleBlock - 1)) == 0)
+            scales[row * (c.d / kScaleBlock) + col / kScaleBlock] = (uint8_t)(finite ? e + 127 : kScaleNan);
     }
-    const float amax = absmax8(x);
-    const bool finite = __float_as_uint(amax) < 0x7f800000u;
-    const int e = finite ? scale_exp<KV>(amax) : 0;
-    const uint2 codes = finite ? encode8<KV>(x, e) : make_uint2(0u, 0u);
-    if (!in) return;
-    *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(pages) + row * c.d + col) = codes;
-    if ((col & (kScaleBlock - 1)) == 0)
-        scales[row * (c.d / kScaleBlock) + col / kScaleBlock] = (uint8_t)(finite ? e + 127 : kScaleNan);
 }
 
+// Eight elements of a cache row as bf16.  (16 per lane would be wider loads, but each of a lane's two 16-byte stores would then
+// fill half of its 32-byte sectors: 46.6 us where this takes 38.5, for 65536 tokens of 4 e4m3 heads, d = 128.)
 template <int KV>
+__device__ __forceinline__ uint4 get8(const PagedCache &c, const void *pages, const uint8_t *scales, long long row, int col) {
+    if constexpr (KV == kKvBf16) {
+        return __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(pages) + row * c.d + col));
+    } else {
+        const uint2 w = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(pages) + row * c.d + col));
+        const Scale2<KV> s = scale_same<KV>(__ldg(scales + row * (c.d / kScaleBlock) + col / kScaleBlock));
+        uint4 x;
+        codes_to_bf16<KV>(w.x, s, s.big, x.x, x.y);
+        codes_to_bf16<KV>(w.y, s, s.big, x.z, x.w);
+        return x;
+    }
+}
+
+// Position and page of packed tokens t .. t + TOK - 1, in lanes 0 .. TOK - 1 (page -1: the token has no row).
+template <int TOK>
+__device__ __forceinline__ void locate_run(const PagedCache &c, const PagedBatch &bt, int t, int &pos, int &pg, int *index_word) {
+    const int lane = threadIdx.x & 31;
+    int b;
+    pos = locate(c, bt, t, b, index_word);
+    const bool first = pos >= 0;
+    const int end = first ? __ldg(bt.cu + b + 1) : t + 1;  // tokens of the first one's sequence end here
+    if (lane > 0) pos = first && lane < TOK && t + lane < end ? pos + lane : -1;
+    int seq = b;
+#pragma unroll 1
+    for (int i = max(1, end - t); i < TOK && t + i < bt.T; ++i) {  // the others: searched one by one
+        const int p = locate(c, bt, t + i, b, index_word);
+        if (lane == i) {
+            pos = p;
+            seq = b;
+        }
+    }
+    pg = -1;
+    if (lane < TOK && pos >= 0) {
+        pg = page_of(c, bt.table, seq, pos);
+        if (pg < 0) record_index(index_word);
+    }
+}
+
+template <int KV, int TOK>
 __global__ void __launch_bounds__(WARPS * 32) append_kernel(const AppendArgs a) {
-    const int t = blockIdx.x * WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int t = (blockIdx.x * WARPS + (threadIdx.x >> 5)) * TOK, lane = threadIdx.x & 31;
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (t >= a.batch.T) return;
     const PagedCache &c = a.cache;
-    const int n = c.Hkv << (c.d_log2 - 3);  // groups of eight elements: a multiple of 8
-    const uint4 *pk = reinterpret_cast<const uint4 *>(a.k + (long long)t * a.k_stride);
-    const uint4 *pv = reinterpret_cast<const uint4 *>(a.v + (long long)t * a.v_stride);
-    uint4 xk[PRE], xv[PRE];
-    auto load = [&](int g0) {
+    constexpr int E = Piece<KV>::E;
+    const int n = (c.Hkv << c.d_log2) / E;  // pieces of a token: an even number
+    const int last = a.batch.T - 1;
+    Piece<KV> k[TOK], v[TOK];
+    auto load = [&](int j) {
 #pragma unroll
-        for (int u = 0; u < PRE; ++u) {
-            const int j = g0 + lane + 32 * u;
-            xk[u] = j < n ? __ldg(pk + j) : make_uint4(0u, 0u, 0u, 0u);
-            xv[u] = j < n ? __ldg(pv + j) : make_uint4(0u, 0u, 0u, 0u);
+        for (int i = 0; i < TOK; ++i) {
+            const bool in = j < n && t + i <= last;
+            const uint4 *pk = reinterpret_cast<const uint4 *>(a.k + (long long)(t + i) * a.k_stride) + j * Piece<KV>::N;
+            const uint4 *pv = reinterpret_cast<const uint4 *>(a.v + (long long)(t + i) * a.v_stride) + j * Piece<KV>::N;
+#pragma unroll
+            for (int x = 0; x < Piece<KV>::N; ++x) {
+                k[i].x[x] = in ? __ldg(pk + x) : make_uint4(0u, 0u, 0u, 0u);
+                v[i].x[x] = in ? __ldg(pv + x) : make_uint4(0u, 0u, 0u, 0u);
+            }
         }
     };
-    load(0);
-    int b;
-    const int pos = locate(c, a.batch, t, b, a.index_word);
-    if (pos < 0) return;
-    const int pg = page_of(c, a.batch.table, b, pos);
-    if (pg < 0) {
-        record_index(a.index_word);
-        return;
-    }
-    for (int g0 = 0;;) {
+    load(lane);
+    int pos, pg;
+    locate_run<TOK>(c, a.batch, t, pos, pg, a.index_word);
+    for (int j0 = 0;;) {
+        const int j = j0 + lane, col = j * E & (c.d - 1), head = j * E >> c.d_log2;
 #pragma unroll
-        for (int u = 0; u < PRE; ++u) {
-            const int j = g0 + lane + 32 * u, col = j * 8 & (c.d - 1), head = j >> (c.d_log2 - 3);
-            const long long row = row_in_page(c, pg, head, pos);
-            put8<KV>(c, c.k, c.k_scale, xk[u], row, col, j < n);
-            put8<KV>(c, c.v, c.v_scale, xv[u], row, col, j < n);
+        for (int i = 0; i < TOK; ++i) {
+            const int p = __shfl_sync(kFull, pos, i), g = __shfl_sync(kFull, pg, i);
+            const long long row = row_in_page(c, g, head, p);
+            put<KV>(c, c.k, c.k_scale, k[i], row, col, j < n && g >= 0);
+            put<KV>(c, c.v, c.v_scale, v[i], row, col, j < n && g >= 0);
         }
-        g0 += 32 * PRE;
-        if (g0 >= n) break;
-        load(g0);
+        j0 += 32;
+        if (j0 >= n) break;
+        load(j0 + lane);
     }
 }
 
 template <int KV>
 __global__ void __launch_bounds__(WARPS * 32) read_kernel(const ReadArgs a) {
     const int t = blockIdx.x * WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (t >= a.batch.T) return;
     const PagedCache &c = a.cache;
-    const int n = c.Hkv << (c.d_log2 - 3);
+    const int n = c.Hkv << (c.d_log2 - 3);  // groups of eight elements
     int b;
     const int pos = locate(c, a.batch, t, b, a.index_word);
     if (pos < 0) return;
@@ -130,44 +187,63 @@ __global__ void __launch_bounds__(WARPS * 32) read_kernel(const ReadArgs a) {
         return;
     }
     uint4 *ok = reinterpret_cast<uint4 *>(a.k) + (long long)t * n, *ov = reinterpret_cast<uint4 *>(a.v) + (long long)t * n;
-    for (int g0 = 0; g0 < n; g0 += 32 * PRE) {
-        uint4 xk[PRE], xv[PRE];
+    constexpr int PRE = 2;  // groups per lane and tensor in flight (more cost registers, and warps with them: 4 take 7.3 us, 2 6.6)
+    for (int j0 = lane; j0 - lane < n; j0 += 32 * PRE) {
+        uint4 k[PRE], v[PRE];
 #pragma unroll
         for (int u = 0; u < PRE; ++u) {
-            const int j = g0 + lane + 32 * u, col = j * 8 & (c.d - 1), head = j >> (c.d_log2 - 3);
+            const int j = j0 + 32 * u, col = j * 8 & (c.d - 1), head = j >> (c.d_log2 - 3);
             if (j >= n) continue;
             const long long row = row_in_page(c, pg, head, pos);
-            xk[u] = get8<KV>(c, c.k, c.k_scale, row, col);
-            xv[u] = get8<KV>(c, c.v, c.v_scale, row, col);
+            k[u] = get8<KV>(c, c.k, c.k_scale, row, col);
+            v[u] = get8<KV>(c, c.v, c.v_scale, row, col);
         }
 #pragma unroll
         for (int u = 0; u < PRE; ++u) {
-            const int j = g0 + lane + 32 * u;
+            const int j = j0 + 32 * u;
             if (j >= n) continue;
-            ok[j] = xk[u];
-            ov[j] = xv[u];
+            ok[j] = k[u];
+            ov[j] = v[u];
         }
     }
+}
+
+template <typename K, typename A>
+static cudaError_t launch(K kernel, int tokens, const A &a, cudaStream_t st) {
+    const long long warps = ((long long)a.batch.T + tokens - 1) / tokens;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((warps + WARPS - 1) / WARPS), 1, 1);
+    cfg.blockDim = dim3(WARPS * 32, 1, 1);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];  // it may start while the kernel before it on the stream ends (and waits for it)
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 }  // namespace cache
 
 cudaError_t launch_append(const AppendArgs &a, cudaStream_t st) {
     using namespace cache;
-    const unsigned grid = (unsigned)((a.batch.T + WARPS - 1) / WARPS);
-    if (a.cache.kv_type == kKvBf16) append_kernel<kKvBf16><<<grid, WARPS * 32, 0, st>>>(a);
-    else if (a.cache.kv_type == kKvE4m3) append_kernel<kKvE4m3><<<grid, WARPS * 32, 0, st>>>(a);
-    else append_kernel<kKvInt8><<<grid, WARPS * 32, 0, st>>>(a);
-    return cudaGetLastError();
+    // two tokens per warp once that leaves the SMs full of warps (65536 tokens of 4 heads, d = 128, int8: 33.7 us, one 34.2, four
+    // 39.9; rows that stay bf16 gain nothing: 17.5 us with one, 18.2 with two, for 16384 tokens of 12 heads, d = 64)
+    const bool two = a.batch.T >= 128 * sm_count();
+    switch (a.cache.kv_type) {
+        case kKvBf16: return launch(append_kernel<kKvBf16, 1>, 1, a, st);
+        case kKvE4m3: return two ? launch(append_kernel<kKvE4m3, 2>, 2, a, st) : launch(append_kernel<kKvE4m3, 1>, 1, a, st);
+        default: return two ? launch(append_kernel<kKvInt8, 2>, 2, a, st) : launch(append_kernel<kKvInt8, 1>, 1, a, st);
+    }
 }
 
 cudaError_t launch_cache_read(const ReadArgs &a, cudaStream_t st) {
     using namespace cache;
-    const unsigned grid = (unsigned)((a.batch.T + WARPS - 1) / WARPS);
-    if (a.cache.kv_type == kKvBf16) read_kernel<kKvBf16><<<grid, WARPS * 32, 0, st>>>(a);
-    else if (a.cache.kv_type == kKvE4m3) read_kernel<kKvE4m3><<<grid, WARPS * 32, 0, st>>>(a);
-    else read_kernel<kKvInt8><<<grid, WARPS * 32, 0, st>>>(a);
-    return cudaGetLastError();
+    switch (a.cache.kv_type) {
+        case kKvBf16: return launch(read_kernel<kKvBf16>, 1, a, st);
+        case kKvE4m3: return launch(read_kernel<kKvE4m3>, 1, a, st);
+        default: return launch(read_kernel<kKvInt8>, 1, a, st);
+    }
 }
 
 }  // namespace pi

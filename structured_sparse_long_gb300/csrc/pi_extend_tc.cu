@@ -119,7 +119,7 @@ __host__ __device__ __forceinline__ long long max_blocks(long long T, long long 
     return T / R + 2 * (B < T ? B : T);
 }
 
-constexpr int PLAN_THREADS = 1024;
+constexpr int PLAN_THREADS = 256, PLAN_CTAS = 8;  // each makes the same sums and writes its share
 
 struct PlanArgs {
     Shape s;
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PlanArgs a) {
     bool sorted = true;
     for (int b = tid; b < bt.B; b += PLAN_THREADS) sorted = sorted && bt.cu[b] <= bt.cu[b + 1];
     if (!__syncthreads_and(sorted)) {
-        if (tid == 0) {
+        if (tid == 0 && blockIdx.x == 0) {
             record_index(index_word);
             plan[0] = plan[1] = 0;
         }
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PlanArgs a) {
         }
         const int total = scan(cnt, upto);
         const int total_slots = a.slots ? scan(slots, slots_upto) : 0;
-        for (int x = tid; x < total; x += PLAN_THREADS) {
+        for (int x = blockIdx.x * PLAN_THREADS + tid; x < total; x += PLAN_CTAS * PLAN_THREADS) {
             int place;
             const int o = owner(upto, x, place);
             const int t0 = bt.cu[b0 + o], n = bt.cu[b0 + o + 1] - t0, ctx = bt.ctx[b0 + o];
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PlanArgs a) {
                 blocks[base + x].per_window = q.per_window;
             }
         }
-        for (int x = tid; x < total_slots; x += PLAN_THREADS) {
+        for (int x = blockIdx.x * PLAN_THREADS + tid; x < total_slots; x += PLAN_CTAS * PLAN_THREADS) {
             int place;
             const int o = owner(slots_upto, x, place);
             const int n = bt.cu[b0 + o + 1] - bt.cu[b0 + o], ctx = bt.ctx[b0 + o];
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PlanArgs a) {
         base += total;
         slot_base += total_slots;
     }
-    if (tid == 0) {
+    if (tid == 0 && blockIdx.x == 0) {
         plan[0] = base;
         plan[1] = slot_base;
     }
@@ -273,6 +273,12 @@ struct ConvertArgs {
 
 constexpr int CONVERT_WARPS = 8;
 
+__device__ __forceinline__ void st_keep(uint4 *p, const uint4 &x, uint64_t policy) {
+    asm volatile("st.global.L2::cache_hint.v4.u32 [%0], {%1, %2, %3, %4}, %5;" ::"l"(p), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w),
+                 "l"(policy)
+                 : "memory");
+}
+
 // Whether some query of the chunk attends a key in x .. y of its sequence.
 __device__ __forceinline__ bool attended(const ConvertArgs &a, int b, int x, int y) {
     const int t0 = a.bt.cu[b], n = a.bt.cu[b + 1] - t0, ctx = a.bt.ctx[b], last = ctx + n - 1;
@@ -292,38 +298,46 @@ __global__ void __launch_bounds__(CONVERT_WARPS * 32) convert_kernel(const Conve
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan is written
     const PagedCache &c = a.c;
     const int lane = threadIdx.x & 31;
-    constexpr int PER_ROW = D / 16, ITER = CHUNK * PER_ROW / 32;  // 16-code pieces; pieces per lane
-    const long long items = (long long)a.plan[1] * c.Hkv * 2;
-    for (long long x = (long long)blockIdx.x * CONVERT_WARPS + (threadIdx.x >> 5); x < items; x += (long long)gridDim.x * CONVERT_WARPS) {
-        const int v = (int)(x & 1);
-        const long long sh = x >> 1;  // slot * Hkv + head
-        const int slot = (int)(sh / c.Hkv), g = (int)(sh - (long long)slot * c.Hkv);
-        const int2 st = a.slots[slot];
-        if (st.y < 0) continue;
-        const int pos = st.y * CHUNK;
-        // the page of the tile (page 16: of its halves)
-        const int half = c.page < CHUNK ? lane >> 4 : 0;
-        int pg = -1;
-        if (pos + half * 16 < c.width << c.page_log2) {
-            pg = __ldg(a.bt.table + (long long)st.x * c.width + ((pos + half * 16) >> c.page_log2));
-            if ((unsigned)pg >= (unsigned)c.n_pages) {
-                pg = -1;
-                if ((lane & 15) == 0 && attended(a, st.x, pos + half * 16, pos + (c.page < CHUNK ? half * 16 + 15 : CHUNK - 1)))
-                    record_index(a.index_word);
-            }
+    constexpr int PER_ROW = D / 8, ITER = CHUNK * PER_ROW / 32;  // pieces of 8 codes (16 bytes of bf16); pieces per lane
+    const int heads = c.Hkv * 2, items = a.plan[1] * heads, step = gridDim.x * CONVERT_WARPS;
+    const int half = c.page < CHUNK ? lane >> 4 : 0;
+    // an item's sequence, tile and page (page 16: of the lane's half): requested an item ahead
+    auto slot_of = [&](int x) -> int2 { return x < items ? __ldg(a.slots + x / heads) : make_int2(0, -1); };
+    auto page = [&](int2 st) -> int {
+        const int pos = st.y * CHUNK + half * 16;
+        return st.y >= 0 && pos < c.width << c.page_log2 ? __ldg(a.bt.table + (long long)st.x * c.width + (pos >> c.page_log2)) : -1;
+    };
+    int x = blockIdx.x * CONVERT_WARPS + (threadIdx.x >> 5);
+    int2 st = slot_of(x), st_next = slot_of(x + step);
+    int pg = page(st);
+    uint64_t keep;  // the tiles are read again soon, by the attention kernel
+    asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
+    for (; x < items; x += step) {
+        const int2 now = st;
+        int p_now = pg;
+        st = st_next;
+        pg = page(st);
+        st_next = slot_of(x + 2 * step);
+        if (now.y < 0) continue;
+        const int v = x & 1, slot = x / heads, g = (x - slot * heads) >> 1, pos = now.y * CHUNK;
+        if ((unsigned)p_now >= (unsigned)c.n_pages) {
+            p_now = -1;
+            if ((lane & 15) == 0 && attended(a, now.x, pos + half * 16, pos + (c.page < CHUNK ? half * 16 + 15 : CHUNK - 1)))
+                record_index(a.index_word);
         }
+        const long long sh = (long long)slot * c.Hkv + g;
         const uint8_t *codes = static_cast<const uint8_t *>(v ? c.v : c.k), *scales = v ? c.v_scale : c.k_scale;
-        uint4 w[ITER];
+        uint2 w[ITER];
         uint32_t sc[ITER];
 #pragma unroll
         for (int u = 0; u < ITER; ++u) {
-            const int piece = u * 32 + lane, r = piece / PER_ROW, col = piece % PER_ROW * 16;
-            const int p = __shfl_sync(0xffffffffu, pg, c.page < CHUNK && r >= 16 ? 16 : 0);
-            w[u] = make_uint4(0u, 0u, 0u, 0u);
+            const int piece = u * 32 + lane, r = piece / PER_ROW, col = piece % PER_ROW * 8;
+            const int p = __shfl_sync(0xffffffffu, p_now, c.page < CHUNK && r >= 16 ? 16 : 0);
+            w[u] = make_uint2(0u, 0u);
             sc[u] = 0u;
             if (p >= 0) {
                 const long long row = row_in_page(c, p, g, pos + r);
-                w[u] = ldg_stream(reinterpret_cast<const uint4 *>(codes + row * D + col));
+                w[u] = __ldg(reinterpret_cast<const uint2 *>(codes + row * D + col));
                 sc[u] = __ldg(scales + row * (D / kScaleBlock) + col / kScaleBlock);
             }
         }
@@ -331,13 +345,10 @@ __global__ void __launch_bounds__(CONVERT_WARPS * 32) convert_kernel(const Conve
 #pragma unroll
         for (int u = 0; u < ITER; ++u) {
             const Scale2<KV> s2 = scale_same<KV>(sc[u]);
-            uint32_t o[8];
-            codes_to_bf16<KV>(w[u].x, s2, s2.big, o[0], o[1]);
-            codes_to_bf16<KV>(w[u].y, s2, s2.big, o[2], o[3]);
-            codes_to_bf16<KV>(w[u].z, s2, s2.big, o[4], o[5]);
-            codes_to_bf16<KV>(w[u].w, s2, s2.big, o[6], o[7]);
-            out[2 * (u * 32 + lane)] = make_uint4(o[0], o[1], o[2], o[3]);
-            out[2 * (u * 32 + lane) + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+            uint4 o;
+            codes_to_bf16<KV>(w[u].x, s2, s2.big, o.x, o.y);
+            codes_to_bf16<KV>(w[u].y, s2, s2.big, o.z, o.w);
+            st_keep(out + u * 32 + lane, o, keep);
         }
     }
 }
@@ -1065,14 +1076,14 @@ cudaError_t launch_extend(const ExtendArgs &e, cudaStream_t st) {
     const int G = s.H / s.Hkv, GP = packed_heads(G), R = BM / GP, ngrp = s.H / GP;
     const bool quant = c.kv_type != kKvBf16, skips = s.mode != kModeEcp && s.S > 0;
     const Layout l = layout(s, c.kv_type, e.batch.B, e.batch.T, (long long)c.width << c.page_log2);
-    if (max_blocks(e.batch.T, e.batch.B, R) * ngrp > 0x7fffffffLL - 1024 || l.n_slots * s.Hkv > 0x7fffffffLL / CHUNK)
+    if (max_blocks(e.batch.T, e.batch.B, R) * ngrp > 0x7fffffffLL - 1024 || l.n_slots * s.Hkv > 0x7fffffffLL / (2 * CHUNK))
         return cudaErrorInvalidConfiguration;
     char *ws = reinterpret_cast<char *>(e.workspace);
     int2 *slots = quant ? reinterpret_cast<int2 *>(ws + l.slots) : nullptr;
     Args a{e, e.workspace, GP, R, R == 32 ? 5 : R == 64 ? 6 : 7, ngrp, skips ? first_skip_multiple(s) : 1,
            skips && s.period % CHUNK == 0, quant ? CHUNK : std::min(CHUNK, c.page), quant ? (int)l.n_slots : c.n_pages,
            make_fastdiv(ngrp), make_fastdiv(G)};
-    plan_kernel<<<1, PLAN_THREADS, 0, st>>>(PlanArgs{s, c, e.batch, R, a.m_first, a.aligned, e.workspace, e.index_word, slots});
+    plan_kernel<<<PLAN_CTAS, PLAN_THREADS, 0, st>>>(PlanArgs{s, c, e.batch, R, a.m_first, a.aligned, e.workspace, e.index_word, slots});
     cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
     if (!quant) return s.d == 64 ? launch<64, false>(a, c.k, c.v, st) : launch<128, false>(a, c.k, c.v, st);

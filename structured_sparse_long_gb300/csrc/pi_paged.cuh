@@ -91,35 +91,4 @@ __device__ __forceinline__ int locate(const PagedCache &c, const PagedBatch &bt,
     return ctx + t - t0;
 }
 
-// Eight codes and their scale to eight bf16 (exact, see above).
-template <int KV>
-__device__ __forceinline__ uint4 decode8(uint2 c, float scale) {
-    uint32_t o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t two = (i < 2 ? c.x : c.y) >> (16 * (i & 1)) & 0xffffu;
-        float a, b;
-        if (KV == kKvE4m3) {
-            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-            const float2 f = __half22float2(__half2(h));
-            a = f.x;
-            b = f.y;
-        } else {
-            a = (float)(int8_t)(two & 0xffu);
-            b = (float)(int8_t)(two >> 8);
-        }
-        const __nv_bfloat162 r = __floats2bfloat162_rn(a * scale, b * scale);
-        o[i] = *reinterpret_cast<const uint32_t *>(&r);
-    }
-    return make_uint4(o[0], o[1], o[2], o[3]);
-}
-
-// Eight elements of a cache row as bf16.
-template <int KV>
-__device__ __forceinline__ uint4 get8(const PagedCache &c, const void *pages, const uint8_t *scales, long long row, int col) {
-    if (KV == kKvBf16) return __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(pages) + row * c.d + col));
-    const uint2 codes = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(pages) + row * c.d + col));
-    return decode8<KV>(codes, scale_of(__ldg(scales + row * (c.d / kScaleBlock) + col / kScaleBlock)));
-}
-
 }  // namespace pi

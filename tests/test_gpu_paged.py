@@ -171,6 +171,33 @@ def test_tokens_find_their_sequence(B):
     assert torch.equal(got, x[:, 0])
 
 
+@pytest.mark.parametrize("kv,Hkv,d", [("e4m3", 1, 64), ("int8", 3, 64), ("e4m3", 2, 128), ("bf16", 1, 64)])
+def test_append_of_a_long_call(kv, Hkv, d):
+    """Calls long enough for two tokens per warp: sequences that start and end between the two, empty ones, tokens behind
+    the last sequence, a bad page in the middle."""
+    n, ctx = [7001, 0, 12990, 1, 1, 33, 4000], [5, 0, 16, 3, 0, 15, 1]
+    bt = Batch(ctx, n, Hkv, d, 16, kv, seed=d + Hkv, extra_tokens=4)
+    k, v = normal(bt.gen, bt.T, Hkv, d), normal(bt.gen, bt.T, Hkv, d)
+    table = bt.table.copy()
+    table[2, 100] = 2 ** 30
+    before = ref.bits(bt.cache.k).copy()
+    pa.cache_append(k.cuda(), v.cuda(), bt.cache, dev(table), dev(bt.cu), dev(ctx))
+    assert pa.status() == ERR_INDEX
+    seq = np.repeat(np.arange(len(n)), n)
+    pos = np.concatenate([c + np.arange(m) for c, m in zip(ctx, n)])
+    kept = ~((seq == 2) & (pos // 16 == 100))
+    at = bt.table[seq, pos // 16][kept], pos[kept] % 16
+    for x, pages, scales in ((k, bt.cache.k, bt.cache.k_scale), (v, bt.cache.v, bt.cache.v_scale)):
+        rows = x[:len(seq)][torch.from_numpy(kept)]
+        codes, sc = (ref.bits(rows), None) if kv == "bf16" else ref.encode(rows.float().numpy(), kv)
+        got = ref.bits(pages)
+        assert np.array_equal(got[at[0], :, at[1]], codes)
+        assert sc is None or np.array_equal(ref.bits(scales)[at[0], :, at[1]], sc)
+        rest = np.ones(got.shape[:1] + got.shape[2:3], dtype=bool)  # [page, row]
+        rest[at] = False
+        assert np.array_equal(got.transpose(0, 2, 1, 3)[rest], before.transpose(0, 2, 1, 3)[rest])
+
+
 # ------------------------------------------------------------------ attention
 
 EXTEND = [
