@@ -1,4 +1,4 @@
-"""Builds the CUDA library libpi_attn.so for sm_103a with nvcc (no cmake).
+"""Builds the CUDA library libpi_attn.so for sm_103a with nvcc (no cmake), and the binding's CPython extension.
 
 Translation units are compiled in parallel into ``_build/`` and linked into
 ``_lib/libpi_attn.so`` inside the package, next to the Python binding.
@@ -10,6 +10,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -18,6 +19,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_DIR = os.path.join(HERE, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libpi_attn.so")
+NATIVE_SOURCE = "pi_paged_py.c"  # CPython extension of the paged cache's binding
+NATIVE_PATH = os.path.join(LIB_DIR, "_pi_paged" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
 SOURCES = ["api.cu", "pi_simt.cu", "pi_fwd_tc.cu", "pi_bwd_tc.cu", "pi_decode.cu",
            "api_paged.cu", "pi_cache.cu", "pi_extend_tc.cu", "pi_decode_paged.cu"]
@@ -85,6 +88,16 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
                     sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
                 if r.returncode != 0:
                     raise RuntimeError(f"nvcc failed for {cmd[2]}")
+    src = os.path.join(CSRC, NATIVE_SOURCE)
+    if force or _stale(NATIVE_PATH, [src, os.path.join(INCLUDE, "pi_attn.h")]):
+        tmp = NATIVE_PATH + f".tmp{os.getpid()}"
+        _, r = run(["gcc", "-shared", "-fPIC", "-O2", "-Wall", "-Wextra", "-I", sysconfig.get_paths()["include"], "-I", INCLUDE, src,
+                    "-o", tmp])
+        if verbose or r.returncode != 0:
+            sys.stderr.write(r.stdout + r.stderr)
+        if r.returncode != 0:
+            raise RuntimeError("gcc failed for " + src)
+        os.replace(tmp, NATIVE_PATH)
     if force or jobs or _stale(LIB_PATH, objs):
         tmp = LIB_PATH + f".tmp{os.getpid()}"
         cmd = [nv, "-shared", "-o", tmp] + objs + ARCH_FLAGS + [

@@ -246,24 +246,53 @@ def test_binding_refuses_host_tensors_and_wrong_types(monkeypatch):
         paged.PagedCache(z.to(torch.int8), z.to(torch.int8))
     with pytest.raises(ValueError, match="no scales"):
         paged.PagedCache(z, z, z, z)
-    # past the device check (stubbed: no GPU here), everything else is still checked before the library
-    monkeypatch.setattr(paged, "_load", lambda: pytest.fail("the library was reached"))
+    # past the device check (stubbed: no GPU here; host tensors answer get_device() with -1, as their cache does),
+    # everything else is still checked before the library is called
     monkeypatch.setattr(paged._binding, "_expect_like", lambda t, name, like, dtype, shape: None)
-    c = paged.PagedCache(z, z)
-    table, cu, ctx = torch.zeros(1, 4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
-    q, a = torch.zeros(5, 4, 64, dtype=torch.bfloat16), torch.zeros(5, 4)
-    kv = torch.zeros(5, 2, 64, dtype=torch.bfloat16)
-    for bad in (dict(table=table.long()), dict(table=table[0]), dict(cu=cu[:1]), dict(ctx=ctx.float()),
-                dict(table=table.expand(1, 4)[:, ::2]), dict(q=q.float()), dict(q=q[:, :, :32]), dict(q=q.transpose(0, 1)),
-                dict(alpha=None)):
-        kw = {**dict(q=q, cache=c, table=table, cu=cu, ctx=ctx, alpha=a), **bad}
+    monkeypatch.setattr(paged, "_current_device", lambda: -1)
+    monkeypatch.setattr(paged, "_raw_stream", lambda index: 0)
+    native = paged._load_native()
+    calls = []
+    never = ctypes.CFUNCTYPE(ctypes.c_int)(lambda: calls.append(1) or 0)
+    addresses = [ctypes.cast(never, ctypes.c_void_p).value] * 5
+    addresses[2] = ctypes.cast(paged._load().pi_attn_extend_workspace_size, ctypes.c_void_p).value
+    torchs = (torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.empty)
+    native.bind(*addresses, *torchs)
+    try:
+        c = paged.PagedCache(z, z)
+        table, cu = torch.zeros(1, 4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+        ctx = torch.zeros(1, dtype=torch.int32)
+        q, a = torch.zeros(5, 4, 64, dtype=torch.bfloat16), torch.zeros(5, 4)
+        kv = torch.zeros(5, 2, 64, dtype=torch.bfloat16)
+        for bad in (dict(table=table.long()), dict(table=table[0]), dict(cu=cu[:1]), dict(ctx=ctx.float()), dict(ctx=[0]),
+                    dict(table=table.expand(1, 4)[:, ::2]), dict(q=q.float()), dict(q=q[:, :, :32]), dict(q=q.transpose(0, 1)),
+                    dict(q=q[0]), dict(q=None), dict(alpha=None), dict(alpha=a[:4]), dict(alpha=a.double()), dict(alpha=a.T),
+                    dict(k_local=2 ** 31), dict(S=-2 ** 40), dict(out=a), dict(out=q[:4]), dict(out=q.float()), dict(lse=q),
+                    dict(lse=torch.zeros(4, 5).T), dict(workspace=a), dict(workspace=torch.zeros(3, 3, dtype=torch.uint8))):
+            kw = dict(q=q, cache=c, table=table, cu=cu, ctx=ctx, alpha=a, k_local=8, period=16, S=1, out=q.clone(), lse=a.clone())
+            with pytest.raises(ValueError):
+                paged.extend(**{**kw, **bad})
+            if not {"cu", "ctx", "workspace"} & set(bad):
+                del kw["cu"], kw["ctx"]
+                with pytest.raises(ValueError):
+                    paged.decode_paged(lens=torch.zeros(5, dtype=torch.int32), **{**kw, "table": table.expand(5, 4).contiguous(), **bad})
+        for k, v in ((kv[:, :1], kv), (kv, kv[:4]), (kv[:, :, ::2], kv), (kv.float(), kv), (kv, 3)):
+            with pytest.raises(ValueError):
+                paged.cache_append(k, v, c, table, cu, ctx)
+        for bad in (dict(k=kv.float()), dict(v=kv[:4]), dict(rows=-1), dict(start=cu)):
+            with pytest.raises(ValueError):
+                paged.cache_read(**{**dict(cache=c, table=table, cu=cu, start=ctx, rows=5, k=kv, v=kv), **bad})
         with pytest.raises(ValueError):
-            paged.extend(*kw.values(), 8, 16, 1)
-    for k, v in ((kv[:, :1], kv), (kv, kv[:4]), (kv[:, :, ::2], kv), (kv.float(), kv)):
-        with pytest.raises(ValueError):
-            paged.cache_append(k, v, c, table, cu, ctx)
-    with pytest.raises(ValueError):
-        paged.decode_paged(q, c, table, ctx, a, 8, 16, 1)  # five queries, one sequence
+            paged.decode_paged(q, c, table, ctx, a, 8, 16, 1)  # five queries, one sequence
+        # an empty call is none, and one that is right reaches the library
+        assert paged.cache_append(kv[:0], kv[:0], c, table, cu, ctx) is None
+        out, lse = paged.decode_paged(q[:0], c, table[:0], ctx[:0], a[:0], 8, 16, 1, out=q[:0], lse=a[:0])
+        assert out.shape == (0, 4, 64) and lse.shape == (0, 4) and not calls
+        paged.cache_append(kv, kv, c, table, cu, ctx)
+        assert calls == [1]
+    finally:
+        monkeypatch.setattr(paged, "_native", None)
+        paged._load_native()
 
 
 def test_reference_codes_are_torch_codes():
