@@ -293,7 +293,7 @@ int pi_attn_decode(const void *q, const void *k_cache, const void *v_cache, cons
  *   code by the scale, which bf16 holds exactly (a code that was rounded up to 2^128 or
  *   more, which only an element above 0.96 * 2^128 can be, reads as an infinity).  A
  *   block with an infinity or a NaN gets s = 255 and reads back as NaN.
- *   d: 64 or 128; page: 16, 32, 64, 128 or 256 rows; n_pages * Hkv * page < 2^31;
+ *   d: 64 or 128; page: 16, 32, 64, 128 or 256 rows; Hkv <= 65535; n_pages * Hkv * page < 2^31;
  *   all four pointers 16-byte aligned.
  *
  * pi_attn_batch_t -- B sequences and their packed tokens.
@@ -379,7 +379,7 @@ int pi_attn_extend(const void *q, long long q_stride, const pi_attn_cache_t *cac
  *   them (its position is lens[b] - 1).  lens[b] = 0 gives out = 0 and lse = -inf, as does
  *   a length out of range.  q [B, H, d] bf16 with sequences q_stride elements apart,
  *   alpha [B, H] fp32 (NULL in ECP mode), out [B, H, d] bf16, lse [B, H] fp32; table
- *   [B, width] as above.  H / Hkv <= 16; B and Hkv <= 65535.  A row that attends a key on
+ *   [B, width] as above.  H / Hkv <= 16; B <= 65535.  A row that attends a key on
  *   a page out of range is undefined.
  */
 int pi_attn_decode_paged(const void *q, long long q_stride, const pi_attn_cache_t *cache,

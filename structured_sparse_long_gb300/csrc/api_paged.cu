@@ -25,6 +25,7 @@ int make_cache(const pi_attn_cache_t *c, int width, pi::PagedCache &out) {
     const bool quant = c->kv_type != PI_KV_BF16;
     if (quant && (!c->k_scale || !c->v_scale)) return PI_ERR_NULL;
     if (c->n_pages <= 0 || c->Hkv <= 0 || width <= 0) return PI_ERR_SHAPE;
+    if (c->Hkv > 65535) return PI_ERR_UNSUPPORTED;
     if (c->d != 64 && c->d != 128) return PI_ERR_UNSUPPORTED;
     if (c->page < 16 || c->page > 256 || (c->page & (c->page - 1))) return PI_ERR_UNSUPPORTED;
     if ((long long)c->n_pages * c->Hkv > 0x7fffffffLL / c->page) return PI_ERR_UNSUPPORTED;
@@ -154,7 +155,7 @@ int pi_attn_decode_paged(const void *q, long long q_stride, const pi_attn_cache_
     if (rc == PI_OK) rc = make_attention(a.cache, H, k_local, period, S, mode, alpha, a.s);
     if (rc != PI_OK) return rc;
     if (B <= 0) return PI_ERR_SHAPE;
-    if (H / cache->Hkv > 16 || B > 65535 || cache->Hkv > 65535) return PI_ERR_UNSUPPORTED;
+    if (H / cache->Hkv > 16 || B > 65535) return PI_ERR_UNSUPPORTED;
     rc = check_stride(q_stride, H, cache->d);
     if (rc != PI_OK) return rc;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || (alpha && !aligned(alpha, 4)) || !aligned(table, 4) ||

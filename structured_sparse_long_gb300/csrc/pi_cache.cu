@@ -128,9 +128,18 @@ __device__ __forceinline__ void locate_run(const PagedCache &c, const PagedBatch
     }
 }
 
+// The warp's token (or run of tokens) and its 32 pieces of it; a token's warps are neighbours.
+template <typename A>
+__device__ __forceinline__ int token_of(const A &a, int &chunk) {
+    const unsigned w = blockIdx.x * WARPS + (threadIdx.x >> 5), t = w / (unsigned)a.chunks;
+    chunk = (int)(w - t * (unsigned)a.chunks);
+    return (int)t;
+}
+
 template <int KV, int TOK>
 __global__ void __launch_bounds__(WARPS * 32) append_kernel(const AppendArgs a) {
-    const int t = (blockIdx.x * WARPS + (threadIdx.x >> 5)) * TOK, lane = threadIdx.x & 31;
+    int chunk;
+    const int t = token_of(a, chunk) * TOK, lane = threadIdx.x & 31;
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (t >= a.batch.T) return;
@@ -152,65 +161,47 @@ __global__ void __launch_bounds__(WARPS * 32) append_kernel(const AppendArgs a) 
             }
         }
     };
-    load(lane);
+    const int j = chunk * 32 + lane, col = j * E & (c.d - 1), head = j * E >> c.d_log2;
+    load(j);
     int pos, pg;
     locate_run<TOK>(c, a.batch, t, pos, pg, a.index_word);
-    for (int j0 = 0;;) {
-        const int j = j0 + lane, col = j * E & (c.d - 1), head = j * E >> c.d_log2;
 #pragma unroll
-        for (int i = 0; i < TOK; ++i) {
-            const int p = __shfl_sync(kFull, pos, i), g = __shfl_sync(kFull, pg, i);
-            const long long row = row_in_page(c, g, head, p);
-            put<KV>(c, c.k, c.k_scale, k[i], row, col, j < n && g >= 0);
-            put<KV>(c, c.v, c.v_scale, v[i], row, col, j < n && g >= 0);
-        }
-        j0 += 32;
-        if (j0 >= n) break;
-        load(j0 + lane);
+    for (int i = 0; i < TOK; ++i) {
+        const int p = __shfl_sync(kFull, pos, i), g = __shfl_sync(kFull, pg, i);
+        const long long row = row_in_page(c, g, head, p);
+        put<KV>(c, c.k, c.k_scale, k[i], row, col, j < n && g >= 0);
+        put<KV>(c, c.v, c.v_scale, v[i], row, col, j < n && g >= 0);
     }
 }
 
-template <int KV>
+template <int KV, int TOK>
 __global__ void __launch_bounds__(WARPS * 32) read_kernel(const ReadArgs a) {
-    const int t = blockIdx.x * WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    int chunk;
+    const int t = token_of(a, chunk) * TOK, lane = threadIdx.x & 31;
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (t >= a.batch.T) return;
     const PagedCache &c = a.cache;
     const int n = c.Hkv << (c.d_log2 - 3);  // groups of eight elements
-    int b;
-    const int pos = locate(c, a.batch, t, b, a.index_word);
-    if (pos < 0) return;
-    const int pg = page_of(c, a.batch.table, b, pos);
-    if (pg < 0) {
-        record_index(a.index_word);
-        return;
-    }
-    uint4 *ok = reinterpret_cast<uint4 *>(a.k) + (long long)t * n, *ov = reinterpret_cast<uint4 *>(a.v) + (long long)t * n;
-    constexpr int PRE = 2;  // groups per lane and tensor in flight (more cost registers, and warps with them: 4 take 7.3 us, 2 6.6)
-    for (int j0 = lane; j0 - lane < n; j0 += 32 * PRE) {
-        uint4 k[PRE], v[PRE];
-#pragma unroll
-        for (int u = 0; u < PRE; ++u) {
-            const int j = j0 + 32 * u, col = j * 8 & (c.d - 1), head = j >> (c.d_log2 - 3);
-            if (j >= n) continue;
-            const long long row = row_in_page(c, pg, head, pos);
-            k[u] = get8<KV>(c, c.k, c.k_scale, row, col);
-            v[u] = get8<KV>(c, c.v, c.v_scale, row, col);
-        }
-#pragma unroll
-        for (int u = 0; u < PRE; ++u) {
-            const int j = j0 + 32 * u;
-            if (j >= n) continue;
-            ok[j] = k[u];
-            ov[j] = v[u];
-        }
+    int pos, pg;
+    locate_run<TOK>(c, a.batch, t, pos, pg, a.index_word);
+    const int j = chunk * 32 + lane, col = j * 8 & (c.d - 1), head = j >> (c.d_log2 - 3);
+#pragma unroll 2
+    for (int i = 0; i < TOK; ++i) {
+        const int p = __shfl_sync(kFull, pos, i), g = __shfl_sync(kFull, pg, i);
+        if (g < 0 || j >= n) continue;
+        const long long row = row_in_page(c, g, head, p), at = (long long)(t + i) * n + j;
+        const uint4 k = get8<KV>(c, c.k, c.k_scale, row, col), v = get8<KV>(c, c.v, c.v_scale, row, col);
+        reinterpret_cast<uint4 *>(a.k)[at] = k;
+        reinterpret_cast<uint4 *>(a.v)[at] = v;
     }
 }
 
 template <typename K, typename A>
-static cudaError_t launch(K kernel, int tokens, const A &a, cudaStream_t st) {
-    const long long warps = ((long long)a.batch.T + tokens - 1) / tokens;
+static cudaError_t launch(K kernel, int tokens, int piece, A a, cudaStream_t st) {
+    a.chunks = (a.cache.Hkv * a.cache.d / piece + 31) / 32;
+    const long long warps = ((long long)a.batch.T + tokens - 1) / tokens * a.chunks;
+    if (warps > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((warps + WARPS - 1) / WARPS), 1, 1);
     cfg.blockDim = dim3(WARPS * 32, 1, 1);
@@ -231,18 +222,21 @@ cudaError_t launch_append(const AppendArgs &a, cudaStream_t st) {
     // 39.9; rows that stay bf16 gain nothing: 17.5 us with one, 18.2 with two, for 16384 tokens of 12 heads, d = 64)
     const bool two = a.batch.T >= 128 * sm_count();
     switch (a.cache.kv_type) {
-        case kKvBf16: return launch(append_kernel<kKvBf16, 1>, 1, a, st);
-        case kKvE4m3: return two ? launch(append_kernel<kKvE4m3, 2>, 2, a, st) : launch(append_kernel<kKvE4m3, 1>, 1, a, st);
-        default: return two ? launch(append_kernel<kKvInt8, 2>, 2, a, st) : launch(append_kernel<kKvInt8, 1>, 1, a, st);
+        case kKvBf16: return launch(append_kernel<kKvBf16, 1>, 1, 8, a, st);
+        case kKvE4m3: return two ? launch(append_kernel<kKvE4m3, 2>, 2, 16, a, st) : launch(append_kernel<kKvE4m3, 1>, 1, 16, a, st);
+        default: return two ? launch(append_kernel<kKvInt8, 2>, 2, 16, a, st) : launch(append_kernel<kKvInt8, 1>, 1, 16, a, st);
     }
 }
 
 cudaError_t launch_cache_read(const ReadArgs &a, cudaStream_t st) {
     using namespace cache;
+    // four tokens per warp, two of them in flight, once that leaves the SMs full of warps (65536 tokens of 4 e4m3 heads, d = 128:
+    // 35.0 us; one token per warp 38.6, two 35.9, eight 36.4; a tenth as many of 16 int8 heads, d = 64: one 7.2, four 8.4)
+    const bool run = (long long)a.batch.T * a.cache.Hkv * a.cache.d >= (128LL << 10) * sm_count();
     switch (a.cache.kv_type) {
-        case kKvBf16: return launch(read_kernel<kKvBf16>, 1, a, st);
-        case kKvE4m3: return launch(read_kernel<kKvE4m3>, 1, a, st);
-        default: return launch(read_kernel<kKvInt8>, 1, a, st);
+        case kKvBf16: return run ? launch(read_kernel<kKvBf16, 4>, 4, 8, a, st) : launch(read_kernel<kKvBf16, 1>, 1, 8, a, st);
+        case kKvE4m3: return run ? launch(read_kernel<kKvE4m3, 4>, 4, 8, a, st) : launch(read_kernel<kKvE4m3, 1>, 1, 8, a, st);
+        default: return run ? launch(read_kernel<kKvInt8, 4>, 4, 8, a, st) : launch(read_kernel<kKvInt8, 1>, 1, 8, a, st);
     }
 }
 

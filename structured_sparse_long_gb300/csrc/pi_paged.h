@@ -40,6 +40,7 @@ struct AppendArgs {
     PagedCache cache;
     PagedBatch batch;
     int *index_word;
+    int chunks;  // warps per token, set at the launch
 };
 
 struct ReadArgs {
@@ -47,6 +48,7 @@ struct ReadArgs {
     PagedCache cache;
     PagedBatch batch;
     int *index_word;
+    int chunks;
 };
 
 struct ExtendArgs {

@@ -198,6 +198,28 @@ def test_append_of_a_long_call(kv, Hkv, d):
         assert np.array_equal(got.transpose(0, 2, 1, 3)[rest], before.transpose(0, 2, 1, 3)[rest])
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3", "int8"])
+def test_read_of_a_long_call(kv):
+    """Calls long enough for four tokens per warp, across sequences' ends, empty sequences and a bad page."""
+    Hkv, d, n, ctx = 16, 128, [7001, 0, 3990, 1, 1, 2, 33], [5, 0, 16, 3, 0, 7, 15]
+    bt = Batch(ctx, n, Hkv, d, 64, kv, seed=3, extra_tokens=3)
+    k, v = normal(bt.gen, bt.T, Hkv, d), normal(bt.gen, bt.T, Hkv, d)
+    pa.cache_append(k.cuda(), v.cuda(), bt.cache, dev(bt.table), dev(bt.cu), dev(ctx))
+    assert pa.status() == 0
+    table = bt.table.copy()
+    table[2, 30] = -5
+    out = [torch.full((bt.T, Hkv, d), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    pa.cache_read(bt.cache, dev(table), dev(bt.cu), dev(ctx), bt.T, k=out[0], v=out[1])
+    assert pa.status() == ERR_INDEX
+    seq = np.repeat(np.arange(len(n)), n)
+    pos = np.concatenate([c + np.arange(m) for c, m in zip(ctx, n)])
+    kept = np.append(~((seq == 2) & (pos // 64 == 30)), np.zeros(bt.T - len(seq), dtype=bool))
+    for x, got in zip((k, v), out):
+        x, got = x.float().numpy(), got.float().cpu().numpy()
+        want = x[kept] if kv == "bf16" else ref.decode(*ref.encode(x[kept], kv), kv)
+        assert np.array_equal(got[kept], want) and (got[~kept] == 7.0).all()
+
+
 # ------------------------------------------------------------------ attention
 
 EXTEND = [
