@@ -299,6 +299,7 @@ __global__ void __launch_bounds__(CONVERT_WARPS * 32) convert_kernel(const Conve
     const PagedCache &c = a.c;
     const int lane = threadIdx.x & 31;
     constexpr int PER_ROW = D / 8, ITER = CHUNK * PER_ROW / 32;  // pieces of 8 codes (16 bytes of bf16); pieces per lane
+    constexpr int SB = D / kScaleBlock;                          // scale bytes of a row
     const int heads = c.Hkv * 2, items = a.plan[1] * heads, step = gridDim.x * CONVERT_WARPS;
     const int half = c.page < CHUNK ? lane >> 4 : 0;
     // an item's sequence, tile and page (page 16: of the lane's half): requested an item ahead
@@ -326,29 +327,42 @@ __global__ void __launch_bounds__(CONVERT_WARPS * 32) convert_kernel(const Conve
                 record_index(a.index_word);
         }
         const long long sh = (long long)slot * c.Hkv + g;
+        // A tile's 32 rows (page 16: each half's 16) are contiguous: a lane's pieces lie 256 bytes apart, and lane r holds the
+        // scale bytes of row r.
         const uint8_t *codes = static_cast<const uint8_t *>(v ? c.v : c.k), *scales = v ? c.v_scale : c.k_scale;
+        const int p0 = __shfl_sync(0xffffffffu, p_now, 0), p1 = __shfl_sync(0xffffffffu, p_now, 16);
+        const int at = pos & (c.page - 1), at1 = c.page < CHUNK ? -16 : at;  // first row of the second half less 16
+        const uint2 *c0 = reinterpret_cast<const uint2 *>(codes + (long long)row_in_page(c, max(p0, 0), g, at) * D) + lane;
+        const uint2 *c1 = reinterpret_cast<const uint2 *>(codes + (long long)(row_in_page(c, max(p1, 0), g, 0) + at1) * D) + lane;
         uint2 w[ITER];
-        uint32_t sc[ITER];
 #pragma unroll
         for (int u = 0; u < ITER; ++u) {
-            const int piece = u * 32 + lane, r = piece / PER_ROW, col = piece % PER_ROW * 8;
-            const int p = __shfl_sync(0xffffffffu, p_now, c.page < CHUNK && r >= 16 ? 16 : 0);
-            w[u] = make_uint2(0u, 0u);
-            sc[u] = 0u;
-            if (p >= 0) {
-                const long long row = row_in_page(c, p, g, pos + r);
-                w[u] = __ldg(reinterpret_cast<const uint2 *>(codes + row * D + col));
-                sc[u] = __ldg(scales + row * (D / kScaleBlock) + col / kScaleBlock);
-            }
+            const bool in = (u < ITER / 2 ? p0 : p1) >= 0;
+            w[u] = in ? __ldg((u < ITER / 2 ? c0 : c1) + u * 32) : make_uint2(0u, 0u);
         }
-        uint4 *out = reinterpret_cast<uint4 *>((v ? a.v : a.k) + sh * (CHUNK * D));
-#pragma unroll
-        for (int u = 0; u < ITER; ++u) {
-            const Scale2<KV> s2 = scale_same<KV>(sc[u]);
+        uint32_t sc = 0u;
+        const int p = lane < 16 ? p0 : p1;
+        if (p >= 0) {
+            const long long row = row_in_page(c, p, g, 0) + (lane < 16 ? at : at1) + lane;
+            sc = SB == 4 ? __ldg(reinterpret_cast<const uint32_t *>(scales) + row) : __ldg(reinterpret_cast<const uint16_t *>(scales) + row);
+        }
+        uint4 *out = reinterpret_cast<uint4 *>((v ? a.v : a.k) + sh * (CHUNK * D)) + lane;
+        auto piece = [&](const uint2 &x, int u, bool big) {
+            const uint32_t s4 = __shfl_sync(0xffffffffu, sc, u * (32 / PER_ROW) + lane / PER_ROW);
+            const Scale2<KV> s2 = scale_same<KV>(s4 >> (8 * (lane % PER_ROW / 4)) & 0xffu);
             uint4 o;
-            codes_to_bf16<KV>(w[u].x, s2, s2.big, o.x, o.y);
-            codes_to_bf16<KV>(w[u].y, s2, s2.big, o.z, o.w);
-            st_keep(out + u * 32 + lane, o, keep);
+            codes_to_bf16<KV>(x.x, s2, big, o.x, o.y);
+            codes_to_bf16<KV>(x.y, s2, big, o.z, o.w);
+            st_keep(out + u * 32, o, keep);
+        };
+        // e4m3: scales above 2^7 need a second factor (rare)
+        const bool big = KV == kKvE4m3 && __any_sync(0xffffffffu, __vcmpgtu4(sc, 0x86868686u) != 0u);
+        if (!big) {
+#pragma unroll
+            for (int u = 0; u < ITER; ++u) piece(w[u], u, false);
+        } else {
+#pragma unroll
+            for (int u = 0; u < ITER; ++u) piece(w[u], u, true);
         }
     }
 }
