@@ -8,8 +8,8 @@ device; an index out of range is reported by :func:`structured_sparse_long_gb300
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
-import functools
 import importlib.util
 import os
 from typing import Optional
@@ -18,7 +18,7 @@ import torch
 
 from . import _binding
 from . import build as _build
-from ._binding import MODE_ECP, MODE_PI, PI_OK, _check
+from ._binding import MODE_PI, _check
 
 KV_BF16, KV_E4M3, KV_INT8 = 0, 1, 2
 _KV_TYPES = {torch.bfloat16: KV_BF16, torch.float8_e4m3fn: KV_E4M3, torch.int8: KV_INT8}
@@ -127,44 +127,40 @@ class PagedCache:
         return cls(new(dtype, d), new(dtype, d), *((new(torch.uint8, d // SCALE_BLOCK) for _ in range(2)) if quant else ()))
 
 
-def _stream_of(cache, stream):
-    return _raw_stream(cache.index) if stream is None else stream.cuda_stream
-
-
-def _report(name, cache, rc, stream, check):
-    if rc != PI_OK or check:
-        with torch.cuda.device(cache.index):
-            _check(name, rc, stream, check)
-
-
-def _on_its_device(fn):
-    """Runs a call with the cache's device current."""
-    @functools.wraps(fn)
-    def elsewhere(*args, **kwargs):
-        cache = kwargs.get("cache") or next(a for a in args if isinstance(a, PagedCache))
-        with torch.cuda.device(cache.index):
-            return fn(*args, **kwargs)
-    return elsewhere
+@contextlib.contextmanager
+def _place(cache, stream):
+    """The cache's device current and, where a stream is given, that stream: a call's new tensors (outputs, workspace) are then
+    the stream's own, so that none is handed out again while the call still uses it."""
+    if stream is not None and stream.device != cache.device:
+        raise ValueError(f"stream must be on {cache.device}, got {stream.device}")
+    with torch.cuda.device(cache.index):
+        if stream is None:
+            yield
+        else:
+            with torch.cuda.stream(stream):
+                yield
 
 
 def cache_append(k, v, cache: PagedCache, table, cu, ctx, stream=None, check=False) -> None:
     """pi_attn_cache_append: writes the packed rows k, v [T, Hkv, d] bf16 (tokens any stride apart) into the
     pages of their sequences, quantised where the cache holds 8 bits."""
-    if cache.index != _current_device():
-        return _on_its_device(cache_append)(k, v, cache, table, cu, ctx, stream, check)
-    rc = (_native or _load_native()).append(k, v, cache._handle, table, cu, ctx, _stream_of(cache, stream))
+    if stream is not None or cache.index != _current_device():
+        with _place(cache, stream):
+            return cache_append(k, v, cache, table, cu, ctx, None, check)
+    rc = (_native or _load_native()).append(k, v, cache._handle, table, cu, ctx, _raw_stream(cache.index))
     if rc or check:
-        _report("pi_attn_cache_append", cache, rc, stream, check)
+        _check("pi_attn_cache_append", rc, None, check)
 
 
 def cache_read(cache: PagedCache, table, cu, start, rows: int, k=None, v=None, stream=None, check=False):
     """pi_attn_cache_read: rows start[b] .. start[b] + cu[b+1] - cu[b] - 1 of every sequence, packed, as
     bf16 (k, v) [rows, Hkv, d]."""
-    if cache.index != _current_device():
-        return _on_its_device(cache_read)(cache, table, cu, start, rows, k, v, stream, check)
-    rc, k, v = (_native or _load_native()).read(cache._handle, table, cu, start, rows, k, v, _stream_of(cache, stream))
+    if stream is not None or cache.index != _current_device():
+        with _place(cache, stream):
+            return cache_read(cache, table, cu, start, rows, k, v, None, check)
+    rc, k, v = (_native or _load_native()).read(cache._handle, table, cu, start, rows, k, v, _raw_stream(cache.index))
     if rc or check:
-        _report("pi_attn_cache_read", cache, rc, stream, check)
+        _check("pi_attn_cache_read", rc, None, check)
     return k, v
 
 
@@ -179,12 +175,13 @@ def extend(q, cache: PagedCache, table, cu, ctx, alpha, k_local: int, period: in
            out=None, lse=None, workspace=None, stream=None, check=False):
     """pi_attn_extend: the packed new tokens q [T, H, d] bf16 (any token stride) against their sequences' cached
     rows, which hold the chunk's own already.  alpha [T, H] fp32 (None in ECP mode).  Returns (out, lse)."""
-    if cache.index != _current_device():
-        return _on_its_device(extend)(q, cache, table, cu, ctx, alpha, k_local, period, S, mode, out, lse, workspace, stream, check)
+    if stream is not None or cache.index != _current_device():
+        with _place(cache, stream):
+            return extend(q, cache, table, cu, ctx, alpha, k_local, period, S, mode, out, lse, workspace, None, check)
     rc, out, lse = (_native or _load_native()).extend(q, cache._handle, table, cu, ctx, alpha, k_local, period, S, mode, out, lse,
-                                                      workspace, _stream_of(cache, stream))
+                                                      workspace, _raw_stream(cache.index))
     if rc or check:
-        _report("pi_attn_extend", cache, rc, stream, check)
+        _check("pi_attn_extend", rc, None, check)
     return out, lse
 
 
@@ -192,10 +189,11 @@ def decode_paged(q, cache: PagedCache, table, lens, alpha, k_local: int, period:
                  out=None, lse=None, stream=None, check=False):
     """pi_attn_decode_paged: one new token per sequence, q [B, H, d] bf16, against lens[b] cached rows (its own
     among them).  alpha [B, H] fp32 (None in ECP mode).  Returns (out [B, H, d], lse [B, H])."""
-    if cache.index != _current_device():
-        return _on_its_device(decode_paged)(q, cache, table, lens, alpha, k_local, period, S, mode, out, lse, stream, check)
+    if stream is not None or cache.index != _current_device():
+        with _place(cache, stream):
+            return decode_paged(q, cache, table, lens, alpha, k_local, period, S, mode, out, lse, None, check)
     rc, out, lse = (_native or _load_native()).decode(q, cache._handle, table, lens, alpha, k_local, period, S, mode, out, lse,
-                                                      _stream_of(cache, stream))
+                                                      _raw_stream(cache.index))
     if rc or check:
-        _report("pi_attn_decode_paged", cache, rc, stream, check)
+        _check("pi_attn_decode_paged", rc, None, check)
     return out, lse

@@ -540,22 +540,52 @@ def test_captured_step_follows_its_inputs(T, sizes):
     assert pa.status() == 0
 
 
-def test_streams_run_side_by_side():
-    """Two streams with their own tensors and a common cache give what one stream gives."""
-    bt = Batch([300, 200], [364, 240], 2, 128, 64, "e4m3", seed=13)
+@pytest.mark.parametrize("n", [[364, 240], [3, 5]])
+def test_streams_run_side_by_side(n):
+    """Calls on two streams at once, each with inputs of its own, new outputs and (long chunks) a workspace made in the call:
+    what each alone gives."""
+    bt = Batch([300, 200], n, 2, 128, 64, "e4m3", seed=13)
     bt.write()
-    q, a = normal(bt.gen, bt.T, 8, 128).cuda(), torch.rand(bt.T, 8, generator=bt.gen).cuda()
-    table, cu, ctx = dev(bt.table), dev(bt.cu), dev(bt.ctx)
-    want = pa.extend(q, bt.cache, table, cu, ctx, a, 100, 64, 3)
+    sets = [(normal(bt.gen, bt.T, 8, 128).cuda(), torch.rand(bt.T, 8, generator=bt.gen).cuda()) for _ in range(2)]
+    table, cu, ctx, lens = dev(bt.table), dev(bt.cu), dev(bt.ctx), dev(np.add(bt.ctx, n))
+    calls = [lambda q, a, **kw: pa.extend(q, bt.cache, table, cu, ctx, a, 100, 64, 3, **kw),
+             lambda q, a, **kw: pa.decode_paged(q[:2], bt.cache, table, lens, a[:2], 100, 64, 3, **kw)]
+    want = [[call(*x) for call in calls] for x in sets]
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in range(2)]
-    outs = [(torch.empty_like(want[0]), torch.empty_like(want[1])) for _ in range(2)]
+    got = [[], []]
     for _ in range(10):
-        for st, (o, ls) in zip(streams, outs):
-            pa.extend(q, bt.cache, table, cu, ctx, a, 100, 64, 3, out=o, lse=ls, stream=st)
+        for i, st in enumerate(streams):
+            got[i].append([call(*sets[i], stream=st) for call in calls])
     torch.cuda.synchronize()
-    for o, ls in outs:
-        assert torch.equal(o, want[0]) and torch.equal(ls, want[1])
+    for i in range(2):
+        for results in got[i]:
+            for (o, ls), (wo, wl) in zip(results, want[i]):
+                assert torch.equal(o, wo) and torch.equal(ls, wl)
+    assert pa.status() == 0
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_many_sequences(kv):
+    """More sequences than the plan takes in one round, empty ones among them, through the long chunks' kernels; and through
+    the short ones'."""
+    rng, B, H, Hkv, d = np.random.default_rng(8), 600, 16, 4, 64
+    for n in (rng.integers(0, 30, B), rng.integers(0, 3, B)):
+        n[100:140] = 0
+        ctx = rng.integers(0, 50, B)
+        case = ("", kv, H, Hkv, d, 16, list(ctx), list(n), 20, 32, 2, PI)
+        assert few_rows(case) == (n.max() < 3)
+        bt = Batch(list(ctx), list(n), Hkv, d, 16, kv, seed=9, extra_tokens=2)
+        whole = np.add(ctx, n)
+        k, v = (torch.cat([x for x in xs if len(x)]).cuda() for xs in (bt.k, bt.v))
+        pa.cache_append(k, v, bt.cache, dev(bt.table), dev(ref.offsets(whole)), dev(np.zeros(B)))
+        q, a = normal(bt.gen, bt.T, H, d), torch.rand(bt.T, H, generator=bt.gen)
+        out, lse = pa.extend(q.cuda(), bt.cache, dev(bt.table), dev(bt.cu), dev(ctx), a.cuda(), 20, 32, 2)
+        assert pa.status() == 0
+        K, V = bt.held()
+        for b in np.concatenate([np.flatnonzero(n)[::9], np.flatnonzero(n)[-3:]]):
+            t = slice(bt.cu[b], bt.cu[b + 1])
+            ref.check_attention(f"sequence {b}", out[t], lse[t], ref.attention(q[t], K[b], V[b], a[t], ctx[b], 20, 32, 2, PI))
 
 
 def test_offsets_past_32_bits():
