@@ -8,9 +8,9 @@
 // How: the forward's pipeline (128 query rows = GP heads of one KV group x R consecutive positions as the M of
 // every MMA, 32-key tiles, Q and P as TMEM operands, S and O accumulated in TMEM, one softmax thread
 // per row, two persistent CTAs per SM), with what a batch of ragged, paged sequences asks for:
-//   * A plan kernel turns the batch's offsets and contexts into a list of position blocks; it and the
-//     checks run on the device, so that a captured graph follows its inputs.  The attention kernel starts
-//     beside it (programmatic launch) and waits for it once its barriers and TMEM are set up.
+//   * A plan kernel (over 8-bit caches the converting one, see below) turns the batch's offsets and contexts into a list of
+//     position blocks; it and the checks run on the device, so that a captured graph follows its inputs.  The attention
+//     kernel starts beside it (programmatic launch) and waits for it once its barriers and TMEM are set up.
 //   * A sequence's blocks lie on multiples of R positions (a chunk of at most R tokens is one block where it
 //     starts), and key tiles on multiples of 32, so that a tile lies inside one page (page 16: two) and is one
 //     TMA box per 64 columns.  With period % 32 = 0 a skip window falls on whole tiles too; any other
@@ -28,6 +28,8 @@
 //     put so much into the SM's instruction stream that a 65536-token chunk (16 heads on 4, d = 128, band 256,
 //     4 skips of 1024) took 480-640 us against 250 us of the bf16 cache.
 #include <cuda.h>
+
+#include <type_traits>
 
 #include "pi_launch.h"
 #include "pi_mma.cuh"
@@ -99,6 +101,15 @@ __host__ __device__ __forceinline__ SeqTiles seq_tiles(const Shape &s, int m_fir
     return q;
 }
 
+// The tile in a sequence's slot `place` (negative: none).
+__device__ __forceinline__ int slot_tile(const Shape &s, int m_first, const SeqTiles &q, int n, int ctx, int place) {
+    if (!q.band_tiles || place < q.band_tiles) return q.lo + place;
+    const int w = (place - q.band_tiles) / q.per_window, back = (m_first + w) * s.period;
+    const int tile = ((ctx - back) >> 5) + (place - q.band_tiles) % q.per_window;
+    // the window's last tile may lie past it, and a whole tile before the sequence
+    return tile > (ctx + n - 1 - back) >> 5 ? -1 : tile;
+}
+
 // Most slots that a batch can take, from its sizes alone (cap: positions a page table reaches).
 static long long most_slots(const Shape &s, long long B, long long T, long long cap) {
     const long long seqs = std::min(B, T);
@@ -153,7 +164,8 @@ __device__ __forceinline__ PlanBlock plan_block(const PlanArgs &a, int b, int t0
     return k;
 }
 
-__global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PlanArgs a) {
+// What CTA `part` of PLAN_CTAS does for the plan.
+__device__ __forceinline__ void make_plan(const PlanArgs &a, int part) {
     const PagedCache &c = a.c;
     const PagedBatch &bt = a.bt;
     const int R = a.R;
@@ -161,14 +173,13 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PlanArgs a) {
     __shared__ int upto[PLAN_THREADS];  // blocks of the round's sequences up to and including each
     __shared__ int slots_upto[PLAN_THREADS];
     __shared__ int warp_sum[PLAN_THREADS / 32];
-    asm volatile("griddepcontrol.launch_dependents;");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     PlanBlock *blocks = reinterpret_cast<PlanBlock *>(reinterpret_cast<char *>(plan) + PLAN_HEAD);
     // Offsets that decrease would let sequences overlap and their blocks outgrow the plan: nothing is planned.
     bool sorted = true;
     for (int b = tid; b < bt.B; b += PLAN_THREADS) sorted = sorted && bt.cu[b] <= bt.cu[b + 1];
     if (!__syncthreads_and(sorted)) {
-        if (tid == 0 && blockIdx.x == 0) {
+        if (tid == 0 && part == 0) {
             record_index(index_word);
             plan[0] = plan[1] = 0;
         }
@@ -217,7 +228,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PlanArgs a) {
         }
         const int total = scan(cnt, upto);
         const int total_slots = a.slots ? scan(slots, slots_upto) : 0;
-        for (int x = blockIdx.x * PLAN_THREADS + tid; x < total; x += PLAN_CTAS * PLAN_THREADS) {
+        for (int x = part * PLAN_THREADS + tid; x < total; x += PLAN_CTAS * PLAN_THREADS) {
             int place;
             const int o = owner(upto, x, place);
             const int t0 = bt.cu[b0 + o], n = bt.cu[b0 + o + 1] - t0, ctx = bt.ctx[b0 + o];
@@ -235,40 +246,33 @@ __global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PlanArgs a) {
                 blocks[base + x].per_window = q.per_window;
             }
         }
-        for (int x = blockIdx.x * PLAN_THREADS + tid; x < total_slots; x += PLAN_CTAS * PLAN_THREADS) {
+        for (int x = part * PLAN_THREADS + tid; x < total_slots; x += PLAN_CTAS * PLAN_THREADS) {
             int place;
             const int o = owner(slots_upto, x, place);
             const int n = bt.cu[b0 + o + 1] - bt.cu[b0 + o], ctx = bt.ctx[b0 + o];
             const SeqTiles q = seq_tiles(a.s, a.m_first, n, ctx);
-            int tile = q.lo + place;
-            if (q.band_tiles && place >= q.band_tiles) {
-                const int w = (place - q.band_tiles) / q.per_window;
-                tile = ((ctx - (a.m_first + w) * a.s.period) >> 5) + (place - q.band_tiles) % q.per_window;
-                // the window's last tile may lie past it, and a whole tile before the sequence
-                if (tile > (ctx + n - 1 - (a.m_first + w) * a.s.period) >> 5) tile = -1;
-            }
-            a.slots[slot_base + x] = make_int2(b0 + o, tile);
+            a.slots[slot_base + x] = make_int2(b0 + o, slot_tile(a.s, a.m_first, q, n, ctx, place));
         }
         base += total;
         slot_base += total_slots;
     }
-    if (tid == 0 && blockIdx.x == 0) {
+    if (tid == 0 && part == 0) {
         plan[0] = base;
         plan[1] = slot_base;
     }
 }
 
+__global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PlanArgs a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;");
+    make_plan(a, blockIdx.x);
+}
+
 // ------------------------------------------------------------------ 8-bit tiles to bf16
 
 struct ConvertArgs {
-    Shape s;
-    PagedCache c;
-    PagedBatch bt;
-    int m_first;
-    const int *plan;
-    const int2 *slots;
+    PlanArgs p;
     __nv_bfloat16 *k, *v;  // [slots, Hkv, 32, d]
-    int *index_word;
 };
 
 constexpr int CONVERT_WARPS = 8;
@@ -280,7 +284,7 @@ __device__ __forceinline__ void st_keep(uint4 *p, const uint4 &x, uint64_t polic
 }
 
 // Whether some query of the chunk attends a key in x .. y of its sequence.
-__device__ __forceinline__ bool attended(const ConvertArgs &a, int b, int x, int y) {
+__device__ __forceinline__ bool attended(const PlanArgs &a, int b, int x, int y) {
     const int t0 = a.bt.cu[b], n = a.bt.cu[b + 1] - t0, ctx = a.bt.ctx[b], last = ctx + n - 1;
     if (y >= band_lo(ctx, a.s.mode, a.s.k_local) && x <= last) return true;
     if (a.s.mode == kModeEcp || a.s.S == 0 || x > last) return false;
@@ -292,23 +296,60 @@ __device__ __forceinline__ bool attended(const ConvertArgs &a, int b, int x, int
 
 // One warp per (slot, KV head, K or V): 32 rows of codes, all of them in flight at once, to 32 rows of bf16.  Rows of a page
 // out of range become zeros.
-template <int D, int KV>
-__global__ void __launch_bounds__(CONVERT_WARPS * 32) convert_kernel(const ConvertArgs a) {
+// LANES (at most 32 sequences): the kernel makes the plan too, in its first CTAs, and the others find their slots' sequences
+// themselves, one sequence to a lane, instead of waiting for a plan kernel.
+template <int D, int KV, bool LANES>
+__global__ void __launch_bounds__(CONVERT_WARPS * 32) convert_kernel(const ConvertArgs args) {
+    const PlanArgs &a = args.p;
+    static_assert(CONVERT_WARPS * 32 == PLAN_THREADS, "a CTA of the plan");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan is written
+    if (LANES && blockIdx.x < PLAN_CTAS) {
+        make_plan(a, blockIdx.x);
+        return;
+    }
+    const int cta = blockIdx.x - (LANES ? PLAN_CTAS : 0), ctas = gridDim.x - (LANES ? PLAN_CTAS : 0);
     const PagedCache &c = a.c;
     const int lane = threadIdx.x & 31;
     constexpr int PER_ROW = D / 8, ITER = CHUNK * PER_ROW / 32;  // pieces of 8 codes (16 bytes of bf16); pieces per lane
     constexpr int SB = D / kScaleBlock;                          // scale bytes of a row
-    const int heads = c.Hkv * 2, items = a.plan[1] * heads, step = gridDim.x * CONVERT_WARPS;
+    // LANES: sequence `lane`, its slots up to and including its own, and the tiles in them
+    int n = 0, ctx = 0, upto = 0;
+    SeqTiles q{};
+    if (LANES) {
+        bool sorted = true;
+        if (lane < a.bt.B) {
+            const int t0 = a.bt.cu[lane], t1 = a.bt.cu[lane + 1];
+            ctx = a.bt.ctx[lane];
+            sorted = t0 <= t1;
+            if (sequence_ok(c, a.bt, t0, t1, ctx)) n = t1 - t0;  // the plan records what is out of range
+        }
+        if (!__all_sync(0xffffffffu, sorted)) return;
+        if (n > 0) q = seq_tiles(a.s, a.m_first, n, ctx);
+        upto = q.slots;
+#pragma unroll
+        for (int w = 1; w < 32; w <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, upto, w);
+            if (lane >= w) upto += y;
+        }
+    }
+    const int heads = c.Hkv * 2, items = (LANES ? __shfl_sync(0xffffffffu, upto, 31) : a.plan[1]) * heads, step = ctas * CONVERT_WARPS;
     const int half = c.page < CHUNK ? lane >> 4 : 0;
     // an item's sequence, tile and page (page 16: of the lane's half): requested an item ahead
-    auto slot_of = [&](int x) -> int2 { return x < items ? __ldg(a.slots + x / heads) : make_int2(0, -1); };
+    auto slot_of = [&](int x) -> int2 {
+        if (x >= items) return make_int2(0, -1);
+        const int slot = x / heads;
+        if (!LANES) return __ldg(a.slots + slot);
+        const int b = __ffs(__ballot_sync(0xffffffffu, upto > slot)) - 1;
+        auto of = [&](int y) { return __shfl_sync(0xffffffffu, y, b); };
+        const SeqTiles qb{of(q.lo), of(q.band_tiles), of(q.per_window), of(q.slots)};
+        return make_int2(b, slot_tile(a.s, a.m_first, qb, of(n), of(ctx), slot - of(upto) + qb.slots));
+    };
     auto page = [&](int2 st) -> int {
         const int pos = st.y * CHUNK + half * 16;
         return st.y >= 0 && pos < c.width << c.page_log2 ? __ldg(a.bt.table + (long long)st.x * c.width + (pos >> c.page_log2)) : -1;
     };
-    int x = blockIdx.x * CONVERT_WARPS + (threadIdx.x >> 5);
+    int x = cta * CONVERT_WARPS + (threadIdx.x >> 5);
     int2 st = slot_of(x), st_next = slot_of(x + step);
     int pg = page(st);
     uint64_t keep;  // the tiles are read again soon, by the attention kernel
@@ -346,7 +387,7 @@ __global__ void __launch_bounds__(CONVERT_WARPS * 32) convert_kernel(const Conve
             const long long row = row_in_page(c, p, g, 0) + (lane < 16 ? at : at1) + lane;
             sc = SB == 4 ? __ldg(reinterpret_cast<const uint32_t *>(scales) + row) : __ldg(reinterpret_cast<const uint16_t *>(scales) + row);
         }
-        uint4 *out = reinterpret_cast<uint4 *>((v ? a.v : a.k) + sh * (CHUNK * D)) + lane;
+        uint4 *out = reinterpret_cast<uint4 *>((v ? args.v : args.k) + sh * (CHUNK * D)) + lane;
         auto piece = [&](const uint2 &x, int u, bool big) {
             const uint32_t s4 = __shfl_sync(0xffffffffu, sc, u * (32 / PER_ROW) + lane / PER_ROW);
             const Scale2<KV> s2 = scale_same<KV>(s4 >> (8 * (lane % PER_ROW / 4)) & 0xffu);
@@ -1097,17 +1138,24 @@ cudaError_t launch_extend(const ExtendArgs &e, cudaStream_t st) {
     Args a{e, e.workspace, GP, R, R == 32 ? 5 : R == 64 ? 6 : 7, ngrp, skips ? first_skip_multiple(s) : 1,
            skips && s.period % CHUNK == 0, quant ? CHUNK : std::min(CHUNK, c.page), quant ? (int)l.n_slots : c.n_pages,
            make_fastdiv(ngrp), make_fastdiv(G)};
-    plan_kernel<<<PLAN_CTAS, PLAN_THREADS, 0, st>>>(PlanArgs{s, c, e.batch, R, a.m_first, a.aligned, e.workspace, e.index_word, slots});
-    cudaError_t err = cudaGetLastError();
-    if (err != cudaSuccess) return err;
+    const PlanArgs pa{s, c, e.batch, R, a.m_first, a.aligned, e.workspace, e.index_word, slots};
+    cudaError_t err = cudaSuccess;
+    const bool lanes = e.batch.B <= 32;
+    if (!quant || !lanes) {
+        err = launch_dependent(plan_kernel, PLAN_CTAS, PLAN_THREADS, 0, st, pa);
+        if (err != cudaSuccess) return err;
+    }
     if (!quant) return s.d == 64 ? launch<64, false>(a, c.k, c.v, st) : launch<128, false>(a, c.k, c.v, st);
     __nv_bfloat16 *k = reinterpret_cast<__nv_bfloat16 *>(ws + l.k), *v = reinterpret_cast<__nv_bfloat16 *>(ws + l.v);
-    const ConvertArgs ca{s, c, e.batch, a.m_first, e.workspace, slots, k, v, e.index_word};
     const long long items = l.n_slots * s.Hkv * 2;
     const long long grid = std::min<long long>((items + CONVERT_WARPS - 1) / CONVERT_WARPS, 4LL * pi::sm_count());
-    auto convert = s.d == 64 ? (c.kv_type == kKvE4m3 ? convert_kernel<64, kKvE4m3> : convert_kernel<64, kKvInt8>)
-                             : (c.kv_type == kKvE4m3 ? convert_kernel<128, kKvE4m3> : convert_kernel<128, kKvInt8>);
-    err = launch_dependent(convert, grid, CONVERT_WARPS * 32, 0, st, ca);
+    auto convert = [&](auto in_lanes) {
+        constexpr bool L = decltype(in_lanes)::value;
+        auto kernel = s.d == 64 ? (c.kv_type == kKvE4m3 ? convert_kernel<64, kKvE4m3, L> : convert_kernel<64, kKvInt8, L>)
+                                : (c.kv_type == kKvE4m3 ? convert_kernel<128, kKvE4m3, L> : convert_kernel<128, kKvInt8, L>);
+        return launch_dependent(kernel, grid + (L ? PLAN_CTAS : 0), CONVERT_WARPS * 32, 0, st, ConvertArgs{pa, k, v});
+    };
+    err = lanes ? convert(std::true_type{}) : convert(std::false_type{});
     if (err != cudaSuccess) return err;
     return s.d == 64 ? launch<64, true>(a, k, v, st) : launch<128, true>(a, k, v, st);
 }
