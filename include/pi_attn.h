@@ -292,7 +292,8 @@ int pi_attn_decode(const void *q, const void *k_cache, const void *v_cache, cons
  *   (e4m3) or 127 (int8); codes are rounded to nearest even.  Reading multiplies the
  *   code by the scale, which bf16 holds exactly (a code that was rounded up to 2^128 or
  *   more, which only an element above 0.96 * 2^128 can be, reads as an infinity).  A
- *   block with an infinity or a NaN gets s = 255 and reads back as NaN.
+ *   block with an infinity or a NaN gets s = 255 and reads back as NaN.  The two e4m3 codes that are
+ *   NaN themselves are not written; pages filled by other means must not hold them.
  *   d: 64 or 128; page: 16, 32, 64, 128 or 256 rows; Hkv <= 65535; n_pages * Hkv * page < 2^31;
  *   all four pointers 16-byte aligned.
  *
@@ -352,9 +353,8 @@ int pi_attn_cache_read(const pi_attn_cache_t *cache, const pi_attn_batch_t *batc
  *   lse [T, H] fp32, contiguous.  H % Hkv == 0; T * H < 2^31.
  *   A sequence with an offset or length out of range is left out, its rows of out and lse
  *   as they were (where cu decreases anywhere, any of the batch's rows may be); a row that attends a key on a page out of range is undefined.
- *   Non-finite values in cache rows that no query of the chunk attends do not matter;
- *   a non-finite value in a row that some query attends may reach the outputs of the
- *   sequence's other queries within 128 positions.
+ *   A token's results depend on the rows that it attends alone: what the other rows hold, NaN
+ *   and infinities among it, does not matter.
  *   workspace: device buffer of at least pi_attn_extend_workspace_size() bytes for these
  *   sizes (none for short chunks: it may be NULL then), 256-byte aligned, owned by the caller, contents ignored on entry; calls that may
  *   overlap need one each.  It holds the call's plan (about 2.5 T + 160 B bytes) and, for an

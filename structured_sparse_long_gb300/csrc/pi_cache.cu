@@ -87,22 +87,6 @@ __device__ __forceinline__ void put(const PagedCache &c, void *pages, uint8_t *s
     }
 }
 
-// Eight elements of a cache row as bf16.  (16 per lane would be wider loads, but each of a lane's two 16-byte stores would then
-// fill half of its 32-byte sectors: 46.6 us where this takes 38.5, for 65536 tokens of 4 e4m3 heads, d = 128.)
-template <int KV>
-__device__ __forceinline__ uint4 get8(const PagedCache &c, const void *pages, const uint8_t *scales, long long row, int col) {
-    if constexpr (KV == kKvBf16) {
-        return __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(pages) + row * c.d + col));
-    } else {
-        const uint2 w = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(pages) + row * c.d + col));
-        const Scale2<KV> s = scale_same<KV>(__ldg(scales + row * (c.d / kScaleBlock) + col / kScaleBlock));
-        uint4 x;
-        codes_to_bf16<KV>(w.x, s, s.big, x.x, x.y);
-        codes_to_bf16<KV>(w.y, s, s.big, x.z, x.w);
-        return x;
-    }
-}
-
 // Position and page of packed tokens t .. t + TOK - 1, in lanes 0 .. TOK - 1 (page -1: the token has no row).
 template <int TOK>
 __device__ __forceinline__ void locate_run(const PagedCache &c, const PagedBatch &bt, int t, int &pos, int &pg, int *index_word) {

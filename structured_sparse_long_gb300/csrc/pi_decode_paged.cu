@@ -24,6 +24,7 @@
 // loads (length, page table, rows) for small batches and by HBM for large ones.
 #include "pi_mma.cuh"
 #include "pi_paged.cuh"
+#include "pi_row.cuh"
 
 #include "pi_launch.h"
 
@@ -202,10 +203,20 @@ __device__ __forceinline__ void accumulate(const Frag<D, KV> &f, const uint32_t 
 constexpr int sm_warps(int D, int KV, int NH) { return NH == 2 ? 8 : D == 128 && KV == kKvBf16 ? 12 : 16; }
 constexpr int max_warps(int D, int KV, int NH) { return sm_warps(D, KV, NH) / (NH == 2 ? 1 : 2); }
 
+// 64 columns of the row of token at / H and head at % H, position i of sequence b (pi_row.cuh).
+template <int D, int KV>
+__device__ __noinline__ void again(const Args &a, int b, int i, int kvh, int at, int col0) {
+    const int tok = at / a.s.H;
+    row_columns<D, KV, 64>(a.cache,
+                       row_keys(a.s, i, kvh, a.m_first, a.q + tok * a.q_stride + (at - tok * a.s.H) * D,
+                                a.batch.table + (long long)b * a.cache.width, a.alpha ? a.alpha + at : nullptr),
+                       col0, a.out + (long long)at * D);
+}
+
 // NH: groups of 8 columns (1 or 2), a column being one query head of one token
 template <int D, int KV, int NH, bool TOKENS>
 __global__ void __launch_bounds__(max_warps(D, KV, NH) * 32, sm_warps(D, KV, NH) / max_warps(D, KV, NH))
-paged_rows_kernel(const Args a) {
+paged_rows_kernel(const __grid_constant__ Args a) {
     const Shape &s = a.s;
     const PagedCache &c = a.cache;
     constexpr int MAX_W = max_warps(D, KV, NH);
@@ -388,11 +399,21 @@ paged_rows_kernel(const Args a) {
     __syncthreads();
 
     // merge of `n` states, state x at address at(x), for columns col, col + 1 of the head
+    // (a warp holds 64 columns of one row)
     auto finish = [&](int x, int col, float mt, float lt, float x0, float x1) {
-        const float inv = lt > 0.f ? 1.f / lt : 0.f;
+        const float inv = lt == 0.f ? 0.f : 1.f / lt;
         const long long at = row_of(x);
-        *reinterpret_cast<uint32_t *>(a.out + at * D + col) = pack_bf16x2(x0 * inv, x1 * inv);
-        if (col == 0) a.lse[at] = lt > 0.f ? (mt + log2f(lt)) * kLn2 : -INFINITY;
+        const uint32_t pair = pack_bf16x2(x0 * inv, x1 * inv);
+        if (col == 0) a.lse[at] = lt == 0.f ? -INFINITY : (mt + log2f(lt)) * kLn2;
+        if constexpr (TOKENS) {  // a value of another token's key may have made the row non-finite (pi_row.cuh)
+            uint32_t seen = 0u;
+            watch(seen, pair);
+            if (__any_sync(kFull, went_bad(seen) && lt == lt)) {
+                again<D, KV>(a, b, first + x / G, kvh, (int)at, col - 2 * lane);
+                return;
+            }
+        }
+        *reinterpret_cast<uint32_t *>(a.out + at * D + col) = pair;
     };
     const int pairs = cols * (D / 2);
     for (int w = threadIdx.x; w < pairs; w += blockDim.x) {

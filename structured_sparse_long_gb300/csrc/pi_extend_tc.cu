@@ -21,7 +21,8 @@
 //     its output goes from registers to the valid rows only, a full block's through shared memory and TMA.
 //   * Rows of V that no query of the block attends may hold anything (evicted or unwritten rows, NaN among them):
 //     they are zeroed in shared memory before the product, since 0 * NaN is not 0.  Scores of K rows outside
-//     a row's range are replaced before they are used.
+//     a row's range are replaced before they are used.  Where a row that some of the block's queries attend holds a
+//     non-finite value, the others' products are NaN too: such output rows are computed again (pi_row.cuh).
 //   * 8-bit caches: the 32-key tiles that the chunk attends are first turned into bf16 tiles in the workspace (exact,
 //     see pi_paged.cuh), which the same kernel then reads instead of pages.  A key tile serves up to a dozen blocks,
 //     and each of them converting its own (four converter warps per CTA between a ring of raw tiles and the pipeline)
@@ -34,6 +35,7 @@
 #include "pi_launch.h"
 #include "pi_mma.cuh"
 #include "pi_paged.cuh"
+#include "pi_row.cuh"
 #include "pi_tc_ptx.cuh"
 #include "pi_tile.cuh"
 
@@ -290,7 +292,7 @@ __device__ __forceinline__ bool attended(const PlanArgs &a, int b, int x, int y)
     if (a.s.mode == kModeEcp || a.s.S == 0 || x > last) return false;
     // a window's keys are ctx - m * period .. last - m * period
     const int m_hi = min(a.s.S, (last - x) / a.s.period);
-    const int m_lo = max(a.m_first, ctx > y ? (ctx - y + a.s.period - 1) / a.s.period : 0);
+    const int m_lo = max(a.m_first, ctx > y ? (ctx - y - 1) / a.s.period + 1 : 0);
     return m_lo <= m_hi;
 }
 
@@ -520,13 +522,45 @@ __device__ __forceinline__ int tile_range(const Args &a, const PlanBlock &k, int
     return key0;
 }
 
+// The non-finite rows of the CTA's blocks, each by a warp.
+template <int D, bool CONVERTED>
+__device__ __noinline__ void again(const Args &args, int L0, int n_blocks) {
+    const ExtendArgs &ea = args.a;
+    const Shape &s = ea.s;
+    const PagedCache &cache = ea.cache;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, LS = gridDim.x;
+    for (int L = L0; L < n_blocks; L = L < n_blocks - LS ? L + LS : n_blocks) {
+        Block k;
+        load_block<false>(args, L, k);
+#pragma unroll 1
+        for (int r = warp; r < BM; r += THREADS / 32) {
+            const int t = r & (args.R - 1), i = k.p0 + t, h = k.h0 + (r >> args.R_log2);
+            if (i < k.first || i > k.last) continue;
+            const long long row = (long long)(k.tq + t) * s.H + h;
+            __nv_bfloat16 *out = ea.out + row * D;
+            uint32_t seen[4] = {};
+            if (lane < D / 8) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(out + 8 * lane);
+                watch(seen, x);
+            }
+            const float lse = ea.lse[row];
+            if (!__any_sync(0xffffffffu, went_bad(seen)) || lse != lse) continue;  // (a NaN among the row's own scores)
+            const RowKeys keys = row_keys(s, i, k.g, args.m_first, ea.q + (long long)(k.tq + t) * ea.q_stride + (long long)h * D,
+                                          ea.batch.table + (long long)k.b * cache.width, ea.alpha ? ea.alpha + row : nullptr);
+            if (!CONVERTED) row_columns<D, kKvBf16, D>(cache, keys, 0, out);
+            else if (cache.kv_type == kKvE4m3) row_columns<D, kKvE4m3, D>(cache, keys, 0, out);
+            else row_columns<D, kKvInt8, D>(cache, keys, 0, out);
+        }
+    }
+}
+
 constexpr int NO_PAGE = -2;  // a box without an attended row
 
 // CONVERTED: key and value tiles from the workspace (8-bit caches) instead of pages.
 template <int D, bool CONVERTED>
 __global__ void __launch_bounds__(THREADS, 2)
 extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO, const Args args) {
+                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO, const __grid_constant__ Args args) {
     using C = Cfg<D>;
     constexpr int KST = C::KSTAGES, VST = C::VSTAGES, NB = C::NB;
     extern __shared__ uint8_t smem_raw[];
@@ -539,7 +573,7 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     const uint32_t sBar = raw_addr + bar_off;
     uint32_t *misc = reinterpret_cast<uint32_t *>(smem_raw + bar_off + C::NBARS * 8);
     uint32_t *tmem_slot = misc;
-    volatile uint32_t *abort_flag = misc + 1;
+    volatile uint32_t *abort_flag = misc + 1, *bad_flag = misc + 2;  // bad: a non-finite output seen
     auto bar = [&](int idx) -> uint32_t { return sBar + idx * 8; };
 
     const ExtendArgs &ea = args.a;
@@ -550,7 +584,7 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 
     if (warp == 0) {
         for (int idx = lane; idx < C::NBARS; idx += 32) mbar_init(bar(idx), (uint32_t)C::arrivals(idx));
-        if (lane == 0) *abort_flag = 0u;
+        if (lane == 0) *abort_flag = *bad_flag = 0u;
         fence_barrier_init();
         __syncwarp();
         tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
@@ -999,7 +1033,8 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             if (ok && kb > 0) ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_STR), (uint32_t)((kb - 1) & 1), wc));
             if (ok && has_next) ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_QT), (uint32_t)((kb + 1) & 1), wc));
             if (!ok) break;
-            const float inv_l = (l > 0.f) ? 1.f / l : 0.f;
+            const float inv_l = l == 0.f ? 0.f : 1.f / l;
+            uint32_t seen[4] = {};
             tc_fence_after();
             __syncwarp();
             const long long row_g = (long long)(k.tq + trow) * s.H + h;
@@ -1017,6 +1052,7 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                     const float *f = reinterpret_cast<const float *>(x) + 8 * w;
                     const uint4 val = make_uint4(pack_bf16(f[0] * inv_l, f[1] * inv_l), pack_bf16(f[2] * inv_l, f[3] * inv_l),
                                                  pack_bf16(f[4] * inv_l, f[5] * inv_l), pack_bf16(f[6] * inv_l, f[7] * inv_l));
+                    watch(seen, val);
                     if (whole) *reinterpret_cast<uint4 *>(rowp + ((w ^ (r & 7)) << 4)) = val;
                     else if (row_ok) *reinterpret_cast<uint4 *>(orow + oh * 32 + w * 8) = val;
                 }
@@ -1024,7 +1060,8 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             fence_proxy_async_smem();
             tc_fence_before();
             mbar_arrive(bar(C::B_STF));
-            if (row_ok) ea.lse[row_g] = (l > 0.f) ? (m_ref + log2f(l)) * kLn2 : -INFINITY;
+            if (row_ok) ea.lse[row_g] = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * kLn2;
+            if (row_ok && went_bad(seen) && l == l) *bad_flag = 1u;
             k = kn;
             L = Ln;
             if (L < n_blocks && next_block(L) < n_blocks) load_rows(args, next_block(L), kn);
@@ -1039,6 +1076,11 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         tc_fence_after();
         tmem_dealloc(tbase, TMEM_COLS);
     }
+    // ---- rows that a value of another row's key made non-finite: once more, by themselves (pi_row.cuh)
+    if (!*bad_flag || *abort_flag) return;
+    if (warp == 2 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // this thread's stores are done
+    __syncthreads();
+    again<D, CONVERTED>(args, L0, n_blocks);
 }
 
 // ------------------------------------------------------------------ host side

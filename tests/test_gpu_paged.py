@@ -384,6 +384,69 @@ def test_decode_without_rows():
     assert (out[1] == 0).all() and torch.isneginf(lse[1]).all()
 
 
+MASKED = [
+    # kv, H, Hkv, d, page, ctx, n, k_local, period, S, mode
+    ("bf16", 16, 4, 128, 64, [300, 64], [320, 40], 100, 96, 2, PI),
+    ("bf16", 12, 4, 64, 16, [90], [640], 50, 70, 3, PI),
+    ("e4m3", 16, 4, 128, 64, [300, 64], [420, 40], 100, 128, 2, PI),
+    ("int8", 8, 8, 64, 128, [300], [500], 96, 0, 0, ECP),
+    ("bf16", 16, 4, 128, 32, [130, 164, 500], [5, 3, 6], 100, 150, 3, PI),
+    ("e4m3", 12, 4, 64, 16, [90], [30], 20, 25, 3, PI),
+    ("int8", 4, 2, 128, 64, [300], [40], 96, 0, 0, ECP),
+]
+
+
+@pytest.mark.parametrize("case", MASKED, ids=[f"{c[0]}-d{c[3]}-{sum(c[6])}" for c in MASKED])
+def test_a_row_is_made_of_its_own_keys(case):
+    """Values that are not finite, inside the chunk, in its band and under its skips, and one such key: exactly the rows
+    that attend them have them in their results, in their columns (8 bits: blocks); every other is the oracle's."""
+    kv, H, Hkv, d, page, ctx, n, kl, per, S, mode = case
+    bt = Batch(ctx, n, Hkv, d, page, kv, seed=d + sum(n))
+    odd = [float("nan"), float("inf"), float("-inf")]
+    planted = []  # sequence, position, KV head, first column, columns
+    for b, (c, m) in enumerate(zip(ctx, n)):
+        far = [c + m // 3 - per] if S and c + m // 3 >= per else []
+        for x, pos in enumerate([c - 3, c, c + m // 2, c + m - 1] + far):
+            g, col = x % Hkv, (37 * x + 5) % d
+            bt.v[b][pos, g, col] = odd[x % 3]
+            planted.append((b, pos, g, col, 1) if kv == "bf16" else (b, pos, g, col // 32 * 32, 32))
+    key_at = ctx[0] + 2 * n[0] // 3
+    bt.k[0][key_at, Hkv - 1, 7] = odd[0]
+    bt.write()
+    q = normal(bt.gen, bt.T, H, d)
+    alpha = None if mode == ECP else torch.sigmoid(torch.randn(bt.T, H, generator=bt.gen))
+    out, lse = pa.extend(q.cuda(), bt.cache, dev(bt.table), dev(bt.cu), dev(ctx), None if alpha is None else alpha.cuda(), kl, per, S, mode)
+    torch.cuda.synchronize()
+    assert pa.status() == 0
+    K, V = ([torch.nan_to_num(x, nan=0.0, posinf=0.0, neginf=0.0) for x in xs] for xs in bt.held())
+    bad, bad_lse = np.zeros((bt.T, H, d), dtype=bool), np.zeros((bt.T, H), dtype=bool)
+    G = H // Hkv
+    for b, (c, m) in enumerate(zip(ctx, n)):
+        for i in range(c, c + m):
+            t = bt.cu[b] + i - c
+            keys = set(range(max(0, (i // kl - 1) * kl if mode == ECP else i - kl), i + 1))
+            keys |= {i - x * per for x in range(1, S + 1) if x * per > kl and i >= x * per}
+            for pb, pos, g, col, w in planted:
+                if pb == b and pos in keys:
+                    bad[t, g * G:(g + 1) * G, col:col + w] = True
+            if b == 0 and key_at in keys:
+                bad[t, H - G:] = bad_lse[t, H - G:] = True
+    assert bad.any() and not bad.all()
+    got, got_lse = out.float().cpu(), lse.cpu()
+    assert not torch.isfinite(got[torch.from_numpy(bad)]).any(), "a row without a value that it attends"
+    assert torch.isnan(got_lse[torch.from_numpy(bad_lse)]).all()
+    for b, (c, m) in enumerate(zip(ctx, n)):
+        t = slice(bt.cu[b], bt.cu[b + 1])
+        ro, rl, size = ref.attention(q[t], K[b], V[b], None if alpha is None else alpha[t], c, kl, per, S, mode)
+        o = np.where(bad[t], ro, got[t].numpy().astype(np.float64))
+        z = np.where(bad_lse[t], rl, got_lse[t].numpy().astype(np.float64))
+        off = np.abs(o - ro)
+        assert np.isfinite(o).all(), f"sequence {b}: {int((~np.isfinite(o)).sum())} outputs have another row's value"
+        # rounding as in check_attention; what stands in for a bad result is the oracle's own
+        assert (off <= 2.0 ** -8 * np.abs(ro) + (2.0 ** -8 + 2.0 ** -12) * size + 1e-30).all()
+        assert (np.abs(z - rl) <= 2.0 ** -12 + 2.0 ** -22 * np.abs(rl)).all()
+
+
 # ------------------------------------------------------------------ indexes out of range
 
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
