@@ -3,8 +3,8 @@
  * ABI (include/pi_attn.h) in one native function each.
  *
  * A serving step makes these calls for every layer, and its kernels take a few microseconds: checks and marshalling in
- * Python and ctypes took longer than they do.  On the host an append takes 4.3 us (6.9 with both in Python, tuned), a decode
- * step 4.5 us with its outputs given and 11 without, most of which is torch.empty's.  Tensors are reached through their
+ * Python and ctypes took longer than they do.  On the host an append takes 4.4 us (6.9 with both in Python, tuned), a decode
+ * step 4.5 us with its outputs given and 9 without, most of the difference being torch's for two new tensors.  Tensors are reached through their
  * Python methods, so nothing here depends on torch's headers or binary interface.
  */
 #define PY_SSIZE_T_CLEAN
@@ -33,7 +33,7 @@ static extend_size_fn f_extend_size;
 static extend_fn f_extend;
 static decode_fn f_decode;
 
-static PyObject *g_bf16, *g_fp32, *g_int32, *g_uint8, *g_empty;                                  /* torch's objects */
+static PyObject *g_bf16, *g_fp32, *g_int32, *g_uint8, *g_empty, *g_empty_like;                   /* torch's objects */
 static PyObject *s_data_ptr, *s_dtype, *s_shape, *s_stride, *s_get_device, *s_is_contiguous;     /* interned names */
 static PyObject *kw_empty;                                                                       /* ("dtype", "device") */
 
@@ -146,12 +146,14 @@ static PyObject *empty(const handle_t *h, PyObject *dtype, int n, const long lon
     return r;
 }
 
-/* The caller's output buffer, checked, or (None) a new one: a new reference in *out. */
+/* The caller's output buffer, checked, or (None) a new one: a new reference in *out.  like: a tensor of its type, shape and
+ * device, or NULL (a decode call takes 9.0 us on the host with empty_like and 12.5 with empty).  Its strides fall from size to
+ * size, whatever their gaps, so what is like it is contiguous. */
 static void *output(PyObject *given, const char *name, const handle_t *h, PyObject *dtype, int n, long long *shape, const char *want,
-                    PyObject **out) {
+                    PyObject *like, PyObject **out) {
     if (given == Py_None) {
         int ok = 1;
-        if (!(*out = empty(h, dtype, n, shape))) return NULL;
+        if (!(*out = like ? PyObject_CallOneArg(g_empty_like, like) : empty(h, dtype, n, shape))) return NULL;
         void *p = (void *)(uintptr_t)call_int(*out, s_data_ptr, &ok);
         if (ok) return p ? p : (void *)h;
     } else {
@@ -231,7 +233,7 @@ static PyObject *py_read(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     if (rows < 0) return PyErr_Format(PyExc_ValueError, "rows must not be negative");
     long long shape[3] = {rows, h->cache.Hkv, h->cache.d};
     const char *want = "a contiguous bf16 [rows, Hkv, d] on the cache's device";
-    if ((pk = output(a[5], "k", h, g_bf16, 3, shape, want, &k)) && (pv = output(a[6], "v", h, g_bf16, 3, shape, want, &v)) &&
+    if ((pk = output(a[5], "k", h, g_bf16, 3, shape, want, NULL, &k)) && (pv = output(a[6], "v", h, g_bf16, 3, shape, want, k, &v)) &&
         !batch(a[1], a[2], a[3], rows, h, &b))
         r = Py_BuildValue("iOO", rows ? f_read(&h->cache, &b, pk, pv, stream) : PI_OK, k, v);
     Py_XDECREF(k);
@@ -240,8 +242,8 @@ static PyObject *py_read(PyObject *self, PyObject *const *a, Py_ssize_t n) {
 }
 
 /* alpha's address (NULL for None), out and lse of an attention's T rows: 0, or -1 with an error. */
-static int rows_of(PyObject *alpha, PyObject *out, PyObject *lse, const handle_t *h, long long T, long long H, int mode, float **pa,
-                   void **po, float **pl, PyObject **o, PyObject **l) {
+static int rows_of(PyObject *q, PyObject *alpha, PyObject *out, PyObject *lse, const handle_t *h, long long T, long long H, int mode,
+                   float **pa, void **po, float **pl, PyObject **o, PyObject **l) {
     long long s2[2] = {T, H}, s3[3] = {T, H, h->cache.d};
     *pa = NULL;
     if (alpha != Py_None) {
@@ -250,8 +252,9 @@ static int rows_of(PyObject *alpha, PyObject *out, PyObject *lse, const handle_t
         PyErr_SetString(PyExc_ValueError, "alpha is needed in pi mode");
         return -1;
     }
-    if (!(*po = output(out, "out", h, g_bf16, 3, s3, "a contiguous bf16 [T, H, d] on the cache's device", o))) return -1;
-    if (!(*pl = output(lse, "lse", h, g_fp32, 2, s2, "a contiguous fp32 [T, H] on the cache's device", l))) return -1;
+    if (!(*po = output(out, "out", h, g_bf16, 3, s3, "a contiguous bf16 [T, H, d] on the cache's device", q, o))) return -1;
+    PyObject *like = alpha != Py_None ? alpha : NULL;
+    if (!(*pl = output(lse, "lse", h, g_fp32, 2, s2, "a contiguous fp32 [T, H] on the cache's device", like, l))) return -1;
     return 0;
 }
 
@@ -267,7 +270,7 @@ static PyObject *py_extend(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     pi_attn_batch_t b;
     PyObject *o = NULL, *l = NULL, *w = NULL, *r = NULL;
     if (PyErr_Occurred() || ints(a + 6, 4, p) || packed(a[0], "q", h, &T, &H, &qs, &q) || batch(a[2], a[3], a[4], T, h, &b)) return NULL;
-    if (rows_of(a[5], a[10], a[11], h, T, H, p[3], &alpha, &out, &lse, &o, &l)) goto done;
+    if (rows_of(a[0], a[5], a[10], a[11], h, T, H, p[3], &alpha, &out, &lse, &o, &l)) goto done;
     if (T == 0) {
         r = Py_BuildValue("iOO", PI_OK, o, l);
         goto done;
@@ -281,7 +284,7 @@ static PyObject *py_extend(PyObject *self, PyObject *const *a, Py_ssize_t n) {
             PyErr_Format(PyExc_ValueError, "workspace must hold %zu bytes, got %lld", need, bytes);
             goto done;
         }
-    } else if (need && !(ws = output(Py_None, "workspace", h, g_uint8, 1, &bytes, "", &w))) {
+    } else if (need && !(ws = output(Py_None, "workspace", h, g_uint8, 1, &bytes, "", NULL, &w))) {
         goto done;
     }
     r = Py_BuildValue("iOO",
@@ -310,7 +313,7 @@ static PyObject *py_decode(PyObject *self, PyObject *const *a, Py_ssize_t n) {
         !(lens = dense(a[3], "lens", h, g_int32, 1, s, "a contiguous int32 [B] on the cache's device")))
         return NULL;
     if (B > INT32_MAX || s[1] > INT32_MAX) return PyErr_Format(PyExc_ValueError, "more than 2^31 - 1 sequences or page-table entries");
-    if (!rows_of(a[4], a[9], a[10], h, B, H, p[3], &alpha, &out, &lse, &o, &l))
+    if (!rows_of(a[0], a[4], a[9], a[10], h, B, H, p[3], &alpha, &out, &lse, &o, &l))
         r = Py_BuildValue("iOO",
                           B ? f_decode(q, qs, &h->cache, table, lens, (int)B, (int)s[1], alpha, (int)H, p[0], p[1], p[2], p[3], out, lse,
                                        stream)
@@ -321,10 +324,10 @@ static PyObject *py_decode(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     return r;
 }
 
-/* bind(append, read, extend size, extend, decode: addresses; bfloat16, float32, int32, uint8, empty: torch's) */
+/* bind(append, read, extend size, extend, decode: addresses; bfloat16, float32, int32, uint8, empty, empty_like: torch's) */
 static PyObject *py_bind(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     (void)self;
-    if (n != 10) return PyErr_Format(PyExc_TypeError, "bind takes 10 arguments");
+    if (n != 11) return PyErr_Format(PyExc_TypeError, "bind takes 11 arguments");
     void *f[5];
     for (int i = 0; i < 5; ++i) f[i] = PyLong_AsVoidPtr(a[i]);
     if (PyErr_Occurred()) return NULL;
@@ -333,8 +336,8 @@ static PyObject *py_bind(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     f_extend_size = (extend_size_fn)f[2];
     f_extend = (extend_fn)f[3];
     f_decode = (decode_fn)f[4];
-    PyObject **slots[5] = {&g_bf16, &g_fp32, &g_int32, &g_uint8, &g_empty};
-    for (int i = 0; i < 5; ++i) {
+    PyObject **slots[6] = {&g_bf16, &g_fp32, &g_int32, &g_uint8, &g_empty, &g_empty_like};
+    for (int i = 0; i < 6; ++i) {
         Py_INCREF(a[5 + i]);
         Py_XSETREF(*slots[i], a[5 + i]);
     }

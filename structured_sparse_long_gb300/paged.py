@@ -75,7 +75,7 @@ def _load_native():
         spec.loader.exec_module(module)
         module.bind(*(ctypes.cast(getattr(lib, "pi_attn_" + n), ctypes.c_void_p).value
                       for n in ("cache_append", "cache_read", "extend_workspace_size", "extend", "decode_paged")),
-                    torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.empty)
+                    torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.empty, torch.empty_like)
         _native = module
     return _native
 

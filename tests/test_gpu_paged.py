@@ -447,6 +447,23 @@ def test_a_row_is_made_of_its_own_keys(case):
         assert (np.abs(z - rl) <= 2.0 ** -12 + 2.0 ** -22 * np.abs(rl)).all()
 
 
+@pytest.mark.parametrize("n,H,shape,strides", [(5, 4, (5, 4, 64), (576, 64, 1)), (1, 4, (1, 4, 64), (1, 64, 1)), (4, 1, (4, 1, 64), (64, 1000, 1)),
+                                               (1, 1, (1, 1, 64), (8, 7, 1)), (300, 4, (300, 4, 64), (264, 64, 1))])
+def test_new_outputs_are_contiguous(n, H, shape, strides):
+    """Whatever the strides between the queries' tokens (and of dimensions of size one)."""
+    bt = Batch([40], [n], 1, 64, 16, "bf16", seed=n)
+    bt.write()
+    q = torch.empty_strided(shape, strides, dtype=torch.bfloat16, device="cuda").copy_(normal(bt.gen, *shape))
+    a = torch.full((n, H), 0.5, device="cuda")
+    call = lambda x: pa.extend(x, bt.cache, dev(bt.table), dev(bt.cu), dev([40]), a, 20, 16, 2)  # noqa: E731
+    out, lse = call(q)
+    want, want_lse = call(q.clone(memory_format=torch.contiguous_format))
+    assert out.is_contiguous() and lse.is_contiguous() and torch.equal(out, want) and torch.equal(lse, want_lse)
+    if n == 1:
+        out, lse = pa.decode_paged(q, bt.cache, dev(bt.table), dev([41]), a, 20, 16, 2)
+        assert out.is_contiguous() and lse.is_contiguous() and out.shape == q.shape
+
+
 # ------------------------------------------------------------------ indexes out of range
 
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
