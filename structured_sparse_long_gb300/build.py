@@ -1,4 +1,4 @@
-"""Builds the CUDA library libpi_attn.so for sm_103a with nvcc (no cmake), and the binding's CPython extension.
+"""Builds the CUDA library libpi_attn.so for sm_103a with nvcc (no cmake), and the binding's extension module.
 
 Translation units are compiled in parallel into ``_build/`` and linked into
 ``_lib/libpi_attn.so`` inside the package, next to the Python binding.
@@ -6,6 +6,8 @@ Translation units are compiled in parallel into ``_build/`` and linked into
 from __future__ import annotations
 
 import concurrent.futures
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -19,7 +21,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_DIR = os.path.join(HERE, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libpi_attn.so")
-NATIVE_SOURCE = "pi_paged_py.c"  # CPython extension of the paged cache's binding
+NATIVE_SOURCE = "pi_paged_py.cpp"  # extension module of the paged cache's binding
 NATIVE_PATH = os.path.join(LIB_DIR, "_pi_paged" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
 SOURCES = ["api.cu", "pi_simt.cu", "pi_fwd_tc.cu", "pi_bwd_tc.cu", "pi_decode.cu",
@@ -49,6 +51,15 @@ def _stale(target: str, deps) -> bool:
         return True
     t = os.path.getmtime(target)
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _native_command(target: str) -> list:
+    """The host compiler's command for the binding's extension module (torch is found, not imported)."""
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    lib = os.path.join(torch, "lib")
+    return ["g++", "-shared", "-fPIC", "-O2", "-std=c++17", "-Wall", "-Wextra", "-isystem", os.path.join(torch, "include"),
+            "-I", sysconfig.get_paths()["include"], "-I", INCLUDE, os.path.join(CSRC, NATIVE_SOURCE), "-o", target,
+            "-L" + lib, "-Wl,-rpath," + lib, "-ltorch_python", "-ltorch_cpu", "-lc10"]
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
@@ -81,24 +92,26 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         r = subprocess.run(cmd, capture_output=True, text=True)
         return cmd, r
 
+    # the binding depends on the version of torch that it was compiled against
+    native, torch_stamp = NATIVE_PATH + f".tmp{os.getpid()}", os.path.join(BUILD_DIR, "torch_version.txt")
+    version = importlib.metadata.version("torch")
+    new_native = (force or _stale(NATIVE_PATH, [os.path.join(CSRC, NATIVE_SOURCE), os.path.join(INCLUDE, "pi_attn.h")])
+                  or not os.path.exists(torch_stamp) or open(torch_stamp).read() != version)
+    compiled = bool(jobs)
+    if new_native:
+        jobs.append(_native_command(native))
     if jobs:
         with concurrent.futures.ThreadPoolExecutor(max_workers=len(jobs)) as ex:
             for cmd, r in ex.map(run, jobs):
                 if verbose or ptxas_info or r.returncode != 0:
                     sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
                 if r.returncode != 0:
-                    raise RuntimeError(f"nvcc failed for {cmd[2]}")
-    src = os.path.join(CSRC, NATIVE_SOURCE)
-    if force or _stale(NATIVE_PATH, [src, os.path.join(INCLUDE, "pi_attn.h")]):
-        tmp = NATIVE_PATH + f".tmp{os.getpid()}"
-        _, r = run(["gcc", "-shared", "-fPIC", "-O2", "-Wall", "-Wextra", "-I", sysconfig.get_paths()["include"], "-I", INCLUDE, src,
-                    "-o", tmp])
-        if verbose or r.returncode != 0:
-            sys.stderr.write(r.stdout + r.stderr)
-        if r.returncode != 0:
-            raise RuntimeError("gcc failed for " + src)
-        os.replace(tmp, NATIVE_PATH)
-    if force or jobs or _stale(LIB_PATH, objs):
+                    raise RuntimeError(f"{os.path.basename(cmd[0])} failed for " + next(x for x in cmd if x.startswith(CSRC + os.sep)))
+    if new_native:
+        os.replace(native, NATIVE_PATH)
+        with open(torch_stamp, "w") as fh:
+            fh.write(version)
+    if force or compiled or _stale(LIB_PATH, objs):
         tmp = LIB_PATH + f".tmp{os.getpid()}"
         cmd = [nv, "-shared", "-o", tmp] + objs + ARCH_FLAGS + [
             "-cudart", "shared", "-Xlinker", "-rpath," + _cuda_lib_dir(nv)]

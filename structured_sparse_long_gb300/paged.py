@@ -1,4 +1,4 @@
-"""Binding of the paged key/value cache: argument marshalling only, in a native extension (csrc/pi_paged_py.c), since a
+"""Binding of the paged key/value cache: argument marshalling only, in a native extension (csrc/pi_paged_py.cpp), since a
 serving step makes these calls for every layer.
 
 A :class:`PagedCache` holds one layer's pages (bf16, e4m3 or int8; include/pi_attn.h has the
@@ -40,7 +40,7 @@ class _BatchStruct(ctypes.Structure):  # pi_attn_batch_t
                 ("B", ctypes.c_int), ("T", ctypes.c_int), ("width", ctypes.c_int)]
 
 
-class _Handle(ctypes.Structure):  # handle_t of csrc/pi_paged_py.c
+class _Handle(ctypes.Structure):  # Handle of csrc/pi_paged_py.cpp
     _fields_ = [("cache", _CacheStruct), ("device", ctypes.c_int)]
 
 
@@ -74,8 +74,7 @@ def _load_native():
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
         module.bind(*(ctypes.cast(getattr(lib, "pi_attn_" + n), ctypes.c_void_p).value
-                      for n in ("cache_append", "cache_read", "extend_workspace_size", "extend", "decode_paged")),
-                    torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.empty, torch.empty_like)
+                      for n in ("cache_append", "cache_read", "extend_workspace_size", "extend", "decode_paged")))
         _native = module
     return _native
 

@@ -645,6 +645,35 @@ def test_streams_run_side_by_side(n):
     assert pa.status() == 0
 
 
+def test_threads_call_side_by_side():
+    """Four host threads, each with a cache, a stream and outputs of its own, make the same calls at once that one makes alone."""
+    from concurrent.futures import ThreadPoolExecutor
+
+    def work(x, stream):
+        bt, q, a = x
+        with torch.cuda.stream(stream):
+            got = []
+            for _ in range(20):
+                pa.cache_append(bt.k[0][:64].cuda(), bt.v[0][:64].cuda(), bt.cache, dev(bt.table), dev([0, 64]), dev([0]))
+                got.append(pa.extend(q, bt.cache, dev(bt.table), dev(bt.cu), dev(bt.ctx), a, 64, 32, 3))
+                got.append(pa.decode_paged(q[-1:], bt.cache, dev(bt.table), dev([bt.ctx[0] + bt.n[0]]), a[-1:], 64, 32, 3))
+                got.append(pa.cache_read(bt.cache, dev(bt.table), dev([0, 100]), dev([0]), 100))
+        stream.synchronize()
+        return got
+
+    jobs = []
+    for x in range(4):
+        bt = Batch([100], [3 if x % 2 else 700], 4, 64, 32, ["bf16", "e4m3", "int8"][x % 3], seed=x)
+        bt.write()
+        jobs.append((bt, normal(bt.gen, bt.T, 16, 64).cuda(), torch.rand(bt.T, 16, generator=bt.gen).cuda()))
+    torch.cuda.synchronize()
+    want = [work(x, torch.cuda.current_stream()) for x in jobs]
+    with ThreadPoolExecutor(4) as pool:
+        got = list(pool.map(work, jobs, [torch.cuda.Stream() for _ in jobs]))
+    for w, g in zip(want, got):
+        assert all(torch.equal(x, y) for u, v in zip(w, g) for x, y in zip(u, v))
+
+
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 def test_many_sequences(kv):
     """More sequences than the plan takes in one round, empty ones among them, through the long chunks' kernels; and through

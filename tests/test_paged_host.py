@@ -256,8 +256,7 @@ def test_binding_refuses_host_tensors_and_wrong_types(monkeypatch):
     never = ctypes.CFUNCTYPE(ctypes.c_int)(lambda: calls.append(1) or 0)
     addresses = [ctypes.cast(never, ctypes.c_void_p).value] * 5
     addresses[2] = ctypes.cast(paged._load().pi_attn_extend_workspace_size, ctypes.c_void_p).value
-    torchs = (torch.bfloat16, torch.float32, torch.int32, torch.uint8, torch.empty, torch.empty_like)
-    native.bind(*addresses, *torchs)
+    native.bind(*addresses)
     try:
         c = paged.PagedCache(z, z)
         table, cu = torch.zeros(1, 4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
