@@ -22,6 +22,8 @@
 // The partial states (m, l, o) meet in shared memory, and across a cluster through distributed shared
 // memory.  With a few hundred keys per sequence the step is bound by the latency of its dependent
 // loads (length, page table, rows) for small batches and by HBM for large ones.
+#include <type_traits>
+
 #include "pi_mma.cuh"
 #include "pi_paged.cuh"
 #include "pi_row.cuh"
@@ -203,14 +205,14 @@ __device__ __forceinline__ void accumulate(const Frag<D, KV> &f, const uint32_t 
 constexpr int sm_warps(int D, int KV, int NH) { return NH == 2 ? 8 : D == 128 && KV == kKvBf16 ? 12 : 16; }
 constexpr int max_warps(int D, int KV, int NH) { return sm_warps(D, KV, NH) / (NH == 2 ? 1 : 2); }
 
-// 64 columns of the row of token at / H and head at % H, position i of sequence b (pi_row.cuh).
+// The row of token at / H and head at % H, position i of sequence b, by itself (pi_row.cuh).
 template <int D, int KV>
-__device__ __noinline__ void again(const Args &a, int b, int i, int kvh, int at, int col0) {
+__device__ __noinline__ void again(const Args &a, int b, int i, int kvh, int at) {
     const int tok = at / a.s.H;
-    row_columns<D, KV, 64>(a.cache,
-                       row_keys(a.s, i, kvh, a.m_first, a.q + tok * a.q_stride + (at - tok * a.s.H) * D,
-                                a.batch.table + (long long)b * a.cache.width, a.alpha ? a.alpha + at : nullptr),
-                       col0, a.out + (long long)at * D);
+    attend_row<D, KV>(a.cache,
+                      row_keys(a.s, i, kvh, a.m_first, a.q + tok * a.q_stride + (at - tok * a.s.H) * D,
+                               a.batch.table + (long long)b * a.cache.width, a.alpha ? a.alpha + at : nullptr),
+                      a.out + (long long)at * D);
 }
 
 // NH: groups of 8 columns (1 or 2), a column being one query head of one token
@@ -219,9 +221,8 @@ __global__ void __launch_bounds__(max_warps(D, KV, NH) * 32, sm_warps(D, KV, NH)
 paged_rows_kernel(const __grid_constant__ Args a) {
     const Shape &s = a.s;
     const PagedCache &c = a.cache;
-    constexpr int MAX_W = max_warps(D, KV, NH);
     constexpr int PART = D + 4;  // floats of a column's partial state: o[D], m, l, padding to 16 bytes
-    extern __shared__ __align__(16) float part[];  // [warps + 1][columns][PART]
+    extern __shared__ __align__(16) float part[];  // [warps][columns][PART]
     const int P = gridDim.x, rank = blockIdx.x, kvh = blockIdx.y, warps = blockDim.x >> 5;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int G = s.H / s.Hkv, h0 = kvh * G;
@@ -232,6 +233,7 @@ paged_rows_kernel(const __grid_constant__ Args a) {
     int b, first, last, tok0;
     if constexpr (!TOKENS) {
         b = tok0 = blockIdx.z;
+        if (32 * threadIdx.x < c.width) asm volatile("prefetch.global.L1 [%0];" ::"l"(a.batch.table + (long long)b * c.width + 32 * threadIdx.x));
         last = __ldg(a.lens + b) - 1;
         if (last < -1 || last >= (long long)c.width << c.page_log2) {
             if (threadIdx.x == 0) record_index(a.index_word);
@@ -243,16 +245,29 @@ paged_rows_kernel(const __grid_constant__ Args a) {
             for (int j = threadIdx.x; j < a.batch.B; j += blockDim.x)
                 if (__ldg(a.batch.cu + j) > __ldg(a.batch.cu + j + 1)) record_index(a.index_word);
         // sequence b's token groups are numbered from (cu[b] + b (group - 1)) / group on, which leaves each its ceil(n / group)
-        const int id = blockIdx.z;
-        auto start = [&](int j) -> long long { return ((long long)__ldg(a.batch.cu + j) + (long long)j * (a.group - 1)) / a.group; };
-        b = find_sequence(a.batch.B, [&](int j) { return start(j) <= id; });
-        if (b >= a.batch.B) return;
-        const int t0 = __ldg(a.batch.cu + b), t1 = __ldg(a.batch.cu + b + 1), ctx = __ldg(a.batch.ctx + b);
+        const int id = blockIdx.z, B = a.batch.B;
+        auto start = [&](int j, int at) -> long long { return ((long long)at + (long long)j * (a.group - 1)) / a.group; };
+        int t0, t1, ctx;
+        if (B <= 32) {  // a sequence per lane, so that one round of loads has everything
+            const bool in = lane < B;
+            const int c0 = in ? __ldg(a.batch.cu + lane) : 0, c1 = in ? __ldg(a.batch.cu + lane + 1) : 0, x = in ? __ldg(a.batch.ctx + lane) : 0;
+            b = __popc(__ballot_sync(kFull, in && start(lane + 1, c1) <= id));
+            t0 = __shfl_sync(kFull, c0, b & 31);
+            t1 = __shfl_sync(kFull, c1, b & 31);
+            ctx = __shfl_sync(kFull, x, b & 31);
+            if (b >= B) return;
+        } else {
+            b = find_sequence(B, [&](int j) { return start(j, __ldg(a.batch.cu + j)) <= id; });
+            if (b >= B) return;
+            t0 = __ldg(a.batch.cu + b);
+            t1 = __ldg(a.batch.cu + b + 1);
+            ctx = __ldg(a.batch.ctx + b);
+        }
         if (!sequence_ok(c, a.batch, t0, t1, ctx)) {
             if (threadIdx.x == 0) record_index(a.index_word);
             return;
         }
-        const long long x = (id - start(b)) * a.group;
+        const long long x = (id - start(b, t0)) * a.group;
         if (x < 0 || x >= t1 - t0) return;
         const int x0 = (int)x;
         tok0 = t0 + x0;
@@ -396,88 +411,84 @@ paged_rows_kernel(const __grid_constant__ Args a) {
                 if (g == 0) *reinterpret_cast<float2 *>(ps + D) = make_float2(m[nh][e], sum);
             }
         }
-    __syncthreads();
-
-    // merge of `n` states, state x at address at(x), for columns col, col + 1 of the head
-    // (a warp holds 64 columns of one row)
-    auto finish = [&](int x, int col, float mt, float lt, float x0, float x1) {
-        const float inv = lt == 0.f ? 0.f : 1.f / lt;
-        const long long at = row_of(x);
-        const uint32_t pair = pack_bf16x2(x0 * inv, x1 * inv);
-        if (col == 0) a.lse[at] = lt == 0.f ? -INFINITY : (mt + log2f(lt)) * kLn2;
-        if constexpr (TOKENS) {  // a value of another token's key may have made the row non-finite (pi_row.cuh)
-            uint32_t seen = 0u;
-            watch(seen, pair);
-            if (__any_sync(kFull, went_bad(seen) && lt == lt)) {
-                again<D, KV>(a, b, first + x / G, kvh, (int)at, col - 2 * lane);
-                return;
+    // ---- and meet: four columns of a row per thread, all the cluster's states at once (a merge in each CTA first and then one
+    // of the CTAs' took 10.4 us where this takes 9.1, 32 drafts of 5 tokens in clusters of three)
+    constexpr int PER_ROW = D / 4, BATCH = 12;  // threads of a row; states in flight
+    const int states = P * warps, items = cols * PER_ROW;
+    const uint32_t base = smem_addr(part);
+    auto meet = [&](auto across) {
+        for (int w0 = (rank * warps + warp) * 32; w0 < items; w0 += states * 32) {
+            const bool in = w0 + lane < items;
+            const int x = in ? (w0 + lane) / PER_ROW : cols - 1, col = 4 * (lane % PER_ROW);
+            float mt = -INFINITY, lt = 0.f;
+            float4 ot = make_float4(0.f, 0.f, 0.f, 0.f);
+            int wp = 0, cta = 0;
+#pragma unroll 1
+            for (int y0 = 0; y0 < states; y0 += BATCH) {
+                float2 ml[BATCH];
+                float4 ov[BATCH];
+#pragma unroll
+                for (int y = 0; y < BATCH; ++y) {
+                    ml[y] = make_float2(-INFINITY, 0.f);
+                    ov[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (y0 + y >= states) continue;
+                    const uint32_t at = (uint32_t)((wp * cols + x) * PART) * 4u;
+                    if constexpr (across.value) {
+                        const uint32_t there = peer_addr(base + at, cta);
+                        ml[y] = ld_peer2(there + D * 4);
+                        ov[y] = ld_peer4(there + col * 4);
+                    } else {
+                        const float *ps = part + at / 4;
+                        ml[y] = *reinterpret_cast<const float2 *>(ps + D);
+                        ov[y] = *reinterpret_cast<const float4 *>(ps + col);
+                    }
+                    if (++wp == warps) {
+                        wp = 0;
+                        ++cta;
+                    }
+                }
+                float mn = mt;
+#pragma unroll
+                for (int y = 0; y < BATCH; ++y) mn = fmaxf(mn, ml[y].x);
+                const float ref = mn == -INFINITY ? 0.f : mn, corr = exp2f(mt - ref);
+                mt = mn;
+                lt *= corr;
+                ot = make_float4(ot.x * corr, ot.y * corr, ot.z * corr, ot.w * corr);
+#pragma unroll
+                for (int y = 0; y < BATCH; ++y) {
+                    const float e = exp2f(ml[y].x - ref);
+                    lt = fmaf(e, ml[y].y, lt);
+                    ot = make_float4(fmaf(e, ov[y].x, ot.x), fmaf(e, ov[y].y, ot.y), fmaf(e, ov[y].z, ot.z), fmaf(e, ov[y].w, ot.w));
+                }
             }
+            const float inv = lt == 0.f ? 0.f : 1.f / lt;
+            const uint2 four = make_uint2(pack_bf16x2(ot.x * inv, ot.y * inv), pack_bf16x2(ot.z * inv, ot.w * inv));
+            const long long at = row_of(x);
+            bool mine = in;
+            if constexpr (TOKENS) {  // a value of another token's key may have made a row non-finite (pi_row.cuh)
+                uint32_t seen = 0u;
+                watch(seen, four.x);
+                watch(seen, four.y);
+                unsigned bad = __ballot_sync(kFull, in && went_bad(seen) && lt == lt);
+                while (bad) {
+                    const int y = __shfl_sync(kFull, x, __ffs(bad) - 1);
+                    again<D, KV>(a, b, first + y / G, kvh, (int)row_of(y));
+                    bad &= ~__ballot_sync(kFull, x == y);
+                    mine = mine && x != y;
+                }
+            }
+            if (mine) *reinterpret_cast<uint2 *>(a.out + at * D + col) = four;
+            if (in && col == 0) a.lse[at] = lt == 0.f ? -INFINITY : (mt + log2f(lt)) * kLn2;
         }
-        *reinterpret_cast<uint32_t *>(a.out + at * D + col) = pair;
     };
-    const int pairs = cols * (D / 2);
-    for (int w = threadIdx.x; w < pairs; w += blockDim.x) {
-        const int x = w / (D / 2), col = 2 * (w % (D / 2));
-        float2 ml[MAX_W], ov[MAX_W];
-#pragma unroll
-        for (int y = 0; y < MAX_W; ++y)
-            if (y < warps) {
-                const float *ps = part + (y * cols + x) * PART;
-                ml[y] = *reinterpret_cast<const float2 *>(ps + D);
-                ov[y] = *reinterpret_cast<const float2 *>(ps + col);
-            }
-        float mt = -INFINITY;
-#pragma unroll
-        for (int y = 0; y < MAX_W; ++y)
-            if (y < warps) mt = fmaxf(mt, ml[y].x);
-        float lt = 0.f, x0 = 0.f, x1 = 0.f;
-        const float ref = mt == -INFINITY ? 0.f : mt;
-#pragma unroll
-        for (int y = 0; y < MAX_W; ++y)
-            if (y < warps) {
-                const float e = exp2f(ml[y].x - ref);
-                lt = fmaf(e, ml[y].y, lt);
-                x0 = fmaf(e, ov[y].x, x0);
-                x1 = fmaf(e, ov[y].y, x1);
-            }
-        if (P == 1) {
-            finish(x, col, mt, lt, x0, x1);
-        } else {  // the CTA's state, behind the warps'
-            float *ps = part + (warps * cols + x) * PART;
-            *reinterpret_cast<float2 *>(ps + col) = make_float2(x0, x1);
-            if (col == 0) *reinterpret_cast<float2 *>(ps + D) = make_float2(mt, lt);
-        }
+    if (P == 1) {
+        __syncthreads();
+        meet(std::false_type{});
+        return;
     }
-    if (P == 1) return;
     cluster_sync();
-    const uint32_t base = smem_addr(part + warps * cols * PART);
-    for (int w = rank * blockDim.x + threadIdx.x; w < pairs; w += P * blockDim.x) {
-        const int x = w / (D / 2), col = 2 * (w % (D / 2));
-        float2 ml[MAX_P], ov[MAX_P];
-#pragma unroll
-        for (int y = 0; y < MAX_P; ++y)
-            if (y < P) {
-                const uint32_t at = peer_addr(base + (uint32_t)(x * PART) * 4u, y);
-                ml[y] = ld_peer2(at + D * 4);
-                ov[y] = ld_peer2(at + col * 4);
-            }
-        float mt = -INFINITY;
-#pragma unroll
-        for (int y = 0; y < MAX_P; ++y)
-            if (y < P) mt = fmaxf(mt, ml[y].x);
-        float lt = 0.f, x0 = 0.f, x1 = 0.f;
-        const float ref = mt == -INFINITY ? 0.f : mt;
-#pragma unroll
-        for (int y = 0; y < MAX_P; ++y)
-            if (y < P) {
-                const float e = exp2f(ml[y].x - ref);
-                lt = fmaf(e, ml[y].y, lt);
-                x0 = fmaf(e, ov[y].x, x0);
-                x1 = fmaf(e, ov[y].y, x1);
-            }
-        finish(x, col, mt, lt, x0, x1);
-    }
-    cluster_sync();  // every CTA's shared memory stays until the others have read it
+    meet(std::true_type{});
+    cluster_leave();  // a CTA's shared memory stays until the others have read it
 }
 
 // Warps per CTA and CTAs per cluster for `pairs` (token group, KV head) pairs of up to `tiles` key tiles each.  A warp takes
@@ -515,14 +526,14 @@ static cudaError_t launch(const Args &a, int groups, long long keys, cudaStream_
     cudaGetDevice(&dev);
     if (configured.needed(dev)) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (max_warps(D, KV, NH) + 1) * 8 * NH * (D + 4) * 4);
+                                                   max_warps(D, KV, NH) * 8 * NH * (D + 4) * 4);
         if (e != cudaSuccess) return e;
         configured.mark(dev);
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)sp.ctas, (unsigned)a.s.Hkv, (unsigned)groups);
     cfg.blockDim = dim3((unsigned)sp.warps * 32, 1, 1);
-    cfg.dynamicSmemBytes = (size_t)((sp.warps + 1) * cols * (D + 4) * 4);
+    cfg.dynamicSmemBytes = (size_t)(sp.warps * cols * (D + 4) * 4);
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

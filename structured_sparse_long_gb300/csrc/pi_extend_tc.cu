@@ -547,9 +547,9 @@ __device__ __noinline__ void again(const Args &args, int L0, int n_blocks) {
             if (!__any_sync(0xffffffffu, went_bad(seen)) || lse != lse) continue;  // (a NaN among the row's own scores)
             const RowKeys keys = row_keys(s, i, k.g, args.m_first, ea.q + (long long)(k.tq + t) * ea.q_stride + (long long)h * D,
                                           ea.batch.table + (long long)k.b * cache.width, ea.alpha ? ea.alpha + row : nullptr);
-            if (!CONVERTED) row_columns<D, kKvBf16, D>(cache, keys, 0, out);
-            else if (cache.kv_type == kKvE4m3) row_columns<D, kKvE4m3, D>(cache, keys, 0, out);
-            else row_columns<D, kKvInt8, D>(cache, keys, 0, out);
+            if (!CONVERTED) attend_row<D, kKvBf16>(cache, keys, out);
+            else if (cache.kv_type == kKvE4m3) attend_row<D, kKvE4m3>(cache, keys, out);
+            else attend_row<D, kKvInt8>(cache, keys, out);
         }
     }
 }

@@ -130,6 +130,10 @@ __device__ __forceinline__ uint32_t smem_addr(const void *p) { return static_cas
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// Before a CTA ends whose shared memory others read: past it, all have (their values were used; no writes need to be seen).
+__device__ __forceinline__ void cluster_leave() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
 // Address of another CTA's copy of a shared-memory location, and a load from there.
 __device__ __forceinline__ uint32_t peer_addr(uint32_t local, uint32_t rank) {
     uint32_t r;
@@ -139,6 +143,11 @@ __device__ __forceinline__ uint32_t peer_addr(uint32_t local, uint32_t rank) {
 __device__ __forceinline__ float2 ld_peer2(uint32_t addr) {
     float2 f;
     asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(f.x), "=f"(f.y) : "r"(addr));
+    return f;
+}
+__device__ __forceinline__ float4 ld_peer4(uint32_t addr) {
+    float4 f;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(f.x), "=f"(f.y), "=f"(f.z), "=f"(f.w) : "r"(addr));
     return f;
 }
 

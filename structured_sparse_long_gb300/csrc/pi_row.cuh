@@ -37,11 +37,11 @@ __device__ __forceinline__ void unpack8(const uint4 &x, float (&f)[8]) {
     }
 }
 
-// COLS (64 or 128) columns of the row from col0 on, to out + col0 ...  For the whole warp.
-template <int D, int KV, int COLS>
-__device__ __forceinline__ void row_columns(const PagedCache &c, const RowKeys &k, int col0, __nv_bfloat16 *out) {
-    constexpr int NC = COLS / 64;
-    const int lane = threadIdx.x & 31, col = col0 + 8 * (lane & 7);
+// The row, to out[d].  For the whole warp.
+template <int D, int KV>
+__device__ __forceinline__ void attend_row(const PagedCache &c, const RowKeys &k, __nv_bfloat16 *out) {
+    constexpr int NC = D / 64;
+    const int lane = threadIdx.x & 31, col = 8 * (lane & 7);
     const int n_band = k.i - k.lo + 1, n = n_band + k.n_skip;
     float m = -INFINITY, l = 0.f, o[NC][8] = {};
     for (int k0 = 0; k0 < n; k0 += 32) {  // a key per lane for the scores
