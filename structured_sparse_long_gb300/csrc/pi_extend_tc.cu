@@ -166,7 +166,93 @@ __device__ __forceinline__ PlanBlock plan_block(const PlanArgs &a, int b, int t0
     return k;
 }
 
-// What CTA `part` of PLAN_CTAS does for the plan.
+__device__ __forceinline__ PlanBlock *plan_blocks(const PlanArgs &a) {
+    return reinterpret_cast<PlanBlock *>(reinterpret_cast<char *>(a.plan) + PLAN_HEAD);
+}
+
+// n tokens at ctx ..: blocks at multiples of R, or one where a short chunk starts
+__device__ __forceinline__ int first_block(int n, int ctx, int R) { return n <= R ? ctx : ctx / R * R; }
+__device__ __forceinline__ int count_blocks(int n, int ctx, int R) { return (ctx + n - 1 - first_block(n, ctx, R)) / R + 1; }
+
+// Block `x` of the plan: the one at `place` of sequence b, whose bf16 tiles (8-bit caches) are in slot and the following.
+__device__ __forceinline__ void write_block(const PlanArgs &a, int x, int b, int t0, int n, int ctx, int place, int slot) {
+    PlanBlock *to = plan_blocks(a) + x;
+    const PlanBlock k = plan_block(a, b, t0, n, ctx, first_block(n, ctx, a.R) + place * a.R);
+    int4 *out = reinterpret_cast<int4 *>(to);
+    out[0] = make_int4(k.p0, k.tq, k.first, k.last);
+    out[1] = make_int4(k.b, k.lo, k.n_band, k.n_tiles);
+    out[2] = make_int4(k.cpb, (int)k.inv_cpb, k.full_lo, k.full_hi);
+    if (!a.slots) return;
+    const SeqTiles q = seq_tiles(a.s, a.m_first, n, ctx);
+    // a tile of the band (or any, where they are all in one run) is in slot + x - slot_lo, one of skip window w in
+    // slot_windows + w * per_window + x - (its first tile)
+    out[3] = make_int4(slot, q.lo, q.band_tiles ? slot + q.band_tiles : -1, ctx);
+    to->per_window = q.per_window;
+}
+
+// A warp's view of a batch of at most 32 sequences, one to a lane.
+struct Lanes {
+    int t0, n, ctx, slots_upto;  // n = 0: none, or out of range; slots of the sequences up to and including this one
+    SeqTiles q;
+    bool sorted;  // the warp's: offsets do not decrease
+
+    __device__ __forceinline__ Lanes() : t0(0), n(0), ctx(0), slots_upto(0), q{}, sorted(true) {}
+    __device__ __forceinline__ Lanes(const PlanArgs &a, bool record) : t0(0), n(0), ctx(0), slots_upto(0), q{} {
+        const int lane = threadIdx.x & 31;
+        sorted = true;
+        if (lane < a.bt.B) {
+            const int t1 = a.bt.cu[lane + 1];
+            t0 = a.bt.cu[lane];
+            ctx = a.bt.ctx[lane];
+            sorted = t0 <= t1;
+            if (sequence_ok(a.c, a.bt, t0, t1, ctx)) n = t1 - t0;
+            else if (record) record_index(a.index_word);
+        }
+        sorted = __all_sync(0xffffffffu, sorted);
+        if (a.slots) {
+            if (n > 0) q = seq_tiles(a.s, a.m_first, n, ctx);
+            slots_upto = sums(q.slots);
+        }
+    }
+    static __device__ __forceinline__ int sums(int x) {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int w = 1; w < 32; w <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, w);
+            if (lane >= w) x += y;
+        }
+        return x;
+    }
+};
+
+// What CTA `part` of PLAN_CTAS does for the plan of at most 32 sequences: one round of loads, no barrier (with make_plan
+// below a 1024-token chunk over bf16 pages takes 13.4 us instead of 12.6).  The kernels that use it need no list of slots.
+__device__ __forceinline__ void make_short_plan(const PlanArgs &a, int part) {
+    const int lane = threadIdx.x & 31, wid = part * (PLAN_THREADS / 32) + (threadIdx.x >> 5);
+    const Lanes v(a, wid == 0);
+    const int cnt = v.n > 0 ? count_blocks(v.n, v.ctx, a.R) : 0, upto = Lanes::sums(cnt);
+    const int total = v.sorted ? __shfl_sync(0xffffffffu, upto, 31) : 0;
+    for (int x0 = wid * 32; x0 < total; x0 += PLAN_CTAS * PLAN_THREADS) {
+        const int x = x0 + lane;
+        int o = 0;  // the sequence of block x: as many have ended before
+#pragma unroll
+        for (int step = 16; step > 0; step >>= 1)
+            if (__shfl_sync(0xffffffffu, upto, o + step - 1) <= x) o += step;
+        auto of = [&](int y) { return __shfl_sync(0xffffffffu, y, o); };
+        const int t0 = of(v.t0), n = of(v.n), ctx = of(v.ctx), place = x - of(upto - cnt), slot = of(v.slots_upto - v.q.slots);
+        if (x < total) write_block(a, x, o, t0, n, ctx, place, slot);
+    }
+    if (wid == 0 && lane == 31) {
+        a.plan[0] = total;
+        a.plan[1] = v.sorted ? v.slots_upto : 0;
+        if (!v.sorted) record_index(a.index_word);
+    }
+}
+
+// (for the conversion, whose registers it would crowd; in the plan's own kernel a call costs 0.7 us)
+__device__ __noinline__ void make_short_plan_apart(const PlanArgs &a, int part) { make_short_plan(a, part); }
+
+// The same for any number of sequences, PLAN_THREADS at a time; with the list of slots.
 __device__ __forceinline__ void make_plan(const PlanArgs &a, int part) {
     const PagedCache &c = a.c;
     const PagedBatch &bt = a.bt;
@@ -176,7 +262,6 @@ __device__ __forceinline__ void make_plan(const PlanArgs &a, int part) {
     __shared__ int slots_upto[PLAN_THREADS];
     __shared__ int warp_sum[PLAN_THREADS / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    PlanBlock *blocks = reinterpret_cast<PlanBlock *>(reinterpret_cast<char *>(plan) + PLAN_HEAD);
     // Offsets that decrease would let sequences overlap and their blocks outgrow the plan: nothing is planned.
     bool sorted = true;
     for (int b = tid; b < bt.B; b += PLAN_THREADS) sorted = sorted && bt.cu[b] <= bt.cu[b + 1];
@@ -187,8 +272,6 @@ __device__ __forceinline__ void make_plan(const PlanArgs &a, int part) {
         }
         return;
     }
-    // n tokens at ctx ..: blocks at multiples of R, or one where a short chunk starts
-    auto start = [&](int n, int ctx) { return n <= R ? ctx : ctx / R * R; };
     // inclusive sums over the CTA's threads into buf; returns the total
     auto scan = [&](int x, int *buf) -> int {
         int sum = x;
@@ -224,7 +307,7 @@ __device__ __forceinline__ void make_plan(const PlanArgs &a, int part) {
             const int t0 = bt.cu[b], t1 = bt.cu[b + 1], ctx = bt.ctx[b];
             if (!sequence_ok(c, bt, t0, t1, ctx)) record_index(index_word);
             else if (t1 > t0) {
-                cnt = (ctx + (t1 - t0) - 1 - start(t1 - t0, ctx)) / R + 1;
+                cnt = count_blocks(t1 - t0, ctx, R);
                 if (a.slots) slots = seq_tiles(a.s, a.m_first, t1 - t0, ctx).slots;
             }
         }
@@ -234,19 +317,7 @@ __device__ __forceinline__ void make_plan(const PlanArgs &a, int part) {
             int place;
             const int o = owner(upto, x, place);
             const int t0 = bt.cu[b0 + o], n = bt.cu[b0 + o + 1] - t0, ctx = bt.ctx[b0 + o];
-            const PlanBlock k = plan_block(a, b0 + o, t0, n, ctx, start(n, ctx) + place * R);
-            int4 *out = reinterpret_cast<int4 *>(blocks + base + x);
-            out[0] = make_int4(k.p0, k.tq, k.first, k.last);
-            out[1] = make_int4(k.b, k.lo, k.n_band, k.n_tiles);
-            out[2] = make_int4(k.cpb, (int)k.inv_cpb, k.full_lo, k.full_hi);
-            if (a.slots) {
-                const SeqTiles q = seq_tiles(a.s, a.m_first, n, ctx);
-                // a tile of the band (or any, where they are all in one run) is in slot + x - slot_lo, one of skip
-                // window w in slot_windows + w * per_window + x - (its first tile)
-                const int slot = slot_base + (o > 0 ? slots_upto[o - 1] : 0);
-                out[3] = make_int4(slot, q.lo, q.band_tiles ? slot + q.band_tiles : -1, ctx);
-                blocks[base + x].per_window = q.per_window;
-            }
+            write_block(a, base + x, b0 + o, t0, n, ctx, place, a.slots ? slot_base + (o > 0 ? slots_upto[o - 1] : 0) : 0);
         }
         for (int x = part * PLAN_THREADS + tid; x < total_slots; x += PLAN_CTAS * PLAN_THREADS) {
             int place;
@@ -264,10 +335,11 @@ __device__ __forceinline__ void make_plan(const PlanArgs &a, int part) {
     }
 }
 
-__global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const PlanArgs a) {
+__global__ void __launch_bounds__(PLAN_THREADS) plan_kernel(const __grid_constant__ PlanArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
-    make_plan(a, blockIdx.x);
+    if (a.bt.B <= 32) make_short_plan(a, blockIdx.x);
+    else make_plan(a, blockIdx.x);
 }
 
 // ------------------------------------------------------------------ 8-bit tiles to bf16
@@ -301,13 +373,13 @@ __device__ __forceinline__ bool attended(const PlanArgs &a, int b, int x, int y)
 // LANES (at most 32 sequences): the kernel makes the plan too, in its first CTAs, and the others find their slots' sequences
 // themselves, one sequence to a lane, instead of waiting for a plan kernel.
 template <int D, int KV, bool LANES>
-__global__ void __launch_bounds__(CONVERT_WARPS * 32) convert_kernel(const ConvertArgs args) {
+__global__ void __launch_bounds__(CONVERT_WARPS * 32, D == 64 ? 4 : 3) convert_kernel(const __grid_constant__ ConvertArgs args) {
     const PlanArgs &a = args.p;
     static_assert(CONVERT_WARPS * 32 == PLAN_THREADS, "a CTA of the plan");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;");
     if (LANES && blockIdx.x < PLAN_CTAS) {
-        make_plan(a, blockIdx.x);
+        make_short_plan_apart(a, blockIdx.x);
         return;
     }
     const int cta = blockIdx.x - (LANES ? PLAN_CTAS : 0), ctas = gridDim.x - (LANES ? PLAN_CTAS : 0);
@@ -315,26 +387,9 @@ __global__ void __launch_bounds__(CONVERT_WARPS * 32) convert_kernel(const Conve
     const int lane = threadIdx.x & 31;
     constexpr int PER_ROW = D / 8, ITER = CHUNK * PER_ROW / 32;  // pieces of 8 codes (16 bytes of bf16); pieces per lane
     constexpr int SB = D / kScaleBlock;                          // scale bytes of a row
-    // LANES: sequence `lane`, its slots up to and including its own, and the tiles in them
-    int n = 0, ctx = 0, upto = 0;
-    SeqTiles q{};
-    if (LANES) {
-        bool sorted = true;
-        if (lane < a.bt.B) {
-            const int t0 = a.bt.cu[lane], t1 = a.bt.cu[lane + 1];
-            ctx = a.bt.ctx[lane];
-            sorted = t0 <= t1;
-            if (sequence_ok(c, a.bt, t0, t1, ctx)) n = t1 - t0;  // the plan records what is out of range
-        }
-        if (!__all_sync(0xffffffffu, sorted)) return;
-        if (n > 0) q = seq_tiles(a.s, a.m_first, n, ctx);
-        upto = q.slots;
-#pragma unroll
-        for (int w = 1; w < 32; w <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, upto, w);
-            if (lane >= w) upto += y;
-        }
-    }
+    const Lanes v = LANES ? Lanes(a, false) : Lanes();  // (the plan records what is out of range)
+    if (LANES && !v.sorted) return;
+    const int upto = v.slots_upto;
     const int heads = c.Hkv * 2, items = (LANES ? __shfl_sync(0xffffffffu, upto, 31) : a.plan[1]) * heads, step = ctas * CONVERT_WARPS;
     const int half = c.page < CHUNK ? lane >> 4 : 0;
     // an item's sequence, tile and page (page 16: of the lane's half): requested an item ahead
@@ -344,8 +399,8 @@ __global__ void __launch_bounds__(CONVERT_WARPS * 32) convert_kernel(const Conve
         if (!LANES) return __ldg(a.slots + slot);
         const int b = __ffs(__ballot_sync(0xffffffffu, upto > slot)) - 1;
         auto of = [&](int y) { return __shfl_sync(0xffffffffu, y, b); };
-        const SeqTiles qb{of(q.lo), of(q.band_tiles), of(q.per_window), of(q.slots)};
-        return make_int2(b, slot_tile(a.s, a.m_first, qb, of(n), of(ctx), slot - of(upto) + qb.slots));
+        const SeqTiles qb{of(v.q.lo), of(v.q.band_tiles), of(v.q.per_window), of(v.q.slots)};
+        return make_int2(b, slot_tile(a.s, a.m_first, qb, of(v.n), of(v.ctx), slot - of(upto) + qb.slots));
     };
     auto page = [&](int2 st) -> int {
         const int pos = st.y * CHUNK + half * 16;
@@ -363,7 +418,8 @@ __global__ void __launch_bounds__(CONVERT_WARPS * 32) convert_kernel(const Conve
         pg = page(st);
         st_next = slot_of(x + 2 * step);
         if (now.y < 0) continue;
-        const int v = x & 1, slot = x / heads, g = (x - slot * heads) >> 1, pos = now.y * CHUNK;
+        const bool val = x & 1;
+        const int slot = x / heads, g = (x - slot * heads) >> 1, pos = now.y * CHUNK;
         if ((unsigned)p_now >= (unsigned)c.n_pages) {
             p_now = -1;
             if ((lane & 15) == 0 && attended(a, now.x, pos + half * 16, pos + (c.page < CHUNK ? half * 16 + 15 : CHUNK - 1)))
@@ -372,7 +428,7 @@ __global__ void __launch_bounds__(CONVERT_WARPS * 32) convert_kernel(const Conve
         const long long sh = (long long)slot * c.Hkv + g;
         // A tile's 32 rows (page 16: each half's 16) are contiguous: a lane's pieces lie 256 bytes apart, and lane r holds the
         // scale bytes of row r.
-        const uint8_t *codes = static_cast<const uint8_t *>(v ? c.v : c.k), *scales = v ? c.v_scale : c.k_scale;
+        const uint8_t *codes = static_cast<const uint8_t *>(val ? c.v : c.k), *scales = val ? c.v_scale : c.k_scale;
         const int p0 = __shfl_sync(0xffffffffu, p_now, 0), p1 = __shfl_sync(0xffffffffu, p_now, 16);
         const int at = pos & (c.page - 1), at1 = c.page < CHUNK ? -16 : at;  // first row of the second half less 16
         const uint2 *c0 = reinterpret_cast<const uint2 *>(codes + (long long)row_in_page(c, max(p0, 0), g, at) * D) + lane;
@@ -389,7 +445,7 @@ __global__ void __launch_bounds__(CONVERT_WARPS * 32) convert_kernel(const Conve
             const long long row = row_in_page(c, p, g, 0) + (lane < 16 ? at : at1) + lane;
             sc = SB == 4 ? __ldg(reinterpret_cast<const uint32_t *>(scales) + row) : __ldg(reinterpret_cast<const uint16_t *>(scales) + row);
         }
-        uint4 *out = reinterpret_cast<uint4 *>((v ? args.v : args.k) + sh * (CHUNK * D)) + lane;
+        uint4 *out = reinterpret_cast<uint4 *>((val ? args.v : args.k) + sh * (CHUNK * D)) + lane;
         auto piece = [&](const uint2 &x, int u, bool big) {
             const uint32_t s4 = __shfl_sync(0xffffffffu, sc, u * (32 / PER_ROW) + lane / PER_ROW);
             const Scale2<KV> s2 = scale_same<KV>(s4 >> (8 * (lane % PER_ROW / 4)) & 0xffu);
@@ -601,6 +657,7 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     const uint32_t tbase = *tmem_slot;
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan is written, and the tiles are converted
 
+    // (The first block's entry of the plan is loaded beside the number of blocks: the grid is no larger than the plan's room.)
     const int n_blocks = args.plan[0] * args.ngrp;
     const int L0 = blockIdx.x, LS = gridDim.x;
     auto next_block = [&](int L) -> int { return (L < n_blocks - LS) ? L + LS : n_blocks; };
@@ -641,10 +698,10 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     // Walks the tiles of every block of the CTA: issue(block, the next one, is there one, tile, tiles so far, planes and
     // row) by the whole warp, with the entries of a block's first 32 tiles requested a block ahead.
     auto walk_tiles = [&](auto &&issue) {
-        if (L0 >= n_blocks) return true;
         Block k, kn;
         int e0, e1, row;
         load_block<CONVERTED>(args, L0, k);
+        if (L0 >= n_blocks) return true;
         lookup(k, 0, e0, e1, row);
         uint32_t n = 0;
         for (int L = L0;;) {
@@ -747,10 +804,10 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             return ok;
         };
         bool ok = true;
+        Block k0;
+        load_block<CONVERTED>(args, L0, k0);
         if (L0 < n_blocks) {
-            Block k;
-            load_block<CONVERTED>(args, L0, k);
-            if (lane == 0) issue_q(k);
+            if (lane == 0) issue_q(k0);
             q_loads = 1;
             __syncwarp();
         }
@@ -788,7 +845,7 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         uint32_t gs = 0;
         int kb = 0;
         bool ok = true;
-        int n_next = L0 < n_blocks ? plan_at(args, L0)[1].w : 0;
+        int n_next = plan_at(args, L0)[1].w;
         for (int L = L0; ok && L < n_blocks; L = next_block(L), ++kb) {
             const int n_tiles = n_next;
             if (next_block(L) < n_blocks) n_next = plan_at(args, next_block(L))[1].w;
@@ -846,7 +903,7 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             load_rows(args, L, kn);
             load_tiles(args, L, kn);
         };
-        if (L0 < n_blocks) load(L0);
+        load(L0);
         for (int L = L0; ok && L < n_blocks; L = next_block(L)) {
             const PlanBlock k = kn;
             if (next_block(L) < n_blocks) load(next_block(L));
@@ -912,9 +969,9 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         int kb = 0;
         PlanBlock k{}, kn{};  // this block and the next one (its rows; its tiles are loaded before the epilogue)
         float al_next = 1.f;
+        load_rows(args, L0, k);
+        load_tiles(args, L0, k);
         if (L0 < n_blocks) {
-            load_rows(args, L0, k);
-            load_tiles(args, L0, k);
             if (next_block(L0) < n_blocks) load_rows(args, next_block(L0), kn);
             al_next = alpha_of(k, L0);
         }
