@@ -94,7 +94,7 @@ __device__ __forceinline__ void locate_run(const PagedCache &c, const PagedBatch
     int b;
     pos = locate(c, bt, t, b, index_word);
     const bool first = pos >= 0;
-    const int end = first ? __ldg(bt.cu + b + 1) : t + 1;  // tokens of the first one's sequence end here
+    const int end = first ? ld_now(bt.cu + b + 1) : t + 1;  // tokens of the first one's sequence end here
     if (lane > 0) pos = first && lane < TOK && t + lane < end ? pos + lane : -1;
     int seq = b;
 #pragma unroll 1
@@ -140,8 +140,8 @@ __global__ void __launch_bounds__(WARPS * 32) append_kernel(const AppendArgs a) 
             const uint4 *pv = reinterpret_cast<const uint4 *>(a.v + (long long)(t + i) * a.v_stride) + j * Piece<KV>::N;
 #pragma unroll
             for (int x = 0; x < Piece<KV>::N; ++x) {
-                k[i].x[x] = in ? __ldg(pk + x) : make_uint4(0u, 0u, 0u, 0u);
-                v[i].x[x] = in ? __ldg(pv + x) : make_uint4(0u, 0u, 0u, 0u);
+                k[i].x[x] = in ? ld_now(pk + x) : make_uint4(0u, 0u, 0u, 0u);
+                v[i].x[x] = in ? ld_now(pv + x) : make_uint4(0u, 0u, 0u, 0u);
             }
         }
     };

@@ -83,13 +83,13 @@ __device__ __forceinline__ void load_k(Frag<D, KV> &f, const PagedCache &c, int 
     if constexpr (KV == kKvBf16) {
         const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(c.k) + (long long)row * D) + t;
 #pragma unroll
-        for (int x = 0; x < f.C; ++x) f.k[half][x] = row >= 0 ? ldg_stream(p + 4 * x) : make_uint4(0u, 0u, 0u, 0u);
+        for (int x = 0; x < f.C; ++x) f.k[half][x] = row >= 0 ? ld_stream(p + 4 * x) : make_uint4(0u, 0u, 0u, 0u);
     } else {
         const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(c.k) + (long long)row * D) + t;
 #pragma unroll
-        for (int x = 0; x < f.C; ++x) f.k[half][x] = row >= 0 ? ldg_stream(p + 4 * x) : make_uint4(0u, 0u, 0u, 0u);
-        if (D == 128) f.ks[half] = row >= 0 ? __ldg(reinterpret_cast<const uint32_t *>(c.k_scale) + row) : 0u;
-        else f.ks[half] = row >= 0 ? __ldg(reinterpret_cast<const uint16_t *>(c.k_scale) + row) : 0u;
+        for (int x = 0; x < f.C; ++x) f.k[half][x] = row >= 0 ? ld_stream(p + 4 * x) : make_uint4(0u, 0u, 0u, 0u);
+        if (D == 128) f.ks[half] = row >= 0 ? ld_now(reinterpret_cast<const uint32_t *>(c.k_scale) + row) : 0u;
+        else f.ks[half] = row >= 0 ? ld_now(reinterpret_cast<const uint16_t *>(c.k_scale) + row) : 0u;
     }
 }
 
@@ -98,18 +98,18 @@ __device__ __forceinline__ void load_v(Frag<D, KV> &f, const PagedCache &c, int 
     if constexpr (KV == kKvBf16) {
         const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(c.v) + (long long)row * D) + g;
 #pragma unroll
-        for (int x = 0; x < f.CV; ++x) f.v[which][x] = row >= 0 ? ldg_stream(p + 8 * x) : make_uint4(0u, 0u, 0u, 0u);
+        for (int x = 0; x < f.CV; ++x) f.v[which][x] = row >= 0 ? ld_stream(p + 8 * x) : make_uint4(0u, 0u, 0u, 0u);
     } else {
         const uint8_t *p = static_cast<const uint8_t *>(c.v) + (long long)row * D + g * (D / 8);
         if constexpr (D == 128) {
-            const uint4 x = row >= 0 ? ldg_stream(reinterpret_cast<const uint4 *>(p)) : make_uint4(0u, 0u, 0u, 0u);
+            const uint4 x = row >= 0 ? ld_stream(reinterpret_cast<const uint4 *>(p)) : make_uint4(0u, 0u, 0u, 0u);
             f.v[which][0] = x.x; f.v[which][1] = x.y; f.v[which][2] = x.z; f.v[which][3] = x.w;
         } else {
-            const uint2 x = row >= 0 ? __ldg(reinterpret_cast<const uint2 *>(p)) : make_uint2(0u, 0u);
+            const uint2 x = row >= 0 ? ld_now(reinterpret_cast<const uint2 *>(p)) : make_uint2(0u, 0u);
             f.v[which][0] = x.x; f.v[which][1] = x.y;
         }
         // elements (D / 8) g ... lie in one block of 32
-        f.vs[which] = row >= 0 ? __ldg(c.v_scale + (long long)row * (D / kScaleBlock) + g * (D / 8) / kScaleBlock) : 0u;
+        f.vs[which] = row >= 0 ? ld_now(c.v_scale + (long long)row * (D / kScaleBlock) + g * (D / 8) / kScaleBlock) : 0u;
     }
 }
 
@@ -155,7 +155,7 @@ __device__ __forceinline__ void load_q(uint2 (&q)[D / 16], const __nv_bfloat16 *
     for (int x = 0; x < D / 32; ++x) {
         // bf16 cache: elements 32 x + 8 t ...; 8 bits: halves of 64 (x / 2) + 16 t ...
         const int at = KV == kKvBf16 ? 4 * x + t : 8 * (x >> 1) + 2 * t + (x & 1);
-        const uint4 u = ok ? __ldg(p + at) : make_uint4(0u, 0u, 0u, 0u);
+        const uint4 u = ok ? ld_now(p + at) : make_uint4(0u, 0u, 0u, 0u);
         q[2 * x] = make_uint2(u.x, u.y);
         q[2 * x + 1] = make_uint2(u.z, u.w);
     }
@@ -236,7 +236,7 @@ paged_rows_kernel(const __grid_constant__ Args a) {
         // the table's first entries are on their way while the length is (5.76 -> 5.70 us; copied to shared memory, 5.58 instead
         // of 5.30 in a later state)
         if (32 * threadIdx.x < c.width) asm volatile("prefetch.global.L1 [%0];" ::"l"(a.batch.table + (long long)b * c.width + 32 * threadIdx.x));
-        last = __ldg(a.lens + b) - 1;
+        last = ld_now(a.lens + b) - 1;
         if (last < -1 || last >= (long long)c.width << c.page_log2) {
             if (threadIdx.x == 0) record_index(a.index_word);
             last = -1;
@@ -245,25 +245,25 @@ paged_rows_kernel(const __grid_constant__ Args a) {
     } else {
         if (blockIdx.z == 0 && kvh == 0 && rank == 0)  // offsets that decrease may hide their sequence from the search below
             for (int j = threadIdx.x; j < a.batch.B; j += blockDim.x)
-                if (__ldg(a.batch.cu + j) > __ldg(a.batch.cu + j + 1)) record_index(a.index_word);
+                if (ld_now(a.batch.cu + j) > ld_now(a.batch.cu + j + 1)) record_index(a.index_word);
         // sequence b's token groups are numbered from (cu[b] + b (group - 1)) / group on, which leaves each its ceil(n / group)
         const int id = blockIdx.z, B = a.batch.B;
         auto start = [&](int j, int at) -> long long { return ((long long)at + (long long)j * (a.group - 1)) / a.group; };
         int t0, t1, ctx;
         if (B <= 32) {  // a sequence per lane, so that one round of loads has everything
             const bool in = lane < B;
-            const int c0 = in ? __ldg(a.batch.cu + lane) : 0, c1 = in ? __ldg(a.batch.cu + lane + 1) : 0, x = in ? __ldg(a.batch.ctx + lane) : 0;
+            const int c0 = in ? ld_now(a.batch.cu + lane) : 0, c1 = in ? ld_now(a.batch.cu + lane + 1) : 0, x = in ? ld_now(a.batch.ctx + lane) : 0;
             b = __popc(__ballot_sync(kFull, in && start(lane + 1, c1) <= id));
             t0 = __shfl_sync(kFull, c0, b & 31);
             t1 = __shfl_sync(kFull, c1, b & 31);
             ctx = __shfl_sync(kFull, x, b & 31);
             if (b >= B) return;
         } else {
-            b = find_sequence(B, [&](int j) { return start(j, __ldg(a.batch.cu + j)) <= id; });
+            b = find_sequence(B, [&](int j) { return start(j, ld_now(a.batch.cu + j)) <= id; });
             if (b >= B) return;
-            t0 = __ldg(a.batch.cu + b);
-            t1 = __ldg(a.batch.cu + b + 1);
-            ctx = __ldg(a.batch.ctx + b);
+            t0 = ld_now(a.batch.cu + b);
+            t1 = ld_now(a.batch.cu + b + 1);
+            ctx = ld_now(a.batch.ctx + b);
         }
         if (!sequence_ok(c, a.batch, t0, t1, ctx)) {
             if (threadIdx.x == 0) record_index(a.index_word);
@@ -291,7 +291,7 @@ paged_rows_kernel(const __grid_constant__ Args a) {
         for (int e = 0; e < 2; ++e) {
             const int y = 8 * nh + 2 * t + e;
             tok[nh][e] = TOKENS ? y / G : 0;
-            const float al = a.alpha && y < cols ? __ldg(a.alpha + row_of(y)) : 1.f;
+            const float al = a.alpha && y < cols ? ld_now(a.alpha + row_of(y)) : 1.f;
             offb[nh][e] = a.alpha ? log2f(al) : 0.f;
             offs[nh][e] = log2f(1.f - al);
         }

@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(CONVERT_WARPS * 32, D == 64 ? 4 : 3) convert_k
     auto slot_of = [&](int x) -> int2 {
         if (x >= items) return make_int2(0, -1);
         const int slot = x / heads;
-        if (!LANES) return __ldg(a.slots + slot);
+        if (!LANES) return ld_now(a.slots + slot);
         const int b = __ffs(__ballot_sync(0xffffffffu, upto > slot)) - 1;
         auto of = [&](int y) { return __shfl_sync(0xffffffffu, y, b); };
         const SeqTiles qb{of(v.q.lo), of(v.q.band_tiles), of(v.q.per_window), of(v.q.slots)};
@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(CONVERT_WARPS * 32, D == 64 ? 4 : 3) convert_k
     };
     auto page = [&](int2 st) -> int {
         const int pos = st.y * CHUNK + half * 16;
-        return st.y >= 0 && pos < c.width << c.page_log2 ? __ldg(a.bt.table + (long long)st.x * c.width + (pos >> c.page_log2)) : -1;
+        return st.y >= 0 && pos < c.width << c.page_log2 ? ld_now(a.bt.table + (long long)st.x * c.width + (pos >> c.page_log2)) : -1;
     };
     int x = cta * CONVERT_WARPS + (threadIdx.x >> 5);
     int2 st = slot_of(x), st_next = slot_of(x + step);
@@ -437,13 +437,13 @@ __global__ void __launch_bounds__(CONVERT_WARPS * 32, D == 64 ? 4 : 3) convert_k
 #pragma unroll
         for (int u = 0; u < ITER; ++u) {
             const bool in = (u < ITER / 2 ? p0 : p1) >= 0;
-            w[u] = in ? __ldg((u < ITER / 2 ? c0 : c1) + u * 32) : make_uint2(0u, 0u);
+            w[u] = in ? ld_now((u < ITER / 2 ? c0 : c1) + u * 32) : make_uint2(0u, 0u);
         }
         uint32_t sc = 0u;
         const int p = lane < 16 ? p0 : p1;
         if (p >= 0) {
             const long long row = row_in_page(c, p, g, 0) + (lane < 16 ? at : at1) + lane;
-            sc = SB == 4 ? __ldg(reinterpret_cast<const uint32_t *>(scales) + row) : __ldg(reinterpret_cast<const uint16_t *>(scales) + row);
+            sc = SB == 4 ? ld_now(reinterpret_cast<const uint32_t *>(scales) + row) : ld_now(reinterpret_cast<const uint16_t *>(scales) + row);
         }
         uint4 *out = reinterpret_cast<uint4 *>((val ? args.v : args.k) + sh * (CHUNK * D)) + lane;
         auto piece = [&](const uint2 &x, int u, bool big) {
@@ -683,10 +683,10 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         const int *table = ea.batch.table + (long long)k.b * cache.width;
         row = key0 & (cache.page - 1);
         if (args.box == CHUNK) {
-            if (lo <= hi) e0 = __ldg(table + (key0 >> cache.page_log2));
+            if (lo <= hi) e0 = ld_now(table + (key0 >> cache.page_log2));
         } else {
-            if (lo <= min(hi, key0 + 15)) e0 = __ldg(table + (key0 >> cache.page_log2));
-            if (max(lo, key0 + 16) <= hi) e1 = __ldg(table + ((key0 + 16) >> cache.page_log2));
+            if (lo <= min(hi, key0 + 15)) e0 = ld_now(table + (key0 >> cache.page_log2));
+            if (max(lo, key0 + 16) <= hi) e1 = ld_now(table + ((key0 + 16) >> cache.page_log2));
         }
     };
     // page-table entry (or slot) -> plane of the page maps (one past the last, which reads as zeros, where there is no page)
@@ -962,7 +962,7 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         auto alpha_of = [&](const PlanBlock &d, int L) -> float {
             const int i = d.p0 + trow;
             if (!ea.alpha || i < d.first || i > d.last) return 1.f;
-            return __ldg(ea.alpha + (long long)(d.tq + trow) * s.H + first_head(args, L) + hh);
+            return ld_now(ea.alpha + (long long)(d.tq + trow) * s.H + first_head(args, L) + hh);
         };
         bool ok = true;
         uint32_t gsm = 0;

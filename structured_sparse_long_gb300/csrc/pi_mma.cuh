@@ -32,10 +32,10 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&t);
 }
 
-// 16 bytes that are read once: past L1.
-__device__ __forceinline__ uint4 ldg_stream(const uint4 *p) {
+// 16 bytes that are read once: past L1 (coherent, see ld_now).
+__device__ __forceinline__ uint4 ld_stream(const uint4 *p) {
     uint4 r;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
     return r;
 }
 
@@ -115,10 +115,10 @@ __device__ __forceinline__ void codes_to_bf16(uint32_t w, const Scale2<KV> &s, b
 template <int KV>
 __device__ __forceinline__ uint4 get8(const PagedCache &c, const void *pages, const uint8_t *scales, long long row, int col) {
     if constexpr (KV == kKvBf16) {
-        return __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(pages) + row * c.d + col));
+        return ld_now(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(pages) + row * c.d + col));
     } else {
-        const uint2 w = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(pages) + row * c.d + col));
-        const Scale2<KV> s = scale_same<KV>(__ldg(scales + row * (c.d / kScaleBlock) + col / kScaleBlock));
+        const uint2 w = ld_now(reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(pages) + row * c.d + col));
+        const Scale2<KV> s = scale_same<KV>(ld_now(scales + row * (c.d / kScaleBlock) + col / kScaleBlock));
         uint4 x;
         codes_to_bf16<KV>(w.x, s, s.big, x.x, x.y);
         codes_to_bf16<KV>(w.y, s, s.big, x.z, x.w);

@@ -26,12 +26,20 @@ constexpr int kScaleBlock = 32;       // elements per scale byte
 constexpr int kScaleNan = 255;        // byte of a block with a non-finite element
 constexpr int kMinScaleExp = -120;
 
+// A load of what the kernel before this one may have written.  These kernels start before that one ends (programmatic launch, and
+// griddepcontrol.wait before the first load), so nothing is constant for a kernel's life, as the non-coherent loads of __ldg
+// want it; they could also be moved above the wait.
+template <typename T>
+__device__ __forceinline__ T ld_now(const T *p) {
+    return *p;
+}
+
 __device__ __forceinline__ void record_index(int *word) { atomicCAS(word, kStatusOk, kStatusIndex); }
 
 // Row of the cache (of the [n_pages * Hkv * page] rows) that holds position pos of sequence b for
 // KV head 0, or -1 for a page-table entry outside the pool.  pos must be inside [0, width * page).
 __device__ __forceinline__ int page_of(const PagedCache &c, const int *table, long long b, int pos) {
-    const int pg = __ldg(table + b * c.width + (pos >> c.page_log2));
+    const int pg = ld_now(table + b * c.width + (pos >> c.page_log2));
     return (unsigned)pg < (unsigned)c.n_pages ? pg : -1;
 }
 __device__ __forceinline__ int row_in_page(const PagedCache &c, int pg, int g, int pos) {
@@ -81,9 +89,9 @@ __device__ __forceinline__ bool sequence_ok(const PagedCache &c, const PagedBatc
 // Position of packed token t in its sequence b, or -1 (t behind the last sequence, or an index out of
 // range, which is recorded).  For the whole warp.
 __device__ __forceinline__ int locate(const PagedCache &c, const PagedBatch &bt, int t, int &b, int *index_word) {
-    b = find_sequence(bt.B, [&](int j) { return __ldg(bt.cu + j) <= t; });
+    b = find_sequence(bt.B, [&](int j) { return ld_now(bt.cu + j) <= t; });
     if (b >= bt.B) return -1;
-    const int t0 = __ldg(bt.cu + b), t1 = __ldg(bt.cu + b + 1), ctx = __ldg(bt.ctx + b);
+    const int t0 = ld_now(bt.cu + b), t1 = ld_now(bt.cu + b + 1), ctx = ld_now(bt.ctx + b);
     if (!sequence_ok(c, bt, t0, t1, ctx) || t < t0 || t >= t1) {
         record_index(index_word);
         return -1;

@@ -59,7 +59,7 @@ __device__ __forceinline__ void attend_row(const PagedCache &c, const RowKeys &k
             for (int x = 0; x < D / 8; ++x) {
                 float a[8], b[8];
                 unpack8(get8<KV>(c, c.k, c.k_scale, row, 8 * x), a);
-                unpack8(__ldg(reinterpret_cast<const uint4 *>(k.q) + x), b);
+                unpack8(ld_now(reinterpret_cast<const uint4 *>(k.q) + x), b);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) dot = fmaf(a[e], b[e], dot);
             }

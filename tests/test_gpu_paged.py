@@ -645,6 +645,67 @@ def test_streams_run_side_by_side(n):
     assert pa.status() == 0
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3", "int8"])
+@pytest.mark.parametrize("H,Hkv,d,B", [(16, 4, 128, 3), (4, 4, 64, 40)])
+def test_steps_without_a_pause(kv, H, Hkv, d, B):
+    """A hundred generation steps enqueued one behind the other, and as a replayed graph of single steps, give what steps with a
+    synchronisation after each call give: every call sees what the calls before it wrote (its kernel starts early)."""
+    page, steps, first = 16, 100, 37
+    gen = torch.Generator().manual_seed(B)
+    width = (first + steps) // page + 1
+    order = torch.randperm(B * width, generator=gen).int().view(B, width).cuda()
+    new = normal(gen, steps, B, H + 2 * Hkv, d).cuda()
+    alpha = torch.rand(steps, B, H, generator=gen).cuda()
+    draft = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+
+    def run(pause=False, graph=False):
+        cache = pa.PagedCache.empty(B * width, Hkv, page, d, ref.DTYPE[kv])
+        lens = torch.full((B,), first, dtype=torch.int32, device="cuda")
+        table = torch.full_like(order, -1)
+        table[:, :first // page + 1] = order[:, :first // page + 1]
+        at = torch.zeros(1, dtype=torch.int64, device="cuda")
+        out = [torch.zeros(steps, B, H, d, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        x, a = torch.empty_like(new[0]), torch.empty_like(alpha[0])
+
+        def step():
+            stop = torch.cuda.synchronize if pause else lambda: None
+            x.copy_(new.index_select(0, at)[0])
+            a.copy_(alpha.index_select(0, at)[0])
+            table.scatter_(1, (lens // page).long()[:, None], order.gather(1, (lens // page).long()[:, None]))
+            stop()
+            pa.cache_append(x[:, H:H + Hkv], x[:, H + Hkv:], cache, table, draft, lens)
+            stop()
+            o1, _ = pa.extend(x[:, :H], cache, table, draft, lens, a, 20, 16, 2)
+            stop()
+            lens.add_(1)
+            o2, _ = pa.decode_paged(x[:, :H], cache, table, lens, a, 20, 16, 2)
+            stop()
+            out[0].index_copy_(0, at, o1[None])
+            out[1].index_copy_(0, at, o2[None])
+            at.add_(1)
+
+        if graph:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                step()  # a first step outside the capture
+            s.synchronize()
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                step()
+            for _ in range(steps - 1):
+                g.replay()
+        else:
+            for _ in range(steps):
+                step()
+        torch.cuda.synchronize()
+        assert pa.status() == 0
+        return out + [cache.k.view(torch.uint8), cache.v.view(torch.uint8)]
+
+    want = run(pause=True)
+    for got in (run(), run(graph=True)):
+        assert all(torch.equal(x, y) for x, y in zip(want, got))
+
+
 def test_threads_call_side_by_side():
     """Four host threads, each with a cache, a stream and outputs of its own, make the same calls at once that one makes alone."""
     from concurrent.futures import ThreadPoolExecutor
