@@ -5,7 +5,7 @@
 // written, or the other way round, so HBM bandwidth bounds long calls and the chain of dependent
 // loads (sequence, page, row) the short ones.
 //
-// A warp takes one packed token, or two neighbouring ones of a long call: its lanes take a token's Hkv * d elements K and V
+// A warp takes a packed token (long reads: four neighbouring ones): its lanes take the token's Hkv * d elements K and V
 // together, 8 at a time, or 16 where they are quantised, so that a block of 32 elements lies in two neighbouring lanes and
 // its largest magnitude takes one shuffle.  The tokens' sequence is searched by the whole warp (two rounds of probes for up
 // to 1024 sequences) while their elements are in flight.
@@ -120,42 +120,32 @@ __device__ __forceinline__ int token_of(const A &a, int &chunk) {
     return (int)t;
 }
 
-template <int KV, int TOK>
+template <int KV>
 __global__ void __launch_bounds__(WARPS * 32) append_kernel(const AppendArgs a) {
     int chunk;
-    const int t = token_of(a, chunk) * TOK, lane = threadIdx.x & 31;
+    const int t = token_of(a, chunk), lane = threadIdx.x & 31;
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (t >= a.batch.T) return;
     const PagedCache &c = a.cache;
-    constexpr int E = Piece<KV>::E;
+    constexpr int E = Piece<KV>::E, N = Piece<KV>::N;
     const int n = (c.Hkv << c.d_log2) / E;  // pieces of a token: an even number
-    const int last = a.batch.T - 1;
-    Piece<KV> k[TOK], v[TOK];
-    auto load = [&](int j) {
-#pragma unroll
-        for (int i = 0; i < TOK; ++i) {
-            const bool in = j < n && t + i <= last;
-            const uint4 *pk = reinterpret_cast<const uint4 *>(a.k + (long long)(t + i) * a.k_stride) + j * Piece<KV>::N;
-            const uint4 *pv = reinterpret_cast<const uint4 *>(a.v + (long long)(t + i) * a.v_stride) + j * Piece<KV>::N;
-#pragma unroll
-            for (int x = 0; x < Piece<KV>::N; ++x) {
-                k[i].x[x] = in ? ld_now(pk + x) : make_uint4(0u, 0u, 0u, 0u);
-                v[i].x[x] = in ? ld_now(pv + x) : make_uint4(0u, 0u, 0u, 0u);
-            }
-        }
-    };
     const int j = chunk * 32 + lane, col = j * E & (c.d - 1), head = j * E >> c.d_log2;
-    load(j);
-    int pos, pg;
-    locate_run<TOK>(c, a.batch, t, pos, pg, a.index_word);
+    const uint4 *pk = reinterpret_cast<const uint4 *>(a.k + (long long)t * a.k_stride) + j * N;
+    const uint4 *pv = reinterpret_cast<const uint4 *>(a.v + (long long)t * a.v_stride) + j * N;
+    Piece<KV> k, v;
 #pragma unroll
-    for (int i = 0; i < TOK; ++i) {
-        const int p = __shfl_sync(kFull, pos, i), g = __shfl_sync(kFull, pg, i);
-        const long long row = row_in_page(c, g, head, p);
-        put<KV>(c, c.k, c.k_scale, k[i], row, col, j < n && g >= 0);
-        put<KV>(c, c.v, c.v_scale, v[i], row, col, j < n && g >= 0);
+    for (int x = 0; x < N; ++x) {
+        k.x[x] = j < n ? ld_now(pk + x) : make_uint4(0u, 0u, 0u, 0u);
+        v.x[x] = j < n ? ld_now(pv + x) : make_uint4(0u, 0u, 0u, 0u);
     }
+    int pos, pg;
+    locate_run<1>(c, a.batch, t, pos, pg, a.index_word);
+    pos = __shfl_sync(kFull, pos, 0);
+    pg = __shfl_sync(kFull, pg, 0);
+    const long long row = row_in_page(c, pg, head, pos);
+    put<KV>(c, c.k, c.k_scale, k, row, col, j < n && pg >= 0);
+    put<KV>(c, c.v, c.v_scale, v, row, col, j < n && pg >= 0);
 }
 
 template <int KV, int TOK>
@@ -202,13 +192,11 @@ static cudaError_t launch(K kernel, int tokens, int piece, A a, cudaStream_t st)
 
 cudaError_t launch_append(const AppendArgs &a, cudaStream_t st) {
     using namespace cache;
-    // two tokens per warp once that leaves the SMs full of warps (65536 tokens of 4 heads, d = 128, int8: 33.7 us, one 34.2, four
-    // 39.9; rows that stay bf16 gain nothing: 17.5 us with one, 18.2 with two, for 16384 tokens of 12 heads, d = 64)
-    const bool two = a.batch.T >= 128 * sm_count();
+    // a token per warp (65536 tokens of 4 heads, d = 128, int8: 32.9 us; two per warp 34.3, four 39.9)
     switch (a.cache.kv_type) {
-        case kKvBf16: return launch(append_kernel<kKvBf16, 1>, 1, 8, a, st);
-        case kKvE4m3: return two ? launch(append_kernel<kKvE4m3, 2>, 2, 16, a, st) : launch(append_kernel<kKvE4m3, 1>, 1, 16, a, st);
-        default: return two ? launch(append_kernel<kKvInt8, 2>, 2, 16, a, st) : launch(append_kernel<kKvInt8, 1>, 1, 16, a, st);
+        case kKvBf16: return launch(append_kernel<kKvBf16>, 1, 8, a, st);
+        case kKvE4m3: return launch(append_kernel<kKvE4m3>, 1, 16, a, st);
+        default: return launch(append_kernel<kKvInt8>, 1, 16, a, st);
     }
 }
 
