@@ -52,17 +52,19 @@ __device__ __forceinline__ uint2 encode8(const uint4 &x, int e) {
         float y[4];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            y[2 * j] = __uint_as_float(w[2 * i + j] << 16) * inv;
-            y[2 * j + 1] = __uint_as_float(w[2 * i + j] & 0xffff0000u) * inv;
+            y[2 * j] = __uint_as_float(w[2 * i + j] << 16);
+            y[2 * j + 1] = __uint_as_float(w[2 * i + j] & 0xffff0000u);
         }
         if (KV == kKvE4m3) {
-            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
-            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0] * inv, y[1] * inv), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2] * inv, y[3] * inv), __NV_SATFINITE, __NV_E4M3);
             o[i] = lo | hi << 16;
         } else {
-            o[i] = 0;
+            // in 2^23 .. 2^24 the step is 1: the sum's rounding is the code's, and its low byte the code
+            uint32_t c[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) o[i] |= ((uint32_t)__float2int_rn(y[j]) & 0xffu) << (8 * j);
+            for (int j = 0; j < 4; ++j) c[j] = __float_as_uint(fmaf(y[j], inv, 12582912.f));
+            o[i] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
         }
     }
     return make_uint2(o[0], o[1]);
