@@ -4,7 +4,7 @@
 // A serving step makes these calls for every layer, and its kernels take a few microseconds, so their host time is what a caller
 // waits for.  Tensors are reached through torch's C++ interface: a check is a load, and a new tensor is made without parsing
 // Python arguments.  Calls one after the other from Python, with new outputs each (the same through the tensors' Python
-// methods, from C): one-token append 2.9 us (4.4), one-token attention 6.2 (9.5; its kernel takes 5.7), read of a ragged batch 7.6
+// methods, from C): one-token append 2.9 us (4.4), one-token attention 6.2 (9.5; its kernel takes 5.0), read of a ragged batch 7.6
 // (10.8; its kernel 7.3).
 // The interpreter lock is released where a call may wait (an allocation, a full launch queue).
 #include <torch/csrc/Exceptions.h>
