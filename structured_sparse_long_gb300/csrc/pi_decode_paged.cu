@@ -588,23 +588,35 @@ static int token_group(int G) { return std::max(1, 8 / G); }
 
 // Whether a call's chunks are so short that this kernel beats the tensor-core pipeline (pi_extend_tc.cu), whose blocks of 128
 // rows take about the same time however few of them hold queries.  Judged by the sizes that the host knows, as if all
-// sequences had the same length: the grid fits the SMs at once, or has at most 1.5 times as many CTAs as there would be
-// blocks (four times over an 8-bit cache, whose tiles the pipeline has to convert first).  Measured in us (this kernel /
-// pipeline), band 256, 4 skips, contexts of 8000:
-//   16 heads on 4, d = 128, bf16:  4 sequences x 32 tokens 11.2 / 13.5, x 64 15.7 / 13.7; 32 x 4 16.2 / 16.1, x 8 24.2 / 15.4;
-//                                  128 x 2 28.0 / 31.4, x 4 45.0 / 31.2;
-//                           e4m3:  32 x 8 20.3 / 29.0, x 16 35.0 / 28.3; 128 x 8 65 / 74, x 16 113 / 74
-//   12 on 12, d = 64, bf16: 32 x 16 20.2 / 21.6, x 32 34.7 / 20.6; 128 x 8 39.4 / 55.3, x 16 58.4 / 53.8
+// sequences had the same length, by two estimates in us: this kernel's launch and its rounds of tiles over the SMs' warps
+// (a CTA's start and merge count as six tiles), and the pipeline's launches and its turns of blocks, tile by tile, with the
+// conversion of an 8-bit cache.  Fitted to 84 shapes (16 heads on 4, d = 128, and 12 on 12, d = 64; 1 to 128 sequences of 2 to
+// 256 tokens; three types), of which it gets all but one right and that one 10 % wrong; of 108 others (other heads, bands and
+// skips, up to 8000 tokens) nine are 8 to 30 % slower than they could be.  For instance (this kernel / pipeline):
+//   16 heads on 4, d = 128, band 256, bf16:  1 sequence x 128 tokens 10.0 / 12.7, x 256 15.0 / 12.9; 32 x 4 15.6 / 14.2, x 8 16.9 / 14.1
+//                                     e4m3:  32 x 8 19.2 / 21.5, x 16 34.8 / 21.2; 128 x 4 41.3 / 55.6, x 8 68.1 / 54.8
+//   12 on 12, d = 64, band 128, bf16:  1 x 256 8.4 / 16.3; 32 x 16 13.6 / 17.2, x 32 23.5 / 24.0; 128 x 16 37.7 / 40.7
 bool extend_few_rows(const ExtendArgs &e) {
     const Shape &s = e.s;
+    const PagedCache &c = e.cache;
     const int G = s.H / s.Hkv, group = token_group(G);
     const long long T = e.batch.T, B = std::min<long long>(e.batch.B, T);
     if (G > 16 || s.Hkv > 65535 || (T + e.batch.B * (long long)(group - 1)) / group > 65535) return false;
-    if (decp::most_keys(s, e.cache, group) >= (1LL << 30)) return false;
-    const long long n = (T + B - 1) / B, ctas = B * ((n + group - 1) / group) * s.Hkv;
+    if (decp::most_keys(s, c, group) >= (1LL << 30)) return false;
+    const bool quant = c.kv_type != kKvBf16;
+    const long long n = (T + B - 1) / B, cap = (long long)c.width << c.page_log2;
+    const long long band = std::min(cap, s.mode == kModeEcp ? 2LL * s.k_local : s.k_local + 1LL);
+    const long long last = s.mode != kModeEcp && s.S > 0 ? std::min<long long>(s.S, cap / s.period) : 0;
+    const long long windows = last > 0 ? std::max(0LL, last - first_skip_multiple(s) + 1) : 0;
+    const long long tiles = (std::min(cap, band + group - 1) + windows * group + decp::KEYS - 1) / decp::KEYS;
+    const long long ctas = B * ((n + group - 1) / group) * s.Hkv, sms = sm_count();
+    const double rounds = (double)ctas * (double)(tiles + 6) / (double)(sms * decp::sm_warps(s.d, c.kv_type, group * G > 8 ? 2 : 1));
+    const double few = 6.0 + (quant ? 1.8 : 1.4) * rounds;
     const int heads = packed_heads(G), rows = 128 / heads;
-    const long long blocks = B * ((n + rows - 1) / rows) * (s.H / heads);
-    return ctas <= 2LL * sm_count() || 2 * ctas <= (e.cache.kv_type == kKvBf16 ? 3 : 8) * blocks;
+    const long long turns = (B * ((n + rows - 1) / rows) * (s.H / heads) - 1) / (2 * sms) + 1, m = std::min<long long>(n, rows);
+    const double block = (double)(band + m) / 32 + 1 + (double)windows * ((double)((m - 1) / 32) + 1.5);
+    const double converted = (double)(B * s.Hkv) * s.d / 64 * ((double)(band + n) / 32 + 1 + (double)windows * ((double)n / 32 + 1.5));
+    return few <= 7.5 + 0.45 * (double)turns * block + (quant ? 1.0 + 0.001 * converted : 0.0);
 }
 
 cudaError_t launch_extend_few(const ExtendArgs &e, cudaStream_t st) {
