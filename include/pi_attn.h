@@ -363,7 +363,9 @@ int pi_attn_cache_read(const pi_attn_cache_t *cache, const pi_attn_batch_t *batc
  *   sequence and skip window.  Deterministic.
  *
  * pi_attn_extend_workspace_size -- those bytes (0: none, or sizes that pi_attn_extend refuses);
- * of the cache only its sizes, type and pointers' alignment matter.
+ * of the cache only its sizes, type and pointers' alignment matter.  The sizes choose between
+ * two kernels, one of which needs none: a batch with fewer tokens may need more than one with more, so
+ * ask for each size that is used.
  */
 size_t pi_attn_extend_workspace_size(const pi_attn_cache_t *cache, int B, int T, int width, int H,
                                      int k_local, int period, int S, int mode);
