@@ -426,7 +426,7 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                     uint32_t sr[32], dr[32];
                     tmem_ld32(tS, sr);
                     tmem_ld32(tP, dr);
-                    tmem_wait_ld();
+                    tmem_wait_ld(sr, dr);
                     const bool v = clo <= chi;
                     const int cs = v ? clo : 0;
                     const float p = v ? fast_exp2(fmaf(select32(reinterpret_cast<const float *>(sr), cs), sc, bo)) : 0.f;
@@ -460,7 +460,7 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                         uint32_t sr[16], dr[16];
                         tmem_ld16(tS + half * 16, sr);
                         tmem_ld16(tP + half * 16, dr);
-                        tmem_wait_ld();
+                        tmem_wait_ld(sr, dr);
                         uint32_t pw[8], pp[8];
 #pragma unroll
                         for (int c = 0; c < 16; c += 2) {
@@ -492,7 +492,7 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                     uint32_t sr[16], dr[16];
                     tmem_ld16(tS + half * 16, sr);
                     tmem_ld16(tP + half * 16, dr);
-                    tmem_wait_ld();
+                    tmem_wait_ld(sr, dr);
                     uint32_t pw[8], pp[8];
 #pragma unroll
                     for (int c = 0; c < 16; c += 2) {
@@ -537,7 +537,7 @@ bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 uint32_t a1[16], a2[16];
                 tmem_ld16(tbase + lane_base + C::A1_COL + oc * 16, a1);
                 tmem_ld16(tbase + lane_base + C::A2_COL + oc * 16, a2);
-                tmem_wait_ld();
+                tmem_wait_ld(a1, a2);
                 uint32_t pk[8];
 #pragma unroll
                 for (int c = 0; c < 16; c += 2) {
@@ -951,7 +951,7 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                     uint32_t sr[32], dr[32];
                     tmem_ld32(bcol + C::ST_COL + qb * 32, sr);
                     tmem_ld32(bcol + C::DPT_COL + qb * 32, dr);
-                    tmem_wait_ld();
+                    tmem_wait_ld(sr, dr);
                     const int cq = v ? clo : 0;
                     const float p = v ? fast_exp2(fmaf(select32(reinterpret_cast<const float *>(sr), cs), sc, xb[cq])) : 0.f;
                     const float z = p * (select32(reinterpret_cast<const float *>(dr), cs) - xb[QC + cq]);
@@ -978,7 +978,7 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                     uint32_t sr[32], dr[32];
                     tmem_ld32(bcol + C::ST_COL + q * 32, sr);
                     tmem_ld32(bcol + C::DPT_COL + q * 32, dr);
-                    tmem_wait_ld();
+                    tmem_wait_ld(sr, dr);
                     uint32_t pp[16], pz[16];
 #pragma unroll
                     for (int c = 0; c < 32; c += 2) {
@@ -1008,7 +1008,7 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                 uint32_t sr[32], dr[32];
                 tmem_ld32(bcol + C::ST_COL + q * 32, sr);
                 tmem_ld32(bcol + C::DPT_COL + q * 32, dr);
-                tmem_wait_ld();
+                tmem_wait_ld(sr, dr);
                 uint32_t pp[16], pz[16];
 #pragma unroll
                 for (int c = 0; c < 32; c += 2) {
@@ -1048,7 +1048,7 @@ bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
                 uint32_t xk[16], xv[16];
                 tmem_ld16(tbase + lane_base + C::DK_COL + oc * 16, xk);
                 tmem_ld16(tbase + lane_base + C::DV_COL + oc * 16, xv);
-                tmem_wait_ld();
+                tmem_wait_ld(xk, xv);
                 uint32_t pk[8], pv[8];
 #pragma unroll
                 for (int c = 0; c < 16; c += 2) {

@@ -996,7 +996,7 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 const uint32_t tS = tbase + lane_base + buf * CHUNK;
                 uint32_t ra[CHUNK];
                 tmem_ld32(tS, ra);
-                tmem_wait_ld32(ra);
+                tmem_wait_ld(ra);
                 // Tiles inside every query's band: P with the running reference; the maximum only once some P
                 // exceeds 2^12, which a sum above 2^12 is the first sign of.
                 const bool fast = t >= k.full_lo && t <= k.full_hi && __all_sync(0xffffffffu, m_ref != -INFINITY);
@@ -1043,7 +1043,7 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                         lsum = tile_exp(ra, sc, bo);
                         if (!fast || pass > 0 || !__any_sync(0xffffffffu, !(lsum <= kRescaleSum))) break;
                         tmem_ld32(tS, ra);
-                        tmem_wait_ld32(ra);
+                        tmem_wait_ld(ra);
                         const float mt = fmaf(tile_raw_max(ra), sc, off_band);
                         if (mt > m_ref + kRescaleThreshold) {
                             corr = fast_exp2(m_ref - mt);
@@ -1071,7 +1071,7 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                     for (int oc = 0; oc < D / 16; ++oc) {
                         uint32_t x[16];
                         tmem_ld16(tbase + lane_base + C::O_COL + oc * 16, x);
-                        tmem_wait_ld16(x);
+                        tmem_wait_ld(x);
 #pragma unroll
                         for (int c = 0; c < 16; ++c) x[c] = __float_as_uint(__uint_as_float(x[c]) * f);
                         tmem_st16(tbase + lane_base + C::O_COL + oc * 16, x);
@@ -1101,8 +1101,7 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 uint32_t x[64];
                 tmem_ld32(tbase + lane_base + C::O_COL + oh * 32, x);
                 tmem_ld32(tbase + lane_base + C::O_COL + oh * 32 + 32, x + 32);
-                tmem_wait_ld32(x);
-                tmem_wait_ld32(x + 32);
+                tmem_wait_ld(x);
                 uint8_t *rowp = smem + C::Q_OFF + (oh >> 1) * C::Q_DBLK + r * ROW_BYTES;
 #pragma unroll
                 for (int w = 0; w < 8; ++w) {

@@ -653,7 +653,7 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                     // the gate tile: this row's head's 8 hidden pre-activations, then alpha
                     uint32_t pre[kGateHidden];
                     tmem_ld8(tbase + lane_base + buf * CHUNK + hh * kGateHidden, pre);
-                    tmem_wait_ld();
+                    tmem_wait_ld(pre);
                     tc_fence_before();
                     mbar_arrive(bar(C::B_PR + buf));  // the buffer is free for the next S
                     al = gate_alpha(pre, args.gate_b1 + h * kGateHidden, args.gate_w2 + h * kGateHidden,
@@ -667,7 +667,7 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 const uint32_t tS = tbase + lane_base + buf * CHUNK;
                 uint32_t ra[CHUNK];
                 tmem_ld32(tS, ra);
-                tmem_wait_ld();
+                tmem_wait_ld(ra);
                 if (k == 0 && warp == 4 && lane == 0) stamp_tile(184, t);
 
                 // Full tile (the same for every thread of the CTA): P with the running reference;
@@ -733,7 +733,7 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                         lsum = tile_exp(ra, sc, bo);
                         if (!fast || pass > 0 || !__any_sync(0xffffffffu, !(lsum <= kRescaleSum))) break;
                         tmem_ld32(tS, ra);
-                        tmem_wait_ld();
+                        tmem_wait_ld(ra);
                         const float mt = fmaf(tile_raw_max(ra), sc, off_band);
                         if (mt > m_ref + kRescaleThreshold) {
                             corr = fast_exp2(m_ref - mt);
@@ -765,7 +765,7 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                     for (int oc = 0; oc < D / 16; ++oc) {
                         uint32_t x[16];
                         tmem_ld16(tbase + lane_base + C::O_COL + oc * 16, x);
-                        tmem_wait_ld();
+                        tmem_wait_ld(x);
 #pragma unroll
                         for (int c = 0; c < 16; ++c) x[c] = __float_as_uint(__uint_as_float(x[c]) * f);
                         tmem_st16(tbase + lane_base + C::O_COL + oc * 16, x);
@@ -798,7 +798,7 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 uint32_t x[64];
                 tmem_ld32(tbase + lane_base + C::O_COL + oh * 32, x);
                 tmem_ld32(tbase + lane_base + C::O_COL + oh * 32 + 32, x + 32);
-                tmem_wait_ld();
+                tmem_wait_ld(x);
                 uint8_t *rowp = smem + C::Q_OFF + (oh >> 1) * C::Q_DBLK + r * ROW_BYTES;
 #pragma unroll
                 for (int w = 0; w < 8; ++w) {  // 8 columns -> one 16-byte chunk of the row

@@ -215,7 +215,21 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t *r) {
         : "r"(taddr));
 }
 #undef PI_R8
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Ties registers to this place of the program (no instruction): what uses them later comes after it.
+template <int N>
+__device__ __forceinline__ void tie(uint32_t (&r)[N]) {
+    static_assert(N % 8 == 0, "eight at a time");
+#pragma unroll
+    for (int i = 0; i < N; i += 8)
+        asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7]));
+}
+// Waits for the TMEM loads issued before, whose registers are r ...  They are named because nothing else keeps the compiler from using
+// their values before the wait, while the load is in flight.
+template <int... N>
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&...r)[N]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+    (tie(r), ...);
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *v) {

@@ -17,18 +17,6 @@ constexpr int CHUNK = 32;                 // keys per tile (TMA box rows; the N 
 constexpr float kRescaleThreshold = 12.f;
 constexpr float kRescaleSum = 4096.f;  // a tile's sum of P above this is the first sign of such a logit
 
-// Waits for the TMEM loads issued before, of which r[0 .. 31] (r[0 .. 15]) is one.  The registers are operands: without them
-// nothing keeps the compiler from using their values before the wait, while the load is in flight.
-__device__ __forceinline__ void tmem_wait_ld32(uint32_t *r) {
-#define PI_R4(i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3])
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : PI_R4(0), PI_R4(4), PI_R4(8), PI_R4(12), PI_R4(16), PI_R4(20), PI_R4(24), PI_R4(28)::"memory");
-}
-__device__ __forceinline__ void tmem_wait_ld16(uint32_t *r) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;" : PI_R4(0), PI_R4(4), PI_R4(8), PI_R4(12)::"memory");
-#undef PI_R4
-}
-
 // Phase 1 of a tile for one row (general path): mask the scores outside [clo, chi] and return
 // the tile's largest logit in log2 units (prior included).  A skip tile holds at most one
 // valid column per row (its diagonal), read with a select tree instead of a full pass.
