@@ -32,7 +32,9 @@
  *
  *   lse_i = ln sum_{j in U(i)} exp(z_ij);  out_i = sum_j exp(z_ij - lse_i) v_j.
  *   A row with no finite logit (alpha_i = 0 and P(i) empty) gets out_i = 0 and
- *   lse_i = -inf.
+ *   lse_i = -inf.  Sums run in fp32 over weights of at most one: out_i is finite
+ *   while every |v_j| is below 2^127 over the number of keys of U(i); a key whose
+ *   weight is below 2^-114 of the row's largest may be left out.
  *
  * Layouts (all contiguous, row-major, element strides implied by the shape):
  *   q, out, dq, dout : [B, H,   N, d]

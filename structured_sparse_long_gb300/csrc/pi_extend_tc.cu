@@ -998,7 +998,7 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 tmem_ld32(tS, ra);
                 tmem_wait_ld(ra);
                 // Tiles inside every query's band: P with the running reference; the maximum only once some P
-                // exceeds 2^12, which a sum above 2^12 is the first sign of.
+                // exceeds 1, which a sum above 1 is the first sign of.
                 const bool fast = t >= k.full_lo && t <= k.full_hi && __all_sync(0xffffffffu, m_ref != -INFINITY);
                 float corr = 1.f, lsum, bo;
                 bool need_o = false, diag = false;
@@ -1022,12 +1022,13 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                         off = off_skip;
                     }
                     const float mt = tile_max(reinterpret_cast<float *>(ra), clo, chi, sk, sc, off);
-                    if (mt > m_ref + kRescaleThreshold) {
+                    if (mt > m_ref) {
+                        const float m_new = mt + kHeadroom;
                         if (m_ref != -INFINITY) {
-                            corr = fast_exp2(m_ref - mt);
+                            corr = fast_exp2(m_ref - m_new);
                             need_o = t > 0;
                         }
-                        m_ref = mt;
+                        m_ref = m_new;
                     }
                     l *= corr;
                     mu = (m_ref == -INFINITY) ? 0.f : m_ref;
@@ -1045,10 +1046,11 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                         tmem_ld32(tS, ra);
                         tmem_wait_ld(ra);
                         const float mt = fmaf(tile_raw_max(ra), sc, off_band);
-                        if (mt > m_ref + kRescaleThreshold) {
-                            corr = fast_exp2(m_ref - mt);
+                        if (mt > m_ref) {
+                            const float m_new = mt + kHeadroom;
+                            corr = fast_exp2(m_ref - m_new);
                             need_o = true;
-                            m_ref = mt;
+                            m_ref = m_new;
                         }
                         l *= corr;
                         bo = off_band - m_ref;

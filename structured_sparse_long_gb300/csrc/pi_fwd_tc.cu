@@ -29,8 +29,9 @@
 //     TMEM (each whole warp runs its loop, one elected lane issues the copies, the
 //     MMAs and the commits).
 //   * Warps 4-7 run the softmax, one thread per row (TMEM lane = row): masks,
-//     adds the prior, keeps the running max m and sum l (rescaling O in TMEM only
-//     when the max grows by more than 2^12), writes P as bf16 over its S, and at
+//     adds the prior, keeps a reference m at or above the running max and the sum l
+//     (rescaling O in TMEM only when the max outgrows m, which is set 12 log2 units
+//     above it), writes P as bf16 over its S, and at
 //     the end of the block normalises O and stages it in shared memory.
 //   * The fused gate (GATE) puts one more tile in front of a block's key tiles: the
 //     W1 rows of the block's heads, so that its S product is the heads' hidden
@@ -671,8 +672,8 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 if (k == 0 && warp == 4 && lane == 0) stamp_tile(184, t);
 
                 // Full tile (the same for every thread of the CTA): P with the running reference;
-                // the maximum is only needed when some P exceeds 2^12 (the lazy-rescale bound),
-                // which a sum above 2^12 is the first sign of.  Rows with no reference yet take the
+                // the maximum is only needed when some P exceeds 1 (a logit above the reference),
+                // which a sum above 1 is the first sign of.  Rows with no reference yet take the
                 // general path, as do the debug modes that record per-row ranges.
                 const bool fast = (DBG == 0 || DBG == 3) && tk >= bd.full_lo && tk <= bd.full_hi &&
                                   __all_sync(0xffffffffu, m_ref != -INFINITY);
@@ -700,12 +701,13 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                     float *fa = reinterpret_cast<float *>(ra);
                     const float mt = tile_max(fa, clo, chi, sk, sc, off);
                     if (k == 0 && warp == 4 && lane == 0) stamp_tile(200, t);
-                    if (mt > m_ref + kRescaleThreshold) {
+                    if (mt > m_ref) {
+                        const float m_new = mt + kHeadroom;
                         if (m_ref != -INFINITY) {
-                            corr = fast_exp2(m_ref - mt);
+                            corr = fast_exp2(m_ref - m_new);
                             need_o = (tk > 0);
                         }
-                        m_ref = mt;
+                        m_ref = m_new;
                     }
                     l *= corr;
                     mu = (m_ref == -INFINITY) ? 0.f : m_ref;
@@ -727,7 +729,7 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                     lsum = tile_exp_diag(ra, clo, zdiag, mu);
                 } else {
                     // one copy of the exponentials: on the fast path, a second pass only when the
-                    // first found P above the lazy-rescale bound (S is still in TMEM)
+                    // first found a sum of P above 1 (S is still in TMEM)
 #pragma unroll 1
                     for (int pass = 0;; ++pass) {
                         lsum = tile_exp(ra, sc, bo);
@@ -735,10 +737,11 @@ fwd_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                         tmem_ld32(tS, ra);
                         tmem_wait_ld(ra);
                         const float mt = fmaf(tile_raw_max(ra), sc, off_band);
-                        if (mt > m_ref + kRescaleThreshold) {
-                            corr = fast_exp2(m_ref - mt);
+                        if (mt > m_ref) {
+                            const float m_new = mt + kHeadroom;
+                            corr = fast_exp2(m_ref - m_new);
                             need_o = true;  // m_ref was set by an earlier tile, so t > 0
-                            m_ref = mt;
+                            m_ref = m_new;
                         }
                         l *= corr;
                         bo = off_band - m_ref;

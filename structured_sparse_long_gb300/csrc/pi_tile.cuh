@@ -10,12 +10,15 @@ namespace pi {
 namespace tc {
 
 constexpr int CHUNK = 32;                 // keys per tile (TMA box rows; the N of the S products)
-// A row's reference m moves, and its O is rescaled, once a logit exceeds it by this much (log2 units): P stays below
-// 2^12, which costs bf16 and fp32 nothing in relative precision (values of V above 2^100 would overflow first).  A row's
-// first tile may hold a single key, so a smaller bound makes rescales common: 2^8 took C4 242 us, the fused gate C8 270 us
-// and a 16384-token chunk over bf16 pages 76 us, 2^12 takes 238, 254 and 70 us, 2^16 and 2^24 the same.
-constexpr float kRescaleThreshold = 12.f;
-constexpr float kRescaleSum = 4096.f;  // a tile's sum of P above this is the first sign of such a logit
+// A row's reference m is set this much (log2 units) above its largest logit so far, and moves, with O rescaled, once a logit exceeds
+// it.  P is then at most 1, so that the unnormalised O is at most the sum of the values' magnitudes: it overflows only where
+// values reach fp32's largest over the row's number of keys.  (Set to the maximum and left to lag behind by as much, P reached
+// 2^12, and a band of 300 values of 2^112 overflowed.)  A relative weight is lost below 2^-114 at the latest, 2^-126 being
+// the smallest P.  A row's first tile may hold a single key, so a smaller distance makes rescales common: 8 took C4
+// 242 us, the fused gate C8 270 us and a 16384-token chunk over bf16 pages 76 us, 12 takes 237, 254 and 70 us, 16 and 24 the
+// same.
+constexpr float kHeadroom = 12.f;
+constexpr float kRescaleSum = 1.f;  // a tile's sum of P above this is the first sign of a logit above the reference
 
 // Phase 1 of a tile for one row (general path): mask the scores outside [clo, chi] and return
 // the tile's largest logit in log2 units (prior included).  A skip tile holds at most one
