@@ -233,6 +233,7 @@ PyObject *extend(PyObject *const *a) {
             PyErr_Format(PyExc_ValueError, "workspace must hold %zu bytes, got %lld", need, (long long)bytes[0]);
             throw Refused{};
         }
+        if (bytes[0] == 0) ws = nullptr;  // (an empty tensor has no address; the call takes none where it needs none)
     } else if (need) {
         made = new_tensor(h, at::kByte, bytes);
         ws = made.data_ptr();

@@ -1,0 +1,71 @@
+"""Host tests of what the paged cache's calls hand to the library: the C functions are replaced by ones that record their
+arguments, so that nothing is launched, here or on a machine with a GPU."""
+import ctypes
+
+import pytest
+import torch
+
+from structured_sparse_long_gb300 import build as pbuild
+from structured_sparse_long_gb300 import paged
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """Arguments of every pi_attn_extend that the binding makes, on host tensors: (workspace, bytes)."""
+    pbuild.build()
+    lib = paged._load()
+    monkeypatch.setattr(paged._binding, "_expect_like", lambda t, name, like, dtype, shape: None)
+    monkeypatch.setattr(paged, "_current_device", lambda: -1)
+    monkeypatch.setattr(paged, "_raw_stream", lambda index: 0)
+    seen = []
+    P, I, L, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_size_t
+    extend_t = ctypes.CFUNCTYPE(I, P, L, P, P, P, I, I, I, I, I, P, P, P, Z, P)
+    record = extend_t(lambda *a: seen.append((a[12], a[13])) or 0)
+    never = ctypes.CFUNCTYPE(I)(lambda: 1 / 0)
+    address = lambda f: ctypes.cast(f, P).value  # noqa: E731
+    native = paged._load_native()
+    native.bind(address(never), address(never), address(lib.pi_attn_extend_workspace_size), address(record), address(never))
+    yield seen
+    monkeypatch.setattr(paged, "_native", None)
+    paged._load_native()
+
+
+def short_call(workspace):
+    """One token of four heads on two: a call that needs no workspace."""
+    z = torch.zeros(2, 2, 16, 64, dtype=torch.bfloat16)
+    cache = paged.PagedCache(z, z)
+    q, a = torch.zeros(1, 4, 64, dtype=torch.bfloat16), torch.zeros(1, 4)
+    table, cu, ctx = torch.zeros(1, 4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    assert paged.extend_workspace_size(cache, 1, 1, 4, 4, 8, 16, 1) == 0
+    paged.extend(q, cache, table, cu, ctx, a, 8, 16, 1, workspace=workspace)
+
+
+def test_an_empty_workspace_is_no_workspace(calls):
+    """What extend_workspace_size() asks for is accepted, zero bytes as well: an empty tensor goes in as a null pointer (it has no
+    address of its own, and any other may lie on no multiple of 256)."""
+    room = torch.zeros(1024, dtype=torch.uint8)
+    for workspace in (None, torch.empty(0, dtype=torch.uint8), room[256:256]):
+        short_call(workspace)
+        assert calls.pop() == (None, 0)
+    short_call(room)
+    assert calls.pop() == (room.data_ptr(), 1024)
+
+
+def test_a_workspace_that_is_needed_is_handed_on(calls):
+    """20 query heads on one KV head: always the long chunks' kernels, which need a workspace of the size asked for."""
+    z = torch.zeros(2, 1, 16, 64, dtype=torch.bfloat16)
+    cache = paged.PagedCache(z, z)
+    q, a = torch.zeros(1, 20, 64, dtype=torch.bfloat16), torch.zeros(1, 20)
+    batch = torch.zeros(1, 4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    need = paged.extend_workspace_size(cache, 1, 1, 4, 20, 8, 16, 1)
+    assert need > 0
+    paged.extend(q, cache, *batch, a, 8, 16, 1)
+    pointer, size = calls.pop()
+    assert pointer and size == need
+    mine = torch.zeros(need, dtype=torch.uint8)
+    paged.extend(q, cache, *batch, a, 8, 16, 1, workspace=mine)
+    assert calls.pop() == (mine.data_ptr(), need)
+    for small in (mine[:need - 1], mine[:0]):
+        with pytest.raises(ValueError, match="workspace must hold"):
+            paged.extend(q, cache, *batch, a, 8, 16, 1, workspace=small)
+    assert not calls
