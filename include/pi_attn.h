@@ -331,6 +331,7 @@ typedef struct {
  *   k, v [T, Hkv, d] bf16; a token's Hkv * d elements are contiguous, tokens lie k_stride
  *   (v_stride) elements apart: at least Hkv * d, below 2^38, a multiple of 8 (else PI_ERR_SHAPE), so
  *   that both may be slices of one projection's output.  16-byte aligned.
+ *   T * ceil(Hkv * d / 256) < 2^31, here and in pi_attn_cache_read (else PI_ERR_UNSUPPORTED).
  *   A token whose sequence or page is out of range is not written.
  */
 int pi_attn_cache_append(const void *k, const void *v, long long k_stride, long long v_stride,
@@ -352,7 +353,8 @@ int pi_attn_cache_read(const pi_attn_cache_t *cache, const pi_attn_batch_t *batc
  * or ECP mode (bidirectional: PI_ERR_UNSUPPORTED).
  *   q [T, H, d] bf16 with tokens q_stride elements apart (rules as for
  *   pi_attn_cache_append), alpha [T, H] fp32 (NULL in ECP mode), out [T, H, d] bf16 and
- *   lse [T, H] fp32, contiguous.  H % Hkv == 0; T * H < 2^31.
+ *   lse [T, H] fp32, contiguous.  H % Hkv == 0; T * H < 2^31, and over an 8-bit cache at most
+ *   2^30 / Hkv rows in the workspace (else PI_ERR_UNSUPPORTED).
  *   A sequence with an offset or length out of range is left out, its rows of out and lse
  *   as they were (where cu decreases anywhere, any of the batch's rows may be); a row that attends a key on a page out of range is undefined.
  *   A token's results depend on the rows that it attends alone: what the other rows hold, NaN

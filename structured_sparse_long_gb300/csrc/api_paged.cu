@@ -87,6 +87,7 @@ int pi_attn_cache_append(const void *k, const void *v, long long k_stride, long 
     if (rc == PI_OK) rc = check_stride(k_stride, cache->Hkv, cache->d);
     if (rc == PI_OK) rc = check_stride(v_stride, cache->Hkv, cache->d);
     if (rc != PI_OK) return rc;
+    if (!pi::rows_fit(a.cache, batch->T)) return PI_ERR_UNSUPPORTED;
     if (!aligned(k, 16) || !aligned(v, 16)) return PI_ERR_ALIGN;
     a.k = static_cast<const __nv_bfloat16 *>(k);
     a.v = static_cast<const __nv_bfloat16 *>(v);
@@ -101,6 +102,7 @@ int pi_attn_cache_read(const pi_attn_cache_t *cache, const pi_attn_batch_t *batc
     int rc = make_cache(cache, batch->width, a.cache);
     if (rc == PI_OK) rc = make_batch(batch, a.batch);
     if (rc != PI_OK) return rc;
+    if (!pi::rows_fit(a.cache, batch->T)) return PI_ERR_UNSUPPORTED;
     if (!aligned(k, 16) || !aligned(v, 16)) return PI_ERR_ALIGN;
     a.k = static_cast<__nv_bfloat16 *>(k);
     a.v = static_cast<__nv_bfloat16 *>(v);
@@ -117,7 +119,8 @@ size_t pi_attn_extend_workspace_size(const pi_attn_cache_t *cache, int B, int T,
         return 0;
     a.batch.B = B;
     a.batch.T = T;
-    return pi::extend_workspace_bytes(a);
+    size_t bytes;
+    return pi::extend_workspace(a, bytes) ? bytes : 0;
 }
 
 int pi_attn_extend(const void *q, long long q_stride, const pi_attn_cache_t *cache, const pi_attn_batch_t *batch,
@@ -130,14 +133,14 @@ int pi_attn_extend(const void *q, long long q_stride, const pi_attn_cache_t *cac
     if (rc == PI_OK) rc = make_attention(a.cache, H, k_local, period, S, mode, alpha, a.s);
     if (rc == PI_OK) rc = check_stride(q_stride, H, cache->d);
     if (rc != PI_OK) return rc;
-    if ((long long)batch->T * H > 0x7fffffffLL) return PI_ERR_UNSUPPORTED;
+    size_t need;
+    if (!pi::extend_workspace(a, need)) return PI_ERR_UNSUPPORTED;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || (alpha && !aligned(alpha, 4))) return PI_ERR_ALIGN;
     a.q = static_cast<const __nv_bfloat16 *>(q);
     a.q_stride = q_stride;
     a.alpha = mode != PI_MODE_ECP ? alpha : nullptr;
     a.out = static_cast<__nv_bfloat16 *>(out);
     a.lse = lse;
-    const size_t need = pi::extend_workspace_bytes(a);
     if (need > 0 && (!workspace || workspace_bytes < need)) return PI_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return PI_ERR_ALIGN;
     a.workspace = static_cast<int *>(workspace);

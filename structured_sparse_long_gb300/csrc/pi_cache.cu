@@ -176,8 +176,7 @@ __global__ void __launch_bounds__(WARPS * 32) read_kernel(const ReadArgs a) {
 template <typename K, typename A>
 static cudaError_t launch(K kernel, int tokens, int piece, A a, cudaStream_t st) {
     a.chunks = (a.cache.Hkv * a.cache.d / piece + 31) / 32;
-    const long long warps = ((long long)a.batch.T + tokens - 1) / tokens * a.chunks;
-    if (warps > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    const long long warps = ((long long)a.batch.T + tokens - 1) / tokens * a.chunks;  // (fits: rows_fit)
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((warps + WARPS - 1) / WARPS), 1, 1);
     cfg.blockDim = dim3(WARPS * 32, 1, 1);

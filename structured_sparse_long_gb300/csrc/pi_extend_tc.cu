@@ -112,7 +112,8 @@ __device__ __forceinline__ int slot_tile(const Shape &s, int m_first, const SeqT
     return tile > (ctx + n - 1 - back) >> 5 ? -1 : tile;
 }
 
-// Most slots that a batch can take, from its sizes alone (cap: positions a page table reaches).
+// Most slots that a batch can take, from its sizes alone (cap: positions a page table reaches); below 2^60 for any that the
+// C ABI lets through.
 static long long most_slots(const Shape &s, long long B, long long T, long long cap) {
     const long long seqs = std::min(B, T);
     const long long band = std::min<long long>(cap, s.mode == kModeEcp ? 2LL * s.k_local : s.k_local);
@@ -1217,10 +1218,18 @@ static cudaError_t launch(const Args &a, const void *k, const void *v, cudaStrea
 
 }  // namespace ext
 
-size_t extend_workspace_bytes(const ExtendArgs &e) {
-    if (extend_few_rows(e)) return 0;
+bool extend_workspace(const ExtendArgs &e, size_t &bytes) {
+    const Shape &s = e.s;
     const PagedCache &c = e.cache;
-    return ext::layout(e.s, c.kv_type, e.batch.B, e.batch.T, (long long)c.width << c.page_log2).bytes;
+    const long long T = e.batch.T, B = e.batch.B, cap = (long long)c.width << c.page_log2;
+    bytes = 0;
+    if (T * s.H > 0x7fffffffLL) return false;  // rows of lse
+    if (extend_few_rows(e)) return true;
+    const int GP = packed_heads(s.H / s.Hkv);
+    if (ext::max_blocks(T, B, ext::BM / GP) * (s.H / GP) > 0x7fffffffLL - 1024) return false;
+    if (c.kv_type != kKvBf16 && ext::most_slots(s, B, T, cap) > 0x7fffffffLL / (2 * ext::CHUNK) / s.Hkv) return false;
+    bytes = ext::layout(s, c.kv_type, B, T, cap).bytes;
+    return true;
 }
 
 cudaError_t launch_extend(const ExtendArgs &e, cudaStream_t st) {
@@ -1231,8 +1240,6 @@ cudaError_t launch_extend(const ExtendArgs &e, cudaStream_t st) {
     const int G = s.H / s.Hkv, GP = packed_heads(G), R = BM / GP, ngrp = s.H / GP;
     const bool quant = c.kv_type != kKvBf16, skips = s.mode != kModeEcp && s.S > 0;
     const Layout l = layout(s, c.kv_type, e.batch.B, e.batch.T, (long long)c.width << c.page_log2);
-    if (max_blocks(e.batch.T, e.batch.B, R) * ngrp > 0x7fffffffLL - 1024 || l.n_slots * s.Hkv > 0x7fffffffLL / (2 * CHUNK))
-        return cudaErrorInvalidConfiguration;
     char *ws = reinterpret_cast<char *>(e.workspace);
     int2 *slots = quant ? reinterpret_cast<int2 *>(ws + l.slots) : nullptr;
     Args a{e, e.workspace, GP, R, R == 32 ? 5 : R == 64 ? 6 : 7, ngrp, skips ? first_skip_multiple(s) : 1,

@@ -43,6 +43,9 @@ struct AppendArgs {
     int chunks;  // warps per token, set at the launch
 };
 
+// Warps of a token in append and read, of 256 elements each or more, and whether a launch holds those of T tokens.
+inline bool rows_fit(const PagedCache &c, long long T) { return T * ((c.Hkv * (long long)c.d + 255) / 256) <= 0x7fffffffLL; }
+
 struct ReadArgs {
     __nv_bfloat16 *k, *v;  // [T, Hkv, d]
     PagedCache cache;
@@ -60,7 +63,7 @@ struct ExtendArgs {
     Shape s;                 // H, Hkv, d, k_local, period, S, mode, scale_log2
     PagedCache cache;
     PagedBatch batch;
-    int *workspace;          // extend_workspace_bytes()
+    int *workspace;          // extend_workspace()
     int *status, *index_word;
     uint64_t timeout_ns;
 };
@@ -87,7 +90,8 @@ cudaError_t launch_cache_read(const ReadArgs &a, cudaStream_t st);
 
 // attention over a paged cache: a chunk of new tokens per sequence (pi_extend_tc.cu), one new token per
 // sequence (pi_decode_paged.cu)
-size_t extend_workspace_bytes(const ExtendArgs &a);
+// the workspace of a call; false where its kernels cannot number the rows, blocks or tiles of its sizes
+bool extend_workspace(const ExtendArgs &a, size_t &bytes);
 cudaError_t launch_extend(const ExtendArgs &a, cudaStream_t st);
 // the same for few tokens per sequence (pi_decode_paged.cu), and whether a call is one of those
 cudaError_t launch_extend_few(const ExtendArgs &a, cudaStream_t st);

@@ -69,3 +69,43 @@ def test_a_workspace_that_is_needed_is_handed_on(calls):
         with pytest.raises(ValueError, match="workspace must hold"):
             paged.extend(q, cache, *batch, a, 8, 16, 1, workspace=small)
     assert not calls
+
+
+# ------------------------------------------------------------------ sizes past the kernels' limits, through the C ABI
+
+PI_ERR_UNSUPPORTED = -3
+A16 = 0x10000  # fake, 256-byte aligned, never dereferenced: validation fails first
+
+
+def sizes(T, B=1, Hkv=1, width=4, kv_type=1):
+    cache = paged._CacheStruct(A16, A16, A16, A16, kv_type, 4, Hkv, 256, 128)
+    return ctypes.byref(cache), ctypes.byref(paged._BatchStruct(A16, A16, A16, B, T, width))
+
+
+def test_rows_past_the_grids_are_refused():
+    """A launch has at most 2^31 - 1 warps, of 256 elements of a token each."""
+    pbuild.build()
+    lib = paged._load()
+    for T, Hkv in ((2 ** 31 - 1, 64), (2 ** 30, 5), (2 ** 16, 65535)):
+        for kv_type in (0, 1, 2):
+            c, b = sizes(T, Hkv=Hkv, kv_type=kv_type)
+            assert lib.pi_attn_cache_append(A16, A16, Hkv * 128, Hkv * 128, c, b, None) == PI_ERR_UNSUPPORTED
+            assert lib.pi_attn_cache_read(c, b, A16, A16, None) == PI_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("T,B,H,Hkv,width,k_local", [
+    (2 ** 16, 2 ** 16, 20, 1, 2 ** 12, 2 ** 20),      # 2^31 converted tiles
+    (2 ** 20, 2 ** 20, 128, 128, 2 ** 13, 2 ** 11),   # 2^26 of each of 128 heads
+    (2 ** 30, 2 ** 30, 1, 1, 2 ** 22, 2 ** 30),       # a workspace of 2^68 bytes
+    (2 ** 31 - 1, 5, 2, 1, 4, 8),                     # 2^32 rows
+])
+def test_chunks_past_the_conversion_are_refused(T, B, H, Hkv, width, k_local):
+    """What the 8-bit kernels cannot number is refused as unsupported, and no workspace size is made up for it.  (All of these are
+    calls of the long chunks' kernels, whatever the device: 20 heads on one, or more than 65535 groups of tokens.)"""
+    pbuild.build()
+    lib = paged._load()
+    for kv_type in (1, 2):
+        c, b = sizes(T, B, Hkv, width, kv_type)
+        assert lib.pi_attn_extend_workspace_size(c, B, T, width, H, k_local, 1, 0, 0) == 0
+        args = (A16, H * 128, c, b, A16, H, k_local, 1, 0, 0, A16, A16, A16, 2 ** 64 - 1, None)
+        assert lib.pi_attn_extend(*args) == PI_ERR_UNSUPPORTED
