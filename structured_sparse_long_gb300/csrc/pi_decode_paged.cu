@@ -566,12 +566,17 @@ static cudaError_t launch_types(const Args &a, int groups, long long keys, cudaS
     }
 }
 
-// Keys of the longest list of `tokens` consecutive queries.
-static long long most_keys(const Shape &s, const PagedCache &c, int tokens) {
-    const long long cap = (long long)c.width << c.page_log2;
-    const long long band = s.mode == kModeEcp ? 2LL * s.k_local : (long long)s.k_local + 1;
-    return std::min(cap, band + tokens - 1) + (s.mode == kModeEcp ? 0 : std::min<long long>(s.S, cap) * tokens);
-}
+// The longest band and the most skips of a query, at the last position that a page table reaches.
+struct MostKeys {
+    long long cap, band, windows;
+    MostKeys(const Shape &s, const PagedCache &c) : cap((long long)c.width << c.page_log2), windows(0) {
+        band = std::min(cap, s.mode == kModeEcp ? 2LL * s.k_local : s.k_local + 1LL);
+        if (s.mode != kModeEcp && s.S > 0)
+            windows = std::max(0LL, std::min<long long>(s.S, cap / s.period) - first_skip_multiple(s) + 1);
+    }
+    // keys of the longest list of `tokens` consecutive queries
+    long long list(int tokens) const { return std::min(cap, band + tokens - 1) + windows * tokens; }
+};
 
 }  // namespace decp
 
@@ -580,7 +585,7 @@ cudaError_t launch_decode_paged(const DecodePagedArgs &d, cudaStream_t st) {
     const Shape &s = d.s;
     Args a{d.q, d.q_stride, d.alpha, d.lens, PagedBatch{d.table, nullptr, nullptr, s.B, s.B}, d.out, d.lse, s, d.cache, d.index_word,
            s.mode != kModeEcp && s.S > 0 ? first_skip_multiple(s) : 1, 1};
-    return launch_types<false>(a, s.B, most_keys(s, d.cache, 1), st);
+    return launch_types<false>(a, s.B, MostKeys(s, d.cache).list(1), st);
 }
 
 // Tokens per CTA: as many as 8 columns hold (16 took a batch of five drafted tokens, 4 heads per KV head, 15.0 us, 8 10.4).
@@ -602,13 +607,11 @@ bool extend_few_rows(const ExtendArgs &e) {
     const int G = s.H / s.Hkv, group = token_group(G);
     const long long T = e.batch.T, B = std::min<long long>(e.batch.B, T);
     if (G > 16 || s.Hkv > 65535 || (T + e.batch.B * (long long)(group - 1)) / group > 65535) return false;
-    if (decp::most_keys(s, c, group) >= (1LL << 30)) return false;
+    const decp::MostKeys most(s, c);
+    if (most.list(group) >= (1LL << 30)) return false;
     const bool quant = c.kv_type != kKvBf16;
-    const long long n = (T + B - 1) / B, cap = (long long)c.width << c.page_log2;
-    const long long band = std::min(cap, s.mode == kModeEcp ? 2LL * s.k_local : s.k_local + 1LL);
-    const long long last = s.mode != kModeEcp && s.S > 0 ? std::min<long long>(s.S, cap / s.period) : 0;
-    const long long windows = last > 0 ? std::max(0LL, last - first_skip_multiple(s) + 1) : 0;
-    const long long tiles = (std::min(cap, band + group - 1) + windows * group + decp::KEYS - 1) / decp::KEYS;
+    const long long n = (T + B - 1) / B, band = most.band, windows = most.windows;
+    const long long tiles = (most.list(group) + decp::KEYS - 1) / decp::KEYS;
     const long long ctas = B * ((n + group - 1) / group) * s.Hkv, sms = sm_count();
     const double rounds = (double)ctas * (double)(tiles + 6) / (double)(sms * decp::sm_warps(s.d, c.kv_type, group * G > 8 ? 2 : 1));
     const double few = 6.0 + (quant ? 1.8 : 1.4) * rounds;
@@ -625,7 +628,7 @@ cudaError_t launch_extend_few(const ExtendArgs &e, cudaStream_t st) {
     const int group = token_group(s.H / s.Hkv);
     Args a{e.q, e.q_stride, e.alpha, nullptr, e.batch, e.out, e.lse, s, e.cache, e.index_word,
            s.mode != kModeEcp && s.S > 0 ? first_skip_multiple(s) : 1, group};
-    return launch_types<true>(a, (int)((e.batch.T + e.batch.B * (long long)(group - 1)) / group), most_keys(s, e.cache, group), st);
+    return launch_types<true>(a, (int)((e.batch.T + e.batch.B * (long long)(group - 1)) / group), MostKeys(s, e.cache).list(group), st);
 }
 
 }  // namespace pi

@@ -109,3 +109,14 @@ def test_chunks_past_the_conversion_are_refused(T, B, H, Hkv, width, k_local):
         assert lib.pi_attn_extend_workspace_size(c, B, T, width, H, k_local, 1, 0, 0) == 0
         args = (A16, H * 128, c, b, A16, H, k_local, 1, 0, 0, A16, A16, A16, 2 ** 64 - 1, None)
         assert lib.pi_attn_extend(*args) == PI_ERR_UNSUPPORTED
+
+
+def test_skips_are_counted_as_far_as_the_table_reaches():
+    """A token attends no more skips than lie before it: 128 of 2^20 positions under a table of 2^27 positions, however
+    large S is, so a single token stays a short call, which needs no workspace."""
+    pbuild.build()
+    lib = paged._load()
+    for S in (128, 2 ** 20, 2 ** 27, 2 ** 31 - 1):
+        for H, Hkv in ((4, 4), (16, 4)):
+            c, _ = sizes(1, 1, Hkv, 2 ** 19)
+            assert lib.pi_attn_extend_workspace_size(c, 1, 1, 2 ** 19, H, 8, 2 ** 20, S, 0) == 0
