@@ -367,7 +367,8 @@ int pi_attn_cache_read(const pi_attn_cache_t *cache, const pi_attn_batch_t *batc
  *   sequence and skip window.  Deterministic.
  *
  * pi_attn_extend_workspace_size -- those bytes (0: none, or sizes that pi_attn_extend refuses);
- * of the cache only its sizes, type and pointers' alignment matter.  The sizes choose between
+ * of the cache only its sizes, type and pointers' alignment matter, and of the device, which has to be current as it is
+ * in the call, its number of SMs.  The sizes choose between
  * two kernels, one of which needs none: a batch with fewer tokens may need more than one with more, so
  * ask for each size that is used.
  */

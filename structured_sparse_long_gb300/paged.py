@@ -165,8 +165,11 @@ def cache_read(cache: PagedCache, table, cu, start, rows: int, k=None, v=None, s
 
 def extend_workspace_size(cache: PagedCache, B: int, T: int, width: int, H: int, k_local: int, period: int, S: int,
                           mode: int = MODE_PI) -> int:
-    """pi_attn_extend_workspace_size: bytes of device workspace that :func:`extend` needs for B sequences with T packed
-    tokens and page tables of `width` entries (0: none, or sizes that it refuses)."""
+    """pi_attn_extend_workspace_size: bytes of workspace on the cache's device that :func:`extend` needs for B sequences with T
+    packed tokens and page tables of `width` entries (0: none, or sizes that it refuses)."""
+    if cache.index != _current_device():
+        with _place(cache, None):
+            return extend_workspace_size(cache, B, T, width, H, k_local, period, S, mode)
     return int(_load().pi_attn_extend_workspace_size(ctypes.byref(cache._struct.cache), B, T, width, H, k_local, period, S, mode))
 
 

@@ -120,3 +120,33 @@ def test_skips_are_counted_as_far_as_the_table_reaches():
         for H, Hkv in ((4, 4), (16, 4)):
             c, _ = sizes(1, 1, Hkv, 2 ** 19)
             assert lib.pi_attn_extend_workspace_size(c, 1, 1, 2 ** 19, H, 8, 2 ** 20, S, 0) == 0
+
+
+def test_the_workspace_size_is_the_cache_devices(calls, monkeypatch):
+    """The size depends on the device (its SMs choose the kernel): it is asked for with the cache's device current, as the call's is."""
+    import contextlib
+    current, asked = [3], []
+
+    @contextlib.contextmanager
+    def place(cache, stream):
+        before, current[0] = current[0], cache.index
+        yield
+        current[0] = before
+
+    lib = paged._load()
+    real = lib.pi_attn_extend_workspace_size
+
+    class Library:
+        @staticmethod
+        def pi_attn_extend_workspace_size(*args):
+            asked.append(current[0])
+            return real(*args)
+
+    z = torch.zeros(2, 1, 16, 64, dtype=torch.bfloat16)
+    cache = paged.PagedCache(z, z)
+    with monkeypatch.context() as m:
+        m.setattr(paged, "_current_device", lambda: current[0])
+        m.setattr(paged, "_place", place)
+        m.setattr(paged, "_load", lambda: Library)
+        assert paged.extend_workspace_size(cache, 1, 1, 4, 20, 8, 16, 1) > 0
+    assert asked == [cache.index] and current == [3]
