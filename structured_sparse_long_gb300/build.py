@@ -1,12 +1,13 @@
 """Builds the CUDA library libpi_attn.so for sm_103a with nvcc (no cmake), and the binding's extension module.
 
 Translation units are compiled in parallel into ``_build/`` and linked into
-``_lib/libpi_attn.so`` inside the package, next to the Python binding.
+``_lib/libpi_attn.so`` inside the package, next to the Python binding.  The library needs no torch: where the extension
+module of the paged cache's binding cannot be compiled, the library is built all the same, the compiler's message goes to
+stderr, and the paged cache's calls raise.
 """
 from __future__ import annotations
 
 import concurrent.futures
-import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -53,9 +54,20 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _torch_dir() -> str:
+    """The folder of the installed torch, which is found, not imported ("": none)."""
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec and spec.origin else ""
+
+
+def _torch_version() -> str:
+    path = os.path.join(_torch_dir(), "version.py")
+    return open(path).read() if os.path.exists(path) else ""
+
+
 def _native_command(target: str) -> list:
-    """The host compiler's command for the binding's extension module (torch is found, not imported)."""
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    """The host compiler's command for the binding's extension module."""
+    torch = _torch_dir()
     lib = os.path.join(torch, "lib")
     return ["g++", "-shared", "-fPIC", "-O2", "-std=c++17", "-Wall", "-Wextra", "-isystem", os.path.join(torch, "include"),
             "-I", sysconfig.get_paths()["include"], "-I", INCLUDE, os.path.join(CSRC, NATIVE_SOURCE), "-o", target,
@@ -94,24 +106,37 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
 
     # the binding depends on the version of torch that it was compiled against
     native, torch_stamp = NATIVE_PATH + f".tmp{os.getpid()}", os.path.join(BUILD_DIR, "torch_version.txt")
-    version = importlib.metadata.version("torch")
+    version = _torch_version()
     new_native = (force or _stale(NATIVE_PATH, [os.path.join(CSRC, NATIVE_SOURCE), os.path.join(INCLUDE, "pi_attn.h")])
                   or not os.path.exists(torch_stamp) or open(torch_stamp).read() != version)
-    compiled = bool(jobs)
-    if new_native:
-        jobs.append(_native_command(native))
-    if jobs:
-        with concurrent.futures.ThreadPoolExecutor(max_workers=len(jobs)) as ex:
-            for cmd, r in ex.map(run, jobs):
-                if verbose or ptxas_info or r.returncode != 0:
+    native_error = ""
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:
+        if new_native and _torch_dir():
+            native_run = ex.submit(run, _native_command(native))
+        for cmd, r in ex.map(run, jobs):
+            if verbose or ptxas_info or r.returncode != 0:
+                sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
+            if r.returncode != 0:
+                raise RuntimeError("nvcc failed for " + next(x for x in cmd if x.startswith(CSRC + os.sep)))
+        if new_native and _torch_dir():
+            try:
+                cmd, r = native_run.result()
+                if verbose or r.returncode != 0:
                     sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
-                if r.returncode != 0:
-                    raise RuntimeError(f"{os.path.basename(cmd[0])} failed for " + next(x for x in cmd if x.startswith(CSRC + os.sep)))
-    if new_native:
+                native_error = "" if r.returncode == 0 else "it does not compile"
+            except OSError as e:  # no compiler
+                native_error = str(e)
+        elif new_native:
+            native_error = "torch is not installed"
+    if native_error:
+        sys.stderr.write(f"the paged cache's binding is not built: {native_error}\n")
+        if os.path.exists(NATIVE_PATH):
+            os.remove(NATIVE_PATH)  # of other sources, or for another torch
+    elif new_native:
         os.replace(native, NATIVE_PATH)
         with open(torch_stamp, "w") as fh:
             fh.write(version)
-    if force or compiled or _stale(LIB_PATH, objs):
+    if force or jobs or _stale(LIB_PATH, objs):
         tmp = LIB_PATH + f".tmp{os.getpid()}"
         cmd = [nv, "-shared", "-o", tmp] + objs + ARCH_FLAGS + [
             "-cudart", "shared", "-Xlinker", "-rpath," + _cuda_lib_dir(nv)]
