@@ -466,6 +466,7 @@ paged_rows_kernel(const __grid_constant__ Args a) {
                 }
             }
             const float inv = lt == 0.f ? 0.f : 1.f / lt;
+            if (lt == 0.f) ot = make_float4(0.f, 0.f, 0.f, 0.f);  // no finite logit: 0, whatever the values are
             const uint2 four = make_uint2(pack_bf16x2(ot.x * inv, ot.y * inv), pack_bf16x2(ot.z * inv, ot.w * inv));
             const long long at = row_of(x);
             bool mine = in;

@@ -96,7 +96,7 @@ __device__ __forceinline__ void attend_row(const PagedCache &c, const RowKeys &k
         for (int e = 0; e < 8; ++e) {
             x[e] += __shfl_xor_sync(0xffffffffu, x[e], 8);
             x[e] += __shfl_xor_sync(0xffffffffu, x[e], 16);
-            x[e] *= inv;
+            x[e] = l == 0.f ? 0.f : x[e] * inv;  // (no finite logit: 0, whatever the values are)
         }
         if (lane < 8)
             *reinterpret_cast<uint4 *>(out + col + 64 * y) =
