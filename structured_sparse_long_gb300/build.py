@@ -27,7 +27,8 @@ NATIVE_PATH = os.path.join(LIB_DIR, "_pi_paged" + (sysconfig.get_config_var("EXT
 
 SOURCES = ["api.cu", "pi_simt.cu", "pi_fwd_tc.cu", "pi_bwd_tc.cu", "pi_decode.cu",
            "api_paged.cu", "pi_cache.cu", "pi_extend_tc.cu", "pi_decode_paged.cu"]
-HEADERS = ["pi_common.cuh", "pi_launch.h", "pi_tc_ptx.cuh", "pi_paged.h", "pi_paged.cuh", "pi_mma.cuh", "pi_tile.cuh", "pi_row.cuh"]
+HEADERS = ["pi_common.cuh", "pi_launch.h", "pi_tc_ptx.cuh", "pi_paged.h", "pi_plan.cuh", "pi_paged.cuh", "pi_mma.cuh", "pi_tile.cuh",
+           "pi_row.cuh"]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

@@ -248,9 +248,8 @@ paged_rows_kernel(const __grid_constant__ Args a) {
         if (blockIdx.z == 0 && kvh == 0 && rank == 0)  // offsets that decrease may hide their sequence from the search below
             for (int j = threadIdx.x; j < a.batch.B; j += blockDim.x)
                 if (ld_now(a.batch.cu + j) > ld_now(a.batch.cu + j + 1)) record_index(a.index_word);
-        // sequence b's token groups are numbered from (cu[b] + b (group - 1)) / group on, which leaves each its ceil(n / group)
         const int id = blockIdx.z, B = a.batch.B;
-        auto start = [&](int j, int at) -> long long { return ((long long)at + (long long)j * (a.group - 1)) / a.group; };
+        auto start = [&](int j, int at) -> long long { return plan::group_start(j, at, a.group); };
         int t0, t1, ctx;
         if (B <= 32) {  // a sequence per lane, so that one round of loads has everything
             const bool in = lane < B;

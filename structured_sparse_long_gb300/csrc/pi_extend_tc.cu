@@ -35,6 +35,7 @@
 #include "pi_launch.h"
 #include "pi_mma.cuh"
 #include "pi_paged.cuh"
+#include "pi_plan.cuh"
 #include "pi_row.cuh"
 #include "pi_tc_ptx.cuh"
 #include "pi_tile.cuh"
@@ -43,6 +44,8 @@ namespace pi {
 namespace ext {
 
 using namespace tc;
+using namespace plan;
+static_assert(TILE == CHUNK, "one size of tile");
 
 constexpr int BM = 128;         // rows per block (MMA M)
 constexpr int TMEM_COLS = 256;  // per CTA, two CTAs per SM
@@ -51,88 +54,6 @@ constexpr int THREADS = 256;
 
 // ------------------------------------------------------------------ the plan
 
-// A position block of one sequence and its key tiles, the same for every group of heads.
-struct PlanBlock {
-    int p0, tq, first, last;  // positions first .. last hold queries; row 0 is position p0 and packed token tq
-                              // (possibly before the sequence's own)
-    int b, lo, n_band, n_tiles;  // sequence; first band key of the first query; tiles from lo rounded down to 32, and all
-    int cpb;                     // tiles per skip window
-    uint32_t inv_cpb;            // ceil(2^32 / cpb), 0 for one tile
-    int full_lo, full_hi;        // tiles inside the band of every query
-    int slot, slot_lo, slot_windows, ctx;  // 8-bit caches: where the sequence's bf16 tiles are (SeqTiles);
-    int per_window, pad[3];                // slot_windows < 0: all in one run
-};
-static_assert(sizeof(PlanBlock) == 80, "16-byte loads");
-
-// The bf16 tiles of a sequence over an 8-bit cache, `slots` of them from slot on: either all tiles from its first
-// attended key to its last (band_tiles = 0: tile x, keys 32 x ..., in slot + x - lo), or the band's tiles followed by
-// `per_window` for each skip window, whichever is fewer (a long chunk's windows overlap).
-struct SeqTiles {
-    int lo;          // first tile of all, or of the band
-    int band_tiles;
-    int per_window;
-    int slots;
-};
-
-__host__ __device__ __forceinline__ SeqTiles seq_tiles(const Shape &s, int m_first, int n, int ctx) {
-    const int last = ctx + n - 1, band0 = band_lo(ctx, s.mode, s.k_local);
-    int windows = 0;
-    if (s.mode != kModeEcp && s.S > 0) {
-        const int m_last = last / s.period < s.S ? last / s.period : s.S;
-        windows = m_last >= m_first ? m_last - m_first + 1 : 0;
-    }
-    SeqTiles q;
-    q.lo = band0 >> 5;
-    q.band_tiles = (last >> 5) - q.lo + 1;
-    q.per_window = ((n - 1) >> 5) + 2;
-    q.slots = q.band_tiles;
-    if (windows > 0) {
-        const long long far = (long long)ctx - (long long)(m_first + windows - 1) * s.period;
-        int lo = far > 0 ? (int)(far >> 5) : 0;
-        if (q.lo < lo) lo = q.lo;
-        const long long each = q.band_tiles + (long long)windows * q.per_window;
-        const int all = (last >> 5) - lo + 1;
-        if (all <= each) {
-            q.lo = lo;
-            q.band_tiles = 0;
-            q.slots = all;
-        } else {
-            q.slots = (int)each;
-        }
-    }
-    return q;
-}
-
-// The tile in a sequence's slot `place` (negative: none).
-__device__ __forceinline__ int slot_tile(const Shape &s, int m_first, const SeqTiles &q, int n, int ctx, int place) {
-    if (!q.band_tiles || place < q.band_tiles) return q.lo + place;
-    const int w = (place - q.band_tiles) / q.per_window, back = (m_first + w) * s.period;
-    const int tile = ((ctx - back) >> 5) + (place - q.band_tiles) % q.per_window;
-    // the window's last tile may lie past it, and a whole tile before the sequence
-    return tile > (ctx + n - 1 - back) >> 5 ? -1 : tile;
-}
-
-// Most slots that a batch can take, from its sizes alone (cap: positions a page table reaches); below 2^60 for any that the
-// C ABI lets through.
-static long long most_slots(const Shape &s, long long B, long long T, long long cap) {
-    const long long seqs = std::min(B, T);
-    const long long band = std::min<long long>(cap, s.mode == kModeEcp ? 2LL * s.k_local : s.k_local);
-    long long windows = 0, reach = band;
-    if (s.mode != kModeEcp && s.S > 0) {
-        windows = std::min<long long>(s.S, cap / s.period);
-        reach = std::min<long long>(cap, std::max(band, windows * s.period));
-    }
-    const long long each = (T + seqs * band) / 32 + 2 * seqs + windows * (T / 32 + 2 * seqs);
-    const long long all = (T + seqs * reach) / 32 + 2 * seqs;
-    return std::min(each, all);
-}
-constexpr int PLAN_HEAD = 32;  // bytes before the blocks: [0] their number, [1] the slots used
-
-__host__ __device__ __forceinline__ long long max_blocks(long long T, long long B, int R) {
-    // n tokens lie in at most floor(n / R) + 2 blocks, and a sequence without tokens in none
-    return T / R + 2 * (B < T ? B : T);
-}
-
 constexpr int PLAN_THREADS = 256, PLAN_CTAS = 8;  // each makes the same sums and writes its share
 
 struct PlanArgs {
@@ -140,55 +61,26 @@ struct PlanArgs {
     PagedCache c;
     PagedBatch bt;
     int R, m_first;
-    int aligned;  // period % 32 == 0: every skip window has the same place in its tiles
     int *plan, *index_word;
     int2 *slots;  // 8-bit caches: [slot] sequence and tile (negative: before the sequence); else null
 };
-
-__device__ __forceinline__ PlanBlock plan_block(const PlanArgs &a, int b, int t0, int n, int ctx, int p0) {
-    const Shape &s = a.s;
-    PlanBlock k;
-    k.p0 = p0;
-    k.tq = t0 + p0 - ctx;
-    k.first = max(p0, ctx);
-    k.last = min(p0 + a.R, ctx + n) - 1;
-    k.b = b;
-    k.lo = band_lo(k.first, s.mode, s.k_local);
-    const int key0 = k.lo & ~(CHUNK - 1);
-    k.n_band = (k.last - key0) / CHUNK + 1;
-    int windows = 0;
-    if (s.mode != kModeEcp && s.S > 0) windows = max(0, min(s.S, k.last / s.period) - a.m_first + 1);
-    k.cpb = a.aligned ? (k.last >> 5) - (k.first >> 5) + 1 : ((k.last - k.first) >> 5) + 2;
-    k.inv_cpb = 0xffffffffu / (uint32_t)k.cpb + 1u;
-    k.n_tiles = k.n_band + windows * k.cpb;
-    k.full_lo = (band_lo(k.last, s.mode, s.k_local) - key0 + CHUNK - 1) / CHUNK;
-    const int span = k.first - (CHUNK - 1) - key0;
-    k.full_hi = span >= 0 ? span / CHUNK : -1;
-    return k;
-}
 
 __device__ __forceinline__ PlanBlock *plan_blocks(const PlanArgs &a) {
     return reinterpret_cast<PlanBlock *>(reinterpret_cast<char *>(a.plan) + PLAN_HEAD);
 }
 
-// n tokens at ctx ..: blocks at multiples of R, or one where a short chunk starts
-__device__ __forceinline__ int first_block(int n, int ctx, int R) { return n <= R ? ctx : ctx / R * R; }
-__device__ __forceinline__ int count_blocks(int n, int ctx, int R) { return (ctx + n - 1 - first_block(n, ctx, R)) / R + 1; }
-
 // Block `x` of the plan: the one at `place` of sequence b, whose bf16 tiles (8-bit caches) are in slot and the following.
 __device__ __forceinline__ void write_block(const PlanArgs &a, int x, int b, int t0, int n, int ctx, int place, int slot) {
     PlanBlock *to = plan_blocks(a) + x;
-    const PlanBlock k = plan_block(a, b, t0, n, ctx, first_block(n, ctx, a.R) + place * a.R);
+    PlanBlock k = plan_block(a.s, a.m_first, a.R, b, t0, n, ctx, first_block(n, ctx, a.R) + place * a.R);
     int4 *out = reinterpret_cast<int4 *>(to);
     out[0] = make_int4(k.p0, k.tq, k.first, k.last);
     out[1] = make_int4(k.b, k.lo, k.n_band, k.n_tiles);
     out[2] = make_int4(k.cpb, (int)k.inv_cpb, k.full_lo, k.full_hi);
     if (!a.slots) return;
-    const SeqTiles q = seq_tiles(a.s, a.m_first, n, ctx);
-    // a tile of the band (or any, where they are all in one run) is in slot + x - slot_lo, one of skip window w in
-    // slot_windows + w * per_window + x - (its first tile)
-    out[3] = make_int4(slot, q.lo, q.band_tiles ? slot + q.band_tiles : -1, ctx);
-    to->per_window = q.per_window;
+    place_slots(k, seq_tiles(a.s, a.m_first, n, ctx), slot, ctx);
+    out[3] = make_int4(k.slot, k.slot_lo, k.slot_windows, k.ctx);
+    to->per_window = k.per_window;
 }
 
 // A warp's view of a batch of at most 32 sequences, one to a lane.
@@ -515,7 +407,7 @@ struct Args {
     const int *plan;
     int GP, R, R_log2, ngrp;
     int m_first;
-    int aligned;  // period % 32 == 0
+    int aligned;  // skips_aligned()
     int box;      // rows of a TMA box: min(32, page)
     int n_planes; // pages, or slots of converted tiles
     FastDiv div_ngrp, div_G;
@@ -553,30 +445,6 @@ __device__ __forceinline__ void load_block(const Args &a, int L, Block &k) {
     if (CONVERTED) load_slots(a, L, k);
     k.h0 = first_head(a, L);
     k.g = a.div_G.div(k.h0);
-}
-
-// Tile ti of a block: its first key (negative: a tile wholly before the sequence), whether it is a skip tile,
-// and its skip distance.
-__device__ __forceinline__ int tile_key0(const Args &a, const PlanBlock &k, int ti, int &back, bool &skip) {
-    skip = ti >= k.n_band;
-    if (!skip) {
-        back = 0;
-        return (k.lo & ~(CHUNK - 1)) + ti * CHUNK;
-    }
-    const uint32_t x = (uint32_t)(ti - k.n_band);
-    const uint32_t w = k.inv_cpb ? __umulhi(x, k.inv_cpb) : x;
-    back = (a.m_first + (int)w) * a.a.s.period;
-    return ((k.first - back) & ~(CHUNK - 1)) + (int)(x - w * (uint32_t)k.cpb) * CHUNK;
-}
-
-// Keys of tile ti that some query of the block attends or may attend: lo .. hi (empty: lo > hi).
-__device__ __forceinline__ int tile_range(const Args &a, const PlanBlock &k, int ti, int &lo, int &hi) {
-    int back;
-    bool skip;
-    const int key0 = tile_key0(a, k, ti, back, skip);
-    lo = max(key0, skip ? max(0, k.first - back) : k.lo);
-    hi = min(key0 + CHUNK - 1, k.last - back);
-    return key0;
 }
 
 // The non-finite rows of the CTA's blocks, each by a warp.
@@ -670,15 +538,13 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         row = 0;
         if (t0 + lane >= k.n_tiles) return;
         int lo, hi;
-        const int key0 = tile_range(args, k, t0 + lane, lo, hi);
+        const int key0 = tile_range(args.m_first, args.a.s.period, k, t0 + lane, lo, hi);
         if (CONVERTED) {
             if (lo > hi) return;
             int back;
             bool skip;
-            tile_key0(args, k, t0 + lane, back, skip);
-            e0 = skip && k.slot_windows >= 0
-                     ? k.slot_windows + (back / s.period - args.m_first) * k.per_window + (key0 >> 5) - ((k.ctx - back) >> 5)
-                     : k.slot + (key0 >> 5) - k.slot_lo;
+            tile_key0(args.m_first, args.a.s.period, k, t0 + lane, back, skip);
+            e0 = tile_slot(args.m_first, s.period, k, key0, back, skip);
             return;
         }
         const int *table = ea.batch.table + (long long)k.b * cache.width;
@@ -916,7 +782,7 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 if (w && ragged) {
                     // rows of V that no query attends: zero
                     int lo, hi;
-                    const int key0 = tile_range(args, k, t, lo, hi);
+                    const int key0 = tile_range(args.m_first, args.a.s.period, k, t, lo, hi);
                     if (lo > key0 || hi < key0 + CHUNK - 1) {  // the same for the warp
                         if (key0 + lane < lo || key0 + lane > hi) {
                             uint8_t *row = smem + C::V_OFF + st * C::KV_STAGE + lane * ROW_BYTES;
@@ -1010,7 +876,7 @@ extend_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 } else {
                     int back, chi;
                     bool sk;
-                    const int key0 = tile_key0(args, k, t, back, sk);
+                    const int key0 = tile_key0(args.m_first, args.a.s.period, k, t, back, sk);
                     float off;
                     if (!sk) {
                         clo = max(lo_i - key0, 0);
@@ -1243,9 +1109,9 @@ cudaError_t launch_extend(const ExtendArgs &e, cudaStream_t st) {
     char *ws = reinterpret_cast<char *>(e.workspace);
     int2 *slots = quant ? reinterpret_cast<int2 *>(ws + l.slots) : nullptr;
     Args a{e, e.workspace, GP, R, R == 32 ? 5 : R == 64 ? 6 : 7, ngrp, skips ? first_skip_multiple(s) : 1,
-           skips && s.period % CHUNK == 0, quant ? CHUNK : std::min(CHUNK, c.page), quant ? (int)l.n_slots : c.n_pages,
+           skips_aligned(s), quant ? CHUNK : std::min(CHUNK, c.page), quant ? (int)l.n_slots : c.n_pages,
            make_fastdiv(ngrp), make_fastdiv(G)};
-    const PlanArgs pa{s, c, e.batch, R, a.m_first, a.aligned, e.workspace, e.index_word, slots};
+    const PlanArgs pa{s, c, e.batch, R, a.m_first, e.workspace, e.index_word, slots};
     cudaError_t err = cudaSuccess;
     const bool lanes = e.batch.B <= 32;
     if (!quant || !lanes) {

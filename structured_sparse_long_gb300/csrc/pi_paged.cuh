@@ -19,6 +19,7 @@
 
 #include "pi_common.cuh"
 #include "pi_paged.h"
+#include "pi_plan.cuh"
 
 namespace pi {
 
@@ -86,15 +87,9 @@ __device__ __forceinline__ int scale_exp(float amax) {
 template <typename F>
 __device__ __forceinline__ int find_sequence(int B, F below) {
     const int lane = threadIdx.x & 31;
-    int lo = 0, len = B;
-    while (len > 0) {
-        const int step = (len + 31) >> 5;
-        const int k = (lane + 1) * step;
-        const int c = __popc(__ballot_sync(0xffffffffu, k <= len && below(lo + k)));
-        lo += c * step;
-        len = min(step - 1, len - c * step);
-    }
-    return lo;
+    SearchRange r(B);
+    while (r.len > 0) r.narrow(__popc(__ballot_sync(0xffffffffu, r.inside(lane) && below(r.place(lane)))));
+    return r.lo;
 }
 
 // Whether a sequence's offsets and context are in range: its tokens inside the batch, its rows inside
