@@ -111,7 +111,7 @@ def load_peaks():
 
 
 KERNEL_SOURCES = {
-    "fwd": ("pi_fwd_tc.cu", "pi_common.cuh", "pi_launch.h", "pi_tc_ptx.cuh"),
+    "fwd": ("pi_fwd_tc.cu", "pi_common.cuh", "pi_launch.h", "pi_tc_ptx.cuh", "pi_tile.cuh"),
     "bwd": ("pi_bwd_tc.cu", "pi_common.cuh", "pi_launch.h", "pi_tc_ptx.cuh"),
     "dec": ("pi_decode.cu", "pi_common.cuh", "pi_launch.h", "pi_tc_ptx.cuh"),
 }
