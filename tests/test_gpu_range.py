@@ -97,3 +97,28 @@ def test_large_values_over_pages(case, kv):
     ref.check_attention(name, out, lse, want)
     out, lse = pa.decode_paged(q[-1:].cuda(), cache, table, at(N), None if da is None else da[-1:], kl, per, S, mode)
     ref.check_attention(name + " token", out, lse, [x[-1:] for x in want])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("slope", [0.2, 0.37, 1.0, -0.4])
+@pytest.mark.parametrize("k_local,mode", [(250, PI), (96, ECP), (200, BIDIR)])
+def test_logits_that_rise_along_the_keys(d, slope, k_local, mode):
+    """Logits that rise (or fall) by `slope` log2 units per key over runs of 300 keys: the reference moves within tiles, between them,
+    in tiles with and without masks.
+
+    A logit z is a sum of d products of one sign in 32 bits, off by at most d 2^-24 |z|, and |z| <= 300 |slope| ln 2 and a bit;
+    a weight is off by as much, relative, lse by as much, and the output by twice that of sum p |v|, beside the roundings of
+    paged_ref.check_attention."""
+    N, H, Hkv, S, per = 700, 4, 2, (0 if mode == ECP else 2), 256
+    q, _, v = inputs(d, N, H, Hkv, 1.0, lambda j: j < 0, seed=9)
+    gen = torch.Generator().manual_seed(1)
+    rise = slope * (torch.arange(N) % 300) / 1.4427 / d ** 0.5
+    k = (rise[:, None] * q[0, 0, 0].float() + 0.01 * torch.randn(1, Hkv, N, d, generator=gen)).to(torch.bfloat16)
+    alpha = None if mode == ECP else torch.full((1, H, N), 0.5)
+    out, lse = pa.fwd(q.cuda(), k.cuda(), v.cuda(), None if alpha is None else alpha.cuda(), k_local, per, S, mode)
+    out, lse = out.float().cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64)
+    ro, rl = oracle.fwd(q, k, v, alpha, k_local, per, S, mode)
+    size, _ = oracle.fwd(q, k, v.abs(), alpha, k_local, per, S, mode)
+    eps = d * 2.0 ** -24 * (300 * abs(slope) * 0.6932 + 8)
+    assert (np.abs(out - ro) <= 2.0 ** -8 * np.abs(ro) + (2.0 ** -8 + 2.0 ** -12 + 2 * eps) * size).all()
+    assert (np.abs(lse - rl) <= 2.0 ** -12 + eps + 2.0 ** -22 * np.abs(rl)).all()
