@@ -310,7 +310,8 @@ int pi_attn_decode(const void *q, const void *k_cache, const void *v_cache, cons
  *   These three live on the device; the kernels check them (PI_ERR_INDEX).
  *
  * Ownership, asynchrony and errors are those of the other calls.  Sequences that share
- * pages may read them; two tokens of one call written to the same row race.
+ * pages may read them; two tokens of one call written to the same row race.  Outputs may
+ * overlap neither an input nor the cache.
  */
 typedef enum { PI_KV_BF16 = 0, PI_KV_E4M3 = 1, PI_KV_INT8 = 2 } pi_kv_type_t;
 
@@ -358,7 +359,11 @@ int pi_attn_cache_read(const pi_attn_cache_t *cache, const pi_attn_batch_t *batc
  *   A sequence with an offset or length out of range is left out, its rows of out and lse
  *   as they were (where cu decreases anywhere, any of the batch's rows may be); a row that attends a key on a page out of range is undefined.
  *   A token's results depend on the rows that it attends alone: what the other rows hold, NaN
- *   and infinities among it, does not matter.
+ *   and infinities among it, does not matter.  Weights are rounded to bf16 (2^-8 of each at
+ *   most) for their product with the values, as in pi_attn_fwd; lse sums them unrounded.
+ *   The kernels are chosen by B and T, as if all sequences were equally long: a long chunk and many
+ *   single tokens take less time as two calls (2000 tokens and 63 single ones, 16 heads on 4, d = 128:
+ *   26 us in one call, 24 in two over bf16, 44 and 29 over e4m3).
  *   workspace: device buffer of at least pi_attn_extend_workspace_size() bytes for these
  *   sizes (none for short chunks: it may be NULL then), 256-byte aligned, owned by the caller, contents ignored on entry; calls that may
  *   overlap need one each.  It holds the call's plan (about 2.5 T + 160 B bytes) and, for an
@@ -387,7 +392,8 @@ int pi_attn_extend(const void *q, long long q_stride, const pi_attn_cache_t *cac
  *   a length out of range.  q [B, H, d] bf16 with sequences q_stride elements apart,
  *   alpha [B, H] fp32 (NULL in ECP mode), out [B, H, d] bf16, lse [B, H] fp32; table
  *   [B, width] as above.  H / Hkv <= 16; B <= 65535.  A row that attends a key on
- *   a page out of range is undefined.
+ *   a page out of range is undefined.  Weights are rounded as in pi_attn_extend
+ *   (pi_attn_decode keeps them in fp32: its outputs are closer by up to 2^-8 of sum p |v|).
  */
 int pi_attn_decode_paged(const void *q, long long q_stride, const pi_attn_cache_t *cache,
                          const int *table, const int *lens, int B, int width, const float *alpha,

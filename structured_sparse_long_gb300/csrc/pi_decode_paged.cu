@@ -338,8 +338,8 @@ paged_rows_kernel(const __grid_constant__ Args a) {
     }
 
     // ---- the warp's tiles.  Lanes 0-15 hold the rows of one tile, 16-31 those of the warp's next one.  (Requesting the next
-    // tile's K after this one's scores, and its V after P V, took 15.8 us where this takes 12.7: the waits for the older
-    // loads also wait for the newer ones.)
+    // tile's K after this one's scores, and its V after P V, took 64 sequences 15.8 us instead of 12.7 in an earlier state that takes
+    // 10.0 now: the waits for the older loads also wait for the newer ones.)
     const int step = P * warps;
     int tile = rank * warps + warp;
     Frag<D, KV> f;
@@ -415,7 +415,7 @@ paged_rows_kernel(const __grid_constant__ Args a) {
             }
         }
     // ---- and meet: four columns of a row per thread, all the cluster's states at once (a merge in each CTA first and then one
-    // of the CTAs' took 10.4 us where this takes 9.1, 16 drafts of up to 5 tokens in clusters of three)
+    // of the CTAs' took 10.6 us where this takes 9.1, 16 drafts of up to 5 tokens in clusters of three)
     constexpr int PER_ROW = D / 4, BATCH = 12;  // threads of a row; states in flight
     const int states = P * warps, items = cols * PER_ROW;
     const uint32_t base = smem_addr(part);
