@@ -307,7 +307,7 @@ int pi_attn_decode(const void *q, const void *k_cache, const void *v_cache, cons
  *   none; cu[0] = 0, cu does not decrease, and cu[B] <= T.  Tokens cu[B] .. T - 1 belong to no sequence: nothing
  *   of theirs is written.  ctx [B] int32: the position of a sequence's first token, i.e.
  *   the rows it has in the cache already.  ctx[b] + cu[b+1] - cu[b] <= width * page.
- *   These three live on the device; the kernels check them (PI_ERR_INDEX).
+ *   These three live on the device; the kernels check them (PI_ERR_INDEX).  B <= 2^30.
  *
  * Ownership, asynchrony and errors are those of the other calls.  Sequences that share
  * pages may read them; two tokens of one call written to the same row race.  Outputs may

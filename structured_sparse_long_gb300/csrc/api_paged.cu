@@ -9,6 +9,7 @@
 
 namespace {
 
+constexpr int kMaxSequences = 1 << 30;              // what the search of a token's sequence numbers in an int
 constexpr uint64_t kWaitTimeoutNs = 2000000000ull;  // bound on every device-side wait
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -45,6 +46,7 @@ int make_cache(const pi_attn_cache_t *c, int width, pi::PagedCache &out) {
 int make_batch(const pi_attn_batch_t *b, pi::PagedBatch &out) {
     if (!b->table || !b->cu || !b->ctx) return PI_ERR_NULL;
     if (b->B <= 0 || b->T <= 0) return PI_ERR_SHAPE;
+    if (b->B > kMaxSequences) return PI_ERR_UNSUPPORTED;
     if (!aligned(b->table, 4) || !aligned(b->cu, 4) || !aligned(b->ctx, 4)) return PI_ERR_ALIGN;
     out.table = b->table; out.cu = b->cu; out.ctx = b->ctx; out.B = b->B; out.T = b->T;
     return PI_OK;
@@ -114,7 +116,7 @@ size_t pi_attn_extend_workspace_size(const pi_attn_cache_t *cache, int B, int T,
                                      int mode) {
     static const float some_alpha = 0.f;
     pi::ExtendArgs a{};
-    if (B <= 0 || T <= 0 || make_cache(cache, width, a.cache) != PI_OK ||
+    if (B <= 0 || T <= 0 || B > kMaxSequences || make_cache(cache, width, a.cache) != PI_OK ||
         make_attention(a.cache, H, k_local, period, S, mode, &some_alpha, a.s) != PI_OK)
         return 0;
     a.batch.B = B;

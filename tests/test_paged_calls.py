@@ -150,3 +150,15 @@ def test_the_workspace_size_is_the_cache_devices(calls, monkeypatch):
         m.setattr(paged, "_load", lambda: Library)
         assert paged.extend_workspace_size(cache, 1, 1, 4, 20, 8, 16, 1) > 0
     assert asked == [cache.index] and current == [3]
+
+
+def test_more_sequences_than_the_search_can_number():
+    """The search's probes lie up to 32 times a 32nd of B, rounded up, which has to fit an int."""
+    pbuild.build()
+    lib = paged._load()
+    for B in (2 ** 30 + 1, 2 ** 31 - 31, 2 ** 31 - 1):
+        c, b = sizes(20, B=B)
+        assert lib.pi_attn_cache_append(A16, A16, 128, 128, c, b, None) == PI_ERR_UNSUPPORTED
+        assert lib.pi_attn_cache_read(c, b, A16, A16, None) == PI_ERR_UNSUPPORTED
+        assert lib.pi_attn_extend(A16, 128, c, b, A16, 1, 8, 1, 0, 0, A16, A16, A16, 2 ** 64 - 1, None) == PI_ERR_UNSUPPORTED
+        assert lib.pi_attn_extend_workspace_size(c, B, 20, 4, 1, 8, 1, 0, 0) == 0
