@@ -400,6 +400,113 @@ int pi_attn_decode_paged(const void *q, long long q_stride, const pi_attn_cache_
                          int H, int k_local, int period, int S, int mode, void *out, float *lse,
                          void *stream);
 
+/* ------------------------------------------------------------------------
+ * Rotary positions: the elements of a query or key row turned in pairs by angles that grow
+ * with its position.
+ *
+ * pi_attn_rotary_t -- which elements turn, and how fast.
+ *   rot: a row's first rot elements turn, a multiple of 16, at most d; the others stay.  Pair t < rot / 2 is
+ *   (x_a, x_b) with a = t, b = t + rot / 2, or, interleaved != 0, a = 2 t, b = 2 t + 1.  At position p
+ *     y_a = scale (x_a cos - x_b sin),  y_b = scale (x_a sin + x_b cos),  angle 2 pi p step[t] / 2^64.
+ *   step [rot / 2] (device, 8-byte aligned): turns per position in units of 2^-64, i.e. frequency f (radians
+ *   per position) as round(f 2^64 / 2 pi) mod 2^64.  Products of a position and a step wrap as turns do, so
+ *   that an angle is off by at most |p| 2^-65 turns, and 2^-24 of a half turn for its 32-bit form, however far p is.
+ *   scale: any finite number (a scaled context's factor; else 1).
+ * Elements are turned in 32 bits and rounded once.
+ */
+typedef struct {
+    const unsigned long long *step;
+    int rot, interleaved;
+    float scale;
+} pi_attn_rotary_t;
+
+/*
+ * pi_attn_rotary -- q [B, H, N, d] and k [B, Hkv, N, d] turned by their positions, before pi_attn_fwd, or (back != 0)
+ * their gradients, after pi_attn_bwd: the transpose, i.e. the angle negated and the same scale.
+ *   Each tensor has strides {batch, head, position} in elements, the d elements of a row being contiguous: tensors may
+ *   lie in a projection's output, and q_out and k_out in the layout that pi_attn_fwd takes, or the other way round.
+ *   Strides: >= 0, below 2^38, multiples of 8 (bf16) or 4 (fp32), and for outputs at least d, all where the dimension
+ *   is larger than 1 (else PI_ERR_SHAPE); pointers 16-byte aligned.  An output is its own input, with the same strides, or
+ *   overlaps no other tensor; an output's rows do not overlap each other.
+ *   Hkv = 0: q alone (k, k_out and their strides are not used).  pos [B, N] int32 (device): the rows' positions, of any
+ *   sign; NULL: start, start + 1, ... with start >= 0, start + N <= 2^31.  f32: fp32 tensors instead of bf16.
+ *   d in {32, 64, 128}; B * N * (H + Hkv) * d < 2^45, B * N < 2^31, H and Hkv <= 65535 (else PI_ERR_UNSUPPORTED).  Deterministic.
+ */
+int pi_attn_rotary(const void *q, const long long *q_strides, const void *k, const long long *k_strides,
+                   const pi_attn_rotary_t *rotary, const int *pos, int start, int B, int H, int Hkv, int N, int d, int f32,
+                   int back, void *q_out, const long long *q_out_strides, void *k_out, const long long *k_out_strides,
+                   void *stream);
+
+/* ------------------------------------------------------------------------
+ * A speculative serving step: a tree of drafted tokens per sequence goes through the paged cache.
+ *
+ * A sequence's new tokens are the nodes of a tree: node j (its j-th packed token) has the parent
+ * parent[cu[b] + j], a node number below j, or -1 where it follows the last cached token.  Node j's key and value
+ * rows lie in cache row ctx[b] + j, as pi_attn_cache_append writes them; its position in the text is ctx[b] plus its
+ * depth (the number of its ancestors).  parent [T] int32 (device).  A sequence has at most PI_ATTN_TREE_MAX
+ * nodes; one with more, or with a parent out of range, is left out like one with an offset out of range (PI_ERR_INDEX).
+ * parent = NULL: every sequence's tokens follow one another (no bound on their number).
+ */
+#define PI_ATTN_TREE_MAX 256
+
+/*
+ * pi_attn_rotary_append -- pi_attn_cache_append with the queries and keys turned by their positions on the way:
+ *   q [T, H, d] bf16 to q_out [T, H, d], k into the cache (quantised from the 32-bit result where it holds 8 bits),
+ *   v into the cache as it is.  Token strides as for pi_attn_cache_append, also for q_out, which may be q itself (with q's
+ *   stride).  A token whose sequence or page is out of range is left out, its row of q_out as it was; so are the
+ *   rows of tokens behind the last sequence.  H <= 65535 (else PI_ERR_UNSUPPORTED).
+ */
+int pi_attn_rotary_append(const void *q, long long q_stride, const void *k, long long k_stride, const void *v, long long v_stride,
+                          const pi_attn_rotary_t *rotary, const pi_attn_cache_t *cache, const pi_attn_batch_t *batch,
+                          const int *parent, int H, void *q_out, long long q_out_stride, void *stream);
+
+/*
+ * pi_attn_extend_tree -- pi_attn_extend for a tree of drafted tokens per sequence, whose rows the cache holds.
+ *   The node at position i attends U(i): a position below ctx[b] is the sequence's cached row of that number, one
+ *   from ctx[b] on is the node's ancestor (or itself) at that depth.  Arguments, layouts and errors as pi_attn_extend,
+ *   with parent [T] (not NULL); a sequence that is left out keeps its rows of out and lse.  H / Hkv <= 16; T * H < 2^31
+ *   (else PI_ERR_UNSUPPORTED).  A node's results depend on the rows that it attends alone.  Weights are rounded as in
+ *   pi_attn_extend.  Deterministic.
+ */
+int pi_attn_extend_tree(const void *q, long long q_stride, const pi_attn_cache_t *cache, const pi_attn_batch_t *batch,
+                        const int *parent, const float *alpha, int H, int k_local, int period, int S, int mode, void *out,
+                        float *lse, void *stream);
+
+/*
+ * pi_attn_verify_tree -- which of a tree's drafted tokens the target accepts, and the token after them.
+ *   Node 0 of every sequence is its last sampled token: it is accepted.  At an accepted node x with target probabilities
+ *   p = target[cu[b] + x] its children are tested in their order.  With draft probabilities q = draft[cu[b] + x], from which the
+ *   children were drawn independently, a child with token v and random number r is accepted when
+ *     r q_v s < w_v,   w = max(p - a q, 0),   a = 0 and s = 1 at first;   when it is not, a += s and then s = sum w
+ *   (w / s is what is left of p after the children tested so far).  Without draft probabilities (draft NULL: the
+ *   children are chosen tokens) q_v is 1, and a child that is not accepted takes its w_v out: s -= w_v, w_v = 0.  The first accepted child
+ *   is the next node; where there is none the walk ends, and the next token is the lowest v at which the running sum of
+ *   w exceeds u_next[b] times the whole sum (w = p where no w is left).  So the accepted tokens and the next one are
+ *   distributed as the target's own.  Children of other roots than node 0 are not tested.
+ *   target, draft [T, V] fp32 with rows target_stride, draft_stride elements apart (>= V, below 2^38); elements that are negative or
+ *   not finite count as 0.  tokens [T] int32 in [0, V) (node 0's is not read); u [T], u_next [B] fp32 in [0, 1) (what is outside counts
+ *   as the nearest in it, NaN as 0).  cu [B + 1], parent [T] as above.
+ *   Writes path [T] int32: the accepted nodes of sequence b from path[cu[b]] on, the rest of its places -1; count [B]: how
+ *   many; next [B]: the next token, or -1 where no p is above 0.  A sequence without tokens, or one that is left out, gets
+ *   count 0 and next -1, and keeps its places of path.  w, s and a carry 48 bits or more.  1 <= B <= 65535, T > 0, 0 < V <= 2^30.
+ *   Deterministic.
+ */
+int pi_attn_verify_tree(const float *target, long long target_stride, const float *draft, long long draft_stride,
+                        const int *tokens, const int *cu, const int *parent, const float *u, const float *u_next, int B, int T,
+                        int V, int *path, int *count, int *next, void *stream);
+
+/*
+ * pi_attn_cache_keep -- the rows of an accepted path moved together: of sequence b row ctx[b] + path[cu[b] + j] goes to row
+ *   ctx[b] + j, for j < count[b], keys and values, in each of n_caches layers that share the page table.
+ *   path [T], count [B] int32 (device) as pi_attn_verify_tree writes them: ascending node numbers.  caches: n_caches
+ *   descriptors (host memory, read before the call returns) of the same type and sizes (else PI_ERR_SHAPE), whose rows do not overlap.
+ *   A sequence with an offset, length, count or path out of range is left out; so is a row whose source or place is
+ *   on a page out of range.  Sequences must not share pages that rows are moved in.  B * ceil(2 Hkv (row bytes / 16 + 1) / 256) < 2^31
+ *   (else PI_ERR_UNSUPPORTED).
+ */
+int pi_attn_cache_keep(const pi_attn_cache_t *caches, int n_caches, const pi_attn_batch_t *batch, const int *path,
+                       const int *count, void *stream);
+
 /*
  * pi_attn_status -- synchronises `stream`, reads the current device's status
  * word, resets it to PI_OK and returns what it held (PI_OK, PI_ERR_DEVICE_TIMEOUT or

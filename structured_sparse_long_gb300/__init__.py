@@ -13,9 +13,12 @@ from ._binding import (MODE_ECP, MODE_PI, MODE_PI_BIDIR, PiAttnError, bwd, bwd_n
                        strerror)
 from .paged import (KV_BF16, KV_E4M3, KV_INT8, PagedCache, cache_append, cache_read, decode_paged,  # noqa: F401
                     extend, extend_workspace_size)
+from .step import (TREE_MAX, CacheLayers, Rotary, cache_keep, extend_tree, rotary, rotary_append,  # noqa: F401
+                   rotary_bwd, rotary_frequencies, verify_tree)
 
 __all__ = ["fwd", "fwd_gated", "fwd_shard", "bwd", "bwd_shard", "decode", "bwd_noalloc",
            "bwd_workspace_size", "status", "strerror", "debug_counts", "debug_probs", "debug_trace",
            "debug_wait_timeout", "load", "lib_path", "PiAttnError", "MODE_PI", "MODE_ECP",
            "MODE_PI_BIDIR", "PagedCache", "cache_append", "cache_read", "extend", "extend_workspace_size", "decode_paged", "KV_BF16",
-           "KV_E4M3", "KV_INT8"]
+           "KV_E4M3", "KV_INT8", "Rotary", "rotary_frequencies", "rotary", "rotary_bwd", "rotary_append", "extend_tree",
+           "verify_tree", "CacheLayers", "cache_keep", "TREE_MAX"]

@@ -11,6 +11,7 @@
 // to 1024 sequences) while their elements are in flight.
 #include "pi_mma.cuh"
 #include "pi_paged.cuh"
+#include "pi_quant.cuh"
 
 namespace pi {
 namespace cache {
@@ -44,30 +45,9 @@ __device__ __forceinline__ float absmax32(const Piece<kKvE4m3> &p) {
 // Eight elements to eight codes, given the block's scale exponent.
 template <int KV>
 __device__ __forceinline__ uint2 encode8(const uint4 &x, int e) {
-    const float inv = __uint_as_float((uint32_t)(127 - e) << 23);  // 2^-e, -e in [-122, 120]
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    uint32_t o[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        float y[4];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            y[2 * j] = __uint_as_float(w[2 * i + j] << 16);
-            y[2 * j + 1] = __uint_as_float(w[2 * i + j] & 0xffff0000u);
-        }
-        if (KV == kKvE4m3) {
-            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0] * inv, y[1] * inv), __NV_SATFINITE, __NV_E4M3);
-            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2] * inv, y[3] * inv), __NV_SATFINITE, __NV_E4M3);
-            o[i] = lo | hi << 16;
-        } else {
-            // in 2^23 .. 2^24 the step is 1: the sum's rounding is the code's, and its low byte the code
-            uint32_t c[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) c[j] = __float_as_uint(fmaf(y[j], inv, 12582912.f));
-            o[i] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
-        }
-    }
-    return make_uint2(o[0], o[1]);
+    float y[8];
+    unpack8(x, y);
+    return encode_codes<KV>(y, e);
 }
 
 // A piece into the cache (`in`: this lane has one; the others of the warp take part in the block maxima only).

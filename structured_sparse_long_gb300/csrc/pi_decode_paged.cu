@@ -27,6 +27,7 @@
 #include "pi_mma.cuh"
 #include "pi_paged.cuh"
 #include "pi_row.cuh"
+#include "pi_tree.cuh"
 
 #include "pi_launch.h"
 
@@ -37,20 +38,23 @@ constexpr int MAX_P = 8;   // CTAs per cluster (portable limit)
 constexpr int KEYS = 16;   // keys per tile: the rows of S^T
 constexpr unsigned kFull = 0xffffffffu;
 
-// One step of decode (TOKENS = false: sequence b's one query at position lens[b] - 1), or a few new tokens per
-// sequence (TOKENS: packed queries as in pi_attn_extend, at most `group` of them per CTA).
+// One step of decode (sequence b's one query at position lens[b] - 1), or a few new tokens per sequence, at most `group` of
+// them per CTA: packed queries as in pi_attn_extend, or the nodes of a drafted tree.
+enum Kind { kSingle, kTokens, kTree };
 struct Args {
     const __nv_bfloat16 *q;
     long long q_stride;
     const float *alpha;
     const int *lens;
-    PagedBatch batch;  // B, table; cu, ctx and T with TOKENS
+    PagedBatch batch;  // B, table; all but for kSingle cu, ctx and T
     __nv_bfloat16 *out;
     float *lse;
     Shape s;
     PagedCache cache;
     int *index_word;
     int m_first, group;
+    const int *parent;  // kTree: [T]
+    int group0;         // kTree: the launch's first group of tokens
 };
 
 // ---- what a lane holds of a tile -------------------------------------------------------------
@@ -208,19 +212,24 @@ constexpr int sm_warps(int D, int KV, int NH) { return NH == 2 ? 8 : D == 128 ? 
 constexpr int max_warps(int D, int KV, int NH) { return sm_warps(D, KV, NH) / (NH == 2 ? 1 : 2); }
 
 // The row of token at / H and head at % H, position i of sequence b, by itself (pi_row.cuh).
-template <int D, int KV>
-__device__ __noinline__ void again(const Args &a, int b, int i, int kvh, int at) {
+template <int D, int KV, bool TREE>
+__device__ __noinline__ void again(const Args &a, int b, int i, int kvh, int at, int ctx, int t0) {
     const int tok = at / a.s.H;
-    attend_row<D, KV>(a.cache,
-                      row_keys(a.s, i, kvh, a.m_first, a.q + tok * a.q_stride + (at - tok * a.s.H) * D,
-                               a.batch.table + (long long)b * a.cache.width, a.alpha ? a.alpha + at : nullptr),
-                      a.out + (long long)at * D);
+    RowKeys k = row_keys(a.s, i, kvh, a.m_first, a.q + tok * a.q_stride + (at - tok * a.s.H) * D,
+                         a.batch.table + (long long)b * a.cache.width, a.alpha ? a.alpha + at : nullptr);
+    if (TREE) {
+        k.parent = a.parent + t0;
+        k.ctx = ctx;
+        k.node = tok - t0;
+    }
+    attend_row<D, KV, TREE>(a.cache, k, a.out + (long long)at * D);
 }
 
 // NH: groups of 8 columns (1 or 2), a column being one query head of one token
-template <int D, int KV, int NH, bool TOKENS>
+template <int D, int KV, int NH, Kind KIND>
 __global__ void __launch_bounds__(max_warps(D, KV, NH) * 32, sm_warps(D, KV, NH) / max_warps(D, KV, NH))
 paged_rows_kernel(const __grid_constant__ Args a) {
+    constexpr bool TOKENS = KIND != kSingle, TREE = KIND == kTree;
     const Shape &s = a.s;
     const PagedCache &c = a.cache;
     constexpr int PART = D + 4;  // floats of a column's partial state: o[D], m, l, padding to 16 bytes
@@ -232,7 +241,9 @@ paged_rows_kernel(const __grid_constant__ Args a) {
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // ---- the CTA's sequence b, its queries' positions first .. last and their first packed token tok0
-    int b, first, last, tok0;
+    int b, first, last, tok0, n_tok = 1;
+    TreeGroup *tree = nullptr;
+    if constexpr (TREE) tree = tree_group();
     if constexpr (!TOKENS) {
         b = tok0 = blockIdx.z;
         // the table's first entries are on their way while the length is (5.76 -> 5.70 us; copied to shared memory, 5.58 instead
@@ -245,10 +256,10 @@ paged_rows_kernel(const __grid_constant__ Args a) {
         }
         first = last;
     } else {
-        if (blockIdx.z == 0 && kvh == 0 && rank == 0)  // offsets that decrease may hide their sequence from the search below
+        if (blockIdx.z == 0 && kvh == 0 && rank == 0 && (!TREE || a.group0 == 0))  // offsets that decrease may hide their sequence from the search below
             for (int j = threadIdx.x; j < a.batch.B; j += blockDim.x)
                 if (ld_now(a.batch.cu + j) > ld_now(a.batch.cu + j + 1)) record_index(a.index_word);
-        const int id = blockIdx.z, B = a.batch.B;
+        const int id = (TREE ? a.group0 : 0) + blockIdx.z, B = a.batch.B;
         auto start = [&](int j, int at) -> long long { return plan::group_start(j, at, a.group); };
         int t0, t1, ctx;
         if (B <= 32) {  // a sequence per lane, so that one round of loads has everything
@@ -276,8 +287,15 @@ paged_rows_kernel(const __grid_constant__ Args a) {
         tok0 = t0 + x0;
         first = ctx + x0;
         last = min(first + a.group, ctx + t1 - t0) - 1;
+        n_tok = last - first + 1;
+        if constexpr (TREE) {  // first and last: the lowest and the highest position of the nodes
+            if (!tree_walk(*tree, s, a.parent + t0, t1 - t0, x0, n_tok, ctx, first, last)) {
+                if (threadIdx.x == 0) record_index(a.index_word);
+                return;
+            }
+        }
     }
-    const int n_tok = TOKENS ? last - first + 1 : 1, cols = n_tok * G;
+    const int cols = n_tok * G;
     // column x: token x / G, head x % G
     auto row_of = [&](int x) -> long long { return TOKENS ? (long long)(tok0 + x / G) * s.H + h0 + x % G : (long long)b * s.H + h0 + x; };
 
@@ -299,7 +317,12 @@ paged_rows_kernel(const __grid_constant__ Args a) {
     }
     // ---- the key list: the band lo .. last, then for each skip distance m * period, m = m_first ..., the n_tok keys that
     // many before the queries (some may lie before the sequence)
-    const int lo = last >= 0 ? band_lo(first, s.mode, s.k_local) : 0, n_band = last - lo + 1;
+    const int lo = last >= 0 ? band_lo(first, s.mode, s.k_local) : 0;
+    int n_band = last - lo + 1, n_cached = n_band;
+    if constexpr (TREE) {  // the band's cached keys, then the nodes that some of the queries attend
+        n_cached = max(tree->ctx - lo, 0);
+        n_band = n_cached + tree->n_rows;
+    }
     int n_keys = n_band;
     if (last >= 0 && s.mode != kModeEcp && s.S > 0) n_keys += n_tok * max(0, min(s.S, last / s.period) - a.m_first + 1);
     const int n_tiles = (n_keys + KEYS - 1) / KEYS;
@@ -309,12 +332,16 @@ paged_rows_kernel(const __grid_constant__ Args a) {
         tag = -0x7fffffff;  // attended by nobody
         if (kk >= n_keys) return;
         int pos;
-        if (kk < n_band) {
+        if (kk < n_cached) {
             pos = tag = lo + kk;
+        } else if (TREE && kk < n_band) {
+            const int node = tree->row[kk - n_cached];
+            pos = tree->ctx + node;
+            tag = kNodeTag + tree->mask[node];
         } else {
             const int x = kk - n_band, w = TOKENS ? x / n_tok : x, u = TOKENS ? x - w * n_tok : 0;
-            pos = first + u - (a.m_first + w) * s.period;
-            if (pos < 0) return;
+            pos = (TREE ? tree->pos[u] : first + u) - (a.m_first + w) * s.period;
+            if (pos < 0 || (TREE && pos >= tree->ctx)) return;
             tag = -1 - u;
         }
         const int pg = page_of(c, a.batch.table, b, pos);
@@ -367,10 +394,14 @@ paged_rows_kernel(const __grid_constant__ Args a) {
             float pr[4];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int i = first + tok[nh][e];
+                const int i = TREE ? tree->pos[tok[nh][e]] : first + tok[nh][e];
                 const int lo_i = TOKENS ? band_lo(i, s.mode, s.k_local) : lo;
                 auto logit = [&](int tg, float x) -> float {
                     if (tg >= 0) return tg >= lo_i && tg <= i ? fmaf(x, s.scale_log2, offb[nh][e]) : -INFINITY;
+                    if (TREE && tg < -kTreeGroup && tg >= kNodeTag) {
+                        const int by = (tg - kNodeTag) >> tok[nh][e];
+                        return by & 1 ? fmaf(x, s.scale_log2, offb[nh][e]) : by >> kTreeGroup & 1 ? fmaf(x, s.scale_log2, offs[nh][e]) : -INFINITY;
+                    }
                     return tg == -1 - tok[nh][e] ? fmaf(x, s.scale_log2, offs[nh][e]) : -INFINITY;
                 };
                 const float z0 = logit(tag0, sc[nh][e]), z1 = logit(tag1, sc[nh][2 + e]);
@@ -476,7 +507,8 @@ paged_rows_kernel(const __grid_constant__ Args a) {
                 unsigned bad = __ballot_sync(kFull, in && went_bad(seen) && lt == lt);
                 while (bad) {
                     const int y = __shfl_sync(kFull, x, __ffs(bad) - 1);
-                    again<D, KV>(a, b, first + y / G, kvh, (int)row_of(y));
+                    if constexpr (TREE) again<D, KV, true>(a, b, tree->pos[y / G], kvh, (int)row_of(y), tree->ctx, tok0 - tree->node0);
+                    else again<D, KV, false>(a, b, first + y / G, kvh, (int)row_of(y), 0, 0);
                     bad &= ~__ballot_sync(kFull, x == y);
                     mine = mine && x != y;
                 }
@@ -520,11 +552,11 @@ static Split split(int sm_w, int max_w, long long tiles, long long pairs) {
     return best;
 }
 
-template <int D, int KV, int NH, bool TOKENS>
+template <int D, int KV, int NH, Kind KIND>
 static cudaError_t launch(const Args &a, int groups, long long keys, cudaStream_t st) {
     const int cols = a.group * (a.s.H / a.s.Hkv);
     const Split sp = split(sm_warps(D, KV, NH), max_warps(D, KV, NH), (keys + KEYS - 1) / KEYS, (long long)groups * a.s.Hkv);
-    auto *kernel = paged_rows_kernel<D, KV, NH, TOKENS>;
+    auto *kernel = paged_rows_kernel<D, KV, NH, KIND>;
     static PerDeviceOnce configured;  // shared memory above the 48 KB default
     int dev = 0;
     cudaGetDevice(&dev);
@@ -551,18 +583,18 @@ static cudaError_t launch(const Args &a, int groups, long long keys, cudaStream_
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-template <int D, int KV, bool TOKENS>
+template <int D, int KV, Kind KIND>
 static cudaError_t launch_shape(const Args &a, int groups, long long keys, cudaStream_t st) {
-    return a.group * (a.s.H / a.s.Hkv) <= 8 ? launch<D, KV, 1, TOKENS>(a, groups, keys, st) : launch<D, KV, 2, TOKENS>(a, groups, keys, st);
+    return a.group * (a.s.H / a.s.Hkv) <= 8 ? launch<D, KV, 1, KIND>(a, groups, keys, st) : launch<D, KV, 2, KIND>(a, groups, keys, st);
 }
 
-template <bool TOKENS>
+template <Kind KIND>
 static cudaError_t launch_types(const Args &a, int groups, long long keys, cudaStream_t st) {
     const bool d64 = a.s.d == 64;
     switch (a.cache.kv_type) {
-        case kKvBf16: return d64 ? launch_shape<64, kKvBf16, TOKENS>(a, groups, keys, st) : launch_shape<128, kKvBf16, TOKENS>(a, groups, keys, st);
-        case kKvE4m3: return d64 ? launch_shape<64, kKvE4m3, TOKENS>(a, groups, keys, st) : launch_shape<128, kKvE4m3, TOKENS>(a, groups, keys, st);
-        default: return d64 ? launch_shape<64, kKvInt8, TOKENS>(a, groups, keys, st) : launch_shape<128, kKvInt8, TOKENS>(a, groups, keys, st);
+        case kKvBf16: return d64 ? launch_shape<64, kKvBf16, KIND>(a, groups, keys, st) : launch_shape<128, kKvBf16, KIND>(a, groups, keys, st);
+        case kKvE4m3: return d64 ? launch_shape<64, kKvE4m3, KIND>(a, groups, keys, st) : launch_shape<128, kKvE4m3, KIND>(a, groups, keys, st);
+        default: return d64 ? launch_shape<64, kKvInt8, KIND>(a, groups, keys, st) : launch_shape<128, kKvInt8, KIND>(a, groups, keys, st);
     }
 }
 
@@ -584,8 +616,8 @@ cudaError_t launch_decode_paged(const DecodePagedArgs &d, cudaStream_t st) {
     using namespace decp;
     const Shape &s = d.s;
     Args a{d.q, d.q_stride, d.alpha, d.lens, PagedBatch{d.table, nullptr, nullptr, s.B, s.B}, d.out, d.lse, s, d.cache, d.index_word,
-           s.mode != kModeEcp && s.S > 0 ? first_skip_multiple(s) : 1, 1};
-    return launch_types<false>(a, s.B, MostKeys(s, d.cache).list(1), st);
+           s.mode != kModeEcp && s.S > 0 ? first_skip_multiple(s) : 1, 1, nullptr, 0};
+    return launch_types<kSingle>(a, s.B, MostKeys(s, d.cache).list(1), st);
 }
 
 // Tokens per CTA: as many as 8 columns hold (16 took a batch of five drafted tokens, 4 heads per KV head, 15.0 us, 8 10.4).
@@ -627,8 +659,27 @@ cudaError_t launch_extend_few(const ExtendArgs &e, cudaStream_t st) {
     const Shape &s = e.s;
     const int group = token_group(s.H / s.Hkv);
     Args a{e.q, e.q_stride, e.alpha, nullptr, e.batch, e.out, e.lse, s, e.cache, e.index_word,
-           s.mode != kModeEcp && s.S > 0 ? first_skip_multiple(s) : 1, group};
-    return launch_types<true>(a, (int)((e.batch.T + e.batch.B * (long long)(group - 1)) / group), MostKeys(s, e.cache).list(group), st);
+           s.mode != kModeEcp && s.S > 0 ? first_skip_multiple(s) : 1, group, nullptr, 0};
+    return launch_types<kTokens>(a, (int)((e.batch.T + e.batch.B * (long long)(group - 1)) / group), MostKeys(s, e.cache).list(group), st);
+}
+
+cudaError_t launch_extend_tree(const ExtendTreeArgs &t, cudaStream_t st) {
+    using namespace decp;
+    const ExtendArgs &e = t.e;
+    const Shape &s = e.s;
+    const int group = token_group(s.H / s.Hkv);
+    const MostKeys most(s, e.cache);
+    const long long keys = std::min(most.cap, most.band) + std::min<long long>(e.batch.T, kTreeMax) + most.windows * group;
+    Args a{e.q, e.q_stride, e.alpha, nullptr, e.batch, e.out, e.lse, s, e.cache, e.index_word,
+           s.mode != kModeEcp && s.S > 0 ? first_skip_multiple(s) : 1, group, t.parent, 0};
+    const long long groups = (e.batch.T + e.batch.B * (long long)(group - 1)) / group;
+    constexpr int MOST = 65535;  // of a grid's third dimension
+    for (long long g0 = 0; g0 < groups; g0 += MOST) {
+        a.group0 = (int)g0;
+        const cudaError_t err = launch_types<kTree>(a, (int)std::min<long long>(MOST, groups - g0), keys, st);
+        if (err != cudaSuccess) return err;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace pi

@@ -9,6 +9,7 @@
 
 #include "pi_mma.cuh"
 #include "pi_paged.cuh"
+#include "pi_quant.cuh"
 
 namespace pi {
 
@@ -18,6 +19,9 @@ struct RowKeys {
     const int *table;        // its sequence's pages
     int kvh, lo, i, m_first, n_skip, period;
     float scale_log2, off_band, off_skip;
+    // a drafted tree's node: its sequence's parents, the positions from which on a key is an ancestor, and its own number
+    const int *parent;
+    int ctx, node;
 };
 
 __device__ __forceinline__ RowKeys row_keys(const Shape &s, int i, int kvh, int m_first, const __nv_bfloat16 *q, const int *table,
@@ -25,20 +29,11 @@ __device__ __forceinline__ RowKeys row_keys(const Shape &s, int i, int kvh, int 
     const int n_skip = s.mode != kModeEcp && s.S > 0 ? max(0, min(s.S, i / s.period) - m_first + 1) : 0;
     const float al = alpha ? *alpha : 1.f;
     return RowKeys{q, table, kvh, band_lo(i, s.mode, s.k_local), i, m_first, n_skip, s.period, s.scale_log2, alpha ? log2f(al) : 0.f,
-                   log2f(1.f - al)};
-}
-
-__device__ __forceinline__ void unpack8(const uint4 &x, float (&f)[8]) {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        f[2 * j] = __uint_as_float(w[j] << 16);
-        f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-    }
+                   log2f(1.f - al), nullptr, 0, 0};
 }
 
 // The row, to out[d].  For the whole warp.
-template <int D, int KV>
+template <int D, int KV, bool TREE = false>
 __device__ __forceinline__ void attend_row(const PagedCache &c, const RowKeys &k, __nv_bfloat16 *out) {
     constexpr int NC = D / 64;
     const int lane = threadIdx.x & 31, col = 8 * (lane & 7);
@@ -49,7 +44,12 @@ __device__ __forceinline__ void attend_row(const PagedCache &c, const RowKeys &k
         int row = -1;
         float z = -INFINITY;
         if (kk < n) {
-            const int pos = kk < n_band ? k.lo + kk : k.i - (k.m_first + kk - n_band) * k.period;
+            int pos = kk < n_band ? k.lo + kk : k.i - (k.m_first + kk - n_band) * k.period;
+            if (TREE && pos >= k.ctx) {
+                int at = k.node;
+                for (int up = k.i - pos; up > 0; --up) at = ld_now(k.parent + at);
+                pos = k.ctx + at;
+            }
             const int pg = page_of(c, k.table, 0, pos);
             if (pg >= 0) row = row_in_page(c, pg, k.kvh, pos);
         }

@@ -44,6 +44,7 @@ class _Handle(ctypes.Structure):  # Handle of csrc/pi_paged_py.cpp
     _fields_ = [("cache", _CacheStruct), ("device", ctypes.c_int)]
 
 
+_STEP = ("rotary", "rotary_append", "extend_tree", "verify_tree", "cache_keep")  # what step.py binds
 _native = None  # the extension module, once loaded and bound to the library
 
 
@@ -59,7 +60,12 @@ def _load():
         lib.pi_attn_extend_workspace_size.argtypes = [C, I, I, I, I, I, I, I, I]
         lib.pi_attn_extend_workspace_size.restype = Z
         lib.pi_attn_extend.argtypes = [P, L, C, B, P, I, I, I, I, I, P, P, P, Z, P]
-        for name in ("cache_append", "cache_read", "decode_paged", "extend"):
+        lib.pi_attn_rotary.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, I, I, P, P, P, P, P]
+        lib.pi_attn_rotary_append.argtypes = [P, L, P, L, P, L, P, C, B, P, I, P, L, P]
+        lib.pi_attn_extend_tree.argtypes = [P, L, C, B, P, P, I, I, I, I, I, P, P, P]
+        lib.pi_attn_verify_tree.argtypes = [P, L, P, L, P, P, P, P, P, I, I, I, P, P, P, P]
+        lib.pi_attn_cache_keep.argtypes = [C, I, B, P, P, P]
+        for name in ("cache_append", "cache_read", "decode_paged", "extend") + _STEP:
             getattr(lib, "pi_attn_" + name).restype = I
     return lib
 
@@ -75,6 +81,7 @@ def _load_native():
         spec.loader.exec_module(module)
         module.bind(*(ctypes.cast(getattr(lib, "pi_attn_" + n), ctypes.c_void_p).value
                       for n in ("cache_append", "cache_read", "extend_workspace_size", "extend", "decode_paged")))
+        module.bind_step(*(ctypes.cast(getattr(lib, "pi_attn_" + n), ctypes.c_void_p).value for n in _STEP))
         _native = module
     return _native
 
@@ -108,6 +115,7 @@ class PagedCache:
         self._struct = _Handle(_CacheStruct(*(None if t is None else t.data_ptr() for t in self._tensors), self.kv_type, n_pages,
                                             Hkv, page, d), self.index)
         self._handle = ctypes.addressof(self._struct)
+        self._layers = None  # this cache alone, as step.CacheLayers
 
     k = property(lambda self: self._tensors[0])
     v = property(lambda self: self._tensors[1])
