@@ -464,8 +464,8 @@ int pi_attn_rotary_append(const void *q, long long q_stride, const void *k, long
  * pi_attn_extend_tree -- pi_attn_extend for a tree of drafted tokens per sequence, whose rows the cache holds.
  *   The node at position i attends U(i): a position below ctx[b] is the sequence's cached row of that number, one
  *   from ctx[b] on is the node's ancestor (or itself) at that depth.  Arguments, layouts and errors as pi_attn_extend,
- *   with parent [T] (not NULL); a sequence that is left out keeps its rows of out and lse.  H / Hkv <= 16; T * H < 2^31
- *   (else PI_ERR_UNSUPPORTED).  A node's results depend on the rows that it attends alone.  Weights are rounded as in
+ *   with parent [T] (not NULL); a sequence that is left out keeps its rows of out and lse.  T * H < 2^31, and
+ *   fewer than 2^31 blocks of 128 rows (else PI_ERR_UNSUPPORTED).  No workspace.  A node's results depend on the rows that it attends alone.  Weights are rounded as in
  *   pi_attn_extend.  Deterministic.
  */
 int pi_attn_extend_tree(const void *q, long long q_stride, const pi_attn_cache_t *cache, const pi_attn_batch_t *batch,

@@ -27,7 +27,7 @@ NATIVE_PATH = os.path.join(LIB_DIR, "_pi_paged" + (sysconfig.get_config_var("EXT
 
 SOURCES = ["api.cu", "pi_simt.cu", "pi_fwd_tc.cu", "pi_bwd_tc.cu", "pi_decode.cu",
            "api_paged.cu", "pi_cache.cu", "pi_extend_tc.cu", "pi_decode_paged.cu",
-           "api_step.cu", "pi_rotary.cu", "pi_verify.cu", "pi_keep.cu"]
+           "api_step.cu", "pi_rotary.cu", "pi_verify.cu", "pi_keep.cu", "pi_tree_tc.cu"]
 HEADERS = ["pi_common.cuh", "pi_launch.h", "pi_tc_ptx.cuh", "pi_paged.h", "pi_plan.cuh", "pi_paged.cuh", "pi_mma.cuh", "pi_tile.cuh",
            "pi_row.cuh", "pi_quant.cuh", "pi_tree.cuh", "pi_step.h", "api_checks.h"]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]

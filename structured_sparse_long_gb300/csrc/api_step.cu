@@ -107,7 +107,7 @@ int pi_attn_extend_tree(const void *q, long long q_stride, const pi_attn_cache_t
     if (rc == PI_OK) rc = make_attention(a.cache, H, k_local, period, S, mode, alpha, a.s);
     if (rc == PI_OK) rc = check_stride(q_stride, H, cache->d);
     if (rc != PI_OK) return rc;
-    if (H / cache->Hkv > 16 || (long long)batch->T * H > 0x7fffffffLL) return PI_ERR_UNSUPPORTED;
+    if ((long long)batch->T * H > 0x7fffffffLL) return PI_ERR_UNSUPPORTED;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(alpha, 4) || !aligned(parent, 4)) return PI_ERR_ALIGN;
     a.q = static_cast<const __nv_bfloat16 *>(q);
     a.q_stride = q_stride;
@@ -115,7 +115,11 @@ int pi_attn_extend_tree(const void *q, long long q_stride, const pi_attn_cache_t
     a.out = static_cast<__nv_bfloat16 *>(out);
     a.lse = lse;
     t.parent = parent;
-    if (!(a.index_word = pi::index_word())) return PI_ERR_CUDA;
+    bool fits;
+    pi::tree_few(t, fits);
+    if (!fits) return PI_ERR_UNSUPPORTED;
+    a.timeout_ns = kWaitTimeoutNs;
+    if (!(a.status = pi::status_word()) || !(a.index_word = pi::index_word())) return PI_ERR_CUDA;
     return map_cuda(pi::launch_extend_tree(t, static_cast<cudaStream_t>(stream)));
 }
 

@@ -663,13 +663,46 @@ cudaError_t launch_extend_few(const ExtendArgs &e, cudaStream_t st) {
     return launch_types<kTokens>(a, (int)((e.batch.T + e.batch.B * (long long)(group - 1)) / group), MostKeys(s, e.cache).list(group), st);
 }
 
+// Whether this kernel beats the tensor-core one for a batch of trees (pi_tree_tc.cu), and whether either can number its work.  As in
+// extend_few_rows, by two estimates in us from the sizes that the host knows, all trees taken as equally large: this kernel's
+// rounds of tiles, and the other's turns of blocks, each a start and tiles of 32 keys.  Fitted to 112 shapes (16 heads on 4, 8 on 1 and 16 on
+// 16, d = 128, and 12 on 12, d = 64; bf16 and e4m3; 1 to 64 trees of 2 to 160 nodes), of which it gets 98 right to 5 % and the others wrong by
+// 6 to 34 %.  For instance (this kernel / the other):
+//   16 heads on 4, d = 128, band 256, bf16:  1 tree of 26 nodes 10.3 / 11.9, of 160 15.1 / 14.6; 8 of 32 17.0 / 12.1, 32 of 32 64.3 / 12.7
+//                                     e4m3:  1 of 26 10.5 / 15.7; 8 of 8 11.8 / 14.5, 8 of 32 20.2 / 15.8
+//   12 on 12, d = 64, band 128, bf16:  1 of 26 7.7 / 9.2; 16 of 16 10.5 / 11.6, 32 of 32 28.3 / 18.7
+bool tree_few(const ExtendTreeArgs &t, bool &fits) {
+    const ExtendArgs &e = t.e;
+    const Shape &s = e.s;
+    const PagedCache &c = e.cache;
+    const int G = s.H / s.Hkv, group = token_group(G);
+    const long long T = e.batch.T, B = std::min<long long>(e.batch.B, T), n = std::min<long long>((T + B - 1) / B, kTreeMax);
+    const decp::MostKeys most(s, c);
+    const int heads = tree_heads(G), rows = 128 / heads;
+    const long long blocks = (T + e.batch.B * (long long)(rows - 1)) / rows * (s.H / heads);
+    const bool tc_fits = blocks <= 0x7fffffffLL && most.band + kTreeMax + most.windows * kTreeMax < (1LL << 30);
+    const bool few_fits = G <= 16 && s.Hkv <= 65535 && most.band + kTreeMax + most.windows * group < (1LL << 30) &&
+                          (T + e.batch.B * (long long)(group - 1)) / group <= 0x7fffffffLL;
+    fits = tc_fits || few_fits;
+    if (!tc_fits || !few_fits) return few_fits;
+    const bool quant = c.kv_type != kKvBf16;
+    const long long sms = sm_count(), tiles = (most.list(group) + std::min<long long>(n, 8 * group) + decp::KEYS - 1) / decp::KEYS;
+    const long long ctas = B * ((n + group - 1) / group) * s.Hkv;
+    const double rounds = (double)ctas * (double)(tiles + 6) / (double)(sms * decp::sm_warps(s.d, c.kv_type, group * G > 8 ? 2 : 1));
+    const long long turns = (B * ((n + rows - 1) / rows) * (s.H / heads) - 1) / (2 * sms) + 1;
+    const double block_tiles = (double)(most.band + n + 6 * most.windows) / 32 + 0.5;
+    return 8.4 + (quant ? 1.8 : 1.7) * rounds <= 1.5 + (double)turns * (6.1 + (quant ? 0.8 : 0.37) * block_tiles);
+}
+
 cudaError_t launch_extend_tree(const ExtendTreeArgs &t, cudaStream_t st) {
     using namespace decp;
+    bool fits;
+    if (!tree_few(t, fits)) return launch_tree_tc(t, st);
     const ExtendArgs &e = t.e;
     const Shape &s = e.s;
     const int group = token_group(s.H / s.Hkv);
     const MostKeys most(s, e.cache);
-    const long long keys = std::min(most.cap, most.band) + std::min<long long>(e.batch.T, kTreeMax) + most.windows * group;
+    const long long keys = most.band + std::min<long long>(e.batch.T, kTreeMax) + most.windows * group;
     Args a{e.q, e.q_stride, e.alpha, nullptr, e.batch, e.out, e.lse, s, e.cache, e.index_word,
            s.mode != kModeEcp && s.S > 0 ? first_skip_multiple(s) : 1, group, t.parent, 0};
     const long long groups = (e.batch.T + e.batch.B * (long long)(group - 1)) / group;

@@ -77,6 +77,16 @@ inline bool keep_fits(const PagedCache &c, long long B) { return B * ((keep_piec
 
 cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t st);               // pi_verify.cu
 cudaError_t launch_keep(const KeepArgs &a, cudaStream_t st);                   // pi_keep.cu
+// Query heads of a KV group in a block of 128 rows of the trees' tensor-core kernel: as many as divide the group, so that a block has
+// few nodes.
+inline int tree_heads(int G) {
+    int heads = 1;
+    while (heads < 16 && G % (2 * heads) == 0) heads *= 2;
+    return heads;
+}
+
+bool tree_few(const ExtendTreeArgs &a, bool &fits);  // pi_decode_paged.cu
+cudaError_t launch_tree_tc(const ExtendTreeArgs &a, cudaStream_t st);          // pi_tree_tc.cu
 cudaError_t launch_extend_tree(const ExtendTreeArgs &a, cudaStream_t st);      // pi_decode_paged.cu
 cudaError_t launch_rotary(const RotaryArgs &a, cudaStream_t st);               // pi_rotary.cu
 cudaError_t launch_rotary_append(const RotaryAppendArgs &a, cudaStream_t st);  // pi_rotary.cu

@@ -242,12 +242,19 @@ TREES = [
     ("bf16", 64, 1, 1, 16, [5] * 70, [3] * 70, 4, 2, 3, False, 3, 1),       # many sequences
     ("bf16", 128, 16, 4, 64, [500, 3], [1, 1], 64, 128, 3, False, 1, 1),    # single nodes
     ("bf16", 128, 16, 4, 64, [900, 700, 801, 64], [64, 50, 33, 64], 128, 256, 3, False, 8, 1),
+    ("int8", 64, 20, 1, 16, [100, 7], [30, 5], 40, 30, 2, False, 6, 1),     # 20 heads on one
+    ("e4m3", 128, 24, 1, 32, [61], [12], 33, 9, 3, False, 12, 1),
 ]
 
 
+MANY = 200  # further trees of 40 nodes: enough for the tensor-core kernel, whatever the other sizes
+
+
+@pytest.mark.parametrize("more", [0, MANY])
 @pytest.mark.parametrize("case", TREES, ids=lambda c: f"{c[0]}-d{c[1]}-h{c[2]}on{c[3]}-p{c[4]}-T{sum(c[6])}{'-ecp' if c[10] else ''}")
-def test_extend_tree(case):
+def test_extend_tree(case, more):
     kv, d, H, Hkv, page, ctx, n, kl, per, S, ecp, deep, roots = case
+    checked, ctx, n = len(n), ctx + [0] * more, n + [40] * more
     cache, table, cu, parents, q, alpha, held = tree_case(kv, d, H, Hkv, page, ctx, n, seed=d + sum(n), deep=deep, roots=roots, extra=2, ecp=ecp)
     T, m = q.shape[0], sum(n)
     out = torch.full((T, H, d), 5.0, device="cuda", dtype=torch.bfloat16)
@@ -256,7 +263,7 @@ def test_extend_tree(case):
     got = pa.extend_tree(q, cache, *args, out=out, lse=lse)
     torch.cuda.synchronize()
     assert got[0] is out and (out[m:] == 5).all() and (lse[m:] == 5).all()
-    for b in range(len(n)):
+    for b in range(checked):
         if not n[b]:
             continue
         rows = slice(cu[b], cu[b + 1])
@@ -280,27 +287,51 @@ def test_a_chain_is_what_extend_attends(kv):
 
 
 @pytest.mark.parametrize("kv", ["bf16", "int8"])
+@pytest.mark.parametrize("more", [0, MANY])
 @pytest.mark.parametrize("n", [12, 100])
-def test_rows_that_a_node_does_not_attend_do_not_matter(kv, n):
+def test_rows_that_a_node_does_not_attend_do_not_matter(kv, n, more):
     """NaN in the rows of some nodes reaches their descendants only; alpha = 0 on a node without skips gives 0 and -inf."""
     H, Hkv, d, ctx = 4, 2, 64, 30
-    cache, table, cu, parents, q, alpha, held = tree_case(kv, d, H, Hkv, 16, [ctx], [n], seed=n)
+    cache, table, cu, parents, q, alpha, held = tree_case(kv, d, H, Hkv, 16, [ctx] + [0] * more, [n] + [40] * more, seed=n)
     alpha[3:n:7] = 0.0
     k, v = (t[ctx:].clone() for t in held[0])
     spoilt = [5, n - 1]
     for j in spoilt:
         v[j] = float("nan")
-    pa.cache_append(k.cuda(), v.cuda(), cache, dev(table), dev(cu), dev([ctx]))
-    out, lse = pa.extend_tree(q, cache, dev(table), dev(cu), dev([ctx]), dev(parents[0]), alpha.cuda(), 300, 400, 2)
+    pa.cache_append(k.cuda(), v.cuda(), cache, dev(table[:1]), dev([0, n]), dev([ctx]))
+    out, lse = pa.extend_tree(q, cache, dev(table), dev(cu), dev([ctx] + [0] * more), dev(sum(parents, [])), alpha.cuda(), 300, 400, 2)
     torch.cuda.synchronize()
+    out, lse, alpha = out[:n], lse[:n], alpha[:n]
     clean = np.array([not set(sref.line(parents[0], j)) & set(spoilt) for j in range(n)])
     assert clean.sum() not in (0, n)
     kh, vh = (torch.cat([h[:ctx], t]) for h, t in zip(held[0], (held[0][0][ctx:], torch.nan_to_num(v, nan=0.0))))
-    want = sref.tree_attention(q.cpu(), kh, vh, alpha, ctx, parents[0], 300, 400, 2, PI)
+    want = sref.tree_attention(q[:n].cpu(), kh, vh, alpha, ctx, parents[0], 300, 400, 2, PI)
     dark = (alpha == 0).any(1).numpy()
     ref.check_attention("clean", out[clean], lse[clean], [w[clean] for w in want])
     assert torch.isnan(out[torch.from_numpy(~clean & ~dark)].float()).all()
     assert (out[torch.from_numpy(dark)] == 0).all() and torch.isneginf(lse[torch.from_numpy(dark)]).all()
+
+
+@pytest.mark.parametrize("more", [0, MANY])
+def test_pages_that_no_node_attends_may_be_gone(more):
+    """Entries below every band, between the skips' keys and before the deepest nodes' bands name no page: nothing is recorded."""
+    ctx, n, kl, per, S, page = 400, 70, 40, 100, 3, 16
+    cache, table, cu, parents, q, alpha, held = tree_case("bf16", 64, 8, 2, page, [ctx] + [0] * more, [n] + [40] * more, seed=2)
+    keep = set()
+    for j, deep in enumerate(sref.depths(parents[0])):
+        i = ctx + deep
+        keep |= {p // page for p in list(range(max(0, i - kl), ctx)) + [i - m * per for m in range(1, S + 1) if i >= m * per]}
+    gone = table.copy()
+    for p in range(ctx // page):
+        if p not in keep:
+            gone[0, p] = -1
+    assert (gone[0] != table[0]).sum() >= 10
+    args = (dev(cu), dev([ctx] + [0] * more), dev(sum(parents, [])), alpha.cuda(), kl, per, S)
+    want = pa.extend_tree(q, cache, dev(table), *args)
+    got = pa.extend_tree(q, cache, dev(gone), *args)
+    assert pa.status() == 0
+    assert torch.equal(got[0][:n], want[0][:n]) and torch.equal(got[1][:n], want[1][:n])
+    ref.check_attention("tree", got[0][:n], got[1][:n], sref.tree_attention(q[:n].cpu(), *held[0], alpha[:n], ctx, parents[0], kl, per, S, PI))
 
 
 # ------------------------------------------------------------------ verification

@@ -106,7 +106,7 @@ def test_tree_is_checked(lib):
         assert tree(lib, **kw) == PI_ERR_NULL
     for kw in (dict(H=3), dict(kl=-1), dict(S=-1), dict(per=0), dict(mode=1, kl=0, S=0), dict(mode=1, S=1), dict(qs=260)):
         assert tree(lib, **kw) == PI_ERR_SHAPE
-    for kw in (dict(mode=2), dict(H=34, qs=34 * 64), dict(b=batch(T=1 << 29))):
+    for kw in (dict(mode=2), dict(b=batch(T=1 << 29)), dict(H=34, qs=34 * 64, b=batch(B=1 << 30))):
         assert tree(lib, **kw) == PI_ERR_UNSUPPORTED
     for kw in (dict(out=A16 + 8), dict(lse=A16 + 2), dict(alpha=A16 + 1), dict(parent=A16 + 3), dict(q=A16 + 4)):
         assert tree(lib, **kw) == PI_ERR_ALIGN
