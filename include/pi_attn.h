@@ -483,8 +483,8 @@ int pi_attn_extend_tree(const void *q, long long q_stride, const pi_attn_cache_t
  *   is the next node; where there is none the walk ends, and the next token is the lowest v at which the running sum of
  *   w exceeds u_next[b] times the whole sum (w = p where no w is left).  So the accepted tokens and the next one are
  *   distributed as the target's own.  Children of other roots than node 0 are not tested.
- *   target, draft [T, V] fp32 with rows target_stride, draft_stride elements apart (>= V, below 2^38); elements that are negative or
- *   not finite count as 0.  tokens [T] int32 in [0, V) (node 0's is not read); u [T], u_next [B] fp32 in [0, 1) (what is outside counts
+ *   target, draft [T, V] fp32 with rows target_stride, draft_stride elements apart (>= V, below 2^38); elements outside [0, 1]
+ *   count as the nearest number in it, NaN as 0.  tokens [T] int32 in [0, V) (node 0's is not read); u [T], u_next [B] fp32 in [0, 1) (what is outside counts
  *   as the nearest in it, NaN as 0).  cu [B + 1], parent [T] as above.
  *   Writes path [T] int32: the accepted nodes of sequence b from path[cu[b]] on, the rest of its places -1; count [B]: how
  *   many; next [B]: the next token, or -1 where no p is above 0.  A sequence without tokens, or one that is left out, gets

@@ -151,4 +151,9 @@ __device__ __forceinline__ float4 ld_peer4(uint32_t addr) {
     return f;
 }
 
+// Two numbers into another CTA's shared memory (seen there past the next cluster_sync()).
+__device__ __forceinline__ void st_peer2(uint32_t addr, float2 f) {
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(f.x), "f"(f.y) : "memory");
+}
+
 }  // namespace pi

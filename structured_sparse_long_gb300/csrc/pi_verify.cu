@@ -10,8 +10,9 @@
 // their running sum says which warp's part holds the next token; that part is summed again, finer.
 //
 // A running sum is compared with a random number: an error in it would pick a neighbour's token as often as it is large.  fp32 sums over
-// 10^5 tokens would do that once in a hundred calls.  Products and sums are carried in pairs of fp32 (48 bits): a GB300 has few fp64 units, and
-// fewer than ten fp64 operations per child remain, in one warp.
+// 10^5 tokens would do that once in a hundred calls.  Products and sums are carried in pairs of fp32 (48 bits), two tokens to an
+// instruction: a GB300 has few fp64 units (the walk and the last search alone, some ten dependent fp64 operations each in one warp, took
+// 3 and 5 us).
 #include "pi_mma.cuh"
 #include "pi_paged.cuh"
 #include "pi_step.h"
@@ -27,6 +28,8 @@ constexpr unsigned kFull = 0xffffffffu;
 struct Pair {
     float hi, lo;
 };
+// (What runs once per call is fetched from L2, a few hundred cycles for every 128 bytes of it, so that loops here are rolled up:
+// unrolled, one warp's search of 128 sums took 4 us.)
 // x + y exactly, hi being their rounded sum.
 __device__ __forceinline__ Pair two_sum(float x, float y) {
     const float s = __fadd_rn(x, y), t = __fsub_rn(s, x);
@@ -37,20 +40,38 @@ __device__ __forceinline__ Pair add(const Pair &x, const Pair &y) {
     const float lo = __fadd_rn(s.lo, __fadd_rn(x.lo, y.lo)), hi = __fadd_rn(s.hi, lo);
     return Pair{hi, __fadd_rn(lo, -__fsub_rn(hi, s.hi))};
 }
-__device__ __forceinline__ double value(const Pair &x) { return (double)x.hi + (double)x.lo; }
-__device__ __forceinline__ Pair pair_of(double x) {
-    const float hi = (float)x;
-    return Pair{hi, (float)(x - (double)hi)};
+__device__ __forceinline__ Pair sub(const Pair &x, const Pair &y) { return add(x, Pair{-y.hi, -y.lo}); }
+__device__ __forceinline__ Pair mul(const Pair &x, const Pair &y) {
+    const float h = __fmul_rn(x.hi, y.hi), l = fmaf(x.hi, y.lo, fmaf(x.lo, y.hi, fmaf(x.hi, y.hi, -h))), hi = __fadd_rn(h, l);
+    return Pair{hi, __fadd_rn(l, -__fsub_rn(hi, h))};
 }
+// (both as add() and mul() leave them)
+__device__ __forceinline__ bool less(const Pair &x, const Pair &y) { return x.hi < y.hi || (x.hi == y.hi && x.lo < y.lo); }
+__device__ __forceinline__ bool positive(const Pair &x) { return x.hi > 0.f; }
 __device__ __forceinline__ Pair warp_sum(Pair x) {
-#pragma unroll
+#pragma unroll 1
     for (int w = 16; w > 0; w >>= 1) x = add(x, Pair{__shfl_xor_sync(kFull, x.hi, w), __shfl_xor_sync(kFull, x.lo, w)});
     return x;
 }
 
-// A probability as it counts: negative or not finite, 0.
-__device__ __forceinline__ float sane(float p) { return p > 0.f && p < INFINITY ? p : 0.f; }
+// A probability as it counts: the nearest number in [0, 1], NaN 0.
+__device__ __forceinline__ float sane(float p) { return __saturatef(p); }
 __device__ __forceinline__ float unit(float u) { return fminf(fmaxf(u, 0.f), 0x1.fffffep-1f); }
+
+// Two numbers at a time, in packed fp32.
+struct Two {
+    uint64_t v;
+    __device__ __forceinline__ Two(uint64_t x) : v(x) {}
+    __device__ __forceinline__ Two(float x, float y) : v(tc::pack2(x, y)) {}
+};
+__device__ __forceinline__ Two operator+(const Two &x, const Two &y) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x.v), "l"(y.v));
+    return Two(r);
+}
+__device__ __forceinline__ Two fma(const Two &x, const Two &y, const Two &z) { return Two(tc::fma2(x.v, y.v, z.v)); }
+__device__ __forceinline__ Two operator*(const Two &x, const Two &y) { return Two(tc::mul2(x.v, y.v)); }
+__device__ __forceinline__ Two operator-(const Two &x, const Two &y) { return fma(y, Two(-1.f, -1.f), x); }  // (the product is exact)
 
 // The node whose rows a pass reads, and its weights.
 struct Weights {
@@ -63,85 +84,136 @@ struct Shared {
     int parent[kTreeMax], token[kTreeMax];
     float u[kTreeMax], p[kTreeMax], q[kTreeMax];  // of each node: its random number, its probabilities at its parent
     int path[kTreeMax], removed[kTreeMax];
-    Pair mine[2][WARPS];        // the warps' sums of this pass and the one before
-    Pair all[MAX_P * WARPS];    // the cluster's
-    Weights w;
-    int pass, len;              // whether there is another pass; the path's length
-    int at;                     // the part that holds the next token, the running sum that it passes, and the one in front of it
-    double goal, before;
+    Pair all[2][MAX_P * WARPS];  // the sums of the cluster's warps, of this pass and the one before
 };
 
+__device__ __forceinline__ bool is_removed(const Weights &w, const Shared &sh, int v) {
+    bool gone = false;
+    for (int r = 0; r < w.removed; ++r) gone = gone || sh.removed[r] == v;
+    return gone;
+}
 __device__ __forceinline__ Pair weight(const Weights &w, const Shared &sh, int v) {
     const float p = sane(ld_now(w.p + v));
-    Pair d{p, 0.f};
-    if (w.q) {
-        const float q = sane(ld_now(w.q + v)), h = __fmul_rn(w.a.hi, q);
-        d = two_sum(p, -h);
-        d.lo = __fsub_rn(d.lo, fmaf(w.a.lo, q, fmaf(w.a.hi, q, -h)));
-        if (!(__fadd_rn(d.hi, d.lo) > 0.f)) d = Pair{0.f, 0.f};
-    }
-    for (int r = 0; r < w.removed; ++r)
-        if (sh.removed[r] == v) d = Pair{0.f, 0.f};
-    return d;
-}
-// The sum of the weights of tokens lo + lane, lo + lane + 32, ... below hi, over the warp.
-__device__ __forceinline__ Pair sum_of(const Weights &w, const Shared &sh, int lo, int hi) {
-    Pair s{0.f, 0.f};
-#pragma unroll 4
-    for (int v = lo + (int)(threadIdx.x & 31); v < hi; v += 32) s = add(s, weight(w, sh, v));
-    return warp_sum(s);
+    if (is_removed(w, sh, v)) return Pair{0.f, 0.f};
+    if (!w.q) return Pair{p, 0.f};
+    const float q = sane(ld_now(w.q + v)), h = __fmul_rn(w.a.hi, q);
+    Pair d = two_sum(p, -h);
+    d.lo = __fsub_rn(d.lo, fmaf(w.a.lo, q, fmaf(w.a.hi, q, -h)));
+    d = add(d, Pair{0.f, 0.f});
+    return positive(d) ? d : Pair{0.f, 0.f};
 }
 
-// Sum over the lanes up to and including this one.
-__device__ __forceinline__ double upto_lane(double x) {
+// The sum of the weights of tokens lo .. hi - 1, over the warp; AHEAD tokens per lane in flight.
+template <bool DRAFT>
+__device__ __forceinline__ Pair sum_of(const Weights &w, const Shared &sh, int lo, int hi) {
+    constexpr int AHEAD = DRAFT ? 8 : 16;
+    const int lane = threadIdx.x & 31;
+    bool some = false;  // a token without a weight among these
+    for (int r = lane; r < w.removed; r += 32) some = some || (sh.removed[r] >= lo && sh.removed[r] < hi);
+    const int removed = __any_sync(kFull, some) ? w.removed : 0;
+    const float *pp = w.p, *qq = w.q;
+    Two hi2(0.f, 0.f), lo2(0.f, 0.f);
+    const Two na_hi(-w.a.hi, -w.a.hi), na_lo(-w.a.lo, -w.a.lo);
+    float p[AHEAD], q[AHEAD];
+    auto take = [&](int v0) {
+#pragma unroll 1
+        for (int r = 0; r < removed; ++r) {
+            const int v = sh.removed[r] - v0;
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i)
+                if (v == 32 * i) p[i] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; i += 2) {
+            Two x(sane(p[i]), sane(p[i + 1])), rest(0.f, 0.f);
+            if (DRAFT) {
+                // d = p - a q rounded, and what that left: p - d = t + r exactly where d > 0 (then d <= p), and t is a q up to d's rounding
+                const Two y(sane(q[i]), sane(q[i + 1])), d = fma(na_hi, y, x), t = x - d, r = (x - t) - d;
+                rest = fma(na_lo, y, fma(na_hi, y, t) + r);
+                float s0, s1;
+                tc::unpack2(d.v, s0, s1);
+                const Two keep(s0 > 0.f ? 1.f : 0.f, s1 > 0.f ? 1.f : 0.f);
+                x = d * keep;
+                rest = rest * keep;
+            }
+            const Two s = hi2 + x, t = s - hi2;
+            const Two err = (hi2 - (s - t)) + (x - t);
+            hi2 = s;
+            lo2 = lo2 + (DRAFT ? err + rest : err);
+        }
+    };
+    int v0 = lo + lane;
+#pragma unroll 1
+    for (; v0 - lane + 32 * AHEAD <= hi; v0 += 32 * AHEAD) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            p[i] = ld_now(pp + v0 + 32 * i);
+            if (DRAFT) q[i] = ld_now(qq + v0 + 32 * i);
+        }
+        take(v0);
+    }
+    if (v0 - lane < hi) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            const bool in = v0 + 32 * i < hi;
+            p[i] = in ? ld_now(pp + v0 + 32 * i) : 0.f;
+            if (DRAFT) q[i] = in ? ld_now(qq + v0 + 32 * i) : 0.f;
+        }
+        take(v0);
+    }
+    Pair x, y;
+    tc::unpack2(hi2.v, x.hi, y.hi);
+    tc::unpack2(lo2.v, x.lo, y.lo);
+    return warp_sum(add(x, y));
+}
+
+__device__ __forceinline__ Pair from_lane(const Pair &x, int lane) { return Pair{__shfl_sync(kFull, x.hi, lane), __shfl_sync(kFull, x.lo, lane)}; }
+// run + the sum over the lanes up to and including this one.  (A lane without a lane so far below it adds 0: with a branch around the
+// addition, whose two sides meet again at the next shuffle, the five steps took 2.7 us.)
+__device__ __forceinline__ Pair upto_lane(Pair x, const Pair &run) {
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const double y = __shfl_up_sync(kFull, x, d);
-        if ((int)(threadIdx.x & 31) >= d) x += y;
+        const float hi = __shfl_up_sync(kFull, x.hi, d), lo = __shfl_up_sync(kFull, x.lo, d);
+        const bool in = (int)(threadIdx.x & 31) >= d;
+        x = add(x, Pair{in ? hi : 0.f, in ? lo : 0.f});
     }
+    return add(run, x);
+}
+// Of the lanes' numbers m (>= 0), the one in which the running sum passes `goal`, `run` being in front of them: the first lane past it,
+// or (where rounding left the goal past them all) the last one above 0; -1: none is.  run: the sum in front of it.
+__device__ __forceinline__ int find_lane(const Pair &m, const Pair &goal, Pair &run) {
+    const Pair here = upto_lane(m, run);
+    const unsigned past = __ballot_sync(kFull, positive(m) && less(goal, here)), some = __ballot_sync(kFull, positive(m));
+    if (!some) return -1;
+    const int x = past ? __ffs(past) - 1 : 31 - __clz(some);
+    const Pair before = from_lane(here, max(x - 1, 0));
+    if (x > 0) run = before;
     return x;
 }
-// Which of n sums (all >= 0) the running sum passes `goal` in: the last one above 0 that begins at or before it, or -1; `before`:
-// the running sum in front of it, given that in front of them all.  With `scale` goal is u times the whole sum.  For a whole warp.
-__device__ __forceinline__ int find_part(const Pair *sums, int n, double u, bool scale, double &goal, double &before) {
-    const int lane = threadIdx.x & 31;
-    constexpr int PER = MAX_P * WARPS / 32;
-    double m[PER], run[PER], all = 0.0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int k = lane * PER + i;
-        m[i] = k < n ? value(sums[k]) : 0.0;
-        run[i] = all;
-        all += m[i];
-    }
-    const double upto = upto_lane(all), start = before + (upto - all);
-    if (scale) goal = u * __shfl_sync(kFull, upto, 31);
+// The same of n numbers get(0), get(1), ..., `per` consecutive ones to a lane.
+template <typename F>
+__device__ __forceinline__ int find(int n, int per, F get, const Pair &goal, Pair &run) {
+    const int first = (int)(threadIdx.x & 31) * per;
+    Pair m{0.f, 0.f};
+#pragma unroll 1
+    for (int i = first; i < min(first + per, n); ++i) m = add(m, get(i));
+    const int x = find_lane(m, goal, run);
+    if (x < 0 || per == 1) return x;
     int at = -1;
-    double mine = 0.0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-        if (m[i] > 0.0 && start + run[i] <= goal) {
-            at = lane * PER + i;
-            mine = start + run[i];
-        }
-    const unsigned who = __ballot_sync(kFull, at >= 0);
-    if (!who) {  // (rounding: the first one above 0)
-#pragma unroll
-        for (int i = PER - 1; i >= 0; --i)
-            if (m[i] > 0.0) {
-                at = lane * PER + i;
-                mine = start + run[i];
-            }
-        const unsigned any = __ballot_sync(kFull, at >= 0);
-        if (!any) return -1;
-        before = __shfl_sync(kFull, mine, __ffs(any) - 1);
-        return __shfl_sync(kFull, at, __ffs(any) - 1);
+    Pair upto = run;
+#pragma unroll 1
+    for (int i = x * per; i < min(x * per + per, n); ++i) {  // the lane's numbers, by all lanes alike
+        const Pair y = get(i);
+        if (!positive(y)) continue;
+        at = i;
+        run = upto;
+        upto = add(upto, y);
+        if (less(goal, upto)) break;
     }
-    before = __shfl_sync(kFull, mine, 31 - __clz(who));
-    return __shfl_sync(kFull, at, 31 - __clz(who));
+    return at;
 }
 
-__global__ void __launch_bounds__(THREADS) verify_kernel(const __grid_constant__ VerifyArgs a, int P) {
+__global__ void __launch_bounds__(THREADS, 2) verify_kernel(const __grid_constant__ VerifyArgs a, int P) {
     __shared__ Shared sh;
     const int rank = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     asm volatile("griddepcontrol.launch_dependents;");
@@ -171,135 +243,110 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(const __grid_constant__
     auto part_lo = [&](int i) -> int { return (int)min((long long)a.V, (long long)(i / WARPS) * share + (i % WARPS) * part); };
     auto part_hi = [&](int i) -> int { return (int)min((long long)a.V, (long long)part_lo(i) + part); };
 
-    // ---- the walk, by warp 0: at node x, whose children up to `last` were not accepted
-    int x = 0, last = 0, len = 1, removed = 0;
-    double w_a = 0.0, s = 1.0;
+    const Pair u_next{unit(ld_now(a.u_next + b)), 0.f};
+    // node 0's rows, which the first pass most often reads
+    for (int v = part_lo(rank * WARPS) + 32 * tid; v < part_hi(rank * WARPS + WARPS - 1); v += 32 * THREADS) {
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.target + t0 * a.target_stride + v));
+        if (a.draft) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.draft + t0 * a.draft_stride + v));
+    }
+    // ---- the walk, by every warp alike (shuffles in a part of the code that one warp alone runs took seven times as long, and what
+    // it found would have to be handed on): at node x, whose children up to `last` were not accepted
+    int x = 0, last = 0, len = 1, passes = 0;
+    Weights w{};
+    Pair s{1.f, 0.f};
     bool summed = false, spent = false;  // the weights' sum is known; it is 0, and p's own is asked for
-    int passes = 0;
-    if (tid == 0) sh.path[0] = 0;
+    if (lane == 0) sh.path[0] = 0;
     for (;;) {
-        if (warp == 0) {
-            bool more = true;
-            if (passes > 0) {  // the sum of a pass
-                Pair t{0.f, 0.f};
-                for (int i = lane; i < P * WARPS; i += 32) t = add(t, sh.all[i]);
-                s = value(warp_sum(t));
-                summed = true;
+        while (!spent) {
+            int c = kTreeMax;  // the next child
+#pragma unroll 1
+            for (int j0 = (last + 1) & ~31; c == kTreeMax && j0 < n; j0 += 32) {
+                const unsigned who = __ballot_sync(kFull, j0 + lane > last && j0 + lane < n && sh.parent[min(j0 + lane, kTreeMax - 1)] == x);
+                if (who) c = j0 + __ffs(who) - 1;
             }
-            while (!spent) {
-                int c = kTreeMax;  // the next child
-                for (int j0 = (last + 1) & ~31; c == kTreeMax && j0 < n; j0 += 32) {
-                    const unsigned who = __ballot_sync(kFull, j0 + lane > last && j0 + lane < n && sh.parent[min(j0 + lane, kTreeMax - 1)] == x);
-                    if (who) c = j0 + __ffs(who) - 1;
-                }
-                if (c == kTreeMax) break;
-                last = c;
-                double w = (double)sh.p[c];
-                if (a.draft) {
-                    w -= w_a * (double)sh.q[c];
-                } else {
-                    bool gone = false;
-                    for (int r = lane; r < removed; r += 32) gone = gone || sh.removed[r] == sh.token[c];
-                    if (__any_sync(kFull, gone)) w = 0.0;
-                }
-                w = w > 0.0 ? w : 0.0;
-                if ((double)sh.u[c] * (double)sh.q[c] * s < w) {
-                    x = c;
-                    if (lane == 0) sh.path[len] = c;
-                    ++len;
-                    removed = 0;
-                    w_a = 0.0;
-                    s = 1.0;
-                    summed = false;
-                } else if (a.draft) {
-                    w_a += s;
-                    summed = false;
-                    break;  // a pass
-                } else {
-                    if (w > 0.0) {
-                        if (lane == 0) sh.removed[removed] = sh.token[c];
-                        ++removed;
-                        __syncwarp();
-                        s -= w;
-                    }
-                    summed = false;
-                }
+            if (c == kTreeMax) break;
+            last = c;
+            Pair left{sh.p[c], 0.f};
+            if (a.draft) {
+                left = sub(left, mul(w.a, Pair{sh.q[c], 0.f}));
+            } else if (w.removed > 0) {  // the same token, chosen twice
+                bool gone = false;
+                for (int r = x + 1 + lane; r < c; r += 32) gone = gone || (sh.parent[r] == x && sh.token[r] == sh.token[c]);
+                if (__any_sync(kFull, gone)) left = Pair{0.f, 0.f};
             }
-            if (summed) {
-                if (s > 0.0 || spent) {
-                    more = false;
-                } else {  // nothing is left of p: the next token is drawn from p itself
-                    spent = true;
-                    w_a = 0.0;
-                    removed = 0;
-                }
-            }
-            if (lane == 0) {
-                const long long row = t0 + x;
-                sh.w.p = a.target + row * a.target_stride;
-                sh.w.q = a.draft && w_a != 0.0 ? a.draft + row * a.draft_stride : nullptr;
-                sh.w.a = pair_of(w_a);
-                sh.w.removed = removed;
-                sh.pass = more;
-                sh.len = len;
+            summed = false;
+            if (positive(left) && less(mul(mul(Pair{sh.u[c], 0.f}, Pair{sh.q[c], 0.f}), s), left)) {
+                x = c;
+                if (lane == 0) sh.path[len] = c;
+                ++len;
+                w.a = Pair{0.f, 0.f};
+                w.removed = 0;
+                s = Pair{1.f, 0.f};
+            } else if (a.draft) {
+                w.a = add(w.a, s);
+                break;  // a pass
+            } else if (positive(left)) {
+                ++w.removed;
+                s = sub(s, left);
             }
         }
-        __syncthreads();
-        if (!sh.pass) break;
-        const Weights w = sh.w;
-        Pair *mine = sh.mine[passes & 1];  // (a peer may still read the other one)
+        if (summed) {
+            if (positive(s) || spent) break;
+            spent = true;  // nothing is left of p: the next token is drawn from p itself
+            w.a = Pair{0.f, 0.f};
+            w.removed = 0;
+        }
+        const long long row = t0 + x;
+        w.p = a.target + row * a.target_stride;
+        w.q = a.draft && positive(w.a) ? a.draft + row * a.draft_stride : nullptr;
+        if (w.removed > 0) {  // the tokens without a weight: x's children (all of them, without draft probabilities)
+            w.removed = 0;
+#pragma unroll 1
+            for (int j0 = x & ~31; j0 < n; j0 += 32) {
+                const bool in = j0 + lane > x && j0 + lane < n && sh.parent[min(j0 + lane, kTreeMax - 1)] == x;
+                const unsigned who = __ballot_sync(kFull, in);
+                if (in) sh.removed[w.removed + __popc(who & ((1u << lane) - 1u))] = sh.token[j0 + lane];
+                w.removed += __popc(who);
+            }
+            __syncwarp();
+        }
         const int i = rank * WARPS + warp;
-        const Pair t = sum_of(w, sh, part_lo(i), part_hi(i));
-        if (lane == 0) mine[warp] = t;
+        const Pair t = w.q ? sum_of<true>(w, sh, part_lo(i), part_hi(i)) : sum_of<false>(w, sh, part_lo(i), part_hi(i));
+        // to every CTA of the cluster (into the half that none of them still reads)
+        Pair *all = sh.all[passes & 1];
+        if (lane < P) st_peer2(peer_addr(smem_addr(&all[i]), lane), make_float2(t.hi, t.lo));
         cluster_sync();
-        if (tid < P * WARPS) {
-            const float2 f = ld_peer2(peer_addr(smem_addr(mine + tid % WARPS), tid / WARPS));
-            sh.all[tid] = Pair{f.x, f.y};
-        }
-        __syncthreads();
         ++passes;
+        s = Pair{0.f, 0.f};
+#pragma unroll 1
+        for (int k = lane; k < P * WARPS; k += 32) s = add(s, all[k]);
+        s = warp_sum(s);
+        summed = true;
     }
 
     // ---- the next token: the part in which the running sum passes u times the whole sum
     if (rank == 0) {
-        for (int j = tid; j < n; j += THREADS) a.path[t0 + j] = j < sh.len ? sh.path[j] : -1;
-        if (tid == 0) a.count[b] = sh.len;
+        for (int j = tid; j < n; j += THREADS) a.path[t0 + j] = j < len ? sh.path[j] : -1;  // (a warp's own writes)
+        if (tid == 0) a.count[b] = len;
     }
-    if (warp == 0) {
-        double goal = 0.0, before = 0.0;
-        const int at = find_part(sh.all, P * WARPS, (double)unit(ld_now(a.u_next + b)), true, goal, before);
-        if (lane == 0) {
-            sh.at = at;
-            sh.goal = goal;
-            sh.before = before;
-            if (at < 0 && rank == 0) a.next[b] = -1;
-        }
-    }
-    __syncthreads();
-    if (sh.at >= 0 && sh.at / WARPS == rank) {  // this CTA has it: the part once more, a piece of it per warp
-        const Weights w = sh.w;
-        const int lo = part_lo(sh.at), hi = part_hi(sh.at), piece = part / WARPS;
-        const Pair t = sum_of(w, sh, min(hi, lo + warp * piece), min(hi, lo + (warp + 1) * piece));
-        if (lane == 0) sh.all[warp] = t;
+    const Pair *all = sh.all[(passes - 1) & 1], goal = mul(u_next, s);
+    Pair run{0.f, 0.f};
+    const int at = find(P * WARPS, (P * WARPS + 31) / 32, [&](int i) { return all[i]; }, goal, run);  // by every warp alike
+    if (at < 0) {
+        if (tid == 0 && rank == 0) a.next[b] = -1;
+    } else if (at / WARPS == rank) {  // this CTA has it: a piece of that part per warp, token by token
+        const int hi = part_hi(at), piece = part / WARPS, per = (piece + 31) / 32, from = part_lo(at) + warp * piece, n_mine = min(from + piece, hi) - from;
+        auto token = [&](int i) { return weight(w, sh, from + i); };
+        Pair m{0.f, 0.f};
+#pragma unroll 2
+        for (int i = lane * per; i < min(lane * per + per, n_mine); ++i) m = add(m, token(i));
+        m = warp_sum(m);
+        Pair *sums = sh.all[passes & 1];  // (its last readers are past the last pass)
+        if (lane == 0) sums[warp] = m;
         __syncthreads();
-        if (warp == 0) {
-            double goal = sh.goal, run = sh.before;
-            const int in = find_part(sh.all, WARPS, 0.0, false, goal, run);
-            // token by token, 32 at a time; where rounding leaves the goal past the last one, that one
-            int token = -1;
-            const int end = min(hi, lo + (in + 1) * piece);
-            for (int v0 = lo + in * piece; in >= 0 && v0 < end; v0 += 32) {
-                const int v = v0 + lane;
-                const double m = v < end ? value(weight(w, sh, v)) : 0.0, upto = run + upto_lane(m);
-                const unsigned past = __ballot_sync(kFull, m > 0.0 && upto > goal), some = __ballot_sync(kFull, m > 0.0);
-                if (past) {
-                    token = v0 + __ffs(past) - 1;
-                    break;
-                }
-                if (some) token = v0 + 31 - __clz(some);
-                run = __shfl_sync(kFull, upto, 31);
-            }
-            if (lane == 0) a.next[b] = token;
+        if (find(WARPS, 1, [&](int i) { return sums[i]; }, goal, run) == warp) {
+            const int x = find(n_mine, per, token, goal, run);
+            if (lane == 0) a.next[b] = x < 0 ? -1 : from + x;
         }
     }
     cluster_leave();  // a CTA's shared memory stays until the others have read it
@@ -309,9 +356,10 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(const __grid_constant__
 
 cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t st) {
     using namespace verify;
-    // as many CTAs per sequence as leave each at least 4096 tokens of the vocabulary and fit the SMs at once
+    // as many CTAs per sequence as leave each at least 1024 tokens of the vocabulary and, at two CTAs per SM, run at once (clusters do
+    // not fill every SM)
     int P = 1;
-    while (P < MAX_P && a.V / (2 * P) >= 4096 && (long long)a.B * 2 * P <= 2LL * sm_count()) P *= 2;
+    while (P < MAX_P && a.V / (2 * P) >= 1024 && (long long)a.B * 2 * P <= 2LL * sm_count() - 16) P *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)P, (unsigned)a.B, 1);
     cfg.blockDim = dim3(THREADS, 1, 1);

@@ -90,7 +90,7 @@ def verify(target, draft, tokens, parent, u, u_next):
     """One sequence: (path, next token), by the residual distributions themselves."""
     def clean(row):
         row = np.asarray(row, dtype=np.float64)
-        return np.where(np.isfinite(row) & (row > 0), row, 0.0)
+        return np.clip(np.nan_to_num(row, nan=0.0, posinf=1.0, neginf=0.0), 0.0, 1.0)
 
     x, path = 0, [0]
     while True:

@@ -415,7 +415,7 @@ def test_verified_tokens_are_distributed_as_the_target():
 
 
 def test_verify_at_the_edges():
-    """Probabilities that are zero, negative or not finite; random numbers at the ends; no weight left; strided rows."""
+    """Probabilities that are zero, outside [0, 1] or not finite; random numbers at the ends; no weight left; strided rows."""
     V = 40
     gen = torch.Generator().manual_seed(1)
     big = probabilities(6, V + 3, gen)
