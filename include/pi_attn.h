@@ -454,7 +454,8 @@ int pi_attn_rotary(const void *q, const long long *q_strides, const void *k, con
  *   q [T, H, d] bf16 to q_out [T, H, d], k into the cache (quantised from the 32-bit result where it holds 8 bits),
  *   v into the cache as it is.  Token strides as for pi_attn_cache_append, also for q_out, which may be q itself (with q's
  *   stride).  A token whose sequence or page is out of range is left out, its row of q_out as it was; so are the
- *   rows of tokens behind the last sequence.  H <= 65535 (else PI_ERR_UNSUPPORTED).
+ *   rows of tokens behind the last sequence.  H <= 65535, T * ceil(H / 4) * d / 512 and
+ *   T * ceil(Hkv d / 512) below 2^31 (else PI_ERR_UNSUPPORTED).
  */
 int pi_attn_rotary_append(const void *q, long long q_stride, const void *k, long long k_stride, const void *v, long long v_stride,
                           const pi_attn_rotary_t *rotary, const pi_attn_cache_t *cache, const pi_attn_batch_t *batch,
@@ -501,8 +502,8 @@ int pi_attn_verify_tree(const float *target, long long target_stride, const floa
  *   path [T], count [B] int32 (device) as pi_attn_verify_tree writes them: ascending node numbers.  caches: n_caches
  *   descriptors (host memory, read before the call returns) of the same type and sizes (else PI_ERR_SHAPE), whose rows do not overlap.
  *   A sequence with an offset, length, count or path out of range is left out; so is a row whose source or place is
- *   on a page out of range.  Sequences must not share pages that rows are moved in.  B * ceil(2 Hkv (row bytes / 16 + 1) / 256) < 2^31
- *   (else PI_ERR_UNSUPPORTED).
+ *   on a page out of range.  Sequences must not share pages that rows are moved in.  B * ceil(2 min(n_caches, 64) Hkv (row bytes / 16 + 1) / 256)
+ *   < 2^31 (else PI_ERR_UNSUPPORTED).
  */
 int pi_attn_cache_keep(const pi_attn_cache_t *caches, int n_caches, const pi_attn_batch_t *batch, const int *path,
                        const int *count, void *stream);

@@ -93,6 +93,7 @@ int pi_attn_rotary_append(const void *q, long long q_stride, const void *k, long
     g.a.k_stride = k_stride; g.a.v_stride = v_stride;
     g.parent = parent;
     g.H = H;
+    if (!pi::rotary_append_fits(g)) return PI_ERR_UNSUPPORTED;
     if (!(g.a.index_word = pi::index_word())) return PI_ERR_CUDA;
     return map_cuda(pi::launch_rotary_append(g, static_cast<cudaStream_t>(stream)));
 }
@@ -151,7 +152,7 @@ int pi_attn_cache_keep(const pi_attn_cache_t *caches, int n_caches, const pi_att
         if (rc != PI_OK) return rc;
         if (c.kv_type != d.kv_type || c.n_pages != d.n_pages || c.Hkv != d.Hkv || c.page != d.page || c.d != d.d) return PI_ERR_SHAPE;
     }
-    if (!pi::keep_fits(a.cache, batch->B)) return PI_ERR_UNSUPPORTED;
+    if (!pi::keep_fits(a.cache, batch->B, std::min(n_caches, pi::kKeepLayers))) return PI_ERR_UNSUPPORTED;
     if (!aligned(path, 4) || !aligned(count, 4)) return PI_ERR_ALIGN;
     a.path = path;
     a.count = count;

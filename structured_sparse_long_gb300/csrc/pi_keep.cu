@@ -32,28 +32,17 @@ __device__ __forceinline__ void move(T *pages, const int2 *rows, int n, long lon
 __global__ void __launch_bounds__(THREADS) keep_kernel(const __grid_constant__ KeepArgs a) {
     __shared__ int2 rows[THREADS];  // source and place of the path's rows, for head 0 (both 0: not moved)
     const PagedCache &c = a.cache;
-    const int b = blockIdx.x / (unsigned)a.chunks, chunk = blockIdx.x - b * a.chunks, layer = blockIdx.y, tid = threadIdx.x;
+    const int b = blockIdx.x / (unsigned)a.chunks, chunk = blockIdx.x - b * a.chunks, tid = threadIdx.x;
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int t0 = ld_now(a.batch.cu + b), t1 = ld_now(a.batch.cu + b + 1), ctx = ld_now(a.batch.ctx + b), n = ld_now(a.count + b);
     bool ok = sequence_ok(c, a.batch, t0, t1, ctx) && n >= 0 && n <= t1 - t0;
-    for (int j = tid; ok && j < n; j += THREADS) {
-        const int x = ld_now(a.path + t0 + j);
-        ok = x > (j > 0 ? ld_now(a.path + t0 + j - 1) : -1) && x < t1 - t0;
-    }
-    if (!__syncthreads_and(ok)) {
-        if (tid == 0) record_index(a.index_word);
-        return;
-    }
-    const bool quant = c.kv_type != kKvBf16;
-    const int row16 = quant ? c.d / 16 : c.d / 8, per_head = row16 + quant, piece = chunk * THREADS + tid;
-    const int col = piece % per_head, head = (piece / per_head) % c.Hkv, val = piece / per_head / c.Hkv;
-    const long long first = (long long)head << c.page_log2;
-    for (int j0 = 0; j0 < n; j0 += THREADS) {
-        const int j = j0 + tid;
-        if (j < n) {
+    // row j of the path: whether it follows the one before it, and (first: this round's) where it lies
+    auto look = [&](int j, bool place) -> bool {
+        const int x = ld_now(a.path + t0 + j), before = j > 0 ? ld_now(a.path + t0 + j - 1) : -1;
+        if (x <= before || x >= t1 - t0) return false;
+        if (place) {
             int2 r = make_int2(0, 0);
-            const int x = ld_now(a.path + t0 + j);
             if (x != j) {
                 const int from = page_of(c, a.batch.table, b, ctx + x), to = page_of(c, a.batch.table, b, ctx + j);
                 if (from < 0 || to < 0) record_index(a.index_word);
@@ -61,9 +50,21 @@ __global__ void __launch_bounds__(THREADS) keep_kernel(const __grid_constant__ K
             }
             rows[tid] = r;
         }
-        __syncthreads();
+        return true;
+    };
+    for (int j = tid; ok && j < n; j += THREADS) ok = look(j, j < THREADS);
+    if (!__syncthreads_and(ok)) {
+        if (tid == 0) record_index(a.index_word);
+        return;
+    }
+    const bool quant = c.kv_type != kKvBf16;
+    const int row16 = quant ? c.d / 16 : c.d / 8, per_head = row16 + quant, item = chunk * THREADS + tid, per_layer = 2 * c.Hkv * per_head;
+    const int layer = item / per_layer, piece = item - layer * per_layer;
+    const int col = piece % per_head, head = (piece / per_head) % c.Hkv, val = piece / per_head / c.Hkv;
+    const long long first = (long long)head << c.page_log2;
+    for (int j0 = 0;;) {
         const int m = min(THREADS, n - j0);
-        if (val < 2) {
+        if (layer < a.layers) {
             if (col < row16) {
                 move(static_cast<uint4 *>(val ? a.v[layer] : a.k[layer]), rows, m, first * row16 + col, row16);
             } else if (c.d == 128) {
@@ -72,6 +73,10 @@ __global__ void __launch_bounds__(THREADS) keep_kernel(const __grid_constant__ K
                 move(reinterpret_cast<uint16_t *>(val ? a.v_scale[layer] : a.k_scale[layer]), rows, m, first, 1);
             }
         }
+        j0 += THREADS;
+        if (j0 >= n) break;
+        __syncthreads();
+        if (j0 + tid < n) look(j0 + tid, true);
         __syncthreads();
     }
 }
@@ -81,9 +86,9 @@ __global__ void __launch_bounds__(THREADS) keep_kernel(const __grid_constant__ K
 cudaError_t launch_keep(const KeepArgs &args, cudaStream_t st) {
     using namespace keep;
     KeepArgs a = args;
-    a.chunks = (keep_pieces(a.cache) + THREADS - 1) / THREADS;
+    a.chunks = (int)(((long long)keep_pieces(a.cache) * a.layers + THREADS - 1) / THREADS);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.batch.B * a.chunks), (unsigned)a.layers, 1);  // (fits: keep_fits)
+    cfg.gridDim = dim3((unsigned)(a.batch.B * a.chunks), 1, 1);  // (fits: keep_fits)
     cfg.blockDim = dim3(THREADS, 1, 1);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];  // it may start while the kernel before it on the stream ends (and waits for it)

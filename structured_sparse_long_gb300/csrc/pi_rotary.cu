@@ -6,8 +6,9 @@
 // multiplications reduce it, exactly, however far the position is.  What is left of a turn, as fp32, goes to sincospi.
 // Every element is read once and written once, so HBM bounds long calls.  The sines of a position are the same for all of its heads:
 //   * rotary_kernel: a thread has 8 pairs (16 elements) of a row and walks over heads with the same 8 sines and cosines.
-//   * append_kernel: a CTA puts its tokens' sines into shared memory, since a cache row's 8-bit blocks of 32 elements do not fall
-//     on the pairs' halves: a lane has 16 contiguous elements of a key row and reads their partners once more (from L1).
+//   * append_kernel: every warp is on its own.  One takes four heads of neighbouring tokens' queries, in the same way; another a token's keys
+//     and values.  A cache row's 8-bit blocks of 32 elements do not fall on the pairs' halves, so there a lane has 16 contiguous
+//     elements of a key row, reads their partners once more (from L1), and the warp's sines lie in shared memory.
 #include "pi_mma.cuh"
 #include "pi_paged.cuh"
 #include "pi_quant.cuh"
@@ -134,6 +135,19 @@ __global__ void __launch_bounds__(THREADS) rotary_kernel(const __grid_constant__
 
 // ------------------------------------------------------------------ a serving step's new tokens
 
+constexpr int QH = 4;  // heads of a warp's queries
+
+// CTAs for the queries, and for the keys and values.
+struct append_size {
+    long long queries, rows;
+};
+static append_size append_blocks(const RotaryAppendArgs &g) {
+    const PagedCache &c = g.a.cache;
+    const long long T = g.a.batch.T, per_warp = 512 / c.d, warps = THREADS / 32;
+    const long long q = (T + per_warp - 1) / per_warp * ((g.H + QH - 1) / QH), kv = T * ((c.Hkv * (long long)c.d + 511) / 512);
+    return append_size{(q + warps - 1) / warps, (kv + warps - 1) / warps};
+}
+
 struct Place {
     int line, pg;  // cache position of the token's row, and its page (-1: the token is left out)
 };
@@ -167,145 +181,189 @@ __device__ __forceinline__ void put16(const PagedCache &c, void *pages, uint8_t 
     }
 }
 
-// TOK tokens per CTA.  A token's work comes in pieces of 16 elements, those of its queries, keys and values each padded to
-// whole warps.
-template <int KV, bool INTER, int TOK>
-__global__ void __launch_bounds__(THREADS) append_kernel(const __grid_constant__ RotaryAppendArgs g) {
-    extern __shared__ float2 turns[];  // [TOK][rot / 2]
-    __shared__ Place place[TOK];
-    static_assert(TOK <= THREADS / 32, "a warp per token");
+// Where packed tokens t .. t + n - 1 go (n <= 31), in lanes 0 .. n - 1: the position of each in its text and its row's place.  For the whole
+// warp.  The first one's sequence is searched; the others' is one of the next 31, whose offsets one round of loads brings (so that a
+// step of single tokens costs no search for each), or, with more empty ones in between, searched too.
+__device__ __forceinline__ void look_up(const RotaryAppendArgs &g, int t, int n, int &pos, Place &place) {
     const PagedCache &c = g.a.cache;
     const PagedBatch &bt = g.a.batch;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rot = g.r.rot, half = rot / 2;
-    const int per_row = c.d / 16, row_log2 = c.d_log2 - 4;
-    const int nq = (g.H * per_row + 31) & ~31, nk = (c.Hkv * per_row + 31) & ~31, n = nq + 2 * nk;
-    const int first = blockIdx.x * TOK, tokens = min(TOK, bt.T - first), items = tokens * n;
+    const int lane = threadIdx.x & 31, B = bt.B;
+    pos = -1;
+    place = Place{0, -1};
+    const int b0 = find_sequence(B, [&](int j) { return ld_now(bt.cu + j) <= t; });
+    if (b0 >= B) return;
+    const int start = ld_now(bt.cu + min(b0 + lane, B)), at = ld_now(bt.ctx + min(b0 + lane, B - 1));
+    int b = B, t0 = 0, t1 = 0, ctx = 0;  // of the lane's token
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+        const int on = __popc(__ballot_sync(kFull, lane > 0 && b0 + lane <= B && start <= t + i));
+        int bi = b0 + on, u0 = __shfl_sync(kFull, start, on & 31), u1 = __shfl_sync(kFull, start, (on + 1) & 31), x = __shfl_sync(kFull, at, on & 31);
+        if (on == 31) {
+            bi = find_sequence(B, [&](int j) { return ld_now(bt.cu + j) <= t + i; });
+            u0 = ld_now(bt.cu + min(bi, B - 1));
+            u1 = ld_now(bt.cu + min(bi, B - 1) + 1);
+            x = ld_now(bt.ctx + min(bi, B - 1));
+        }
+        if (lane == i) {
+            b = bi; t0 = u0; t1 = u1; ctx = x;
+        }
+    }
+    const bool mine = lane < n && t + lane < bt.T && b < B;
+    const bool ok = mine && sequence_ok(c, bt, t0, t1, ctx) && t + lane >= t0 && t + lane < t1;
+    int deep = t + lane - t0;
+    if (g.parent) {
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+            if (!__shfl_sync(kFull, ok, i)) continue;
+            const int u0 = __shfl_sync(kFull, t0, i), u1 = __shfl_sync(kFull, t1, i), d = tree_depth(g.parent, u0, u1 - u0, t + i - u0);
+            if (lane == i) deep = d;
+        }
+    }
+    if (ok && deep >= 0) {
+        pos = ctx + deep;
+        place.line = ctx + t + lane - t0;
+        place.pg = page_of(c, bt.table, b, place.line);
+    }
+    if (mine && place.pg < 0) record_index(g.a.index_word);
+}
+
+// The sines of 8 pairs, group g of a token's: in four quarters of two pairs, quarter by quarter for all groups, so that lanes with
+// neighbouring groups read neighbouring 16 bytes of shared memory.
+__device__ __forceinline__ void read_turns(float2 (&cs)[8], const float4 *turns, int groups, int g) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const float4 x = turns[q * groups + g];
+        cs[2 * q] = make_float2(x.x, x.y);
+        cs[2 * q + 1] = make_float2(x.z, x.w);
+    }
+}
+
+// The first q_blocks CTAs' warps turn queries, the others keys.
+template <int KV, bool INTER>
+__global__ void __launch_bounds__(THREADS, 4) append_kernel(const __grid_constant__ RotaryAppendArgs g, int q_blocks) {
+    extern __shared__ float4 all_turns[];  // [warps][4][rot / 16]
+    const PagedCache &c = g.a.cache;
+    const int lane = threadIdx.x & 31, rot = g.r.rot, half = rot / 2;
+    const int units = c.d / 16, units_log2 = c.d_log2 - 4;
+    using Row = Eight<__nv_bfloat16>;
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-
-    // piece `it`: its token, what it is (0: queries, 1: keys, 2: values), head and first element
-    struct Piece {
-        int tok, kind, head, col;
-        bool in;
-    };
-    auto piece = [&](int it) {
-        Piece p;
-        p.tok = it / n;
-        int x = it - p.tok * n;
-        p.kind = x < nq ? 0 : x < nq + nk ? 1 : 2;
-        x -= p.kind == 0 ? 0 : p.kind == 1 ? nq : nq + nk;
-        p.head = x >> row_log2;
-        p.col = 16 * (x & (per_row - 1));
-        p.in = p.head < (p.kind == 0 ? g.H : c.Hkv);
-        return p;
-    };
-    using Row = Eight<__nv_bfloat16>;
-    Row x0, x1, y0, y1;  // the elements, and (keys, pairs in halves) their partners
-    auto load = [&](const Piece &p) {
-        if (!p.in) {
-            x0.w[0] = x1.w[0] = y0.w[0] = y1.w[0] = make_uint4(0u, 0u, 0u, 0u);
-            return;
-        }
-        const long long t = first + p.tok;
-        const __nv_bfloat16 *r = p.kind == 0 ? g.q + t * g.q_stride : p.kind == 1 ? g.a.k + t * g.a.k_stride : g.a.v + t * g.a.v_stride;
-        r += (long long)p.head * c.d;
-        if (p.kind == 0) {  // 8 pairs, in halves from both of them
-            const bool halves = !INTER && p.col < rot;
-            x0.load(r + (halves ? p.col / 2 : p.col));
-            x1.load(r + (halves ? p.col / 2 + half : p.col + 8));
-        } else {
-            x0.load(r + p.col);
-            x1.load(r + p.col + 8);
-            if (!INTER && p.kind == 1) {
-                const int e0 = p.col, e1 = p.col + 8;
-                y0.load(r + (e0 < half ? e0 + half : e0 < rot ? e0 - half : e0));
-                y1.load(r + (e1 < half ? e1 + half : e1 < rot ? e1 - half : e1));
-            }
-        }
-    };
-    Piece p = piece(threadIdx.x);
-    p.in = p.in && (int)threadIdx.x < items;
-    load(p);
-
-    if (warp < tokens) {  // where the token's row goes, and its sines
-        const int t = first + warp;
-        int b, line = locate(c, bt, t, b, g.a.index_word), pos = line, pg = -1;
-        if (line >= 0) {
-            if (g.parent) {
-                const int t0 = ld_now(bt.cu + b), deep = tree_depth(g.parent, t0, ld_now(bt.cu + b + 1) - t0, t - t0);
-                pos = deep < 0 ? -1 : line - (t - t0) + deep;
-            }
-            if (pos >= 0) pg = page_of(c, bt.table, b, line);
-            if (pg < 0 && lane == 0) record_index(g.a.index_word);
-        }
-        if (lane == 0) place[warp] = Place{line, pg};
-        for (int j = lane; j < half; j += 32) turns[warp * half + j] = turn(g.r, j, pos);
-    }
-    __syncthreads();
-
-    for (int it = threadIdx.x; it < items; it += THREADS) {  // (whole warps)
-        if (it >= THREADS) {
-            p = piece(it);
-            load(p);
-        }
-        const Place pl = place[p.tok];
-        const float2 *cs = turns + p.tok * half;
-        p.in = p.in && pl.pg >= 0;
-        if (p.kind == 0) {
-            const bool halves = !INTER && p.col < rot;
-            if (p.col < rot) {
-                float a[8], b[8];
-                float2 w[8];
+    if ((int)blockIdx.x < q_blocks) {  // ---- queries: 32 / units neighbouring tokens, QH heads, 8 pairs to a lane
+        const unsigned w = blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5), shares = (g.H + QH - 1) / QH;
+        const int share = w % shares, n = 32 >> units_log2, u = lane & (units - 1);
+        const long long t0 = (long long)(w / shares) * n;
+        if (t0 >= g.a.batch.T) return;
+        const int mine = lane >> units_log2, t = (int)t0 + mine, h0 = share * QH;
+        const bool turns = u < rot / 16;
+        const int at_a = turns && !INTER ? 8 * u : 16 * u, at_b = turns && !INTER ? at_a + half : at_a + 8;
+        const bool there = t < g.a.batch.T;
+        const __nv_bfloat16 *x = g.q + (long long)(there ? t : 0) * g.q_stride + (long long)h0 * c.d;
+        Row qa[QH], qb[QH];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) w[j] = cs[p.col / 2 + j];
-                x0.unpack(a);
-                x1.unpack(b);
-                turn_pairs<INTER>(a, b, w);
-                x0.pack(a);
-                x1.pack(b);
+        for (int i = 0; i < QH; ++i)
+            if (there && h0 + i < g.H) {
+                qa[i].load(x + i * c.d + at_a);
+                qb[i].load(x + i * c.d + at_b);
             }
-            if (p.in) {
-                __nv_bfloat16 *r = g.q_out + (first + p.tok) * g.q_out_stride + (long long)p.head * c.d;
-                x0.store(r + (halves ? p.col / 2 : p.col));
-                x1.store(r + (halves ? p.col / 2 + half : p.col + 8));
+        int pos;
+        Place place;
+        look_up(g, (int)t0, n, pos, place);
+        pos = __shfl_sync(kFull, pos, mine);
+        if (__shfl_sync(kFull, place.pg, mine) < 0) return;
+        float2 cs[8];
+        if (turns)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) cs[j] = turn(g.r, 8 * u + j, pos);
+        __nv_bfloat16 *y = g.q_out + (long long)t * g.q_out_stride + (long long)h0 * c.d;
+#pragma unroll
+        for (int i = 0; i < QH; ++i)
+            if (h0 + i < g.H) {
+                if (turns) {
+                    float fa[8], fb[8];
+                    qa[i].unpack(fa);
+                    qb[i].unpack(fb);
+                    turn_pairs<INTER>(fa, fb, cs);
+                    qa[i].pack(fa);
+                    qb[i].pack(fb);
+                }
+                qa[i].store(y + i * c.d + at_a);
+                qb[i].store(y + i * c.d + at_b);
             }
-            continue;
+        return;
+    }
+    // ---- a token's keys and values, 16 neighbouring elements of each to a lane, and (keys, pairs in halves) the partners of their two eights
+    const unsigned w = (blockIdx.x - q_blocks) * (THREADS / 32) + (threadIdx.x >> 5);
+    const int t = (int)(w / (unsigned)g.a.chunks), chunk = (int)(w - t * (unsigned)g.a.chunks);
+    if (t >= g.a.batch.T) return;
+    const int j = chunk * 32 + lane, head = j >> units_log2, col = 16 * (j & (units - 1)), groups = rot / 16;
+    const bool some = head < c.Hkv;
+    const __nv_bfloat16 *pk = g.a.k + (long long)t * g.a.k_stride + (long long)j * 16, *pv = g.a.v + (long long)t * g.a.v_stride + (long long)j * 16;
+    Row k0, k1, y0, y1, v0, v1;
+    k0.w[0] = k1.w[0] = y0.w[0] = y1.w[0] = v0.w[0] = v1.w[0] = make_uint4(0u, 0u, 0u, 0u);
+    if (some) {
+        auto partner = [&](int e) -> int { return e < half ? half : e < rot ? -half : 0; };
+        k0.load(pk);
+        k1.load(pk + 8);
+        v0.load(pv);
+        v1.load(pv + 8);
+        if (!INTER) {
+            y0.load(pk + partner(col));
+            y1.load(pk + 8 + partner(col + 8));
         }
+    }
+    int pos;
+    Place place;
+    look_up(g, t, 1, pos, place);
+    pos = __shfl_sync(kFull, pos, 0);
+    const int pg = __shfl_sync(kFull, place.pg, 0), line = __shfl_sync(kFull, place.line, 0);
+    if (pg < 0) return;
+    const long long row = row_in_page(c, pg, min(head, c.Hkv - 1), line);
+    if constexpr (KV == kKvBf16) {  // values as they are
+        __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(c.v) + row * c.d + col;
+        if (some) {
+            v0.store(to);
+            v1.store(to + 8);
+        }
+    } else {
         float a[8], b[8];
-        x0.unpack(a);
-        x1.unpack(b);
-        if (p.kind == 1 && p.col < rot) {
-            if constexpr (INTER) {
-                float2 w[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) w[j] = cs[p.col / 2 + j];
-                turn_pairs<true>(a, b, w);
-            } else {
-                auto eight = [&](float (&x)[8], const Row &partner, int e) {  // (rot / 2 is a multiple of 8: on one side of it)
-                    float y[8];
-                    partner.unpack(y);
-                    const bool low = e < half;
-                    const float2 *w = cs + (low ? e : e - half);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] = fmaf(x[j], w[j].x, low ? -y[j] * w[j].y : y[j] * w[j].y);
-                };
-                eight(a, y0, p.col);
-                eight(b, y1, p.col + 8);
-            }
+        v0.unpack(a);
+        v1.unpack(b);
+        put16<KV>(c, c.v, c.v_scale, a, b, row, col, some);
+    }
+    float4 *turns = all_turns + (threadIdx.x >> 5) * 4 * groups;
+    for (int i = lane; i < half; i += 32) reinterpret_cast<float2 *>(turns)[2 * ((i >> 1 & 3) * groups + (i >> 3)) + (i & 1)] = turn(g.r, i, pos);
+    __syncwarp();
+    const bool turned = col < rot;  // (rot is a multiple of 16)
+    if (KV == kKvBf16 && !turned) {
+        __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(c.k) + row * c.d + col;
+        if (some) {
+            k0.store(to);
+            k1.store(to + 8);
         }
-        const long long row = row_in_page(c, max(pl.pg, 0), p.head, max(pl.line, 0));
-        if (KV == kKvBf16 && (p.kind == 2 || p.col >= rot)) {  // as they are
-            __nv_bfloat16 *r = static_cast<__nv_bfloat16 *>(p.kind == 1 ? c.k : c.v) + row * c.d + p.col;
-            if (p.in) {
-                x0.store(r);
-                x1.store(r + 8);
-            }
-        } else if (p.kind == 1) {
-            put16<KV>(c, c.k, c.k_scale, a, b, row, p.col, p.in);
+        return;
+    }
+    float a[8], b[8];
+    k0.unpack(a);
+    k1.unpack(b);
+    if (turned) {
+        float2 cs[8];
+        if constexpr (INTER) {
+            read_turns(cs, turns, groups, col / 16);
+            turn_pairs<true>(a, b, cs);
         } else {
-            put16<KV>(c, c.v, c.v_scale, a, b, row, p.col, p.in);
+            auto eight = [&](float (&x)[8], const Row &other, int e) {  // (rot / 2 is a multiple of 8: on one side of it)
+                const float sign = e < half ? -1.f : 1.f;
+                read_turns(cs, turns, groups, (e < half ? e : e - half) / 8);
+                float y[8];
+                other.unpack(y);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = fmaf(x[i], cs[i].x, sign * (y[i] * cs[i].y));
+            };
+            eight(a, y0, col);
+            eight(b, y1, col + 8);
         }
     }
+    put16<KV>(c, c.k, c.k_scale, a, b, row, col, some);
 }
 
 // A launch that may start while the kernel before it on the stream ends (and waits for it).
@@ -324,15 +382,15 @@ static cudaError_t launch(K kernel, dim3 grid, size_t smem, cudaStream_t st, con
     return cudaLaunchKernelEx(&cfg, kernel, a...);
 }
 
-template <int KV, int TOK>
-static cudaError_t launch_append(const RotaryAppendArgs &g, cudaStream_t st) {
-    const dim3 grid((unsigned)((g.a.batch.T - 1) / TOK + 1), 1, 1);
-    const size_t smem = (size_t)TOK * (g.r.rot / 2) * sizeof(float2);
-    return g.r.interleaved ? launch(append_kernel<KV, true, TOK>, grid, smem, st, g) : launch(append_kernel<KV, false, TOK>, grid, smem, st, g);
-}
 template <int KV>
-static cudaError_t launch_append(const RotaryAppendArgs &g, cudaStream_t st) {
-    return g.a.batch.T >= 16 * sm_count() ? launch_append<KV, 8>(g, st) : launch_append<KV, 1>(g, st);
+static cudaError_t launch_append(const RotaryAppendArgs &args, cudaStream_t st) {
+    RotaryAppendArgs g = args;
+    const PagedCache &c = g.a.cache;
+    const append_size n = append_blocks(g);
+    g.a.chunks = (c.Hkv * c.d + 511) / 512;
+    const dim3 grid((unsigned)(n.queries + n.rows), 1, 1);  // (fits: rotary_append_fits)
+    const size_t smem = (size_t)(THREADS / 32) * (g.r.rot / 2) * sizeof(float2);
+    return g.r.interleaved ? launch(append_kernel<KV, true>, grid, smem, st, g, (int)n.queries) : launch(append_kernel<KV, false>, grid, smem, st, g, (int)n.queries);
 }
 
 }  // namespace rot
@@ -345,6 +403,11 @@ cudaError_t launch_rotary(const RotaryArgs &a, cudaStream_t st) {
     auto kernel = a.f32 ? (a.r.interleaved ? rotary_kernel<float, true> : rotary_kernel<float, false>)
                         : (a.r.interleaved ? rotary_kernel<__nv_bfloat16, true> : rotary_kernel<__nv_bfloat16, false>);
     return launch(kernel, grid, 0, st, a, per, q_shares);
+}
+
+bool rotary_append_fits(const RotaryAppendArgs &a) {
+    const rot::append_size n = rot::append_blocks(a);
+    return n.queries + n.rows <= 0x7fffffffLL && n.queries < (1LL << 28) && n.rows < (1LL << 28);  // warps are numbered in 32 bits
 }
 
 cudaError_t launch_rotary_append(const RotaryAppendArgs &a, cudaStream_t st) {

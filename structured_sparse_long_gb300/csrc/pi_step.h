@@ -63,17 +63,17 @@ struct KeepArgs {
     PagedCache cache;  // sizes and type; the layers' pages:
     void *k[kKeepLayers], *v[kKeepLayers];
     uint8_t *k_scale[kKeepLayers], *v_scale[kKeepLayers];
-    int layers, chunks;  // chunks: CTAs per sequence and layer, set at the launch
+    int layers, chunks;  // chunks: CTAs per sequence, set at the launch
     PagedBatch batch;
     const int *path, *count;
     int *index_word;
 };
 
-// 16-byte pieces (and one for the scales of an 8-bit row) of a sequence's row in one layer, and whether a launch holds B of them.
+// 16-byte pieces (and one for the scales of an 8-bit row) of a sequence's row in one layer, and whether a launch holds those of B sequences.
 inline int keep_pieces(const PagedCache &c) {
     return 2 * c.Hkv * (c.kv_type == kKvBf16 ? c.d / 8 : c.d / 16 + 1);
 }
-inline bool keep_fits(const PagedCache &c, long long B) { return B * ((keep_pieces(c) + 255) / 256) <= 0x7fffffffLL; }
+inline bool keep_fits(const PagedCache &c, long long B, int layers) { return B * (((long long)keep_pieces(c) * layers + 255) / 256) <= 0x7fffffffLL; }
 
 cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t st);               // pi_verify.cu
 cudaError_t launch_keep(const KeepArgs &a, cudaStream_t st);                   // pi_keep.cu
@@ -90,5 +90,6 @@ cudaError_t launch_tree_tc(const ExtendTreeArgs &a, cudaStream_t st);          /
 cudaError_t launch_extend_tree(const ExtendTreeArgs &a, cudaStream_t st);      // pi_decode_paged.cu
 cudaError_t launch_rotary(const RotaryArgs &a, cudaStream_t st);               // pi_rotary.cu
 cudaError_t launch_rotary_append(const RotaryAppendArgs &a, cudaStream_t st);  // pi_rotary.cu
+bool rotary_append_fits(const RotaryAppendArgs &a);                             // whether a launch holds it
 
 }  // namespace pi
