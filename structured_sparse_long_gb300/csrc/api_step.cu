@@ -117,7 +117,7 @@ int pi_attn_extend_tree(const void *q, long long q_stride, const pi_attn_cache_t
     a.lse = lse;
     t.parent = parent;
     bool fits;
-    pi::tree_few(t, fits);
+    t.few = pi::tree_few(t, fits);
     if (!fits) return PI_ERR_UNSUPPORTED;
     a.timeout_ns = kWaitTimeoutNs;
     if (!(a.status = pi::status_word()) || !(a.index_word = pi::index_word())) return PI_ERR_CUDA;

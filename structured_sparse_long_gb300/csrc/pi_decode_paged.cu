@@ -243,6 +243,7 @@ paged_rows_kernel(const __grid_constant__ Args a) {
     // ---- the CTA's sequence b, its queries' positions first .. last and their first packed token tok0
     int b, first, last, tok0, n_tok = 1;
     TreeGroup *tree = nullptr;
+    TreeParents parents;
     if constexpr (TREE) tree = tree_group();
     if constexpr (!TOKENS) {
         b = tok0 = blockIdx.z;
@@ -288,11 +289,10 @@ paged_rows_kernel(const __grid_constant__ Args a) {
         first = ctx + x0;
         last = min(first + a.group, ctx + t1 - t0) - 1;
         n_tok = last - first + 1;
-        if constexpr (TREE) {  // first and last: the lowest and the highest position of the nodes
-            if (!tree_walk(*tree, s, a.parent + t0, t1 - t0, x0, n_tok, ctx, first, last)) {
-                if (threadIdx.x == 0) record_index(a.index_word);
-                return;
-            }
+        if constexpr (TREE) load_parents(parents, a.parent + t0, t1 - t0, x0, ctx);  // (and the page table's entries)
+        if constexpr (TREE) {
+            const int at = (band_lo(ctx, s.mode, s.k_local) >> c.page_log2) + 32 * threadIdx.x;
+            if (at <= (ctx + t1 - t0 - 1) >> c.page_log2) asm volatile("prefetch.global.L1 [%0];" ::"l"(a.batch.table + (long long)b * c.width + at));
         }
     }
     const int cols = n_tok * G;
@@ -313,6 +313,12 @@ paged_rows_kernel(const __grid_constant__ Args a) {
             const float al = a.alpha && y < cols ? ld_now(a.alpha + row_of(y)) : 1.f;
             offb[nh][e] = a.alpha ? log2f(al) : 0.f;
             offs[nh][e] = log2f(1.f - al);
+        }
+    }
+    if constexpr (TREE) {  // first and last: the lowest and the highest position of the nodes
+        if (!tree_walk(*tree, parents, s, n_tok, first, last)) {
+            if (threadIdx.x == 0) record_index(a.index_word);
+            return;
         }
     }
     // ---- the key list: the band lo .. last, then for each skip distance m * period, m = m_first ..., the n_tok keys that
@@ -664,13 +670,13 @@ cudaError_t launch_extend_few(const ExtendArgs &e, cudaStream_t st) {
 }
 
 // Whether this kernel beats the tensor-core one for a batch of trees (pi_tree_tc.cu), and whether either can number its work.  As in
-// extend_few_rows, by two estimates in us from the sizes that the host knows, all trees taken as equally large: this kernel's
-// rounds of tiles, and the other's turns of blocks, each a start and tiles of 32 keys.  Fitted to 112 shapes (16 heads on 4, 8 on 1 and 16 on
-// 16, d = 128, and 12 on 12, d = 64; bf16 and e4m3; 1 to 64 trees of 2 to 160 nodes), of which it gets 98 right to 5 % and the others wrong by
-// 6 to 34 %.  For instance (this kernel / the other):
-//   16 heads on 4, d = 128, band 256, bf16:  1 tree of 26 nodes 10.3 / 11.9, of 160 15.1 / 14.6; 8 of 32 17.0 / 12.1, 32 of 32 64.3 / 12.7
-//                                     e4m3:  1 of 26 10.5 / 15.7; 8 of 8 11.8 / 14.5, 8 of 32 20.2 / 15.8
-//   12 on 12, d = 64, band 128, bf16:  1 of 26 7.7 / 9.2; 16 of 16 10.5 / 11.6, 32 of 32 28.3 / 18.7
+// extend_few_rows, by two estimates in us from the sizes that the host knows, all trees taken as equally large: this kernel's waves of
+// rounds of tiles (split()), and the other's turns of blocks, each a start and tiles of 32 keys.  Fitted to 204 shapes (16 heads on 4, 8 on 1 and 16 on
+// 16, d = 128; 12 on 12, 8 on 8 and 7 on 1, d = 64; bf16 and e4m3; 1 to 64 trees of 2 to 160 nodes), of which it gets 190 right to 5 %
+// and the others wrong by 6 to 31 %.  For instance (this kernel / the other):
+//   16 heads on 4, d = 128, band 256, bf16:  1 tree of 26 nodes 9.9 / 11.8, of 160 15.1 / 14.6; 8 of 32 17.0 / 12.1, 32 of 32 64.3 / 12.7
+//                                     e4m3:  1 of 26 10.4 / 15.7; 8 of 8 11.8 / 14.5, 8 of 32 20.2 / 15.8
+//   12 on 12, d = 64, band 128, bf16:  1 of 26 7.6 / 9.2; 16 of 16 10.5 / 11.6, 32 of 32 28.3 / 18.7
 bool tree_few(const ExtendTreeArgs &t, bool &fits) {
     const ExtendArgs &e = t.e;
     const Shape &s = e.s;
@@ -685,19 +691,21 @@ bool tree_few(const ExtendTreeArgs &t, bool &fits) {
                           (T + e.batch.B * (long long)(group - 1)) / group <= 0x7fffffffLL;
     fits = tc_fits || few_fits;
     if (!tc_fits || !few_fits) return few_fits;
-    const bool quant = c.kv_type != kKvBf16;
-    const long long sms = sm_count(), tiles = (most.list(group) + std::min<long long>(n, 8 * group) + decp::KEYS - 1) / decp::KEYS;
-    const long long ctas = B * ((n + group - 1) / group) * s.Hkv;
-    const double rounds = (double)ctas * (double)(tiles + 6) / (double)(sms * decp::sm_warps(s.d, c.kv_type, group * G > 8 ? 2 : 1));
+    const bool quant = c.kv_type != kKvBf16, d64 = s.d == 64;
+    const int nh = group * G > 8 ? 2 : 1, sm_w = decp::sm_warps(s.d, c.kv_type, nh);
+    const long long tiles = (most.list(group) + std::min<long long>(n, 8 * group) + decp::KEYS - 1) / decp::KEYS;
+    const long long pairs = B * ((n + group - 1) / group) * s.Hkv, sms = sm_count();
+    const decp::Split sp = decp::split(sm_w, decp::max_warps(s.d, c.kv_type, nh), tiles, pairs);
+    const long long waves = (pairs * sp.ctas - 1) / (sm_w / sp.warps * sms) + 1, rounds = (tiles - 1) / (sp.warps * sp.ctas) + 1;
+    const double few = 4.3 + (double)waves * ((double)rounds + 1.8) * (d64 ? 1.27 : 1.94) * (quant ? 1.17 : 1.0);
     const long long turns = (B * ((n + rows - 1) / rows) * (s.H / heads) - 1) / (2 * sms) + 1;
     const double block_tiles = (double)(most.band + n + 6 * most.windows) / 32 + 0.5;
-    return 8.4 + (quant ? 1.8 : 1.7) * rounds <= 1.5 + (double)turns * (6.1 + (quant ? 0.8 : 0.37) * block_tiles);
+    return few <= 1.5 + (double)turns * (7.4 + 0.286 * block_tiles * (d64 ? 0.59 : 1.0) * (quant ? 2.3 : 1.0));
 }
 
 cudaError_t launch_extend_tree(const ExtendTreeArgs &t, cudaStream_t st) {
     using namespace decp;
-    bool fits;
-    if (!tree_few(t, fits)) return launch_tree_tc(t, st);
+    if (!t.few) return launch_tree_tc(t, st);
     const ExtendArgs &e = t.e;
     const Shape &s = e.s;
     const int group = token_group(s.H / s.Hkv);

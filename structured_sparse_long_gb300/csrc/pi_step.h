@@ -45,6 +45,7 @@ struct RotaryAppendArgs {
 struct ExtendTreeArgs {
     ExtendArgs e;
     const int *parent;  // [T]
+    bool few;           // tree_few()
 };
 
 struct VerifyArgs {

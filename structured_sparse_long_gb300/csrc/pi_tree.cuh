@@ -48,17 +48,35 @@ __device__ __forceinline__ TreeGroup *tree_group() {
     return &group;
 }
 
-// Nodes node0 .. node0 + n_q - 1 of the n whose parents are given: their positions (lowest and highest in first, last) and the
-// nodes that they attend.  False: more than kTreeMax nodes, or a parent out of range.  For the whole CTA; every thread returns the same.
-__device__ __forceinline__ bool tree_walk(TreeGroup &g, const Shape &s, const int *parent, int n, int node0, int n_q, int ctx, int &first,
-                                          int &last) {
+// A tree's parents on their way, some to a thread of the CTA (of 64 or more).
+struct TreeParents {
+    int held[kTreeMax / 64];
+    int n, node0, ctx;
+};
+__device__ __forceinline__ void load_parents(TreeParents &p, const int *parent, int n, int node0, int ctx) {
+    p.n = n;
+    p.node0 = node0;
+    p.ctx = ctx;
+#pragma unroll
+    for (int i = 0; i < kTreeMax / 64; ++i) {
+        const int j = i * (int)blockDim.x + (int)threadIdx.x;
+        p.held[i] = j < min(n, kTreeMax) ? ld_now(parent + j) : -1;
+    }
+}
+
+// Nodes node0 .. node0 + n_q - 1 of a tree: their positions (lowest and highest in first, last) and the nodes that they attend.  False: more
+// than kTreeMax nodes, or a parent out of range.  For the whole CTA; every thread returns the same.
+__device__ __forceinline__ bool tree_walk(TreeGroup &g, const TreeParents &p, const Shape &s, int n_q, int &first, int &last) {
+    const int n = p.n, node0 = p.node0, ctx = p.ctx;
     if (n > kTreeMax) return false;
     bool ok = true;
-    for (int j = threadIdx.x; j < n; j += blockDim.x) {
-        const int p = ld_now(parent + j);
-        g.parent[j] = p;
+#pragma unroll
+    for (int i = 0; i < kTreeMax / 64; ++i) {
+        const int j = i * (int)blockDim.x + (int)threadIdx.x;
+        if (j >= n) break;
+        g.parent[j] = p.held[i];
         g.mask[j] = 0u;
-        ok = ok && p >= -1 && p < j;
+        ok = ok && p.held[i] >= -1 && p.held[i] < j;
     }
     if (!__syncthreads_and(ok)) return false;
     if ((int)threadIdx.x < n_q) {
