@@ -9,7 +9,6 @@
 // The interpreter lock is released where a call may wait (an allocation, a full launch queue).
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
-#include <torch/csrc/utils/object_ptr.h>
 
 #include <ATen/ops/empty.h>
 
@@ -310,6 +309,11 @@ struct Heads {
         for (int i = 0; i < 3; ++i) stride[i] = t->stride(i);
         p = address(*t, h);
     }
+    Heads(const at::Tensor &made, const Handle &h) {
+        for (int i = 0; i < 4; ++i) size[i] = made.size(i);
+        for (int i = 0; i < 3; ++i) stride[i] = made.stride(i);
+        p = address(made, h);
+    }
 };
 
 int int_of(PyObject *o, const char *what) {
@@ -343,7 +347,7 @@ PyObject *rotary(PyObject *const *a) {
         const int64_t size[4] = {B, heads, N, d};
         if (given[i] == Py_None) {
             made[i] = new_tensor(h, type, size);
-            return Heads(THPObjectPtr(THPVariable_Wrap(made[i])).get(), "out", h, type, size);
+            return Heads(made[i], h);
         }
         return Heads(given[i], i ? "k_out" : "q_out", h, type, size);
     };

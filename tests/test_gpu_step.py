@@ -652,3 +652,82 @@ def test_empty_batches():
     pa.cache_keep(cache, table, cu, ctx, none, dev([0]))
     q, kk = pa.rotary(torch.empty(1, 4, 0, 64, device="cuda"), torch.empty(1, 2, 0, 64, device="cuda"), r)
     assert q.shape == (1, 4, 0, 64) and kk.shape == (1, 2, 0, 64)
+
+
+@pytest.mark.parametrize("B,kv", [(400, "bf16"), (1300, "int8"), (1300, "bf16")])
+def test_many_trees(B, kv):
+    """Hundreds of trees, some empty, on the tensor-core kernel: their blocks are counted by every CTA, or (over 1152) searched."""
+    rng = np.random.default_rng(B)
+    d, H, Hkv, page = 64, 8, 2, 16
+    n = [int(x) if x > 3 else 0 for x in rng.integers(0, 70, B)]
+    n[-1], n[B // 2] = 33, 256
+    cache, table, cu, parents, q, alpha, _ = tree_case(kv, d, H, Hkv, page, [0] * B, n, seed=B, extra=3)
+    T = q.shape[0]
+    out, lse = torch.full((T, H, d), 5.0, device="cuda", dtype=torch.bfloat16), torch.full((T, H), 5.0, device="cuda")
+    ctx = np.zeros(B, dtype=np.int32)
+    pa.extend_tree(q, cache, dev(table), dev(cu), dev(ctx), dev(sum(parents, []) + [-1] * 3), alpha.cuda(), 9, 4, 3, out=out, lse=lse)
+    torch.cuda.synchronize()
+    assert pa.status() == 0 and (out[-3:] == 5).all() and (lse[-3:] == 5).all() and not (lse[:-3] == 5).any()
+    for b in sorted({0, B - 1, B // 2, *rng.integers(0, B, 25).tolist()}):
+        if not n[b]:
+            continue
+        rows = slice(cu[b], cu[b + 1])
+        k, v = (t.cpu() for t in pa.cache_read(cache, dev(table[b:b + 1]), dev([0, n[b]]), dev([0]), n[b]))
+        want = sref.tree_attention(q[rows].cpu(), k, v, alpha[rows], 0, parents[b], 9, 4, 3, PI)
+        ref.check_attention(f"sequence {b}", out[rows], lse[rows], want)
+
+
+def test_offsets_that_decrease_are_reported():
+    """Nothing outside the buffers is touched, and status says so, whichever kernel it is."""
+    cache, table, cu, parents, q, alpha, _ = tree_case("bf16", 64, 8, 2, 16, [0] * 40, [40] * 40, seed=3)
+    bad = cu.copy()
+    bad[20] = 100
+    par = dev(sum(parents, []))
+    pa.extend_tree(q, cache, dev(table), dev(bad), dev([0] * 40), par, alpha.cuda(), 9, 4, 3)
+    assert pa.status() == ERR_INDEX
+    x = torch.ones(q.shape[0], 2, 64, device="cuda", dtype=torch.bfloat16)
+    pa.rotary_append(q, x, x, rope(64, False), cache, dev(table), dev(bad), dev([0] * 40), par)
+    assert pa.status() == ERR_INDEX
+    pa.extend_tree(q[:8], cache, dev(table[:2]), dev([0, 6, 3]), dev([0, 0]), dev([-1] * 8), alpha[:8].cuda(), 9, 4, 3)
+    assert pa.status() == ERR_INDEX
+
+
+def test_two_streams_and_threads():
+    """Calls of several threads on streams of their own, not waiting for one another: each result is the lone call's."""
+    import threading
+    cases = []
+    for seed in range(4):
+        cache, table, cu, parents, q, alpha, _ = tree_case("e4m3", 128, 8, 2, 32, [70, 33], [20, 60], seed=seed)
+        s = verify_case([9, 30], 5000, True, 1.0, seed=seed)
+        args = (q, cache, dev(table), dev(cu), dev([70, 33]), dev(sum(parents, [])), alpha.cuda(), 24, 30, 2)
+        v = (s[2].cuda(), s[3].cuda(), dev(s[4]), dev(s[1]), dev(sum(s[0], [])), s[5].cuda(), s[6].cuda())
+        cases.append((args, v, pa.extend_tree(*args), pa.verify_tree(*v)))
+    torch.cuda.synchronize()
+    got = [None] * 4
+
+    def work(i):
+        st = torch.cuda.Stream()
+        for _ in range(20):
+            got[i] = (pa.extend_tree(*cases[i][0], stream=st), pa.verify_tree(*cases[i][1], stream=st))
+        st.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for (_, _, tree, verified), (a, b) in zip(cases, got):
+        assert all(torch.equal(x, y) for x, y in zip(tree + verified, a + b))
+
+
+def test_a_single_node_is_a_decoded_token():
+    """One node per sequence, as a step without drafts has it: rotary_append and extend_tree against decode_paged's row."""
+    B, H, Hkv, d, page = 5, 8, 2, 128, 32
+    ctx = [100, 31, 0, 64, 7]
+    cache, table, cu, parents, q, alpha, held = tree_case("bf16", d, H, Hkv, page, ctx, [1] * B, seed=6)
+    out, lse = pa.extend_tree(q, cache, dev(table), dev(cu), dev(ctx), dev([-1] * B), alpha.cuda(), 20, 24, 3)
+    one, l1 = pa.decode_paged(q, cache, dev(table), dev([c + 1 for c in ctx]), alpha.cuda(), 20, 24, 3)
+    for b in range(B):
+        want = ref.attention(q[b:b + 1].cpu(), *held[b], alpha[b:b + 1], ctx[b], 20, 24, 3, PI)
+        ref.check_attention("node", out[b:b + 1], lse[b:b + 1], want)
+        ref.check_attention("token", one[b:b + 1], l1[b:b + 1], want)
