@@ -63,15 +63,17 @@ struct Eight {
     }
 };
 
-// The 8 pairs of 16 elements a, b: (a[j], b[j]), or neighbours within each.
+// The 8 pairs of 16 elements a, b: (a[j], b[j]), or neighbours within each; two pairs to an instruction.
 template <bool INTER>
 __device__ __forceinline__ void turn_pairs(float (&a)[8], float (&b)[8], const float2 (&cs)[8]) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        float &x = INTER ? (j < 4 ? a[2 * j] : b[2 * j - 8]) : a[j], &y = INTER ? (j < 4 ? a[2 * j + 1] : b[2 * j - 7]) : b[j];
-        const float x0 = x;
-        x = fmaf(x0, cs[j].x, -y * cs[j].y);
-        y = fmaf(x0, cs[j].y, y * cs[j].x);
+    for (int j = 0; j < 8; j += 2) {
+        float *p = INTER ? (j < 4 ? a + 2 * j : b + 2 * j - 8) : a + j, *q = INTER ? p + 1 : b + j;
+        constexpr int step = INTER ? 2 : 1;
+        const uint64_t x = tc::pack2(p[0], p[step]), y = tc::pack2(q[0], q[step]);
+        const uint64_t c = tc::pack2(cs[j].x, cs[j + 1].x), s = tc::pack2(cs[j].y, cs[j + 1].y), m = tc::pack2(-cs[j].y, -cs[j + 1].y);
+        tc::unpack2(tc::fma2(x, c, tc::mul2(y, m)), p[0], p[step]);
+        tc::unpack2(tc::fma2(x, s, tc::mul2(y, c)), q[0], q[step]);
     }
 }
 
@@ -135,17 +137,21 @@ __global__ void __launch_bounds__(THREADS) rotary_kernel(const __grid_constant__
 
 // ------------------------------------------------------------------ a serving step's new tokens
 
-constexpr int QH = 4;  // heads of a warp's queries
+constexpr int QH = 4;  // heads of a warp's queries at a time
 
-// CTAs for the queries, and for the keys and values.
+// How a launch is cut: heads of a warp's queries, CTAs for the queries, and for the keys and values.
 struct append_size {
+    int q_heads;
     long long queries, rows;
 };
 static append_size append_blocks(const RotaryAppendArgs &g) {
     const PagedCache &c = g.a.cache;
-    const long long T = g.a.batch.T, per_warp = 512 / c.d, warps = THREADS / 32;
-    const long long q = (T + per_warp - 1) / per_warp * ((g.H + QH - 1) / QH), kv = T * ((c.Hkv * (long long)c.d + 511) / 512);
-    return append_size{(q + warps - 1) / warps, (kv + warps - 1) / warps};
+    const long long T = g.a.batch.T, per_warp = 512 / c.d, warps = THREADS / 32, groups = (T + per_warp - 1) / per_warp;
+    // two rounds of heads with the same sines, where that leaves 12 warps per SM (16 heads, d = 128: 4000 tokens 10.5 us, one round 11.4; 2000
+    // tokens 9.2 and 7.4)
+    const int q_heads = groups * ((g.H + 2 * QH - 1) / (2 * QH)) >= 12LL * sm_count() ? 2 * QH : QH;
+    const long long q = groups * ((g.H + q_heads - 1) / q_heads), kv = T * ((c.Hkv * (long long)c.d + 511) / 512);
+    return append_size{q_heads, (q + warps - 1) / warps, (kv + warps - 1) / warps};
 }
 
 struct Place {
@@ -166,12 +172,13 @@ __device__ __forceinline__ void put16(const PagedCache &c, void *pages, uint8_t 
             y.store(p + 8);
         }
     } else {
-        uint32_t m = 0;  // magnitudes compare like their bits; infinities and NaN come out on top
+        float m = 0.f;  // (a NaN stays one)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, max(__float_as_uint(lo[j]) & 0x7fffffffu, __float_as_uint(hi[j]) & 0x7fffffffu));
-        m = max(m, __shfl_xor_sync(kFull, m, 1));
-        const bool finite = m < 0x7f800000u;
-        const int e = finite ? scale_exp<KV>(__uint_as_float(m)) : 0;
+        for (int j = 0; j < 8; ++j) asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(fabsf(lo[j])), "f"(fabsf(hi[j])));
+        const float other = __shfl_xor_sync(kFull, m, 1);
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(other));
+        const bool finite = m < INFINITY;
+        const int e = finite ? scale_exp<KV>(m) : 0;
         const uint2 x = encode_codes<KV>(lo, e), y = encode_codes<KV>(hi, e);
         if (!in) return;
         *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(pages) + row * c.d + col) =
@@ -238,9 +245,9 @@ __device__ __forceinline__ void read_turns(float2 (&cs)[8], const float4 *turns,
     }
 }
 
-// The first q_blocks CTAs' warps turn queries, the others keys.
+// The first q_blocks CTAs' warps turn queries, q_heads of neighbouring tokens each, the others keys.
 template <int KV, bool INTER>
-__global__ void __launch_bounds__(THREADS, 4) append_kernel(const __grid_constant__ RotaryAppendArgs g, int q_blocks) {
+__global__ void __launch_bounds__(THREADS, 4) append_kernel(const __grid_constant__ RotaryAppendArgs g, int q_blocks, int q_heads) {
     extern __shared__ float4 all_turns[];  // [warps][4][rot / 16]
     const PagedCache &c = g.a.cache;
     const int lane = threadIdx.x & 31, rot = g.r.rot, half = rot / 2;
@@ -249,22 +256,25 @@ __global__ void __launch_bounds__(THREADS, 4) append_kernel(const __grid_constan
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if ((int)blockIdx.x < q_blocks) {  // ---- queries: 32 / units neighbouring tokens, QH heads, 8 pairs to a lane
-        const unsigned w = blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5), shares = (g.H + QH - 1) / QH;
+        const unsigned w = blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5), shares = (g.H + q_heads - 1) / q_heads;
         const int share = w % shares, n = 32 >> units_log2, u = lane & (units - 1);
         const long long t0 = (long long)(w / shares) * n;
         if (t0 >= g.a.batch.T) return;
-        const int mine = lane >> units_log2, t = (int)t0 + mine, h0 = share * QH;
+        const int mine = lane >> units_log2, t = (int)t0 + mine, h0 = share * q_heads, h1 = min(h0 + q_heads, g.H);
         const bool turns = u < rot / 16;
         const int at_a = turns && !INTER ? 8 * u : 16 * u, at_b = turns && !INTER ? at_a + half : at_a + 8;
         const bool there = t < g.a.batch.T;
-        const __nv_bfloat16 *x = g.q + (long long)(there ? t : 0) * g.q_stride + (long long)h0 * c.d;
+        const __nv_bfloat16 *x = g.q + (long long)(there ? t : 0) * g.q_stride;
         Row qa[QH], qb[QH];
+        auto load = [&](int h) {
 #pragma unroll
-        for (int i = 0; i < QH; ++i)
-            if (there && h0 + i < g.H) {
-                qa[i].load(x + i * c.d + at_a);
-                qb[i].load(x + i * c.d + at_b);
-            }
+            for (int i = 0; i < QH; ++i)
+                if (there && h + i < h1) {
+                    qa[i].load(x + (h + i) * c.d + at_a);
+                    qb[i].load(x + (h + i) * c.d + at_b);
+                }
+        };
+        load(h0);
         int pos;
         Place place;
         look_up(g, (int)t0, n, pos, place);
@@ -274,21 +284,25 @@ __global__ void __launch_bounds__(THREADS, 4) append_kernel(const __grid_constan
         if (turns)
 #pragma unroll
             for (int j = 0; j < 8; ++j) cs[j] = turn(g.r, 8 * u + j, pos);
-        __nv_bfloat16 *y = g.q_out + (long long)t * g.q_out_stride + (long long)h0 * c.d;
+        __nv_bfloat16 *y = g.q_out + (long long)t * g.q_out_stride;
+#pragma unroll 1
+        for (int h = h0; h < h1; h += QH) {
+            if (h > h0) load(h);
 #pragma unroll
-        for (int i = 0; i < QH; ++i)
-            if (h0 + i < g.H) {
-                if (turns) {
-                    float fa[8], fb[8];
-                    qa[i].unpack(fa);
-                    qb[i].unpack(fb);
-                    turn_pairs<INTER>(fa, fb, cs);
-                    qa[i].pack(fa);
-                    qb[i].pack(fb);
+            for (int i = 0; i < QH; ++i)
+                if (h + i < h1) {
+                    if (turns) {
+                        float fa[8], fb[8];
+                        qa[i].unpack(fa);
+                        qb[i].unpack(fb);
+                        turn_pairs<INTER>(fa, fb, cs);
+                        qa[i].pack(fa);
+                        qb[i].pack(fb);
+                    }
+                    qa[i].store(y + (h + i) * c.d + at_a);
+                    qb[i].store(y + (h + i) * c.d + at_b);
                 }
-                qa[i].store(y + i * c.d + at_a);
-                qb[i].store(y + i * c.d + at_b);
-            }
+        }
         return;
     }
     // ---- a token's keys and values, 16 neighbouring elements of each to a lane, and (keys, pairs in halves) the partners of their two eights
@@ -353,11 +367,15 @@ __global__ void __launch_bounds__(THREADS, 4) append_kernel(const __grid_constan
         } else {
             auto eight = [&](float (&x)[8], const Row &other, int e) {  // (rot / 2 is a multiple of 8: on one side of it)
                 const float sign = e < half ? -1.f : 1.f;
+                const uint64_t sign2 = tc::pack2(sign, sign);
                 read_turns(cs, turns, groups, (e < half ? e : e - half) / 8);
                 float y[8];
                 other.unpack(y);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = fmaf(x[i], cs[i].x, sign * (y[i] * cs[i].y));
+                for (int i = 0; i < 8; i += 2) {
+                    const uint64_t part = tc::mul2(tc::mul2(tc::pack2(y[i], y[i + 1]), tc::pack2(cs[i].y, cs[i + 1].y)), sign2);
+                    tc::unpack2(tc::fma2(tc::pack2(x[i], x[i + 1]), tc::pack2(cs[i].x, cs[i + 1].x), part), x[i], x[i + 1]);
+                }
             };
             eight(a, y0, col);
             eight(b, y1, col + 8);
@@ -390,7 +408,8 @@ static cudaError_t launch_append(const RotaryAppendArgs &args, cudaStream_t st) 
     g.a.chunks = (c.Hkv * c.d + 511) / 512;
     const dim3 grid((unsigned)(n.queries + n.rows), 1, 1);  // (fits: rotary_append_fits)
     const size_t smem = (size_t)(THREADS / 32) * (g.r.rot / 2) * sizeof(float2);
-    return g.r.interleaved ? launch(append_kernel<KV, true>, grid, smem, st, g, (int)n.queries) : launch(append_kernel<KV, false>, grid, smem, st, g, (int)n.queries);
+    return g.r.interleaved ? launch(append_kernel<KV, true>, grid, smem, st, g, (int)n.queries, n.q_heads)
+                           : launch(append_kernel<KV, false>, grid, smem, st, g, (int)n.queries, n.q_heads);
 }
 
 }  // namespace rot
