@@ -35,6 +35,7 @@ namespace pi {
 namespace decp {
 
 constexpr int MAX_P = 8;   // CTAs per cluster (portable limit)
+constexpr int MEET = 12;   // states of a row that meet in one turn
 constexpr int KEYS = 16;   // keys per tile: the rows of S^T
 constexpr unsigned kFull = 0xffffffffu;
 
@@ -453,7 +454,7 @@ paged_rows_kernel(const __grid_constant__ Args a) {
         }
     // ---- and meet: four columns of a row per thread, all the cluster's states at once (a merge in each CTA first and then one
     // of the CTAs' took 10.6 us where this takes 9.1, 16 drafts of up to 5 tokens in clusters of three)
-    constexpr int PER_ROW = D / 4, BATCH = 12;  // threads of a row; states in flight
+    constexpr int PER_ROW = D / 4, BATCH = MEET;  // threads of a row; states in flight
     const int states = P * warps, items = cols * PER_ROW;
     const uint32_t base = smem_addr(part);
     auto meet = [&](auto across) {
@@ -538,15 +539,17 @@ paged_rows_kernel(const __grid_constant__ Args a) {
 // Measured: 64 sequences x 4 KV heads, 17 tiles, bf16, d = 128: 6 warps 10.3 us, 4 warps 12.6, 3 warps in clusters of two 11.8;
 // 32 x 12 pairs of 9 int8 tiles, d = 64: 5 warps 5.5, 4 warps 6.4, 6 warps (two waves) 8.2; one sequence x 4 heads, 17 e4m3
 // tiles: clusters of 6 x 3 warps 5.0, 5 x 4 5.2, 3 x 6 5.3, one CTA of 6 warps 7.2.
+// `most`: warps of a cluster.  Trees have up to MEET of them, whose states of up to 8 columns meet in one turn: a tree of 26 nodes, 16 heads on
+// 4, d = 128, bf16: 2 warps in clusters of 5 9.5 us, 4 in clusters of 5 10.5.
 struct Split {
     int warps, ctas;
 };
-static Split split(int sm_w, int max_w, long long tiles, long long pairs) {
+static Split split(int sm_w, int max_w, long long tiles, long long pairs, int most = MAX_P * 32) {
     Split best{max_w, 1};
     long long least = -1;
     const long long sms = sm_count();
     for (int ctas = 1; ctas <= MAX_P; ++ctas)
-        for (int w = 2; w <= max_w; ++w) {
+        for (int w = 2; w <= max_w && w * ctas <= most; ++w) {
             const long long waves = (pairs * ctas - 1) / (sm_w / w * sms) + 1, rounds = (tiles - 1) / (w * ctas) + 1;
             // half a round for meeting across a cluster; then as few warps in all as do, then small CTAs
             const long long cost = (2 * waves * (rounds + 2) + (ctas > 1 ? 1 : 0)) * 128 + w * ctas;
@@ -561,7 +564,7 @@ static Split split(int sm_w, int max_w, long long tiles, long long pairs) {
 template <int D, int KV, int NH, Kind KIND>
 static cudaError_t launch(const Args &a, int groups, long long keys, cudaStream_t st) {
     const int cols = a.group * (a.s.H / a.s.Hkv);
-    const Split sp = split(sm_warps(D, KV, NH), max_warps(D, KV, NH), (keys + KEYS - 1) / KEYS, (long long)groups * a.s.Hkv);
+    const Split sp = split(sm_warps(D, KV, NH), max_warps(D, KV, NH), (keys + KEYS - 1) / KEYS, (long long)groups * a.s.Hkv, KIND == kTree ? MEET : MAX_P * 32);
     auto *kernel = paged_rows_kernel<D, KV, NH, KIND>;
     static PerDeviceOnce configured;  // shared memory above the 48 KB default
     int dev = 0;
@@ -672,11 +675,11 @@ cudaError_t launch_extend_few(const ExtendArgs &e, cudaStream_t st) {
 // Whether this kernel beats the tensor-core one for a batch of trees (pi_tree_tc.cu), and whether either can number its work.  As in
 // extend_few_rows, by two estimates in us from the sizes that the host knows, all trees taken as equally large: this kernel's waves of
 // rounds of tiles (split()), and the other's turns of blocks, each a start and tiles of 32 keys.  Fitted to 204 shapes (16 heads on 4, 8 on 1 and 16 on
-// 16, d = 128; 12 on 12, 8 on 8 and 7 on 1, d = 64; bf16 and e4m3; 1 to 64 trees of 2 to 160 nodes), of which it gets 190 right to 5 %
-// and the others wrong by 6 to 31 %.  For instance (this kernel / the other):
-//   16 heads on 4, d = 128, band 256, bf16:  1 tree of 26 nodes 9.9 / 11.8, of 160 15.1 / 14.6; 8 of 32 17.0 / 12.1, 32 of 32 64.3 / 12.7
-//                                     e4m3:  1 of 26 10.4 / 15.7; 8 of 8 11.8 / 14.5, 8 of 32 20.2 / 15.8
-//   12 on 12, d = 64, band 128, bf16:  1 of 26 7.6 / 9.2; 16 of 16 10.5 / 11.6, 32 of 32 28.3 / 18.7
+// 16, d = 128; 12 on 12, 8 on 8 and 7 on 1, d = 64; bf16 and e4m3; 1 to 64 trees of 2 to 160 nodes), of which it gets 191 right to 5 %
+// and the others wrong by 6 to 17 %.  For instance (this kernel / the other):
+//   16 heads on 4, d = 128, band 256, bf16:  1 tree of 26 nodes 9.2 / 11.9, of 160 14.8 / 14.6; 8 of 32 16.9 / 12.1, 32 of 32 63.8 / 12.9
+//                                     e4m3:  1 of 26 9.6 / 15.7; 8 of 8 11.7 / 14.4, 8 of 32 20.2 / 15.8
+//   12 on 12, d = 64, band 128, bf16:  1 of 26 7.4 / 9.3; 16 of 16 10.2 / 11.6, 32 of 32 27.9 / 18.8
 bool tree_few(const ExtendTreeArgs &t, bool &fits) {
     const ExtendArgs &e = t.e;
     const Shape &s = e.s;
@@ -695,12 +698,12 @@ bool tree_few(const ExtendTreeArgs &t, bool &fits) {
     const int nh = group * G > 8 ? 2 : 1, sm_w = decp::sm_warps(s.d, c.kv_type, nh);
     const long long tiles = (most.list(group) + std::min<long long>(n, 8 * group) + decp::KEYS - 1) / decp::KEYS;
     const long long pairs = B * ((n + group - 1) / group) * s.Hkv, sms = sm_count();
-    const decp::Split sp = decp::split(sm_w, decp::max_warps(s.d, c.kv_type, nh), tiles, pairs);
+    const decp::Split sp = decp::split(sm_w, decp::max_warps(s.d, c.kv_type, nh), tiles, pairs, decp::MEET);
     const long long waves = (pairs * sp.ctas - 1) / (sm_w / sp.warps * sms) + 1, rounds = (tiles - 1) / (sp.warps * sp.ctas) + 1;
-    const double few = 4.3 + (double)waves * ((double)rounds + 1.8) * (d64 ? 1.27 : 1.94) * (quant ? 1.17 : 1.0);
+    const double few = 2.4 + (double)waves * ((double)rounds + 2.6) * (d64 ? 1.42 : 1.8);
     const long long turns = (B * ((n + rows - 1) / rows) * (s.H / heads) - 1) / (2 * sms) + 1;
     const double block_tiles = (double)(most.band + n + 6 * most.windows) / 32 + 0.5;
-    return few <= 1.5 + (double)turns * (7.4 + 0.286 * block_tiles * (d64 ? 0.59 : 1.0) * (quant ? 2.3 : 1.0));
+    return few <= 1.5 + (double)turns * (6.9 + 0.4 * block_tiles * (d64 ? 0.66 : 1.0) * (quant ? 1.93 : 1.0));
 }
 
 cudaError_t launch_extend_tree(const ExtendTreeArgs &t, cudaStream_t st) {
