@@ -430,7 +430,8 @@ typedef struct {
  *   overlaps no other tensor; an output's rows do not overlap each other.
  *   Hkv = 0: q alone (k, k_out and their strides are not used).  pos [B, N] int32 (device): the rows' positions, of any
  *   sign; NULL: start, start + 1, ... with start >= 0, start + N <= 2^31.  f32: fp32 tensors instead of bf16.
- *   d in {32, 64, 128}; B * N * (H + Hkv) * d < 2^45, B * N < 2^31, H and Hkv <= 65535 (else PI_ERR_UNSUPPORTED).  Deterministic.
+ *   d in {32, 64, 128}; B * N * (H + Hkv) * d < 2^45, B * N < 2^31, H and Hkv <= 65535, no element 2^60 or more from
+ *   its tensor's first (else PI_ERR_UNSUPPORTED).  Deterministic.
  */
 int pi_attn_rotary(const void *q, const long long *q_strides, const void *k, const long long *k_strides,
                    const pi_attn_rotary_t *rotary, const int *pos, int start, int B, int H, int Hkv, int N, int d, int f32,
@@ -489,8 +490,8 @@ int pi_attn_extend_tree(const void *q, long long q_stride, const pi_attn_cache_t
  *   as the nearest in it, NaN as 0).  cu [B + 1], parent [T] as above.
  *   Writes path [T] int32: the accepted nodes of sequence b from path[cu[b]] on, the rest of its places -1; count [B]: how
  *   many; next [B]: the next token, or -1 where no p is above 0.  A sequence without tokens, or one that is left out, gets
- *   count 0 and next -1, and keeps its places of path.  w, s and a carry 48 bits or more.  1 <= B <= 65535, T > 0, 0 < V <= 2^30.
- *   Deterministic.
+ *   count 0 and next -1, and keeps its places of path.  w, s and a carry 48 bits or more.  1 <= B <= 65535, T > 0, 0 < V <= 2^30,
+ *   T * stride < 2^60.  Deterministic.
  */
 int pi_attn_verify_tree(const float *target, long long target_stride, const float *draft, long long draft_stride,
                         const int *tokens, const int *cu, const int *parent, const float *u, const float *u_next, int B, int T,

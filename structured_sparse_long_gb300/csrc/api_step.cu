@@ -35,6 +35,8 @@ int make_tensor(const void *x, const long long *xs, void *y, const long long *ys
     int rc = check_strides(xs, B, heads, N, f32 ? 4 : 8, 0, a);
     if (rc == PI_OK) rc = check_strides(ys, B, heads, N, f32 ? 4 : 8, d, b);
     if (rc != PI_OK) return rc;
+    for (const long long *s : {a, b})  // offsets in bytes fit 63 bits
+        if ((double)s[0] * B + (double)s[1] * heads + (double)s[2] * N >= 0x1p60) return PI_ERR_UNSUPPORTED;
     if (!aligned(x, 16) || !aligned(y, 16)) return PI_ERR_ALIGN;
     t = pi::RotaryTensor{x, y, a[0], a[1], a[2], b[0], b[1], b[2], heads};
     return PI_OK;
@@ -131,6 +133,7 @@ int pi_attn_verify_tree(const float *target, long long target_stride, const floa
     if (B <= 0 || T <= 0 || V <= 0) return PI_ERR_SHAPE;
     if (B > 65535 || V > 1 << 30) return PI_ERR_UNSUPPORTED;
     if (target_stride < V || target_stride >= 1LL << 38 || (draft && (draft_stride < V || draft_stride >= 1LL << 38))) return PI_ERR_SHAPE;
+    if ((double)T * (double)std::max(target_stride, draft ? draft_stride : 0LL) >= 0x1p60) return PI_ERR_UNSUPPORTED;  // offsets in bytes fit 63 bits
     for (const void *p : {(const void *)target, (const void *)draft, (const void *)tokens, (const void *)cu, (const void *)parent, (const void *)u,
                           (const void *)u_next, (const void *)path, (const void *)count, (const void *)next})
         if (!aligned(p, 4)) return PI_ERR_ALIGN;

@@ -130,6 +130,9 @@ __device__ __forceinline__ uint32_t smem_addr(const void *p) { return static_cas
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// Until all CTAs of the cluster run: before one writes into another's shared memory (no memory is handed over).
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 // Before a CTA ends whose shared memory others read: past it, all have (their values were used; no writes need to be seen).
 __device__ __forceinline__ void cluster_leave() {
     asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");

@@ -6,13 +6,12 @@
 // child none, and the next token one pass (that of the last rejection, if the last node had one).
 //
 // A cluster of CTAs takes a sequence, each of them a contiguous share of the vocabulary, a warp of it a contiguous part of the share.  All
-// CTAs make the same walk from the same numbers.  A pass leaves the warps' sums in shared memory, every CTA collects the cluster's, and
-// their running sum says which warp's part holds the next token; that part is summed again, finer.
+// CTAs make the same walk from the same numbers.  In a pass the warps send their sums to every CTA of the cluster, and
+// their running sum says which warp's part holds the next token; that part is gone through token by token.
 //
 // A running sum is compared with a random number: an error in it would pick a neighbour's token as often as it is large.  fp32 sums over
 // 10^5 tokens would do that once in a hundred calls.  Products and sums are carried in pairs of fp32 (48 bits), two tokens to an
-// instruction: a GB300 has few fp64 units (the walk and the last search alone, some ten dependent fp64 operations each in one warp, took
-// 3 and 5 us).
+// instruction: a dependent fp64 operation takes 75 cycles on a GB300, the sum of two pairs 37.
 #include "pi_mma.cuh"
 #include "pi_paged.cuh"
 #include "pi_step.h"
@@ -28,8 +27,6 @@ constexpr unsigned kFull = 0xffffffffu;
 struct Pair {
     float hi, lo;
 };
-// (What runs once per call is fetched from L2, a few hundred cycles for every 128 bytes of it, so that loops here are rolled up:
-// unrolled, one warp's search of 128 sums took 4 us.)
 // x + y exactly, hi being their rounded sum.
 __device__ __forceinline__ Pair two_sum(float x, float y) {
     const float s = __fadd_rn(x, y), t = __fsub_rn(s, x);
@@ -96,11 +93,11 @@ __device__ __forceinline__ Pair weight(const Weights &w, const Shared &sh, int v
     const float p = sane(ld_now(w.p + v));
     if (is_removed(w, sh, v)) return Pair{0.f, 0.f};
     if (!w.q) return Pair{p, 0.f};
-    const float q = sane(ld_now(w.q + v)), h = __fmul_rn(w.a.hi, q);
-    Pair d = two_sum(p, -h);
-    d.lo = __fsub_rn(d.lo, fmaf(w.a.lo, q, fmaf(w.a.hi, q, -h)));
-    d = add(d, Pair{0.f, 0.f});
-    return positive(d) ? d : Pair{0.f, 0.f};
+    // (as in sum_of, so that a part whose sum is above 0 has a token with a weight)
+    const float q = sane(ld_now(w.q + v)), d = fmaf(-w.a.hi, q, p), t = __fsub_rn(p, d), r = __fsub_rn(__fsub_rn(p, t), d);
+    if (!(d > 0.f)) return Pair{0.f, 0.f};
+    const Pair x = add(Pair{d, fmaf(-w.a.lo, q, __fadd_rn(fmaf(-w.a.hi, q, t), r))}, Pair{0.f, 0.f});
+    return positive(x) ? x : Pair{0.f, 0.f};
 }
 
 // The sum of the weights of tokens lo .. hi - 1, over the warp; AHEAD tokens per lane in flight.
@@ -169,7 +166,7 @@ __device__ __forceinline__ Pair sum_of(const Weights &w, const Shared &sh, int l
 
 __device__ __forceinline__ Pair from_lane(const Pair &x, int lane) { return Pair{__shfl_sync(kFull, x.hi, lane), __shfl_sync(kFull, x.lo, lane)}; }
 // run + the sum over the lanes up to and including this one.  (A lane without a lane so far below it adds 0: with a branch around the
-// addition, whose two sides meet again at the next shuffle, the five steps took 2.7 us.)
+// addition the five steps take 670 cycles instead of 320.)
 __device__ __forceinline__ Pair upto_lane(Pair x, const Pair &run) {
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -217,6 +214,7 @@ __global__ void __launch_bounds__(THREADS, 2) verify_kernel(const __grid_constan
     __shared__ Shared sh;
     const int rank = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     asm volatile("griddepcontrol.launch_dependents;");
+    cluster_arrive();  // (before a CTA writes into another's shared memory, that one has to run)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int t0 = ld_now(a.cu + b), t1 = ld_now(a.cu + b + 1), n = t1 - t0;
     bool ok = t0 >= 0 && t0 <= t1 && t1 <= a.T && n <= kTreeMax;
@@ -231,9 +229,11 @@ __global__ void __launch_bounds__(THREADS, 2) verify_kernel(const __grid_constan
             sh.q[tid] = a.draft ? sane(ld_now(a.draft + (long long)(t0 + parent) * a.draft_stride + token)) : 1.f;
         }
     }
-    if (!__syncthreads_and(ok) || n == 0) {  // (all CTAs of the cluster)
+    ok = __syncthreads_and(ok);
+    cluster_wait();
+    if (!ok || n == 0) {  // (all CTAs of the cluster)
         if (tid == 0 && rank == 0) {
-            if (!ok || n != 0) record_index(a.index_word);
+            if (!ok) record_index(a.index_word);
             a.count[b] = 0;
             a.next[b] = -1;
         }
@@ -344,9 +344,10 @@ __global__ void __launch_bounds__(THREADS, 2) verify_kernel(const __grid_constan
         Pair *sums = sh.all[passes & 1];  // (its last readers are past the last pass)
         if (lane == 0) sums[warp] = m;
         __syncthreads();
-        if (find(WARPS, 1, [&](int i) { return sums[i]; }, goal, run) == warp) {
+        const int in = find(WARPS, 1, [&](int i) { return sums[i]; }, goal, run);
+        if (max(in, 0) == warp) {
             const int x = find(n_mine, per, token, goal, run);
-            if (lane == 0) a.next[b] = x < 0 ? -1 : from + x;
+            if (lane == 0) a.next[b] = from + max(x, 0);  // (there is one; else the part's first token)
         }
     }
     cluster_leave();  // a CTA's shared memory stays until the others have read it

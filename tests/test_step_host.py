@@ -74,7 +74,8 @@ def test_rotary_is_checked(lib):
                dict(qs=(-64, 640, 64)), dict(ks=(1 << 38, 640, 64)), dict(qos=(2560, 0, 64)), dict(kos=(1280, 640, 32))):
         assert rotary(lib, **kw) == PI_ERR_SHAPE, kw
     assert rotary(lib, f32=1, qs=(2560, 640, 62)) == PI_ERR_SHAPE
-    for kw in (dict(d=96), dict(d=16), dict(d=256), dict(H=65536), dict(B=1 << 20, N=1 << 11), dict(B=1 << 14, N=1 << 16, H=60000)):
+    for kw in (dict(d=96), dict(d=16), dict(d=256), dict(H=65536), dict(B=1 << 20, N=1 << 11), dict(B=1 << 14, N=1 << 16, H=60000),
+               dict(B=1 << 24, qs=(1 << 37, 640, 64))):
         assert rotary(lib, **kw) == PI_ERR_UNSUPPORTED, kw
     for kw in (dict(q=A16 + 8), dict(ko=A16 + 4), dict(pos=A16 + 2), dict(r=turns(A16 + 4))):
         assert rotary(lib, **kw) == PI_ERR_ALIGN
@@ -119,7 +120,7 @@ def test_verify_is_checked(lib):
     assert verify(lib, draft=A16 + 2) == PI_ERR_ALIGN
     for kw in (dict(B=0), dict(T=0), dict(V=0), dict(ts=99), dict(ds=99), dict(ts=1 << 38)):
         assert verify(lib, **kw) == PI_ERR_SHAPE
-    for kw in (dict(B=65536), dict(V=2 ** 30 + 1, ts=1 << 31, ds=1 << 31)):
+    for kw in (dict(B=65536), dict(V=2 ** 30 + 1, ts=1 << 31, ds=1 << 31), dict(T=2 ** 30, ts=2 ** 37)):
         assert verify(lib, **kw) == PI_ERR_UNSUPPORTED
 
 
