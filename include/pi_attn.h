@@ -426,8 +426,8 @@ typedef struct {
  *   Each tensor has strides {batch, head, position} in elements, the d elements of a row being contiguous: tensors may
  *   lie in a projection's output, and q_out and k_out in the layout that pi_attn_fwd takes, or the other way round.
  *   Strides: >= 0, below 2^38, multiples of 8 (bf16) or 4 (fp32), and for outputs at least d, all where the dimension
- *   is larger than 1 (else PI_ERR_SHAPE); pointers 16-byte aligned.  An output is its own input, with the same strides, or
- *   overlaps no other tensor; an output's rows do not overlap each other.
+ *   is larger than 1 (else PI_ERR_SHAPE); pointers 16-byte aligned.  An output is its own input, with the same strides (else
+ *   PI_ERR_SHAPE), or overlaps no other tensor; an output's rows do not overlap each other.
  *   Hkv = 0: q alone (k, k_out and their strides are not used).  pos [B, N] int32 (device): the rows' positions, of any
  *   sign; NULL: start, start + 1, ... with start >= 0, start + N <= 2^31.  f32: fp32 tensors instead of bf16.
  *   d in {32, 64, 128}; B * N * (H + Hkv) * d < 2^45, B * N < 2^31, H and Hkv <= 65535, no element 2^60 or more from
@@ -501,7 +501,8 @@ int pi_attn_verify_tree(const float *target, long long target_stride, const floa
  * pi_attn_cache_keep -- the rows of an accepted path moved together: of sequence b row ctx[b] + path[cu[b] + j] goes to row
  *   ctx[b] + j, for j < count[b], keys and values, in each of n_caches layers that share the page table.
  *   path [T], count [B] int32 (device) as pi_attn_verify_tree writes them: ascending node numbers.  caches: n_caches
- *   descriptors (host memory, read before the call returns) of the same type and sizes (else PI_ERR_SHAPE), whose rows do not overlap.
+ *   descriptors (host memory, read before the call returns) of the same type and sizes whose pages do not overlap (else
+ *   PI_ERR_SHAPE; looked for among the 64 caches of a launch).
  *   A sequence with an offset, length, count or path out of range is left out; so is a row whose source or place is
  *   on a page out of range.  Sequences must not share pages that rows are moved in.  B * ceil(2 min(n_caches, 64) Hkv (row bytes / 16 + 1) / 256)
  *   < 2^31 (else PI_ERR_UNSUPPORTED).

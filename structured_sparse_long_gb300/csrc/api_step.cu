@@ -1,6 +1,7 @@
 // api_step.cu -- the C ABI of rotary positions and of a speculative serving step (include/pi_attn.h): validation of every argument
 // that the host can see, then one launch on the caller's stream (pi_attn_cache_keep: one per 64 layers).  Offsets, parents, tokens and page-table
 // entries are checked by the kernels.
+#include <algorithm>
 #include <cstdint>
 
 #include "api_checks.h"
@@ -38,8 +39,30 @@ int make_tensor(const void *x, const long long *xs, void *y, const long long *ys
     for (const long long *s : {a, b})  // offsets in bytes fit 63 bits
         if ((double)s[0] * B + (double)s[1] * heads + (double)s[2] * N >= 0x1p60) return PI_ERR_UNSUPPORTED;
     if (!aligned(x, 16) || !aligned(y, 16)) return PI_ERR_ALIGN;
+    if (x == y && (a[0] != b[0] || a[1] != b[1] || a[2] != b[2])) return PI_ERR_SHAPE;
     t = pi::RotaryTensor{x, y, a[0], a[1], a[2], b[0], b[1], b[2], heads};
     return PI_OK;
+}
+
+// Whether pages of these caches, each `rows` rows of d elements, lie in the same memory.
+bool pages_overlap(const pi::KeepArgs &a) {
+    const pi::PagedCache &c = a.cache;
+    const bool quant = c.kv_type != pi::kKvBf16;
+    const size_t rows = (size_t)c.n_pages * c.Hkv * c.page, bytes = rows * c.d * (quant ? 1 : 2), scales = rows * (c.d / 32);  // (a byte per 32 elements)
+    struct Range {
+        uintptr_t at;
+        size_t bytes;
+    } r[4 * pi::kKeepLayers];
+    int n = 0;
+    for (int i = 0; i < a.layers; ++i) {
+        for (const void *p : {a.k[i], a.v[i]}) r[n++] = Range{reinterpret_cast<uintptr_t>(p), bytes};
+        if (quant)
+            for (const void *p : {a.k_scale[i], a.v_scale[i]}) r[n++] = Range{reinterpret_cast<uintptr_t>(p), scales};
+    }
+    std::sort(r, r + n, [](const Range &x, const Range &y) { return x.at < y.at; });
+    for (int i = 1; i < n; ++i)
+        if (r[i].at - r[i - 1].at < r[i - 1].bytes) return true;
+    return false;
 }
 
 }  // namespace
@@ -159,8 +182,7 @@ int pi_attn_cache_keep(const pi_attn_cache_t *caches, int n_caches, const pi_att
     if (!aligned(path, 4) || !aligned(count, 4)) return PI_ERR_ALIGN;
     a.path = path;
     a.count = count;
-    if (!(a.index_word = pi::index_word())) return PI_ERR_CUDA;
-    for (int first = 0; first < n_caches; first += pi::kKeepLayers) {
+    auto take = [&](int first) {  // a launch's layers
         a.layers = std::min(n_caches - first, pi::kKeepLayers);
         for (int i = 0; i < a.layers; ++i) {
             const pi_attn_cache_t &c = caches[first + i];
@@ -168,6 +190,14 @@ int pi_attn_cache_keep(const pi_attn_cache_t *caches, int n_caches, const pi_att
             a.k_scale[i] = static_cast<uint8_t *>(c.k_scale);
             a.v_scale[i] = static_cast<uint8_t *>(c.v_scale);
         }
+    };
+    for (int first = 0; first < n_caches; first += pi::kKeepLayers) {
+        take(first);
+        if (pages_overlap(a)) return PI_ERR_SHAPE;
+    }
+    if (!(a.index_word = pi::index_word())) return PI_ERR_CUDA;
+    for (int first = 0; first < n_caches; first += pi::kKeepLayers) {
+        if (n_caches > pi::kKeepLayers) take(first);
         rc = map_cuda(pi::launch_keep(a, static_cast<cudaStream_t>(stream)));
         if (rc != PI_OK) return rc;
     }

@@ -353,7 +353,7 @@ PyObject *rotary(PyObject *const *a) {
     };
     const Heads qo = output(0, H), ko = keys ? output(1, Hkv) : qo;
     int rc = PI_OK;
-    if (B && N && H) {
+    if (B && N && (H || Hkv)) {
         const Unlocked u;
         rc = f_rotary(q.p, q.stride, k.p, k.stride, &r.rotary, pos, start, (int)B, (int)H, (int)Hkv, (int)N, (int)d, type == at::kFloat, back, qo.p,
                       qo.stride, ko.p, ko.stride, stream);

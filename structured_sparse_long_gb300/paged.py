@@ -115,7 +115,7 @@ class PagedCache:
         self._struct = _Handle(_CacheStruct(*(None if t is None else t.data_ptr() for t in self._tensors), self.kv_type, n_pages,
                                             Hkv, page, d), self.index)
         self._handle = ctypes.addressof(self._struct)
-        self._layers = None  # this cache alone, as step.CacheLayers
+        self._layers = None  # this cache alone, as step.CacheLayers hands it over (without a reference to it: its pages go with it)
 
     k = property(lambda self: self._tensors[0])
     v = property(lambda self: self._tensors[1])
@@ -138,6 +138,8 @@ class PagedCache:
 def _place(cache, stream):
     """The cache's device current and, where a stream is given, that stream: a call's new tensors (outputs, workspace) are then
     the stream's own, so that none is handed out again while the call still uses it."""
+    if cache.index < 0:
+        raise ValueError(f"tensors must be on a CUDA device, got {cache.device}")
     if stream is not None and stream.device != cache.device:
         raise ValueError(f"stream must be on {cache.device}, got {stream.device}")
     with torch.cuda.device(cache.index):

@@ -37,6 +37,13 @@ class _Layers(ctypes.Structure):  # Layers of csrc/pi_paged_py.cpp
     _fields_ = [("first", _Handle), ("caches", ctypes.POINTER(_CacheStruct)), ("n", ctypes.c_int)]
 
 
+def _layers(caches) -> _Layers:
+    array = (_CacheStruct * len(caches))(*(c._struct.cache for c in caches))
+    s = _Layers(caches[0]._struct, array, len(caches))
+    s.array = array  # (lives as long as the struct)
+    return s
+
+
 def rotary_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0, original: int = 0,
                        low: float = 1.0, high: float = 32.0):
     """Radians per position of the rot / 2 pairs, as a list, and the factor of the turned elements.
@@ -106,8 +113,7 @@ class CacheLayers:
             if c.index != first.index or c.kv_type != first.kv_type or c.k.shape != first.k.shape:
                 raise ValueError("the layers' caches must have the same type and sizes and lie on one device")
         self.device, self.index = first.device, first.index
-        self._array = (_CacheStruct * len(self.caches))(*(c._struct.cache for c in self.caches))
-        self._struct = _Layers(first._struct, self._array, len(self.caches))
+        self._struct = _layers(self.caches)
         self._handle = ctypes.addressof(self._struct)
 
 
@@ -187,10 +193,11 @@ def cache_keep(cache, table, cu, ctx, path, count, stream=None, check=False) -> 
     if stream is not None or cache.index != _current_device():
         with _place(cache, stream):
             return cache_keep(cache, table, cu, ctx, path, count, None, check)
+    handle = cache._handle
     if isinstance(cache, PagedCache):
         if cache._layers is None:
-            cache._layers = CacheLayers((cache,))
-        cache = cache._layers
-    rc = (paged._native or _load_native()).keep(cache._handle, table, cu, ctx, path, count, _raw_stream(cache.index))
+            cache._layers = _layers((cache,))
+        handle = ctypes.addressof(cache._layers)
+    rc = (paged._native or _load_native()).keep(handle, table, cu, ctx, path, count, _raw_stream(cache.index))
     if rc or check:
         _check("pi_attn_cache_keep", rc, None, check)

@@ -1,7 +1,9 @@
 """Host tests of rotary positions and of the speculative step: refusals of the C ABI and of the binding before anything is launched,
 frequencies and fixed-point turns, the reference of the verification, and what the binding hands to the library."""
 import ctypes
+import gc
 import math
+import weakref
 
 import numpy as np
 import pytest
@@ -74,6 +76,7 @@ def test_rotary_is_checked(lib):
                dict(qs=(-64, 640, 64)), dict(ks=(1 << 38, 640, 64)), dict(qos=(2560, 0, 64)), dict(kos=(1280, 640, 32))):
         assert rotary(lib, **kw) == PI_ERR_SHAPE, kw
     assert rotary(lib, f32=1, qs=(2560, 640, 62)) == PI_ERR_SHAPE
+    assert rotary(lib, qos=(2568, 640, 64)) == PI_ERR_SHAPE and rotary(lib, kos=(1280, 648, 64)) == PI_ERR_SHAPE  # in place
     for kw in (dict(d=96), dict(d=16), dict(d=256), dict(H=65536), dict(B=1 << 20, N=1 << 11), dict(B=1 << 14, N=1 << 16, H=60000),
                dict(B=1 << 24, qs=(1 << 37, 640, 64))):
         assert rotary(lib, **kw) == PI_ERR_UNSUPPORTED, kw
@@ -129,6 +132,15 @@ def test_keep_is_checked(lib):
     assert keep(lib, path=A16 + 2) == PI_ERR_ALIGN
     for kw in (dict(n_pages=5), dict(Hkv=1), dict(page=64), dict(d=128), dict(kv_type=1, ks=A16, vs=A16)):
         assert keep(lib, caches=[cache(), cache(**kw)]) == PI_ERR_SHAPE
+    # the same rows twice: keys and values of one layer, of two (4 pages x 2 heads x 32 rows x 64 elements; their scales)
+    step_, scales = 4 * 2 * 32 * 64, 4 * 2 * 32 * 2
+    assert keep(lib) == PI_ERR_SHAPE and keep(lib, caches=[cache(v=A16 + 2 * step_ - 16)]) == PI_ERR_SHAPE
+    two = [cache(v=A16 + 2 * step_), cache(k=A16 + 4 * step_, v=A16 + 6 * step_)]
+    for other in (two[0], cache(k=A16 + 4 * step_, v=A16 + 16), cache(k=A16 + 4 * step_, v=A16 + 6 * step_ - 16)):
+        assert keep(lib, caches=two[:1] + [other]) == PI_ERR_SHAPE
+    at = A16 + 2 * step_
+    assert keep(lib, caches=[cache(v=A16 + step_, ks=at, vs=at + scales - 16, kv_type=1)]) == PI_ERR_SHAPE
+    assert keep(lib, caches=[cache(v=A16 + step_, ks=at - 16, vs=at + scales, kv_type=2)]) == PI_ERR_SHAPE
     assert keep(lib, caches=[cache(Hkv=65535, n_pages=1)], b=batch(B=1 << 20)) == PI_ERR_UNSUPPORTED
 
 
@@ -237,6 +249,8 @@ def test_rotary_binding(calls):
     q, k = pa.rotary_bwd(torch.zeros(2, 4, 5, 64), None, r, pos=ints(2, 5))
     a = calls["rotary"]
     assert k is None and a[9] == 0 and a[12:14] == (1, 1) and a[5]
+    pa.rotary(x[:, :0], x[:, 4:6], r)  # (for the call to refuse)
+    assert calls["rotary"][8:10] == (0, 2)
     f = torch.zeros(2, 4, 5, 64)
     for bad in (dict(q=f.double()), dict(q=f[0]), dict(q=f[..., ::2]), dict(q=f, k=f.bfloat16()), dict(q=f, k=f[:, :, :4]), dict(q=f, pos=ints(5)),
                 dict(q=f, pos=ints(2, 5).long()), dict(q=f, q_out=f[:, :3]), dict(q=f, k_out=f), dict(q=f, start=2 ** 40), dict(q=None)):
@@ -282,3 +296,28 @@ def test_step_binding(calls):
         with pytest.raises(ValueError):
             f()
     assert not calls
+
+
+def test_a_cache_goes_with_its_last_reference(calls):
+    """No cycle keeps pages until the collector runs, also not once their rows were moved."""
+    c = pa.PagedCache(torch.zeros(2, 2, 16, 64, dtype=torch.bfloat16), torch.zeros(2, 2, 16, 64, dtype=torch.bfloat16))
+    pages, layers = weakref.ref(c), pa.CacheLayers([c])
+    for x in (c, layers):
+        pa.cache_keep(x, ints(3, 4), ints(4), ints(3), ints(5), ints(3))
+        assert calls["cache_keep"][1] == 1 and paged._CacheStruct.from_address(calls["cache_keep"][0]).k == c.k.data_ptr()
+    gc.disable()
+    try:
+        del x, c, layers
+        assert pages() is None
+    finally:
+        gc.enable()
+
+
+def test_tensors_on_the_host_are_refused(monkeypatch):
+    """With another device current (a call that would change to theirs and look again)."""
+    for m in (paged, step):
+        monkeypatch.setattr(m, "_current_device", lambda: 0)
+    for f in (lambda: pa.rotary(torch.zeros(1, 1, 2, 32), None, pa.Rotary(32, device="cpu")),
+              lambda: pa.verify_tree(torch.zeros(2, 3), None, ints(2), ints(2), ints(2), torch.zeros(2), torch.zeros(1))):
+        with pytest.raises(ValueError, match="CUDA device"):
+            f()
