@@ -12,6 +12,10 @@
 // A running sum is compared with a random number: an error in it would pick a neighbour's token as often as it is large.  fp32 sums over
 // 10^5 tokens would do that once in a hundred calls.  Products and sums are carried in pairs of fp32 (48 bits), two tokens to an
 // instruction: a dependent fp64 operation takes 75 cycles on a GB300, the sum of two pairs 37.
+//
+// What bounds it: few sequences, the chain gather (0.8 us) -> tests (0.2 each; 0.4 where siblings were refused) -> pass (1.7) -> search (1.7); 32 trees
+// over 128001 tokens (29.0 us), their passes one after the other: 6 us the first, whose rows come from HBM, 4.5 the others, about as much
+// arithmetic (25 packed instructions for two tokens) as traffic: the rows kept in shared memory from pass to pass changed nothing (30.7 for 30.2).
 #include "pi_mma.cuh"
 #include "pi_paged.cuh"
 #include "pi_step.h"
@@ -19,8 +23,13 @@
 namespace pi {
 namespace verify {
 
-constexpr int THREADS = 512, WARPS = THREADS / 32;
+// Eight warps, each with 32 loads per lane in flight: the walk and the searches are made by every warp alike and share the SM's issue slots (16
+// warps with 16 loads: 6 drafted tokens of 32000 7.3 instead of 6.7 us, 16 trees of chosen tokens over 50257 12.0 instead of 10.3, 32 trees
+// over 128001 the same; 4 warps: 8.3, 23, 36).
+constexpr int THREADS = 256, WARPS = THREADS / 32;
+static_assert(THREADS >= kTreeMax, "a node to a thread");
 constexpr int MAX_P = 8;  // CTAs per cluster (portable limit)
+constexpr int HELD = 8;   // tokens that a lane holds in the search, at most
 constexpr unsigned kFull = 0xffffffffu;
 
 // A number as an unevaluated sum of two fp32.
@@ -80,6 +89,7 @@ struct Weights {
 struct Shared {
     int parent[kTreeMax], token[kTreeMax];
     float u[kTreeMax], p[kTreeMax], q[kTreeMax];  // of each node: its random number, its probabilities at its parent
+    bool first[kTreeMax];  // whether it is accepted as its parent's first child (a = 0, s = 1)
     int path[kTreeMax], removed[kTreeMax];
     Pair all[2][MAX_P * WARPS];  // the sums of the cluster's warps, of this pass and the one before
 };
@@ -89,12 +99,20 @@ __device__ __forceinline__ bool is_removed(const Weights &w, const Shared &sh, i
     for (int r = 0; r < w.removed; ++r) gone = gone || sh.removed[r] == v;
     return gone;
 }
-__device__ __forceinline__ Pair weight(const Weights &w, const Shared &sh, int v) {
-    const float p = sane(ld_now(w.p + v));
+// The number of tokens to look at for those without a weight, or 0 where none of lo .. hi - 1 is one.  For the whole warp.
+__device__ __forceinline__ int removed_in(const Weights &w, const Shared &sh, int lo, int hi) {
+    bool some = false;
+    for (int r = threadIdx.x & 31; r < w.removed; r += 32) some = some || (sh.removed[r] >= lo && sh.removed[r] < hi);
+    return __any_sync(kFull, some) ? w.removed : 0;
+}
+// The weight of token v with probabilities p and q.
+__device__ __forceinline__ Pair weight(const Weights &w, const Shared &sh, int v, float p, float q) {
+    p = sane(p);
     if (is_removed(w, sh, v)) return Pair{0.f, 0.f};
     if (!w.q) return Pair{p, 0.f};
     // (as in sum_of, so that a part whose sum is above 0 has a token with a weight)
-    const float q = sane(ld_now(w.q + v)), d = fmaf(-w.a.hi, q, p), t = __fsub_rn(p, d), r = __fsub_rn(__fsub_rn(p, t), d);
+    q = sane(q);
+    const float d = fmaf(-w.a.hi, q, p), t = __fsub_rn(p, d), r = __fsub_rn(__fsub_rn(p, t), d);
     if (!(d > 0.f)) return Pair{0.f, 0.f};
     const Pair x = add(Pair{d, fmaf(-w.a.lo, q, __fadd_rn(fmaf(-w.a.hi, q, t), r))}, Pair{0.f, 0.f});
     return positive(x) ? x : Pair{0.f, 0.f};
@@ -103,11 +121,9 @@ __device__ __forceinline__ Pair weight(const Weights &w, const Shared &sh, int v
 // The sum of the weights of tokens lo .. hi - 1, over the warp; AHEAD tokens per lane in flight.
 template <bool DRAFT>
 __device__ __forceinline__ Pair sum_of(const Weights &w, const Shared &sh, int lo, int hi) {
-    constexpr int AHEAD = DRAFT ? 8 : 16;
+    constexpr int AHEAD = DRAFT ? 16 : 32;
     const int lane = threadIdx.x & 31;
-    bool some = false;  // a token without a weight among these
-    for (int r = lane; r < w.removed; r += 32) some = some || (sh.removed[r] >= lo && sh.removed[r] < hi);
-    const int removed = __any_sync(kFull, some) ? w.removed : 0;
+    const int removed = removed_in(w, sh, lo, hi);
     const float *pp = w.p, *qq = w.q;
     Two hi2(0.f, 0.f), lo2(0.f, 0.f);
     const Two na_hi(-w.a.hi, -w.a.hi), na_lo(-w.a.lo, -w.a.lo);
@@ -165,21 +181,21 @@ __device__ __forceinline__ Pair sum_of(const Weights &w, const Shared &sh, int l
 }
 
 __device__ __forceinline__ Pair from_lane(const Pair &x, int lane) { return Pair{__shfl_sync(kFull, x.hi, lane), __shfl_sync(kFull, x.lo, lane)}; }
-// run + the sum over the lanes up to and including this one.  (A lane without a lane so far below it adds 0: with a branch around the
-// addition the five steps take 670 cycles instead of 320.)
-__device__ __forceinline__ Pair upto_lane(Pair x, const Pair &run) {
+// The sum over the lanes up to and including this one, of the first N.  (A lane without a lane so far below it adds 0: with a branch
+// around the addition the five steps take 670 cycles instead of 320.)
+template <int N>
+__device__ __forceinline__ Pair upto_lane(Pair x) {
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
+    for (int d = 1; d < N; d <<= 1) {
         const float hi = __shfl_up_sync(kFull, x.hi, d), lo = __shfl_up_sync(kFull, x.lo, d);
         const bool in = (int)(threadIdx.x & 31) >= d;
         x = add(x, Pair{in ? hi : 0.f, in ? lo : 0.f});
     }
-    return add(run, x);
+    return x;
 }
-// Of the lanes' numbers m (>= 0), the one in which the running sum passes `goal`, `run` being in front of them: the first lane past it,
-// or (where rounding left the goal past them all) the last one above 0; -1: none is.  run: the sum in front of it.
-__device__ __forceinline__ int find_lane(const Pair &m, const Pair &goal, Pair &run) {
-    const Pair here = upto_lane(m, run);
+// Of the lanes' numbers m (>= 0), the one in which the running sum `here` passes `goal`: the first lane past it, or (where
+// rounding left the goal past them all) the last one above 0; -1: none is.  run: the sum in front of it (before: of lane 0).
+__device__ __forceinline__ int find_lane(const Pair &m, const Pair &here, const Pair &goal, Pair &run) {
     const unsigned past = __ballot_sync(kFull, positive(m) && less(goal, here)), some = __ballot_sync(kFull, positive(m));
     if (!some) return -1;
     const int x = past ? __ffs(past) - 1 : 31 - __clz(some);
@@ -187,36 +203,34 @@ __device__ __forceinline__ int find_lane(const Pair &m, const Pair &goal, Pair &
     if (x > 0) run = before;
     return x;
 }
-// The same of n numbers get(0), get(1), ..., `per` consecutive ones to a lane.
-template <typename F>
-__device__ __forceinline__ int find(int n, int per, F get, const Pair &goal, Pair &run) {
-    const int first = (int)(threadIdx.x & 31) * per;
-    Pair m{0.f, 0.f};
-#pragma unroll 1
-    for (int i = first; i < min(first + per, n); ++i) m = add(m, get(i));
-    const int x = find_lane(m, goal, run);
-    if (x < 0 || per == 1) return x;
+// The same of 32 * per numbers m, per <= MOST consecutive ones to a lane, whose sum `all` is.
+template <int MOST>
+__device__ __forceinline__ int find_held(const Pair (&m)[MOST], int per, const Pair &all, const Pair &here, const Pair &goal, Pair &run) {
+    const int x = find_lane(all, here, goal, run);
+    if (x < 0) return x;
     int at = -1;
     Pair upto = run;
-#pragma unroll 1
-    for (int i = x * per; i < min(x * per + per, n); ++i) {  // the lane's numbers, by all lanes alike
-        const Pair y = get(i);
-        if (!positive(y)) continue;
-        at = i;
-        run = upto;
-        upto = add(upto, y);
-        if (less(goal, upto)) break;
+#pragma unroll
+    for (int i = 0; i < MOST; ++i) {  // that lane's numbers, by all lanes alike
+        if (i >= per) break;
+        const Pair y = from_lane(m[i], x);
+        const bool next = positive(y) && (at < 0 || !less(goal, upto));
+        const Pair more = add(upto, y);
+        at = next ? x * per + i : at;
+        run = next ? upto : run;
+        upto = next ? more : upto;
     }
     return at;
 }
 
-__global__ void __launch_bounds__(THREADS, 2) verify_kernel(const __grid_constant__ VerifyArgs a, int P) {
+__global__ void __launch_bounds__(THREADS, 2) verify_kernel(const __grid_constant__ VerifyArgs a, int P, int part) {
     __shared__ Shared sh;
     const int rank = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     asm volatile("griddepcontrol.launch_dependents;");
     cluster_arrive();  // (before a CTA writes into another's shared memory, that one has to run)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int t0 = ld_now(a.cu + b), t1 = ld_now(a.cu + b + 1), n = t1 - t0;
+    const float u_next = ld_now(a.u_next + b);
     bool ok = t0 >= 0 && t0 <= t1 && t1 <= a.T && n <= kTreeMax;
     if (ok && tid < n) {
         const int parent = ld_now(a.parent + t0 + tid), token = ld_now(a.tokens + t0 + tid);
@@ -224,9 +238,12 @@ __global__ void __launch_bounds__(THREADS, 2) verify_kernel(const __grid_constan
         sh.parent[tid] = parent;
         sh.token[tid] = token;
         if (ok && parent >= 0) {
-            sh.u[tid] = unit(ld_now(a.u + t0 + tid));
-            sh.p[tid] = sane(ld_now(a.target + (long long)(t0 + parent) * a.target_stride + token));
-            sh.q[tid] = a.draft ? sane(ld_now(a.draft + (long long)(t0 + parent) * a.draft_stride + token)) : 1.f;
+            const float u = unit(ld_now(a.u + t0 + tid)), p = sane(ld_now(a.target + (long long)(t0 + parent) * a.target_stride + token));
+            const float q = a.draft ? sane(ld_now(a.draft + (long long)(t0 + parent) * a.draft_stride + token)) : 1.f;
+            sh.u[tid] = u;
+            sh.p[tid] = p;
+            sh.q[tid] = q;
+            sh.first[tid] = less(mul(Pair{u, 0.f}, Pair{q, 0.f}), Pair{p, 0.f});
         }
     }
     ok = __syncthreads_and(ok);
@@ -239,11 +256,10 @@ __global__ void __launch_bounds__(THREADS, 2) verify_kernel(const __grid_constan
         }
         return;
     }
-    const int share = ((a.V + P - 1) / P + WARPS * 32 - 1) & ~(WARPS * 32 - 1), part = share / WARPS;
+    const int share = part * WARPS;
     auto part_lo = [&](int i) -> int { return (int)min((long long)a.V, (long long)(i / WARPS) * share + (i % WARPS) * part); };
     auto part_hi = [&](int i) -> int { return (int)min((long long)a.V, (long long)part_lo(i) + part); };
 
-    const Pair u_next{unit(ld_now(a.u_next + b)), 0.f};
     // node 0's rows, which the first pass most often reads
     for (int v = part_lo(rank * WARPS) + 32 * tid; v < part_hi(rank * WARPS + WARPS - 1); v += 32 * THREADS) {
         asm volatile("prefetch.global.L2 [%0];" ::"l"(a.target + t0 * a.target_stride + v));
@@ -254,6 +270,8 @@ __global__ void __launch_bounds__(THREADS, 2) verify_kernel(const __grid_constan
     int x = 0, last = 0, len = 1, passes = 0;
     Weights w{};
     Pair s{1.f, 0.f};
+    constexpr int PER = MAX_P * WARPS / 32;
+    Pair parts[PER], mine, here;  // of the last pass: PER warps' sums, their sum, and that of all up to them
     bool summed = false, spent = false;  // the weights' sum is known; it is 0, and p's own is asked for
     if (lane == 0) sh.path[0] = 0;
     for (;;) {
@@ -267,15 +285,21 @@ __global__ void __launch_bounds__(THREADS, 2) verify_kernel(const __grid_constan
             if (c == kTreeMax) break;
             last = c;
             Pair left{sh.p[c], 0.f};
-            if (a.draft) {
-                left = sub(left, mul(w.a, Pair{sh.q[c], 0.f}));
-            } else if (w.removed > 0) {  // the same token, chosen twice
-                bool gone = false;
-                for (int r = x + 1 + lane; r < c; r += 32) gone = gone || (sh.parent[r] == x && sh.token[r] == sh.token[c]);
-                if (__any_sync(kFull, gone)) left = Pair{0.f, 0.f};
+            bool yes;
+            if (a.draft ? !positive(w.a) : w.removed == 0) {
+                yes = sh.first[c];
+            } else {
+                if (a.draft) {
+                    left = sub(left, mul(w.a, Pair{sh.q[c], 0.f}));
+                } else {  // the same token, chosen twice
+                    bool gone = false;
+                    for (int r = x + 1 + lane; r < c; r += 32) gone = gone || (sh.parent[r] == x && sh.token[r] == sh.token[c]);
+                    if (__any_sync(kFull, gone)) left = Pair{0.f, 0.f};
+                }
+                yes = positive(left) && less(mul(mul(Pair{sh.u[c], 0.f}, Pair{sh.q[c], 0.f}), s), left);
             }
             summed = false;
-            if (positive(left) && less(mul(mul(Pair{sh.u[c], 0.f}, Pair{sh.q[c], 0.f}), s), left)) {
+            if (yes) {
                 x = c;
                 if (lane == 0) sh.path[len] = c;
                 ++len;
@@ -317,10 +341,13 @@ __global__ void __launch_bounds__(THREADS, 2) verify_kernel(const __grid_constan
         if (lane < P) st_peer2(peer_addr(smem_addr(&all[i]), lane), make_float2(t.hi, t.lo));
         cluster_sync();
         ++passes;
-        s = Pair{0.f, 0.f};
-#pragma unroll 1
-        for (int k = lane; k < P * WARPS; k += 32) s = add(s, all[k]);
-        s = warp_sum(s);
+#pragma unroll
+        for (int k = 0; k < PER; ++k) parts[k] = lane * PER + k < P * WARPS ? all[lane * PER + k] : Pair{0.f, 0.f};
+        mine = parts[0];
+#pragma unroll
+        for (int k = 1; k < PER; ++k) mine = add(mine, parts[k]);
+        here = upto_lane<32>(mine);
+        s = from_lane(here, 31);
         summed = true;
     }
 
@@ -329,25 +356,65 @@ __global__ void __launch_bounds__(THREADS, 2) verify_kernel(const __grid_constan
         for (int j = tid; j < n; j += THREADS) a.path[t0 + j] = j < len ? sh.path[j] : -1;  // (a warp's own writes)
         if (tid == 0) a.count[b] = len;
     }
-    const Pair *all = sh.all[(passes - 1) & 1], goal = mul(u_next, s);
+    const Pair goal = mul(Pair{unit(u_next), 0.f}, s);
     Pair run{0.f, 0.f};
-    const int at = find(P * WARPS, (P * WARPS + 31) / 32, [&](int i) { return all[i]; }, goal, run);  // by every warp alike
+    const int at = find_held<PER>(parts, PER, mine, here, goal, run);  // by every warp alike
     if (at < 0) {
         if (tid == 0 && rank == 0) a.next[b] = -1;
-    } else if (at / WARPS == rank) {  // this CTA has it: a piece of that part per warp, token by token
-        const int hi = part_hi(at), piece = part / WARPS, per = (piece + 31) / 32, from = part_lo(at) + warp * piece, n_mine = min(from + piece, hi) - from;
-        auto token = [&](int i) { return weight(w, sh, from + i); };
-        Pair m{0.f, 0.f};
-#pragma unroll 2
-        for (int i = lane * per; i < min(lane * per + per, n_mine); ++i) m = add(m, token(i));
-        m = warp_sum(m);
+    } else if (at / WARPS == rank) {  // this CTA has it: a piece of that part per warp, a few tokens of it to a lane
+        const int hi = part_hi(at), piece = part / WARPS, from = part_lo(at) + warp * piece, n_mine = min(from + piece, hi) - from;
+        const int per = min(HELD, (piece + 31) / 32);
+        const bool held = piece <= 32 * HELD;
+        w.removed = removed_in(w, sh, from, from + n_mine);
+        // tokens lo + lane * per ... of the warp's, as far as its end: their weights, all of them under way at once
+        Pair m[HELD], sum;
+        auto hold = [&](int lo) {
+            float p[HELD], q[HELD];
+#pragma unroll
+            for (int i = 0; i < HELD; ++i) {
+                const int v = lo + lane * per + i;
+                const bool in = i < per && v < n_mine;
+                p[i] = in ? ld_now(w.p + from + v) : 0.f;
+                q[i] = in && w.q ? ld_now(w.q + from + v) : 0.f;
+            }
+            sum = Pair{0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < HELD; ++i) {
+                if (i >= per) break;
+                m[i] = weight(w, sh, from + lo + lane * per + i, p[i], q[i]);
+                sum = add(sum, m[i]);
+            }
+            here = upto_lane<32>(sum);
+        };
+        if (held) {
+            hold(0);
+            mine = from_lane(here, 31);
+        } else {
+            mine = w.q ? sum_of<true>(w, sh, from, from + n_mine) : sum_of<false>(w, sh, from, from + n_mine);
+        }
         Pair *sums = sh.all[passes & 1];  // (its last readers are past the last pass)
-        if (lane == 0) sums[warp] = m;
+        if (lane == 0) sums[warp] = mine;
         __syncthreads();
-        const int in = find(WARPS, 1, [&](int i) { return sums[i]; }, goal, run);
+        const Pair its = lane < WARPS ? sums[lane] : Pair{0.f, 0.f};
+        const int in = find_lane(its, add(run, upto_lane<WARPS>(its)), goal, run);
         if (max(in, 0) == warp) {
-            const int x = find(n_mine, per, token, goal, run);
-            if (lane == 0) a.next[b] = from + max(x, 0);  // (there is one; else the part's first token)
+            int lo = 0, x = 0;
+            if (!held) {  // the 32 * HELD tokens that hold it, or the last ones above 0 (rounding left the goal past them all)
+                Pair upto = run;
+#pragma unroll 1
+                for (int t = 0; t < n_mine; t += 32 * HELD) {
+                    hold(t);
+                    const Pair y = from_lane(here, 31);
+                    if (!positive(y)) continue;
+                    lo = t;
+                    run = upto;
+                    upto = add(upto, y);
+                    if (less(goal, upto)) break;
+                }
+                hold(lo);
+            }
+            x = find_held<HELD>(m, per, sum, add(run, here), goal, run);
+            if (lane == 0) a.next[b] = from + lo + max(x, 0);  // (there is one; else the first)
         }
     }
     cluster_leave();  // a CTA's shared memory stays until the others have read it
@@ -374,7 +441,8 @@ cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t st) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, verify_kernel, a, P);
+    const int part = ((a.V + P - 1) / P + WARPS * 32 - 1) / (WARPS * 32) * 32;  // tokens of a warp
+    return cudaLaunchKernelEx(&cfg, verify_kernel, a, P, part);
 }
 
 }  // namespace pi

@@ -398,6 +398,17 @@ def test_verify_tree(case):
         check_verify(*s, run_verify(*s))
 
 
+@pytest.mark.parametrize("case", [([4, 9, 1], 150001, True, 1.0), ([9, 4], 150001, False, 1.0), ([2] * 160, 40001, True, 1.5)],
+                         ids=["cluster", "cluster-chosen", "one"])
+def test_verify_tree_whose_search_takes_a_warp_several_rounds(case):
+    """More than 256 tokens of the vocabulary to a warp in the last step of the search, over a cluster of CTAs and over one."""
+    s = list(verify_case(*case, seed=4, spread=0.5))
+    for u_next in (None, torch.zeros(len(case[0])), torch.full((len(case[0]),), 1 - 2.0 ** -24)):
+        if u_next is not None:
+            s[6] = u_next
+        check_verify(*s, run_verify(*s))
+
+
 def test_verified_tokens_are_distributed_as_the_target():
     """A token drawn from q and its random numbers on a grid: the first new token's frequencies are p."""
     p, q, g = torch.tensor([0.1, 0.5, 0.0, 0.3, 0.1]), torch.tensor([0.4, 0.1, 0.2, 0.2, 0.1]), 50
