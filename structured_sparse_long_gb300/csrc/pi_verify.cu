@@ -14,8 +14,9 @@
 // instruction: a dependent fp64 operation takes 75 cycles on a GB300, the sum of two pairs 37.
 //
 // What bounds it: few sequences, the chain gather (0.8 us) -> tests (0.2 each; 0.4 where siblings were refused) -> pass (1.7) -> search (1.7); 32 trees
-// over 128001 tokens (29.0 us), their passes one after the other: 6 us the first, whose rows come from HBM, 4.5 the others, about as much
-// arithmetic (25 packed instructions for two tokens) as traffic: the rows kept in shared memory from pass to pass changed nothing (30.7 for 30.2).
+// over 128001 tokens (29.0 us), their passes one after the other: 6 us the first, whose rows come from HBM, 4.5 the others, in which warps wait
+// for loads and at the cluster's barrier (issue slots are 22 % busy, HBM 17 %).  The rows kept in shared memory from pass to pass changed
+// nothing (30.7 for 30.2), nor did two sets of registers in turn (30.2 for 28.9).
 #include "pi_mma.cuh"
 #include "pi_paged.cuh"
 #include "pi_step.h"
@@ -425,7 +426,7 @@ __global__ void __launch_bounds__(THREADS, 2) verify_kernel(const __grid_constan
 cudaError_t launch_verify(const VerifyArgs &a, cudaStream_t st) {
     using namespace verify;
     // as many CTAs per sequence as leave each at least 1024 tokens of the vocabulary and, at two CTAs per SM, run at once (clusters do
-    // not fill every SM)
+    // not fill every SM; at one per SM 32 trees over 128001 tokens took 43.0 us for 29.1)
     int P = 1;
     while (P < MAX_P && a.V / (2 * P) >= 1024 && (long long)a.B * 2 * P <= 2LL * sm_count() - 16) P *= 2;
     cudaLaunchConfig_t cfg = {};
