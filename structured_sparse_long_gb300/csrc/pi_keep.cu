@@ -37,7 +37,7 @@ __global__ void __launch_bounds__(THREADS) keep_kernel(const __grid_constant__ K
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int t0 = ld_now(a.batch.cu + b), t1 = ld_now(a.batch.cu + b + 1), ctx = ld_now(a.batch.ctx + b), n = ld_now(a.count + b);
     bool ok = sequence_ok(c, a.batch, t0, t1, ctx) && n >= 0 && n <= t1 - t0;
-    // row j of the path: whether it follows the one before it, and (first: this round's) where it lies
+    // row j of the path: whether it follows the one before it, and (place) where it lies
     auto look = [&](int j, bool place) -> bool {
         const int x = ld_now(a.path + t0 + j), before = j > 0 ? ld_now(a.path + t0 + j - 1) : -1;
         if (x <= before || x >= t1 - t0) return false;
