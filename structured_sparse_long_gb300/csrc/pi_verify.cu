@@ -155,6 +155,11 @@ __device__ __forceinline__ Pair sum_of(const Weights &w, const Shared &sh, int l
             hi2 = s;
             lo2 = lo2 + (DRAFT ? err + rest : err);
         }
+        // the low words back below half a step of the high ones: left to grow over a row they would be rounded ever coarser (2^26 equal
+        // tokens: 10^-6 off)
+        const Two s = hi2 + lo2;
+        lo2 = lo2 - (s - hi2);
+        hi2 = s;
     };
     int v0 = lo + lane;
 #pragma unroll 1
