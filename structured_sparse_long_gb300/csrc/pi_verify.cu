@@ -114,7 +114,6 @@ __device__ __forceinline__ Pair weight(const Weights &w, const Shared &sh, int v
     // (as in sum_of, so that a part whose sum is above 0 has a token with a weight)
     q = sane(q);
     const float d = fmaf(-w.a.hi, q, p), t = __fsub_rn(p, d), r = __fsub_rn(__fsub_rn(p, t), d);
-    if (!(d > 0.f)) return Pair{0.f, 0.f};
     const Pair x = add(Pair{d, fmaf(-w.a.lo, q, __fadd_rn(fmaf(-w.a.hi, q, t), r))}, Pair{0.f, 0.f});
     return positive(x) ? x : Pair{0.f, 0.f};
 }
@@ -141,11 +140,12 @@ __device__ __forceinline__ Pair sum_of(const Weights &w, const Shared &sh, int l
         for (int i = 0; i < AHEAD; i += 2) {
             Two x(sane(p[i]), sane(p[i + 1])), rest(0.f, 0.f);
             if (DRAFT) {
-                // d = p - a q rounded, and what that left: p - d = t + r exactly where d > 0 (then d <= p), and t is a q up to d's rounding
+                // d = p - a q rounded, and what that left: p - d = t + r exactly where |d| <= p, and t is a q up to d's rounding.  The weight
+                // is above 0 where d + rest is (d alone says so only down to 2^-24 of p, where p is a q up to a's low part)
                 const Two y(sane(q[i]), sane(q[i + 1])), d = fma(na_hi, y, x), t = x - d, r = (x - t) - d;
                 rest = fma(na_lo, y, fma(na_hi, y, t) + r);
                 float s0, s1;
-                tc::unpack2(d.v, s0, s1);
+                tc::unpack2((d + rest).v, s0, s1);
                 const Two keep(s0 > 0.f ? 1.f : 0.f, s1 > 0.f ? 1.f : 0.f);
                 x = d * keep;
                 rest = rest * keep;
