@@ -195,9 +195,10 @@ def cache_keep(cache, table, cu, ctx, path, count, stream=None, check=False) -> 
             return cache_keep(cache, table, cu, ctx, path, count, None, check)
     handle = cache._handle
     if isinstance(cache, PagedCache):
-        if cache._layers is None:
-            cache._layers = _layers((cache,))
-        handle = ctypes.addressof(cache._layers)
+        alone = cache._layers  # (held by this call: another thread's first one may put its own in the cache's place meanwhile)
+        if alone is None:
+            alone = cache._layers = _layers((cache,))
+        handle = ctypes.addressof(alone)
     rc = (paged._native or _load_native()).keep(handle, table, cu, ctx, path, count, _raw_stream(cache.index))
     if rc or check:
         _check("pi_attn_cache_keep", rc, None, check)

@@ -1,0 +1,74 @@
+"""Host tests of what the step's binding keeps alive while a call, or a stream, still reads it."""
+import ctypes
+import threading
+import weakref
+
+import pytest
+import torch
+
+import structured_sparse_long_gb300 as pa
+from structured_sparse_long_gb300 import build as pbuild
+from structured_sparse_long_gb300 import paged, step
+
+
+@pytest.fixture
+def native(monkeypatch):
+    """The extension module with the step's C functions as a test gives them (`native(rotary=..., cache_keep=...)`), on host tensors."""
+    pbuild.build()
+    paged._load()
+    monkeypatch.setattr(paged._binding, "_expect_like", lambda t, name, like, dtype, shape: None)
+    for m in (paged, step):
+        monkeypatch.setattr(m, "_current_device", lambda: -1)
+        monkeypatch.setattr(m, "_raw_stream", lambda index: 0)
+    P, I, L, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.CFUNCTYPE
+    types = dict(rotary=(P, P, P, P, P, P, I, I, I, I, I, I, I, I, P, P, P, P, P), rotary_append=(P, L, P, L, P, L, P, P, P, P, I, P, L, P),
+                 extend_tree=(P, L, P, P, P, P, I, I, I, I, I, P, P, P), verify_tree=(P, L, P, L, P, P, P, P, P, I, I, I, P, P, P, P),
+                 cache_keep=(P, I, P, P, P, P))
+    held = []
+
+    def bind(**given):
+        for name, t in types.items():
+            held.append(F(I, *t)(given.get(name, lambda *a: 0)))
+        paged._load_native().bind_step(*(ctypes.cast(f, P).value for f in held[-len(types):]))
+
+    yield bind
+    monkeypatch.setattr(paged, "_native", None)
+    paged._load_native()
+
+
+def ints(*shape):
+    return torch.zeros(*shape, dtype=torch.int32)
+
+
+def pages(*shape):
+    return torch.zeros(*shape, dtype=torch.bfloat16)
+
+
+def test_two_threads_keep_paths_in_a_cache_for_the_first_time(native, monkeypatch):
+    """Both make the cache's descriptor before either has stored it, and then both are in the library: what each reads there is alive."""
+    made, both_made, both_in, dead, seen = [], threading.Barrier(2), threading.Barrier(2), [], []
+    own = step._layers
+
+    def layers(caches):
+        s = own(caches)
+        made.append(weakref.ref(s))
+        both_made.wait(5)
+        return s
+
+    def keep(caches, n, *rest):
+        both_in.wait(5)
+        dead.append(sum(r() is None for r in made))
+        seen.append(paged._CacheStruct.from_address(caches).k)
+        both_in.wait(5)
+        return 0
+
+    native(cache_keep=keep)
+    monkeypatch.setattr(step, "_layers", layers)
+    c = pa.PagedCache(pages(2, 2, 16, 64), pages(2, 2, 16, 64))
+    args = (ints(3, 4), ints(4), ints(3), ints(5), ints(3))
+    threads = [threading.Thread(target=pa.cache_keep, args=(c, *args)) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert dead == [0, 0] and seen == [c.k.data_ptr()] * 2
