@@ -78,7 +78,9 @@ def rotary_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", f
 class Rotary:
     """Frequencies of rotary positions on a device: a row's first `rot` elements turn in pairs, (t, t + rot / 2) or, interleaved,
     (2 t, 2 t + 1).  Frequencies from :func:`rotary_frequencies`, or given in radians per position (`freqs`, rot / 2 of them);
-    `scale` multiplies the turned elements (default: the scaling's own factor)."""
+    `scale` multiplies the turned elements (default: the scaling's own factor).
+    Its device memory is not handed out again before calls enqueued with it are done, whatever their stream; a captured graph
+    of such calls reads it at every replay, so keep the object as long as the graph."""
 
     def __init__(self, rot: int, base: float = 10000.0, interleaved: bool = False, scaling: str = "none", factor: float = 1.0,
                  original: int = 0, low: float = 1.0, high: float = 32.0, freqs: Optional[Sequence[float]] = None,
@@ -99,6 +101,12 @@ class Rotary:
         self.device, self.index = self.steps.device, self.steps.get_device()
         self._struct = _Rope(_RotaryStruct(self.steps.data_ptr(), rot, int(self.interleaved), self.scale), self.index)
         self._handle = ctypes.addressof(self._struct)
+        self._streams = {_raw_stream(self.index)} if self.index >= 0 else {0}  # that the allocator knows to read the steps
+
+    def _used_on(self, raw: int) -> None:
+        """The steps are about to be read on the current stream, `raw`, which is not the one that they were made on."""
+        self.steps.record_stream(torch.cuda.current_stream(self.index))
+        self._streams.add(raw)
 
 
 class CacheLayers:
@@ -124,7 +132,10 @@ def _turn(q, k, rope, start, pos, q_out, k_out, back, stream, check):
     if stream is not None or rope.index != _current_device():
         with _place(rope, stream):
             return _turn(q, k, rope, start, pos, q_out, k_out, back, None, check)
-    rc, q_out, k_out = (paged._native or _load_native()).rotary(q, k, rope._handle, start, pos, q_out, k_out, back, _raw_stream(rope.index))
+    raw = _raw_stream(rope.index)
+    if raw not in rope._streams:
+        rope._used_on(raw)
+    rc, q_out, k_out = (paged._native or _load_native()).rotary(q, k, rope._handle, start, pos, q_out, k_out, back, raw)
     if rc or check:
         _check("pi_attn_rotary", rc, None, check)
     return q_out, k_out
@@ -149,8 +160,10 @@ def rotary_append(q, k, v, rope: Rotary, cache: PagedCache, table, cu, ctx, pare
     if stream is not None or cache.index != _current_device():
         with _place(cache, stream):
             return rotary_append(q, k, v, rope, cache, table, cu, ctx, parent, q_out, None, check)
-    rc, q_out = (paged._native or _load_native()).rotary_append(q, k, v, rope._handle, cache._handle, table, cu, ctx, parent, q_out,
-                                                                _raw_stream(cache.index))
+    raw = _raw_stream(cache.index)
+    if raw not in rope._streams and rope.index == cache.index:  # (else the call refuses it)
+        rope._used_on(raw)
+    rc, q_out = (paged._native or _load_native()).rotary_append(q, k, v, rope._handle, cache._handle, table, cu, ctx, parent, q_out, raw)
     if rc or check:
         _check("pi_attn_rotary_append", rc, None, check)
     return q_out

@@ -72,3 +72,31 @@ def test_two_threads_keep_paths_in_a_cache_for_the_first_time(native, monkeypatc
     for t in threads:
         t.join()
     assert dead == [0, 0] and seen == [c.k.data_ptr()] * 2
+
+
+def test_a_rotarys_steps_are_known_to_every_stream_that_reads_them(native, monkeypatch):
+    """Else the allocator hands their memory out again once the object is gone, although another stream's call has yet to read it.  Once for
+    each stream, and not for the one that they were made on."""
+    native()
+    r = pa.Rotary(32, device="cpu")
+    known, raw = [], [0]
+
+    class Steps:
+        def record_stream(self, stream):
+            known.append(stream)
+
+    r.steps = Steps()
+    monkeypatch.setattr(step, "_raw_stream", lambda index: raw[0])
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda index=None: raw[0])
+    x = pages(5, 8, 64)
+    c = pa.PagedCache(pages(2, 2, 16, 64), pages(2, 2, 16, 64))
+    calls = (lambda: pa.rotary(pages(1, 2, 3, 64), None, r), lambda: pa.rotary_bwd(pages(1, 2, 3, 64), None, r),
+             lambda: pa.rotary_append(x[:, :4], x[:, 4:6], x[:, 6:], r, c, ints(3, 4), ints(4), ints(3)))
+    for i, call in enumerate(calls):
+        raw[0] = 0
+        call()
+        assert known == list(range(1, i + 1))
+        raw[0] = i + 1
+        call()
+        call()
+        assert known == list(range(1, i + 2))
