@@ -1,11 +1,14 @@
 """GPU tests of rotary positions and of the speculative step at the ends of their ranges: sums over long rows, weights that are nearly
-nothing."""
+nothing, far positions, many trees, a rotary that goes while a stream still reads it."""
+import math
 from fractions import Fraction
 
 import numpy as np
 import pytest
 import torch
 
+import paged_ref as ref
+import step_ref as sref
 import structured_sparse_long_gb300 as pa
 from structured_sparse_long_gb300 import build as pbuild
 
@@ -23,6 +26,122 @@ def built():
 
 def dev(x):
     return torch.as_tensor(np.ascontiguousarray(x), dtype=torch.int32).cuda()
+
+
+# ------------------------------------------------------------------ rotary
+
+PI = Fraction(31415926535897932384626433832795028841971693993751, 10 ** 49)
+
+
+def turned(x, pos, r, sign):
+    """x [n, d] turned by pos [n], and the sum of a pair's magnitudes: as step_ref.rotate, but what is left of a turn is found in fractions."""
+    x = x.astype(np.float64)
+    y, size = x.copy(), np.zeros_like(x)
+    for t, f in enumerate(r.freqs):
+        a, b = (2 * t, 2 * t + 1) if r.interleaved else (t, t + r.rot // 2)
+        w = np.array([sign * 2 * math.pi * float(Fraction(f) * p / (2 * PI) % 1) for p in pos])
+        y[:, a] = r.scale * (x[:, a] * np.cos(w) - x[:, b] * np.sin(w))
+        y[:, b] = r.scale * (x[:, a] * np.sin(w) + x[:, b] * np.cos(w))
+        size[:, a] = size[:, b] = abs(r.scale) * (np.abs(x[:, a]) + np.abs(x[:, b]))
+    return y, size
+
+
+ENDS = [2 ** 31 - 1, -2 ** 31, 2 ** 31 - 2, 1 - 2 ** 31, 2 ** 30 + 1, -2 ** 30 - 1, 2 ** 24 + 1, -2 ** 24 - 1, 2 ** 21 + 1, 2 ** 16 - 1, -1, 0,
+        1234567891, -1987654321]
+
+
+@pytest.mark.parametrize("back", [False, True])
+@pytest.mark.parametrize("inter", [False, True])
+def test_rotary_at_both_ends_of_the_positions(inter, back):
+    """Given positions, and counted ones up to 2^31 - 1.  A step's rounding is 2^-65 turns per position, 2^-34 of a turn here: nothing beside
+    the slack."""
+    d, H, n = 64, 3, len(ENDS)
+    gen = torch.Generator().manual_seed(7)
+    r = pa.Rotary(d, 10000.0, interleaved=inter, scaling="linear", factor=0.7)  # the fastest pair above a radian per position
+    x = torch.randn(1, H, n, d, generator=gen)
+    call = pa.rotary_bwd if back else pa.rotary
+    for pos, start in ((ENDS, 0), (None, 2 ** 31 - n)):
+        y, _ = call(x.cuda(), None, r, start, None if pos is None else dev([pos]))
+        at = pos or list(range(start, 2 ** 31))
+        for h in range(H):
+            want, size = turned(x[0, h].numpy(), at, r, -1 if back else 1)
+            sref.check_rotated(f"head {h}", y[0, h].cpu().numpy().astype(np.float64), want, size, torch.finfo(torch.float32).eps)
+
+
+def test_a_rotary_that_goes_while_another_stream_still_reads_it():
+    """Its steps' memory is not handed out again before the calls enqueued with it are done."""
+    x = torch.randn(1, 2, 50, 64, device="cuda")
+    want, _ = pa.rotary(x, None, pa.Rotary(64), 3)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+    got, _ = pa.rotary(x, None, pa.Rotary(64), 3, stream=side)
+    others = [torch.full((32,), 1 << 60, dtype=torch.int64, device="cuda") for _ in range(100)]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and len(others) == 100
+
+
+# ------------------------------------------------------------------ trees
+
+def test_more_trees_than_a_launch_of_the_short_kernel_has_places():
+    """70000 single nodes of eight heads on one: a CTA takes one each, and a launch has 65535."""
+    B, H, d, page, ctx = 70000, 8, 64, 16, 3
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    cache = pa.PagedCache.empty(B, 1, page, d)
+    for t in (cache.k, cache.v):
+        t[:, :, :ctx + 1] = torch.randn(B, 1, ctx + 1, d, device="cuda", generator=gen).bfloat16()
+    table = torch.randperm(B, device="cuda", generator=gen, dtype=torch.int32)[:, None].contiguous()
+    q = torch.randn(B, H, d, device="cuda", generator=gen).bfloat16()
+    alpha = torch.rand(B, H, device="cuda", generator=gen) * 0.8 + 0.1
+    cu = torch.arange(B + 1, device="cuda", dtype=torch.int32)
+    args = (cache, table, cu, torch.full((B,), ctx, device="cuda", dtype=torch.int32), torch.full((B,), -1, device="cuda", dtype=torch.int32), alpha)
+    out, lse = pa.extend_tree(q, *args, 2, 3, 1)  # the band's keys 1, 2 and 3, and key 0 as a skip
+    k, v = (t[table[:, 0].long(), 0, :ctx + 1].double() for t in (cache.k, cache.v))
+    off = torch.stack([torch.log(1 - alpha.double())] + [torch.log(alpha.double())] * 3, -1)
+    z = torch.einsum("bhd,bkd->bhk", q.double(), k) / math.sqrt(d) + off
+    p = torch.softmax(z, -1)
+    want = (torch.einsum("bhk,bkd->bhd", p, v), torch.logsumexp(z, -1), torch.einsum("bhk,bkd->bhd", p, v.abs()))
+    ref.check_attention("trees", out, lse, [w.cpu().numpy() for w in want])
+    assert pa.status() == 0
+    bad = cu.clone()
+    bad[68001] = 5  # of the second launch's sequences one whose offsets decrease
+    pa.extend_tree(q, cache, table, bad, *args[3:], 2, 3, 1)
+    assert pa.status() == -8
+
+
+@pytest.mark.parametrize("trees", [1, 4])
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_a_tree_at_the_last_positions(kv, trees):
+    """The last rows that a page table reaches, 2^31 - 65536: appended and attended as the same tree is a whole number of pages earlier,
+    bit for bit (the frequencies are 0)."""
+    n, H, Hkv, d, page = 256 if trees > 1 else 20, 16, 4, 128, 256
+    width = 0x7fff0000 // page
+    ctx, kl, per, S = width * page - n, 300, 4096, 3
+    near = 64 * page - n
+    rng, gen = np.random.default_rng(trees), torch.Generator(device="cuda").manual_seed(trees)
+    parents = sum((sref.random_tree(n, rng) for _ in range(trees)), [])
+    T = trees * n
+    r = pa.Rotary(d, freqs=[0.0] * (d // 2))
+    x = torch.randn(T, H + 2 * Hkv, d, device="cuda", generator=gen).bfloat16()
+    alpha = torch.rand(T, H, device="cuda", generator=gen) * 0.8 + 0.1
+    results = []
+    for c, w in ((near, 64), (ctx, width)):
+        cache = pa.PagedCache.empty(64 * trees, Hkv, page, d, ref.DTYPE[kv])
+        table = torch.full((trees, w), -1, device="cuda", dtype=torch.int32)
+        table[:, w - 64:] = torch.arange(64 * trees, device="cuda", dtype=torch.int32).view(trees, 64)
+        fill = torch.Generator(device="cuda").manual_seed(5)
+        old = torch.randn(2, trees * 63 * page, Hkv, d, device="cuda", generator=fill).bfloat16()
+        rows = 63 * page  # (the last page: the tree's, behind what is filled here)
+        start = dev([(w - 64) * page] * trees)
+        pa.cache_append(old[0], old[1], cache, table, dev(np.arange(trees + 1) * rows), start)
+        cu, at, par = dev(np.arange(trees + 1) * n), dev([c] * trees), dev(parents)
+        q = pa.rotary_append(x[:, :H], x[:, H:H + Hkv], x[:, H + Hkv:], r, cache, table, cu, at, par)
+        assert torch.equal(q, x[:, :H])
+        results.append(pa.extend_tree(q, cache, table, cu, at, par, alpha, kl, per, S))
+    assert pa.status() == 0
+    (a, la), (b, lb) = results
+    assert torch.isfinite(a.float()).all() and torch.equal(a, b) and torch.equal(la, lb)
 
 
 # ------------------------------------------------------------------ verification
