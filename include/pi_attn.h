@@ -577,6 +577,13 @@ int pi_attn_debug_trace(const void *q, const void *k, const void *v, const float
  */
 int pi_attn_debug_wait_timeout(int timeout_us, void *stream);
 
+/*
+ * pi_attn_debug_tree_kernel -- which kernel pi_attn_extend_tree takes for these sizes on the current device: 0 the one that
+ * short chunks share, 1 the tensor cores' (tcgen05); or the error that the call would return for them.  Of the cache only its sizes,
+ * type and pointers' alignment matter.  Launches nothing.
+ */
+int pi_attn_debug_tree_kernel(const pi_attn_cache_t *cache, int B, int T, int width, int H, int k_local, int period, int S, int mode);
+
 #ifdef __cplusplus
 }
 #endif

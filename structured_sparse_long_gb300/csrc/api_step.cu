@@ -204,4 +204,18 @@ int pi_attn_cache_keep(const pi_attn_cache_t *caches, int n_caches, const pi_att
     return PI_OK;
 }
 
+int pi_attn_debug_tree_kernel(const pi_attn_cache_t *cache, int B, int T, int width, int H, int k_local, int period, int S, int mode) {
+    const int any = 0;
+    const float alpha = 0.f;
+    const pi_attn_batch_t batch{&any, &any, &any, B, T, width};  // (not read)
+    pi::ExtendTreeArgs t{};
+    int rc = make_cache(cache, width, t.e.cache);
+    if (rc == PI_OK) rc = make_batch(&batch, t.e.batch);
+    if (rc == PI_OK) rc = make_attention(t.e.cache, H, k_local, period, S, mode, &alpha, t.e.s);
+    if (rc != PI_OK) return rc;
+    bool fits = (long long)T * H <= 0x7fffffffLL;
+    const bool few = fits && pi::tree_few(t, fits);
+    return !fits ? PI_ERR_UNSUPPORTED : few ? 0 : 1;
+}
+
 }  // extern "C"

@@ -1,5 +1,6 @@
 """GPU tests of rotary positions and of the speculative step at the ends of their ranges: sums over long rows, weights that are nearly
 nothing, far positions, many trees, a rotary that goes while a stream still reads it."""
+import ctypes
 import math
 from fractions import Fraction
 
@@ -10,7 +11,9 @@ import torch
 import paged_ref as ref
 import step_ref as sref
 import structured_sparse_long_gb300 as pa
+import test_gpu_step as steps
 from structured_sparse_long_gb300 import build as pbuild
+from structured_sparse_long_gb300 import paged
 
 pytestmark = pytest.mark.gpu
 
@@ -108,6 +111,39 @@ def test_more_trees_than_a_launch_of_the_short_kernel_has_places():
     bad[68001] = 5  # of the second launch's sequences one whose offsets decrease
     pa.extend_tree(q, cache, table, bad, *args[3:], 2, 3, 1)
     assert pa.status() == -8
+
+
+def tree_kernel(kv, d, H, Hkv, page, n, width, kl, per, S, ecp=False, extra=0):
+    """0: the short chunks' kernel, 1: the tensor cores'."""
+    kind, a16 = list(ref.DTYPE).index(kv), 0x10000
+    c = paged._CacheStruct(a16, a16, a16 if kind else None, a16 if kind else None, kind, 1, Hkv, page, d)
+    return paged._load().pi_attn_debug_tree_kernel(ctypes.byref(c), len(n), sum(n) + extra, width, H, kl, per, S, pa.MODE_ECP if ecp else pa.MODE_PI)
+
+
+def test_the_cases_of_trees_reach_the_kernel_that_they_are_about():
+    """The tests of tree attention ask for the tensor cores' kernel by many further trees, and have the short one without (but for more than 16
+    heads on one, which it cannot take, and a few large trees)."""
+    seen = []
+    for case in steps.TREES:
+        kv, d, H, Hkv, page, ctx, n, kl, per, S, ecp = case[:11]
+        for more in (0, steps.MANY):
+            m = n + [steps.NODES] * more
+            width = max(-(-(c + x) // page) for c, x in zip(ctx + [0] * more, m)) + 1
+            got = tree_kernel(kv, d, H, Hkv, page, m, width, kl, per, S, ecp, 2)
+            assert got == 1 if more or H // Hkv > 16 else got in (0, 1), case
+            seen.append((bool(more), got, kv))
+    assert {x[2] for x in seen if x[1] == 0} == {x[2] for x in seen if x[1] == 1} == set(ref.DTYPE)
+    assert sum(x[:2] == (False, 0) for x in seen) >= 9
+    for n in (12, 100):
+        for kv in ("bf16", "int8"):
+            assert tree_kernel(kv, 64, 4, 2, 16, [n], 10, 300, 400, 2) == 0
+            assert tree_kernel(kv, 64, 4, 2, 16, [n] + [steps.NODES] * steps.MANY, 18, 300, 400, 2) == 1
+    for B, kv in ((400, "bf16"), (1300, "int8"), (1300, "bf16")):
+        assert tree_kernel(kv, 64, 8, 2, 16, [34] * B, 17, 9, 4, 3) == 1
+    assert tree_kernel("bf16", 64, 8, 1, 16, [1] * 70000, 1, 2, 3, 1) == 0
+    for kv in ("bf16", "e4m3"):
+        assert tree_kernel(kv, 128, 16, 4, 256, [20], 8388352, 300, 4096, 3) == 0
+        assert tree_kernel(kv, 128, 16, 4, 256, [256] * 4, 8388352, 300, 4096, 3) == 1
 
 
 @pytest.mark.parametrize("trees", [1, 4])

@@ -100,3 +100,18 @@ def test_a_rotarys_steps_are_known_to_every_stream_that_reads_them(native, monke
         call()
         call()
         assert known == list(range(1, i + 2))
+
+
+def test_the_trees_kernel_is_told_for_the_sizes_of_a_call():
+    """And a call's own errors for sizes that it refuses; as if on one SM where there is no device."""
+    pbuild.build()
+    f, a16 = paged._load().pi_attn_debug_tree_kernel, 0x10000
+
+    def ask(B=1, T=26, width=1100, H=16, kl=256, per=1024, S=4, mode=0, **kw):
+        c = paged._CacheStruct(*(kw.get(x, y) for x, y in (("k", a16), ("v", a16), ("ks", None), ("vs", None), ("kv", 0), ("pages", 4), ("Hkv", 4),
+                                                           ("page", 64), ("d", 128))))
+        return f(ctypes.byref(c), B, T, width, H, kl, per, S, mode)
+
+    assert ask() in (0, 1) and ask(H=80) == 1  # (20 heads on one)
+    assert ask(k=None) == -1 and ask(B=0) == ask(T=0) == ask(H=6) == ask(per=0) == -2
+    assert ask(d=96) == ask(mode=2) == ask(T=1 << 28) == -3 and ask(v=a16 + 8) == -4
