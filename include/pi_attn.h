@@ -467,8 +467,9 @@ int pi_attn_rotary_append(const void *q, long long q_stride, const void *k, long
  *   The node at position i attends U(i): a position below ctx[b] is the sequence's cached row of that number, one
  *   from ctx[b] on is the node's ancestor (or itself) at that depth.  Arguments, layouts and errors as pi_attn_extend,
  *   with parent [T] (not NULL); a sequence that is left out keeps its rows of out and lse.  T * H < 2^31, and
- *   fewer than 2^31 blocks of 128 rows (else PI_ERR_UNSUPPORTED).  No workspace.  A node's results depend on the rows that it attends alone.  Weights are rounded as in
- *   pi_attn_extend.  Deterministic.
+ *   fewer than 2^31 blocks of 128 rows (else PI_ERR_UNSUPPORTED).  No workspace.  A node's results depend on the rows that it attends alone.  Weights are
+ *   held to 2^-15 of each for their product with the values (two bf16 terms), so that the outputs' own rounding is what tells them
+ *   from 32-bit weights'.  Deterministic.
  */
 int pi_attn_extend_tree(const void *q, long long q_stride, const pi_attn_cache_t *cache, const pi_attn_batch_t *batch,
                         const int *parent, const float *alpha, int H, int k_local, int period, int S, int mode, void *out,

@@ -15,7 +15,8 @@
 //   * The softmax keeps a running maximum and sum per head in 32 bits: a lane holds heads 2t, 2t+1 of keys g,
 //     g + 8, so a tile's maximum takes three shuffles per head; the sums stay per lane until the end.
 //   * O^T += V^T P^T (16 elements of d x 8 heads): P^T is S^T's accumulator rounded to bf16 (half a step
-//     of 2^-7 relative, as in the forward) and transposed by movmatrix; lane 4 g + t holds 16 (8-bit
+//     of 2^-7 relative, as in the forward; drafted trees: two bf16 terms, whose sum is within 2^-15; one tree of 26 nodes 9.9 us either way) and
+//     transposed by movmatrix; lane 4 g + t holds 16 (8-bit
 //     cache: 16 or 8) contiguous bytes of V rows 2t, 2t+1, 2t+8, 2t+9, which two byte permutes per word
 //     turn into the pairs of keys that the product wants.
 //   * 8-bit codes become bf16 in registers (exact, see pi_paged.cuh).
@@ -166,13 +167,13 @@ __device__ __forceinline__ void load_q(uint2 (&q)[D / 16], const __nv_bfloat16 *
     }
 }
 
-// o[nh][j] += V^T P^T; accumulator j holds elements elem(j, g), elem(j, g) + 1 of heads 2t, 2t + 1
+// o[nh][j] += V^T P^T, P being the sum of TERMS matrices; accumulator j holds elements elem(j, g), elem(j, g) + 1 of heads 2t, 2t + 1
 template <int D, int KV>
 __device__ __forceinline__ int elem(int j, int g) {
     return KV == kKvBf16 ? 64 * (j >> 2) + 8 * g + 2 * (j & 3) : (D / 8) * g + 2 * j;
 }
-template <int D, int KV, int NH>
-__device__ __forceinline__ void accumulate(const Frag<D, KV> &f, const uint32_t (&p)[NH][2], float (&o)[NH][D / 16][4]) {
+template <int D, int KV, int NH, int TERMS>
+__device__ __forceinline__ void accumulate(const Frag<D, KV> &f, const uint32_t (&p)[TERMS][NH][2], float (&o)[NH][D / 16][4]) {
     if constexpr (KV == kKvBf16) {
 #pragma unroll
         for (int x = 0; x < f.CV; ++x) {
@@ -185,7 +186,9 @@ __device__ __forceinline__ void accumulate(const Frag<D, KV> &f, const uint32_t 
                 const uint32_t a0 = __byte_perm(r[0][w], r[1][w], 0x5410), a1 = __byte_perm(r[0][w], r[1][w], 0x7632);
                 const uint32_t a2 = __byte_perm(r[2][w], r[3][w], 0x5410), a3 = __byte_perm(r[2][w], r[3][w], 0x7632);
 #pragma unroll
-                for (int nh = 0; nh < NH; ++nh) mma_bf16(o[nh][4 * x + w], a0, a1, a2, a3, p[nh][0], p[nh][1]);
+                for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+                    for (int y = 0; y < TERMS; ++y) mma_bf16(o[nh][4 * x + w], a0, a1, a2, a3, p[y][nh][0], p[y][nh][1]);
             }
         }
     } else {
@@ -199,7 +202,9 @@ __device__ __forceinline__ void accumulate(const Frag<D, KV> &f, const uint32_t 
                 codes_to_bf16<KV>(__byte_perm(f.v[0][w], f.v[1][w], sel), s01, s01.big, a0, a1);
                 codes_to_bf16<KV>(__byte_perm(f.v[2][w], f.v[3][w], sel), s23, s23.big, a2, a3);
 #pragma unroll
-                for (int nh = 0; nh < NH; ++nh) mma_bf16(o[nh][2 * w + h], a0, a1, a2, a3, p[nh][0], p[nh][1]);
+                for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+                    for (int y = 0; y < TERMS; ++y) mma_bf16(o[nh][2 * w + h], a0, a1, a2, a3, p[y][nh][0], p[y][nh][1]);
             }
         }
     }
@@ -395,7 +400,8 @@ paged_rows_kernel(const __grid_constant__ Args a) {
         float sc[NH][4] = {};
         scores<D, KV, NH>(f, q, sc, t);
         if (u == 1 && tile + step < n_tiles) key((tile + (lane < KEYS ? step : 2 * step)) * KEYS + (lane & (KEYS - 1)), row, tag);
-        uint32_t p[NH][2];
+        constexpr int TERMS = TREE ? 2 : 1;  // of a weight, bf16 each
+        uint32_t p[TERMS][NH][2];
 #pragma unroll
         for (int nh = 0; nh < NH; ++nh) {
             float pr[4];
@@ -428,10 +434,18 @@ paged_rows_kernel(const __grid_constant__ Args a) {
                     o[nh][j][2 + e] *= corr;
                 }
             }
-            p[nh][0] = transpose8(pack_bf16x2(pr[0], pr[1]));
-            p[nh][1] = transpose8(pack_bf16x2(pr[2], pr[3]));
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                if constexpr (TREE) {  // the weights' high halves, and what those leave, rounded
+                    const uint32_t u0 = __float_as_uint(pr[2 * x]), u1 = __float_as_uint(pr[2 * x + 1]);
+                    p[0][nh][x] = transpose8(__byte_perm(u0, u1, 0x7632));
+                    p[1][nh][x] = transpose8(pack_bf16x2(pr[2 * x] - __uint_as_float(u0 & 0xffff0000u), pr[2 * x + 1] - __uint_as_float(u1 & 0xffff0000u)));
+                } else {
+                    p[0][nh][x] = transpose8(pack_bf16x2(pr[2 * x], pr[2 * x + 1]));
+                }
+            }
         }
-        accumulate<D, KV, NH>(f, p, o);
+        accumulate<D, KV, NH, TERMS>(f, p, o);
     }
 
     // ---- the warps' partial states to shared memory
@@ -675,11 +689,11 @@ cudaError_t launch_extend_few(const ExtendArgs &e, cudaStream_t st) {
 // Whether this kernel beats the tensor-core one for a batch of trees (pi_tree_tc.cu), and whether either can number its work.  As in
 // extend_few_rows, by two estimates in us from the sizes that the host knows, all trees taken as equally large: this kernel's waves of
 // rounds of tiles (split()), and the other's turns of blocks, each a start and tiles of 32 keys.  Fitted to 204 shapes (16 heads on 4, 8 on 1 and 16 on
-// 16, d = 128; 12 on 12, 8 on 8 and 7 on 1, d = 64; bf16 and e4m3; 1 to 64 trees of 2 to 160 nodes), of which it gets 191 right to 5 %
-// and the others wrong by 6 to 17 %.  For instance (this kernel / the other):
-//   16 heads on 4, d = 128, band 256, bf16:  1 tree of 26 nodes 9.2 / 11.9, of 160 14.8 / 14.6; 8 of 32 16.9 / 12.1, 32 of 32 63.8 / 12.9
-//                                     e4m3:  1 of 26 9.6 / 15.7; 8 of 8 11.7 / 14.4, 8 of 32 20.2 / 15.8
-//   12 on 12, d = 64, band 128, bf16:  1 of 26 7.4 / 9.3; 16 of 16 10.2 / 11.6, 32 of 32 27.9 / 18.8
+// 16, d = 128; 12 on 12, 8 on 8 and 7 on 1, d = 64; bf16 and e4m3; 1 to 64 trees of 2 to 160 nodes), of which it gets 196 right to 5 %
+// and the others wrong by 5 to 21 %.  For instance (this kernel / the other):
+//   16 heads on 4, d = 128, band 256, bf16:  1 tree of 26 nodes 9.3 / 12.9, of 160 15.4 / 15.7; 8 of 32 17.8 / 13.2, 32 of 32 65.0 / 14.0
+//                                     e4m3:  1 of 26 9.9 / 16.5; 8 of 8 12.3 / 15.2, 8 of 32 21.3 / 16.9
+//   12 on 12, d = 64, band 128, bf16:  1 of 26 7.5 / 9.6; 16 of 16 11.5 / 12.7, 32 of 32 28.7 / 20.3
 bool tree_few(const ExtendTreeArgs &t, bool &fits) {
     const ExtendArgs &e = t.e;
     const Shape &s = e.s;

@@ -146,6 +146,24 @@ def test_the_cases_of_trees_reach_the_kernel_that_they_are_about():
         assert tree_kernel(kv, 128, 16, 4, 256, [256] * 4, 8388352, 300, 4096, 3) == 1
 
 
+@pytest.mark.parametrize("more", [0, steps.MANY])
+@pytest.mark.parametrize("kv,d,H,Hkv,ecp", [("bf16", 128, 4, 1, False), ("e4m3", 128, 8, 2, False), ("int8", 64, 3, 3, False), ("bf16", 64, 16, 1, True)])
+def test_weights_of_few_keys_are_not_rounded_to_bf16(kv, d, H, Hkv, ecp, more):
+    """Rows of up to nine keys, where a rounded weight does not drown in the others.  Outputs are rounded once (half a step, 2^-8), weights held to
+    2^-15, and a score's d products are summed in 32 bits (2^-12 of the weights, as in paged_ref.check_attention)."""
+    ctx, n, kl, per, S = [3, 20, 0], [6, 9, 12], 4 if ecp else 5, 7, 0 if ecp else 3
+    cache, table, cu, parents, q, alpha, held = steps.tree_case(kv, d, H, Hkv, 16, ctx + [0] * more, n + [steps.NODES] * more, seed=d + H, ecp=ecp)
+    assert tree_kernel(kv, d, H, Hkv, 16, n + [steps.NODES] * more, table.shape[1], kl, per, S, ecp) == bool(more)
+    mode = pa.MODE_ECP if ecp else pa.MODE_PI
+    out, lse = pa.extend_tree(q, cache, dev(table), dev(cu), dev(ctx + [0] * more), dev(sum(parents, [])), None if ecp else alpha.cuda(), kl, per, S, mode)
+    for b in range(3):
+        rows = slice(cu[b], cu[b + 1])
+        want, _, size = sref.tree_attention(q[rows].cpu(), *held[b], None if ecp else alpha[rows], ctx[b], parents[b], kl, per, S, mode)
+        off = np.abs(out[rows].float().cpu().numpy().astype(np.float64) - want)
+        bound = 2.0 ** -8 * np.abs(want) + (2.0 ** -15 + 2.0 ** -12) * size + 1e-30
+        assert (off <= bound).all(), f"sequence {b}: off by {(off / bound).max():.2f} of its bound"
+
+
 @pytest.mark.parametrize("trees", [1, 4])
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 def test_a_tree_at_the_last_positions(kv, trees):
