@@ -492,7 +492,7 @@ int pi_attn_extend_tree(const void *q, long long q_stride, const pi_attn_cache_t
  *   Writes path [T] int32: the accepted nodes of sequence b from path[cu[b]] on, the rest of its places -1; count [B]: how
  *   many; next [B]: the next token, or -1 where no p is above 0.  A sequence without tokens, or one that is left out, gets
  *   count 0 and next -1, and keeps its places of path.  w, s and a are carried in 48 bits: a weight is right to 2^-46 of its p (and a's
- *   error times q), a sum over a row to 2^-43 + V 2^-54 of the row's p's, several bits better as a rule.  1 <= B <= 65535, T > 0, 0 < V <= 2^30,
+ *   error times q), a sum over a row to 2^-42 + V 2^-54 of the row's p's, several bits better as a rule.  1 <= B <= 65535, T > 0, 0 < V <= 2^30,
  *   T * stride < 2^60.  Deterministic.
  */
 int pi_attn_verify_tree(const float *target, long long target_stride, const float *draft, long long draft_stride,
