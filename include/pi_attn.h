@@ -470,6 +470,8 @@ int pi_attn_rotary_append(const void *q, long long q_stride, const void *k, long
  *   fewer than 2^31 blocks of 128 rows (else PI_ERR_UNSUPPORTED).  No workspace.  A node's results depend on the rows that it attends alone.  Weights are
  *   held to 2^-15 of each for their product with the values (two bf16 terms), so that the outputs' own rounding is what tells them
  *   from 32-bit weights'.  Deterministic.
+ *   One of two kernels takes the call, chosen by B and T as if all trees had equally many nodes.  Trees of very different sizes may still
+ *   go in one call: 16 heads on 4, d = 128, bf16, one tree of 160 nodes and 63 of a single one take 16.6 us, in two calls 15.2 and 15.0.
  */
 int pi_attn_extend_tree(const void *q, long long q_stride, const pi_attn_cache_t *cache, const pi_attn_batch_t *batch,
                         const int *parent, const float *alpha, int H, int k_local, int period, int S, int mode, void *out,

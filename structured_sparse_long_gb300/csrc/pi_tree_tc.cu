@@ -7,7 +7,7 @@
 // than one node's, and since its rows are gathered one by one the few keys of a skip window cost no tile of their own.
 //   warps 0-3   softmax and epilogue, a thread per row: scores from TMEM, masks as 32 bits per tile, a running reference and sum,
 //               P back to TMEM as two bf16 terms, whose sum is within 2^-15 of it (the sum takes the unrounded values; one
-//               term, as in the forward: 48 trees of up to 64 nodes, bf16, 17.4 instead of 18.5 us, and 2.3e-3 instead of 1.7e-3 from
+//               term, as in the forward: 48 trees of up to 64 nodes, bf16, 17.4 instead of 18.6 us, and 2.3e-3 instead of 1.7e-3 from
 //               64 bits, of which the output's own rounding is 1.7e-3)
 //   warps 4-7   producers: the tile's page-table entries a tile ahead, rows of K and V into the swizzled layout of the
 //               products, by cp.async (bf16), or by way of the tile as it is, whose 8-bit codes become bf16 (exact, pi_paged.cuh)

@@ -14,7 +14,7 @@
 // instruction: a dependent fp64 operation takes 75 cycles on a GB300, the sum of two pairs 37.
 //
 // What bounds it: few sequences, the chain gather (0.8 us) -> tests (0.2 each; 0.4 where siblings were refused) -> pass (1.7) -> search (1.7); 32 trees
-// over 128001 tokens (29.0 us), their passes one after the other: 6 us the first, whose rows come from HBM, 4.5 the others, in which warps wait
+// over 128001 tokens (29.6 us), their passes one after the other: 6 us the first, whose rows come from HBM, 4.5 the others, in which warps wait
 // for loads and at the cluster's barrier (issue slots are 22 % busy, HBM 17 %).  The rows kept in shared memory from pass to pass changed
 // nothing (30.7 for 30.2), nor did two sets of registers in turn (30.2 for 28.9).
 #include "pi_mma.cuh"

@@ -51,8 +51,10 @@ def rotary_frequencies(rot: int, base: float = 10000.0, scaling: str = "none", f
     f_t = base^(-2 t / rot), scaled for contexts `factor` times as long as trained on:
       "linear"  f_t / factor (positions interpolated);
       "ntk"     with base * factor^(rot / (rot - 2)): the slowest pair is interpolated, the fastest kept;
-      "yarn"    pairs that make at least `high` turns over the `original` length kept, those with at most `low` interpolated,
-                in between a linear mix; the factor is 0.1 ln(factor) + 1.
+      "yarn"    pairs that make at least `high` turns over the `original` length kept, those with at most `low` interpolated, in
+                between a mix that is linear in the number of turns, as the method was published; the factor is 0.1 ln(factor) + 1.
+                Much model code mixes linearly in the pair's number t instead, between two rounded bounds: the frequencies in
+                between differ by up to three times, so a checkpoint trained with that code needs its own list (Rotary's `freqs`).
     """
     if rot <= 0 or rot % 2:
         raise ValueError("rot must be a positive even number")
