@@ -359,7 +359,8 @@ int pi_attn_cache_read(const pi_attn_cache_t *cache, const pi_attn_batch_t *batc
  *   A sequence with an offset or length out of range is left out, its rows of out and lse
  *   as they were (where cu decreases anywhere, any of the batch's rows may be); a row that attends a key on a page out of range is undefined.
  *   A token's results depend on the rows that it attends alone: what the other rows hold, NaN
- *   and infinities among it, does not matter.  Weights are rounded to bf16 (2^-8 of each at
+ *   and infinities among it, does not matter (but to the last bit: rows beside such a one may be
+ *   computed again, which adds in another order).  Weights are rounded to bf16 (2^-8 of each at
  *   most) for their product with the values, as in pi_attn_fwd; lse sums them unrounded.
  *   The kernels are chosen by B and T, as if all sequences were equally long: a long chunk and many
  *   single tokens take less time as two calls (2000 tokens and 63 single ones, 16 heads on 4, d = 128:
@@ -467,8 +468,8 @@ int pi_attn_rotary_append(const void *q, long long q_stride, const void *k, long
  *   The node at position i attends U(i): a position below ctx[b] is the sequence's cached row of that number, one
  *   from ctx[b] on is the node's ancestor (or itself) at that depth.  Arguments, layouts and errors as pi_attn_extend,
  *   with parent [T] (not NULL); a sequence that is left out keeps its rows of out and lse.  T * H < 2^31, and
- *   fewer than 2^31 blocks of 128 rows (else PI_ERR_UNSUPPORTED).  No workspace.  A node's results depend on the rows that it attends alone.  Weights are
- *   held to 2^-15 of each for their product with the values (two bf16 terms), so that the outputs' own rounding is what tells them
+ *   fewer than 2^31 blocks of 128 rows (else PI_ERR_UNSUPPORTED).  No workspace.  A node's results depend on the rows that it attends alone, as
+ *   pi_attn_extend's do.  Weights are held to 2^-15 of each for their product with the values (two bf16 terms), so that the outputs' own rounding is what tells them
  *   from 32-bit weights'.  Deterministic.
  *   One of two kernels takes the call, chosen by B and T as if all trees had equally many nodes.  Trees of very different sizes may still
  *   go in one call: 16 heads on 4, d = 128, bf16, one tree of 160 nodes and 63 of a single one take 16.6 us, in two calls 15.2 and 15.0.

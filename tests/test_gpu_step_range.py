@@ -164,6 +164,29 @@ def test_weights_of_few_keys_are_not_rounded_to_bf16(kv, d, H, Hkv, ecp, more):
         assert (off <= bound).all(), f"sequence {b}: off by {(off / bound).max():.2f} of its bound"
 
 
+@pytest.mark.parametrize("more", [0, steps.MANY])
+def test_infinite_values_reach_those_that_attend_them(more):
+    """An infinity among a node's values: that element of its own row and its descendants' is the infinity (not a NaN, whichever term of a weight
+    is zero), all other elements are finite and as without it: equal but for the order of sums (rows that share a tile with it are computed again), so
+    off by half a step of each output, 2^-8 twice, and 2^-12 of sums of weighted values below 4."""
+    H, Hkv, d, ctx, n = 8, 2, 64, 20, 30
+    cache, table, cu, parents, q, alpha, held = steps.tree_case("bf16", d, H, Hkv, 16, [ctx] + [0] * more, [n] + [steps.NODES] * more, seed=3)
+    args = (cache, dev(table), dev(cu), dev([ctx] + [0] * more), dev(sum(parents, [])), alpha.cuda(), 300, 400, 2)
+    want, want_lse = (t[:n] for t in pa.extend_tree(q, *args))
+    k, v = (t[ctx:].clone() for t in held[0])
+    v[4, 0, 7], v[4, 1, 60] = float("inf"), -float("inf")
+    pa.cache_append(k.cuda(), v.cuda(), cache, dev(table[:1]), dev([0, n]), dev([ctx]))
+    out, lse = (t[:n] for t in pa.extend_tree(q, *args))
+    below = torch.tensor([4 in sref.line(parents[0], j) for j in range(n)], device="cuda")
+    assert 1 < int(below.sum()) < n
+    assert (out[below, :4, 7] == float("inf")).all() and (out[below, 4:, 60] == -float("inf")).all()
+    other = torch.ones_like(out, dtype=torch.bool)
+    other[below, :4, 7] = other[below, 4:, 60] = False
+    off = (out.float() - want.float()).abs()[other]
+    assert torch.isfinite(out[other]).all() and (off <= 2.0 ** -7 * want.float().abs()[other] + 2.0 ** -10).all()
+    assert torch.equal(lse, want_lse)
+
+
 @pytest.mark.parametrize("trees", [1, 4])
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 def test_a_tree_at_the_last_positions(kv, trees):
