@@ -85,6 +85,25 @@ def test_a_rotary_that_goes_while_another_stream_still_reads_it():
     assert torch.equal(got, want) and len(others) == 100
 
 
+def test_a_rotary_whose_first_call_on_a_stream_is_captured():
+    """The stream is recorded during the capture; replays read the steps, and the object goes after the graph without a trace."""
+    x = torch.randn(1, 2, 50, 64, device="cuda")
+    want, _ = pa.rotary(x, None, pa.Rotary(64), 3)
+    r, side, out = pa.Rotary(64), torch.cuda.Stream(), torch.zeros_like(x)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        pa.rotary(x, None, r, 3, q_out=out)
+    out.zero_()
+    for _ in range(2):
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    del g, r
+    y, _ = pa.rotary(x, None, pa.Rotary(64), 3)
+    assert torch.equal(y, want)
+
+
 # ------------------------------------------------------------------ trees
 
 def test_more_trees_than_a_launch_of_the_short_kernel_has_places():
